@@ -55,6 +55,9 @@ EXPORTED_SYMBOLS = (
     "attn_softmax_rows",
     "attn_softmax_rows_workspace_bytes",
     "attn_layernorm_rows",
+    "attn_qk_norm_rope",
+    "attn_qk_norm_rope_bwd",
+    "attn_qk_norm_rope_bwd_workspace_bytes",
 )
 
 
@@ -142,6 +145,13 @@ def load_library(path: str | None = None):
     lib.attn_softmax_rows_workspace_bytes.restype = ctypes.c_size_t
     lib.attn_layernorm_rows.argtypes = [vp, vp, vp, vp, i64, i, f, vp]
     lib.attn_layernorm_rows.restype = i
+    lib.attn_qk_norm_rope.argtypes = [vp] * 7 + [i64, i64, vp, vp, i] + [vp] * 4 + [i] * 5 + [f, i, vp]
+    lib.attn_qk_norm_rope.restype = i
+    lib.attn_qk_norm_rope_bwd.argtypes = ([vp] * 11 + [i64, i64, vp, vp, i] + [vp] * 6 + [i] * 5 + [f, i, vp,
+                                                                                                   ctypes.c_size_t, vp])
+    lib.attn_qk_norm_rope_bwd.restype = i
+    lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i]
+    lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
     if path is None:
         _lib = lib
     return lib
@@ -347,6 +357,161 @@ def layernorm_rows(x, gamma, beta, eps: float = 1e-5, out=None, stream=None):
                                      x.numel() // N, N, float(eps), _stream_handle(stream))
     _check(st, "attn_layernorm_rows")
     return out
+
+
+def _on_device(device):
+    """A context with `device` current: nothing to do where it is already."""
+    import contextlib
+
+    import torch
+
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _new_for(stream, *tensors):
+    """Tensors allocated here on the current stream and used on `stream`."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _views(named, device):
+    """Checks [B, H, N, d] bf16 views on one device; returns a host array of their strides, three each,
+    and the address of each view's strides in it."""
+    import torch
+
+    flat = []
+    for name, t, shape in named:
+        if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a bf16 CUDA tensor [B, H, N, d] with d contiguous, on q's device")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}")
+        flat += t.stride()[:3]
+    arr = (ctypes.c_int64 * len(flat))(*flat)
+    base = ctypes.addressof(arr)
+    return arr, [base + 24 * i for i in range(len(named))]
+
+
+def _rotation(q, k, positions, inv_freq, sections, weights):
+    """The checks both directions of qk_norm_rope share.  Returns the sections as a host array, their
+    number, and the positions' axis and batch strides."""
+    import torch
+
+    if q.dim() != 4 or k.dim() != 4 or not q.is_cuda:
+        raise ValueError("q and k must be CUDA tensors [B, H, N, d]")
+    B, _, N, d = q.shape
+    if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+        raise ValueError("q and k must share B, N and d")
+    if inv_freq.dtype != torch.float64 or inv_freq.device != q.device or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 tensor of one axis on q's device")
+    if sections is None:
+        sections = (inv_freq.shape[0],)
+    if sum(sections) != inv_freq.shape[0]:
+        raise ValueError("sections must add up to the number of frequencies")
+    if positions.dtype != torch.int32 or positions.device != q.device:
+        raise ValueError("positions must be an int32 tensor on q's device")
+    while positions.dim() < 3 and (positions.dim() < 2 or len(sections) == 1):  # [N] or [B, N]: one axis
+        positions = positions.unsqueeze(0)
+    A = len(sections)
+    if positions.dim() != 3 or positions.shape[0] != A or positions.shape[1] not in (1, B) or positions.shape[2] != N:
+        raise ValueError("positions must be [axes, B, N] (B may be 1; [B, N] or [N] for a single axis)")
+    if N > 1 and positions.stride(2) != 1:
+        raise ValueError("positions must be contiguous along the tokens")
+    for w in weights:
+        if w is not None and (w.dtype != torch.bfloat16 or w.device != q.device or w.shape != (d,) or
+                              not w.is_contiguous()):
+            raise ValueError("norm weights must be contiguous bf16 tensors [d] on q's device")
+    return (ctypes.c_int * A)(*sections), A, positions, positions.stride(0), 0 if positions.shape[1] == 1 else positions.stride(1)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, sections=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Queries and keys made ready for attn_fwd: RMS norm of each head and rotary positions, one pass.
+
+    q, k       : bf16 CUDA views [B, Hq, N, d] and [B, Hk, N, d], d contiguous (64 or 128), other strides
+                 multiples of 8: for example slices of a projection's output, transposed
+    positions  : int32 CUDA [axes, B, N] (B may be 1); [B, N] or [N] for a single axis
+    inv_freq   : float64 CUDA, radians per position of each rotated pair (at most d / 2, a multiple of 8)
+    q_weight, k_weight : bf16 [d] norm weights; None: that tensor is rotated without a norm
+    sections   : how many pairs turn by each position axis, in order (default: all by one axis)
+    interleaved: pairs are neighbours (2i, 2i + 1) instead of halves (i, i + pairs)
+    q_out, k_out : optional bf16 views of the outputs' shapes (a cache's rows, or q and k themselves);
+                 default: new contiguous tensors, the layout attn_fwd reads
+    Returns (q_out, k_out)."""
+    import torch
+
+    lib = load_library()
+    sec, A, positions, pa, pb = _rotation(q, k, positions, inv_freq, sections, (q_weight, k_weight))
+    B, Hq, N, d = q.shape
+    Hk = k.shape[1]
+    with _on_device(q.device):
+        fresh = []
+        if q_out is None:
+            q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+            fresh.append(q_out)
+        if k_out is None:
+            k_out = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
+            fresh.append(k_out)
+        _new_for(stream, *fresh)
+        strides, at = _views((("q", q, q.shape), ("k", k, k.shape), ("q_out", q_out, q.shape), ("k_out", k_out, k.shape)),
+                             q.device)
+        st = lib.attn_qk_norm_rope(q.data_ptr(), at[0], k.data_ptr(), at[1],
+                                   None if q_weight is None else q_weight.data_ptr(),
+                                   None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb,
+                                   inv_freq.data_ptr(), sec, A, q_out.data_ptr(), at[2], k_out.data_ptr(), at[3],
+                                   B, Hq, Hk, N, d, eps, int(bool(interleaved)), _stream_handle(stream))
+    _check(st, "attn_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
+    """Device bytes qk_norm_rope_bwd needs with a norm, on the current device."""
+    return int(load_library().attn_qk_norm_rope_bwd_workspace_bytes(d))
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k_weight=None, sections=None,
+                     eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None, workspace=None, stream=None):
+    """Gradients of qk_norm_rope for upstream gradients of its outputs (attn_bwd's dQ and dK).
+
+    dq_out, dk_out : bf16 CUDA views shaped like q and k; q, k and the rest: as given to qk_norm_rope
+    dq, dk     : optional bf16 views for the gradients of q and k (default: new contiguous tensors)
+    workspace  : optional uint8 CUDA tensor of qk_norm_rope_bwd_workspace_bytes(d) bytes
+    Returns (dq, dk, dq_weight, dk_weight), the weights' gradients fp32 [d], None without a weight."""
+    import torch
+
+    lib = load_library()
+    sec, A, positions, pa, pb = _rotation(q, k, positions, inv_freq, sections, (q_weight, k_weight))
+    B, Hq, N, d = q.shape
+    Hk = k.shape[1]
+    with _on_device(q.device):
+        fresh = []
+        if dq is None:
+            dq = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+            fresh.append(dq)
+        if dk is None:
+            dk = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
+            fresh.append(dk)
+        dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+        dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+        fresh += [t for t in (dwq, dwk) if t is not None]
+        if workspace is None and (dwq is not None or dwk is not None):
+            workspace = torch.empty(lib.attn_qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=q.device)
+            fresh.append(workspace)
+        if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != q.device or
+                                      not workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+        _new_for(stream, *fresh)
+        strides, at = _views((("dq_out", dq_out, q.shape), ("dk_out", dk_out, k.shape), ("q", q, q.shape),
+                              ("k", k, k.shape), ("dq", dq, q.shape), ("dk", dk, k.shape)), q.device)
+        st = lib.attn_qk_norm_rope_bwd(
+            dq_out.data_ptr(), at[0], dk_out.data_ptr(), at[1], q.data_ptr(), at[2], k.data_ptr(), at[3],
+            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+            positions.data_ptr(), pa, pb, inv_freq.data_ptr(), sec, A, dq.data_ptr(), at[4], dk.data_ptr(), at[5],
+            None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), B, Hq, Hk, N, d, eps,
+            int(bool(interleaved)), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), _stream_handle(stream))
+    _check(st, "attn_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
 
 
 def attn_fwd_noalloc(q, k, v, out, lse, causal: bool = False, scale: float | None = None, stream=None):

@@ -360,6 +360,76 @@ size_t attn_softmax_rows_workspace_bytes(int64_t R, int N);
 int attn_layernorm_rows(const void* X, const void* gamma, const void* beta, void* Y, int64_t R, int N, float eps,
                         cudaStream_t stream);
 
+/*
+ * attn_qk_norm_rope - queries and keys made ready for attn_fwd: per token and
+ * head, the RMS norm of the row and the rotation by the token's position, in
+ * one pass over Q and K (the fusion the "IO-Aware Algorithms" page asks of
+ * memory-bound steps: one read and one write).  In fp32,
+ *     y = x / sqrt(mean_j x_j^2 + eps) * weight        (a null weight: y = x),
+ *     (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
+ * for each rotated pair, t = position[axis(i)] * inv_freq[i] for pair i;
+ * elements past the rotated ones keep y.  Rounded to bf16 once, at the end.
+ * The angle is exact modulo a turn for every int32 position, up to the
+ * rounding of inv_freq / (2 pi) to 2^-53 of a turn (times the position).
+ *   Q, Qout : bf16 [B, Hq, N, d] device views, d fastest, 16-byte aligned
+ *   K, Kout : bf16 [B, Hk, N, d] device views; Hq and Hk are independent
+ *   *_strides : host arrays of three strides in elements (batch, head, token),
+ *             multiples of 8 (ATTN_ERR_MISALIGNED), copied by the call; NULL for
+ *             a contiguous tensor.  So Q and K may be slices of a projection's
+ *             output [B, N, ...] and the outputs rows of a cache.  An input stride may
+ *             be 0 (a broadcast axis); a written axis longer than 1 may not
+ *             (ATTN_ERR_INVALID_ARG).  In place (an output with its input's
+ *             address and strides) is allowed, any other overlap is not (not checked).
+ *   q_weight, k_weight : bf16 [d] device, 16-byte aligned, or NULL: that tensor is only rotated
+ *   positions : int32 device, the position of token n of batch b on axis a at
+ *             positions[a * pos_axis_stride + b * pos_batch_stride + n]
+ *             (pos_batch_stride 0: the same for every batch)
+ *   inv_freq : double [sum of sections] device, finite, radians per position
+ *   sections : host array of num_sections (1..4) pair counts, each >= 1: the
+ *             first sections[0] pairs turn by axis 0, the next by axis 1, ...
+ *             Their sum is the number of rotated pairs: at most d / 2, a multiple
+ *             of 8 (ATTN_ERR_UNSUPPORTED otherwise).
+ *   interleaved : 0: pair i is elements (i, i + pairs); otherwise (2 i, 2 i + 1)
+ *   d : 64 or 128;  eps : finite, >= 0;  B, Hq, Hk, N >= 1, products B*N*H < 2^31
+ * Asynchronous on `stream`; no workspace.
+ */
+int attn_qk_norm_rope(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides,
+                      const void* q_weight, const void* k_weight, const int32_t* positions, int64_t pos_axis_stride,
+                      int64_t pos_batch_stride, const double* inv_freq, const int* sections, int num_sections,
+                      void* Qout, const int64_t* qo_strides, void* Kout, const int64_t* ko_strides, int B, int Hq,
+                      int Hk, int N, int d, float eps, int interleaved, cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rope_bwd - gradients of attn_qk_norm_rope for upstream gradients
+ * dQout, dKout of its outputs (attn_bwd's dQ and dK).  With u the upstream row
+ * turned back by the angles and h = x / sqrt(mean x^2 + eps):
+ *     dx = (u w - h mean_j(u_j w_j h_j)) / sqrt(mean x^2 + eps),
+ *     dweight_j = sum over batch, head and token of u_j h_j;
+ * without a weight dx = u, and Q (or K) is not read and may be NULL.
+ *   dQout, Q, dQ : bf16 [B, Hq, N, d] device views, and dKout, K, dK likewise:
+ *             layouts, strides and alignment as above.  dQ may be dQout or Q in
+ *             place (its address and strides).  An expanded input's gradient is that of
+ *             the expanded view: summing it is the caller's.
+ *   dq_weight, dk_weight : fp32 [d] device (written), NULL exactly where the weight is
+ *             NULL (ATTN_ERR_INVALID_ARG otherwise).  Summed in fp32 in a fixed
+ *             order: the same call gives the same bits.
+ *   workspace : device buffer of at least attn_qk_norm_rope_bwd_workspace_bytes(),
+ *             16-byte aligned, owned by the caller, not used by other work while
+ *             this call runs; may be NULL when neither weight is given
+ * Other arguments and errors as attn_qk_norm_rope.  Asynchronous on `stream`.
+ */
+int attn_qk_norm_rope_bwd(const void* dQout, const int64_t* dqo_strides, const void* dKout, const int64_t* dko_strides,
+                          const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides,
+                          const void* q_weight, const void* k_weight, const int32_t* positions, int64_t pos_axis_stride,
+                          int64_t pos_batch_stride, const double* inv_freq, const int* sections, int num_sections,
+                          void* dQ, const int64_t* dq_strides, void* dK, const int64_t* dk_strides, float* dq_weight,
+                          float* dk_weight, int B, int Hq, int Hk, int N, int d, float eps, int interleaved,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Device bytes attn_qk_norm_rope_bwd needs as workspace on the current device:
+ * two fp32 rows of d per CTA; 0 for d other than 64 or 128, or without a device. */
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
+
 #ifdef __cplusplus
 }
 #endif
