@@ -13,8 +13,8 @@
 namespace elsattn {
 namespace {
 
-constexpr int kFwdSteps = 4, kBwdSteps = 1;      // row steps whose loads are in flight together
-constexpr int kFwdCtasPerSm = 2, kBwdCtasPerSm = 2;
+constexpr int kFwdSteps = FU, kBwdSteps = BU;      // slots of a warp's ring of row steps
+constexpr int kFwdCtasPerSm = FC, kBwdCtasPerSm = BC;
 
 // Sizes, alignment and the axis ranges, shared by both directions.
 int fill_params(ReadyParams& p, const int32_t* positions, int64_t pos_axis, int64_t pos_batch, const double* inv_freq,
@@ -51,7 +51,6 @@ int fill_params(ReadyParams& p, const int32_t* positions, int64_t pos_axis, int6
     p.t[0].H = Hq;
     p.t[1].H = Hk;
     for (ReadyTensor& t : p.t) t.steps = (t.H + group - 1) / group;
-    p.part = nullptr;
     return ATTN_OK;
 }
 
@@ -69,25 +68,44 @@ int take_strides(int64_t (&out)[3], const int64_t* s, int B, int H, int N, int d
     return ATTN_OK;
 }
 
-// Whole tokens per warp once there are enough of them to fill the SMs with 16
-// warps each; below that the heads of a token are dealt to more warps.
-void deal_units(ReadyParams& p, int num_sms) {
-    const int total = p.t[0].steps + p.t[1].steps;
-    const int64_t want = (static_cast<int64_t>(total) * p.tokens + num_sms * 16 - 1) / (num_sms * 16);
-    p.steps_per_unit = static_cast<int>(want < 1 ? 1 : want > total ? total : want);
-    p.units_per_token = (total + p.steps_per_unit - 1) / p.steps_per_unit;
-    // units are counted in 32 bits; whole tokens always fit
-    if (static_cast<int64_t>(p.tokens) * p.units_per_token >= (1LL << 32)) {
-        p.steps_per_unit = total;
-        p.units_per_token = 1;
+// How the work is dealt.  A warp works on one tensor: the CTAs are split
+// between Q and K by their share of the steps, a token's angles counting as
+// one step more.  A unit is a whole token once there are enough of them to
+// give the tensor's warps one each; below that a token's heads are dealt to
+// more warps.  Returns the grid.
+unsigned deal_units(ReadyParams& p, int num_sms, int per_sm) {
+    const int64_t most = static_cast<int64_t>(num_sms) * per_sm;
+    const double cost_q = p.t[0].steps + 1, cost_k = p.t[1].steps + 1;
+    int64_t ctas[2];
+    ctas[0] = static_cast<int64_t>(std::lround(most * cost_q / (cost_q + cost_k)));
+    if (ctas[0] < 1) ctas[0] = 1;
+    if (ctas[0] > most - 1) ctas[0] = most - 1;
+    ctas[1] = most - ctas[0];
+    for (int t = 0; t < 2; ++t) {
+        ReadyTensor& r = p.t[t];
+        const int64_t warps = ctas[t] * kReadyWarps;
+        const int64_t want = (static_cast<int64_t>(r.steps) * p.tokens + warps - 1) / warps;
+        r.steps_per_unit = static_cast<int>(want < 1 ? 1 : want > r.steps ? r.steps : want);
+        r.units_per_token = (r.steps + r.steps_per_unit - 1) / r.steps_per_unit;
+        r.units = p.tokens * static_cast<uint32_t>(r.units_per_token);  // below 2 * warps + tokens
+        const int64_t need = (static_cast<int64_t>(r.units) + kReadyWarps - 1) / kReadyWarps;
+        if (need < ctas[t]) ctas[t] = need;
+        r.part = nullptr;
     }
-    p.units = p.tokens * static_cast<uint32_t>(p.units_per_token);
+    p.first_k = static_cast<int>(ctas[0]);
+    return static_cast<unsigned>(ctas[0] + ctas[1]);
 }
 
-unsigned grid_for(const ReadyParams& p, int num_sms, int per_sm) {
-    const int64_t need = (static_cast<int64_t>(p.units) + kReadyWarps - 1) / kReadyWarps;
-    const int64_t most = static_cast<int64_t>(num_sms) * per_sm;
-    return static_cast<unsigned>(need < most ? need : most);
+constexpr int kFwdSmem = kReadyWarps * ReadyRing<128, 2, kFwdSteps>::kBytes;
+constexpr int kBwdSmem = kReadyWarps * ReadyRing<128, 4, kBwdSteps>::kBytes;
+
+// Once per device and kernel (a second call that races with the first sets the same limit again).
+int allow_smem(bool& done, void (*kernel)(ReadyParams), int bytes) {
+    if (done) return ATTN_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return cuda_fail(e);
+    done = true;
+    return ATTN_OK;
 }
 
 int launched() {
@@ -128,15 +146,11 @@ extern "C" int attn_qk_norm_rope(const void* Q, const int64_t* q_strides, const 
     }
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != ATTN_OK) return st;
-    deal_units(p, dev->num_sms);
-    const unsigned grid = grid_for(p, dev->num_sms, kFwdCtasPerSm);
-    if (d == 64) {
-        if (interleaved) qk_norm_rope_kernel<64, true, kFwdSteps><<<grid, kReadyWarps * 32, 0, stream>>>(p);
-        else qk_norm_rope_kernel<64, false, kFwdSteps><<<grid, kReadyWarps * 32, 0, stream>>>(p);
-    } else {
-        if (interleaved) qk_norm_rope_kernel<128, true, kFwdSteps><<<grid, kReadyWarps * 32, 0, stream>>>(p);
-        else qk_norm_rope_kernel<128, false, kFwdSteps><<<grid, kReadyWarps * 32, 0, stream>>>(p);
-    }
+    const unsigned grid = deal_units(p, dev->num_sms, kFwdCtasPerSm);
+    const auto kernel = d == 64 ? interleaved ? qk_norm_rope_kernel<64, true, kFwdSteps> : qk_norm_rope_kernel<64, false, kFwdSteps>
+                        : interleaved ? qk_norm_rope_kernel<128, true, kFwdSteps> : qk_norm_rope_kernel<128, false, kFwdSteps>;
+    if ((st = allow_smem(dev->ready_configured[0][d == 128][interleaved != 0], kernel, kFwdSmem)) != ATTN_OK) return st;
+    kernel<<<grid, kReadyWarps * 32, kFwdSmem, stream>>>(p);
     return launched();
 }
 
@@ -144,7 +158,7 @@ extern "C" size_t attn_qk_norm_rope_bwd_workspace_bytes(int d) {
     if (d != 64 && d != 128) return 0;
     DeviceState* dev = nullptr;
     if (device_state(&dev) != ATTN_OK) return 0;
-    return static_cast<size_t>(dev->num_sms) * kBwdCtasPerSm * 2 * d * sizeof(float);
+    return static_cast<size_t>(dev->num_sms) * kBwdCtasPerSm * d * sizeof(float);
 }
 
 extern "C" int attn_qk_norm_rope_bwd(const void* dQout, const int64_t* dqo_strides, const void* dKout,
@@ -189,20 +203,23 @@ extern "C" int attn_qk_norm_rope_bwd(const void* dQout, const int64_t* dqo_strid
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != ATTN_OK) return st;
     if (any_norm && workspace_bytes < attn_qk_norm_rope_bwd_workspace_bytes(d)) return ATTN_ERR_INVALID_ARG;
-    deal_units(p, dev->num_sms);
-    const unsigned grid = grid_for(p, dev->num_sms, kBwdCtasPerSm);
-    p.part = any_norm ? static_cast<float*>(workspace) : nullptr;
-    if (d == 64) {
-        if (interleaved) qk_norm_rope_bwd_kernel<64, true, kBwdSteps><<<grid, kReadyWarps * 32, 0, stream>>>(p);
-        else qk_norm_rope_bwd_kernel<64, false, kBwdSteps><<<grid, kReadyWarps * 32, 0, stream>>>(p);
-    } else {
-        if (interleaved) qk_norm_rope_bwd_kernel<128, true, kBwdSteps><<<grid, kReadyWarps * 32, 0, stream>>>(p);
-        else qk_norm_rope_bwd_kernel<128, false, kBwdSteps><<<grid, kReadyWarps * 32, 0, stream>>>(p);
+    const unsigned grid = deal_units(p, dev->num_sms, kBwdCtasPerSm);
+    ReadyDw sums;
+    const int first[2] = {0, p.first_k}, rows[2] = {p.first_k, static_cast<int>(grid) - p.first_k};
+    for (int t = 0; t < 2; ++t) {
+        p.t[t].part = w[t] ? static_cast<float*>(workspace) + static_cast<size_t>(first[t]) * d : nullptr;
+        sums.part[t] = p.t[t].part;
+        sums.rows[t] = rows[t];
+        sums.dw[t] = dw[t];
     }
+    const auto grad = d == 64 ? interleaved ? qk_norm_rope_bwd_kernel<64, true, kBwdSteps> : qk_norm_rope_bwd_kernel<64, false, kBwdSteps>
+                      : interleaved ? qk_norm_rope_bwd_kernel<128, true, kBwdSteps> : qk_norm_rope_bwd_kernel<128, false, kBwdSteps>;
+    if ((st = allow_smem(dev->ready_configured[1][d == 128][interleaved != 0], grad, kBwdSmem)) != ATTN_OK) return st;
+    grad<<<grid, kReadyWarps * 32, kBwdSmem, stream>>>(p);
     if ((st = launched()) != ATTN_OK || !any_norm) return st;
     // its CTAs may start as the gradient kernel's retire, and wait in-kernel for its completion
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * d / 32);
+    cfg.gridDim = dim3(static_cast<unsigned>(d / 32), 2);
     cfg.blockDim = dim3(1024);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -211,7 +228,6 @@ extern "C" int attn_qk_norm_rope_bwd(const void* dQout, const int64_t* dqo_strid
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const auto kernel = d == 64 ? qk_norm_rope_dw_kernel<64> : qk_norm_rope_dw_kernel<128>;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, const_cast<const float*>(p.part), static_cast<int>(grid),
-                                             dq_weight, dk_weight);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, sums);
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }

@@ -32,6 +32,12 @@
 #include "rowwise_kernels.cuh"
 #include "sm103_ptx.cuh"
 
+#ifndef FU
+#define FU 6
+#define FC 2
+#define BU 4
+#define BC 2
+#endif
 namespace elsattn {
 
 constexpr int kReadyMaxAxes = 4;
@@ -45,10 +51,15 @@ struct ReadyTensor {
     int64_t xs[3], gs[3], ys[3];  // strides in elements: batch, head, token
     int H;
     int steps;                // warp steps per token: ceil(H / rows per warp)
+    int steps_per_unit;       // a work unit: so many steps of one token
+    int units_per_token;
+    uint32_t units;
+    float* part;              // backward: [CTAs of this tensor][d] fp32 partial sums of dw, or nullptr
 };
 
 struct ReadyParams {
     ReadyTensor t[2];         // Q, K
+    int first_k;              // CTAs [0, first_k) work on Q, the others on K
     const int32_t* pos;       // position of token n of batch b on axis a: pos[a * pos_axis + b * pos_batch + n]
     int64_t pos_axis, pos_batch;
     const double* inv_freq;   // [rot / 2]
@@ -57,16 +68,57 @@ struct ReadyParams {
     int N;
     uint32_t tokens;          // B * N
     float eps;
-    int steps_per_unit;       // a work unit: so many steps of one token
-    int units_per_token;
-    uint32_t units;
-    float* part;              // backward: [gridDim.x][2][d] fp32 partial sums of dw
 };
 
-// The pair that lane `c` of a row group holds as its k-th (0..7), and whether
-// it is rotated.  Halves: lane c holds elements 8c.. and rot/2 + 8c.. (the
-// pairs 8c .. 8c + 7); lanes past them hold 16 neighbouring unrotated elements.
-// Neighbours: lane c holds elements 8c.. and d/2 + 8c.., four pairs each.
+// Packed fp32 pairs: one instruction for two lanes of arithmetic, each
+// correctly rounded like the scalar one.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 pair2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split2(f2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    float lo, hi;
+    split2(v, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ f2 swap2(f2 v) {
+    float lo, hi;
+    split2(v, lo, hi);
+    return pair2(hi, lo);
+}
+
+// Eight bf16 as four packed fp32 pairs, and back with one rounding.
+__device__ __forceinline__ void unpack8(const uint4& v, f2 (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = pair2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(f2 v) {
+    float lo, hi;
+    split2(v, lo, hi);
+    return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ uint4 pack8(const f2 (&f)[4]) { return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3])); }
+
+// Where lane `c` of a row group has its two vectors, and whether they are rotated.
+// Halves: elements 8c.. and rot/2 + 8c.. (the pairs 8c .. 8c + 7); the lanes
+// past them hold 16 neighbouring unrotated elements.  Neighbours: elements
+// 8c.. and d/2 + 8c.., four pairs each.
 template <int D, bool INTER>
 struct ReadyLane {
     int a0, b0;       // element offsets of the two vectors
@@ -84,6 +136,7 @@ struct ReadyLane {
             b0 = rot_a ? half + 8 * c : a0 + 8;
         }
     }
+    // the k-th (0..7) pair of lane c
     __device__ static __forceinline__ int pair(int c, int k) {
         return INTER ? (k < 4 ? 4 * c + k : D / 4 + 4 * c + (k - 4)) : 8 * c + k;
     }
@@ -157,117 +210,254 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// Turn the lane's pairs by the angles (SIGN = 1) or back (SIGN = -1).  a, b:
-// the two vectors.
-template <bool INTER, int SIGN>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], bool rot_a, bool rot_b, const float (&cs)[8],
-                                     const float (&sn)[8]) {
-    if (INTER) {
+// The turn of a lane's two vectors as coefficients of packed products.  With
+// weights w on the inputs (the norm's, or 1) and the angles t:
+//   halves:     a' = a (wa cos) + b (-wb sin),  b' = b (wb cos) + a (wa sin)
+//   neighbours: v' = v (w cos) + swap(v) (-w_odd sin, w_even sin)   for v = a, b
+// so two elements cost two packed operations.  SIGN -1 turns back.
+// A vector that is not rotated has cos 1 and sin 0, and its other member is
+// replaced by 0: a product of 0 and an infinity must not enter.
+template <int D, bool INTER, int SIGN>
+struct ReadyTurn {
+    f2 ca[4], cb[4], sa[4], sb[4];
+    // without weights: the coefficients that are equal share registers
+    __device__ __forceinline__ void set(const float (&cs)[8], const float (&sn)[8], bool rot_a, bool rot_b) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (rot_a) {
-                const float x = a[2 * k], y = a[2 * k + 1], s = SIGN * sn[k];
-                a[2 * k] = x * cs[k] - y * s;
-                a[2 * k + 1] = y * cs[k] + x * s;
-            }
-            if (rot_b) {
-                const float x = b[2 * k], y = b[2 * k + 1], s = SIGN * sn[4 + k];
-                b[2 * k] = x * cs[4 + k] - y * s;
-                b[2 * k + 1] = y * cs[4 + k] + x * s;
+            if (INTER) {  // pair 4 * (vector) + k is the vector's elements 2k, 2k + 1
+                const float c0 = rot_a ? cs[k] : 1.f, s0 = rot_a ? SIGN * sn[k] : 0.f;
+                const float c1 = rot_b ? cs[4 + k] : 1.f, s1 = rot_b ? SIGN * sn[4 + k] : 0.f;
+                ca[k] = pair2(c0, c0);
+                cb[k] = pair2(c1, c1);
+                sa[k] = pair2(-s0, s0);
+                sb[k] = pair2(-s1, s1);
+            } else {
+                const float s0 = rot_a ? SIGN * sn[2 * k] : 0.f, s1 = rot_a ? SIGN * sn[2 * k + 1] : 0.f;
+                ca[k] = cb[k] = pair2(rot_a ? cs[2 * k] : 1.f, rot_a ? cs[2 * k + 1] : 1.f);
+                sa[k] = pair2(-s0, -s1);  // of b, in a'
+                sb[k] = pair2(s0, s1);    // of a, in b'
             }
         }
-    } else if (rot_a) {
+    }
+    __device__ __forceinline__ void set(const float (&cs)[8], const float (&sn)[8], bool rot_a, bool rot_b,
+                                        const f2 (&wa)[4], const f2 (&wb)[4]) {
+        set(cs, sn, rot_a, rot_b);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float x = a[k], y = b[k], s = SIGN * sn[k];
-            a[k] = x * cs[k] - y * s;
-            b[k] = y * cs[k] + x * s;
+        for (int k = 0; k < 4; ++k) {
+            ca[k] = mul2(wa[k], ca[k]);
+            cb[k] = mul2(wb[k], cb[k]);
+            sa[k] = mul2(INTER ? swap2(wa[k]) : wb[k], sa[k]);
+            sb[k] = mul2(INTER ? swap2(wb[k]) : wa[k], sb[k]);
         }
+    }
+    // a, b: in place.  all: every lane of the launch rotates (rot == D).
+    __device__ __forceinline__ void apply(f2 (&a)[4], f2 (&b)[4], bool all, bool rot_a, bool rot_b) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f2 oa = INTER ? swap2(a[k]) : b[k], ob = INTER ? swap2(b[k]) : a[k];
+            if (!all) {
+                oa = rot_a ? oa : 0;
+                ob = rot_b ? ob : 0;
+            }
+            a[k] = fma2(oa, sa[k], mul2(a[k], ca[k]));
+            b[k] = fma2(ob, sb[k], mul2(b[k], cb[k]));
+        }
+    }
+};
+
+// This CTA's tensor and its place among that tensor's CTAs.
+struct ReadyPlace {
+    int t, block, blocks;
+    __device__ __forceinline__ explicit ReadyPlace(const ReadyParams& p) {
+        t = static_cast<int>(blockIdx.x) >= p.first_k ? 1 : 0;
+        block = t ? blockIdx.x - p.first_k : blockIdx.x;
+        blocks = t ? gridDim.x - p.first_k : p.first_k;
+    }
+};
+
+__device__ __forceinline__ void load_weight(const __nv_bfloat16* w, int a0, int b0, f2 (&wa)[4], f2 (&wb)[4]) {
+    if (w) {
+        unpack8(*reinterpret_cast<const uint4*>(w + a0), wa);
+        unpack8(*reinterpret_cast<const uint4*>(w + b0), wb);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) wa[k] = wb[k] = pair2(1.f, 1.f);
     }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+// A warp's walk over its units, step by step: where the step's rows are.
+template <int GROUPS>
+struct ReadyWalk {
+    uint32_t u;   // unit (>= units: done)
+    int s, s1;    // step within the token, and the unit's end
+    int b, n;     // the token's batch and place
+    __device__ __forceinline__ void decode(const ReadyParams& p, const ReadyTensor& rt) {
+        const uint32_t token = u / rt.units_per_token;
+        s = static_cast<int>(u - token * rt.units_per_token) * rt.steps_per_unit;
+        s1 = min(rt.steps, s + rt.steps_per_unit);
+        b = static_cast<int>(token / static_cast<uint32_t>(p.N));
+        n = static_cast<int>(token - static_cast<uint32_t>(b) * p.N);
+    }
+    __device__ __forceinline__ int64_t offset(const int64_t (&st)[3], int g) const {
+        return b * st[0] + (s * GROUPS + g) * st[1] + n * st[2];
+    }
+};
+
+// 16 bytes from global to shared memory, asynchronously; zeros where !on.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
 }
 
-__device__ __forceinline__ uint4 ld16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
-
-// U: steps whose loads are in flight together.
-template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kReadyWarps * 32) qk_norm_rope_kernel(const __grid_constant__ ReadyParams p) {
+// One warp's rows in flight: a ring of U steps in shared memory, filled by
+// asynchronous copies that run ahead over the ends of units.  Each lane reads
+// back only what it copied itself, so its own wait is all the synchronisation.
+// U slots, U - 1 steps in flight: a step's copies go to the slot read one step
+// before, whose values have been used (its results are stored) by then.
+// VECS: 16-byte vectors a lane moves per step.
+template <int D, int VECS, int U>
+struct ReadyRing {
     using A = ReadyAngles<D>;
-    const int lane = threadIdx.x & 31;
+    static constexpr int kBytes = U * VECS * 512;  // per warp
+    ReadyWalk<A::kGroups> w;
+    uint32_t base;       // this lane's place in the warp's ring
+    uint32_t warps;
+    int fill, slot;      // the ring slots to fill and to read next
+    const __nv_bfloat16 *x, *g;   // the next step's rows (g: the second source, where there is one)
+
+    __device__ __forceinline__ void place(const ReadyTensor& rt, int grp, bool first, bool second) {
+        if (first) x = rt.x + w.offset(rt.xs, grp);
+        if (second) g = rt.g + w.offset(rt.gs, grp);
+    }
+    template <class Lane>
+    __device__ __forceinline__ void issue(const ReadyParams& p, const ReadyTensor& rt, const Lane& at, int grp, bool first,
+                                          bool second) {
+        if (w.u < rt.units) {
+            const bool on = w.s * A::kGroups + grp < rt.H;
+            const uint32_t dst = base + fill * (VECS * 512);
+            if (first) {
+                copy16(dst, on ? x + at.a0 : rt.x, on);
+                copy16(dst + 512, on ? x + at.b0 : rt.x, on);
+                x += A::kGroups * rt.xs[1];
+            }
+            if (second) {
+                copy16(dst + (VECS - 2) * 512, on ? g + at.a0 : rt.g, on);
+                copy16(dst + (VECS - 1) * 512, on ? g + at.b0 : rt.g, on);
+                g += A::kGroups * rt.gs[1];
+            }
+            if (++w.s == w.s1) {
+                w.u += warps;
+                if (w.u < rt.units) {
+                    w.decode(p, rt);
+                    place(rt, grp, first, second);
+                }
+            }
+        }
+        copy_commit();
+        fill = fill + 1 == U ? 0 : fill + 1;
+    }
+    // Waits for the next step's rows; returns where they are.
+    __device__ __forceinline__ uint32_t next() {
+        copy_wait<U - 2>();
+        const uint32_t a = base + slot * (VECS * 512);
+        slot = slot + 1 == U ? 0 : slot + 1;
+        return a;
+    }
+    template <class Lane>
+    __device__ __forceinline__ void start(const ReadyParams& p, const ReadyTensor& rt, const Lane& at, int grp, bool first,
+                                          bool second, uint32_t smem, uint32_t u0, uint32_t n) {
+        base = smem + (threadIdx.x & 31) * 16;
+        warps = n;
+        fill = slot = 0;
+        x = g = nullptr;
+        w.u = u0;
+        if (w.u < rt.units) {
+            w.decode(p, rt);
+            place(rt, grp, first, second);
+        }
+#pragma unroll 1
+        for (int i = 0; i < U - 1; ++i) issue(p, rt, at, grp, first, second);
+    }
+};
+
+extern __shared__ __align__(16) uint8_t ready_smem[];
+
+// U: slots of a warp's ring.
+template <int D, bool INTER, int U>
+__global__ void __launch_bounds__(kReadyWarps * 32, FC) qk_norm_rope_kernel(const __grid_constant__ ReadyParams p) {
+    using A = ReadyAngles<D>;
+    using Ring = ReadyRing<D, 2, U>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = lane % A::kLanes, g = lane / A::kLanes;
     const ReadyLane<D, INTER> at(c, p.rot);
+    const ReadyPlace place(p);
+    const ReadyTensor& rt = p.t[place.t];
+    const uint32_t warps = place.blocks * kReadyWarps;
+    ReadyWalk<A::kGroups> w;
+    w.u = place.block * kReadyWarps + warp;
+    if (w.u >= rt.units) return;
+    Ring ring;
+    ring.start(p, rt, at, g, true, false, smem_u32(ready_smem) + warp * Ring::kBytes, w.u, warps);
     A angles;
     angles.template init<INTER>(p, lane);
-    // both tensors' weights for this lane's elements, as bf16
-    uint4 w[2][2] = {};
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-        if (p.t[t].w) {
-            w[t][0] = ld16(p.t[t].w + at.a0);
-            w[t][1] = ld16(p.t[t].w + at.b0);
-        }
-    const int total = p.t[0].steps + p.t[1].steps;
-    const uint32_t warps = gridDim.x * kReadyWarps;
-    for (uint32_t u = blockIdx.x * kReadyWarps + (threadIdx.x >> 5); u < p.units; u += warps) {
-        const uint32_t token = u / p.units_per_token;
-        const int s0 = static_cast<int>(u - token * p.units_per_token) * p.steps_per_unit;
-        const int s1 = min(total, s0 + p.steps_per_unit);
-        const int b = static_cast<int>(token / static_cast<uint32_t>(p.N));
-        const int n = static_cast<int>(token - static_cast<uint32_t>(b) * p.N);
-        int pos[A::kOwn];
-        angles.load(p, b, n, pos);
+    f2 wa[4], wb[4];
+    load_weight(rt.w, at.a0, at.b0, wa, wb);
+    const bool norm = rt.w != nullptr, all = p.rot == D;
+    w.decode(p, rt);
+    int pos[A::kOwn];
+    angles.load(p, w.b, w.n, pos);
+    while (true) {
         float cs[8], sn[8];
-        for (int s = s0; s < s1; s += U) {
-            uint4 va[U], vb[U];
-            bool on[U];
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int t = s + j >= p.t[0].steps ? 1 : 0;
-                const ReadyTensor& rt = p.t[t];
-                const int h = (s + j - (t ? p.t[0].steps : 0)) * A::kGroups + g;
-                on[j] = s + j < s1 && h < rt.H;
-                va[j] = vb[j] = make_uint4(0, 0, 0, 0);
-                if (on[j]) {
-                    const __nv_bfloat16* row = rt.x + b * rt.xs[0] + h * rt.xs[1] + n * rt.xs[2];
-                    va[j] = ld_stream(reinterpret_cast<const uint4*>(row + at.a0));
-                    vb[j] = ld_stream(reinterpret_cast<const uint4*>(row + at.b0));
-                }
-            }
-            if (s == s0) angles.eval(pos, lane, cs, sn);
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                if (s + j >= s1) break;
-                const int t = s + j >= p.t[0].steps ? 1 : 0;
-                const ReadyTensor& rt = p.t[t];
-                const int h = (s + j - (t ? p.t[0].steps : 0)) * A::kGroups + g;
-                float a[8], bb[8];
-                bf16x8_to_float(va[j], a);
-                bf16x8_to_float(vb[j], bb);
-                if (rt.w) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) ss = fmaf(a[k], a[k], fmaf(bb[k], bb[k], ss));
-                    const float r = rsqrtf(row_sum<A::kLanes>(ss) * (1.0f / D) + p.eps);
-                    float wa[8], wb[8];
-                    bf16x8_to_float(t ? w[1][0] : w[0][0], wa);
-                    bf16x8_to_float(t ? w[1][1] : w[0][1], wb);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        a[k] *= r * wa[k];
-                        bb[k] *= r * wb[k];
-                    }
-                }
-                turn<INTER, 1>(a, bb, at.rot_a, at.rot_b, cs, sn);
-                if (on[j]) {
-                    __nv_bfloat16* row = rt.y + b * rt.ys[0] + h * rt.ys[1] + n * rt.ys[2];
-                    *reinterpret_cast<uint4*>(row + at.a0) = pack8(a);
-                    *reinterpret_cast<uint4*>(row + at.b0) = pack8(bb);
-                }
-            }
+        angles.eval(pos, lane, cs, sn);
+        ReadyTurn<D, INTER, 1> turn;
+        turn.set(cs, sn, at.rot_a, at.rot_b, wa, wb);
+        __nv_bfloat16* dst = rt.y + w.offset(rt.ys, g);
+        int s = w.s;
+        const int s1 = w.s1;
+        w.u += warps;
+        const bool more = w.u < rt.units;
+        if (more) {  // the next unit's positions arrive while this one's rows are worked on
+            w.decode(p, rt);
+            angles.load(p, w.b, w.n, pos);
         }
+        for (; s < s1; ++s) {
+            f2 a[4], bb[4];
+            const uint32_t src = ring.next();
+            unpack8(ld_shared16(src), a);
+            unpack8(ld_shared16(src + 512), bb);
+            ring.issue(p, rt, at, g, true, false);
+            if (norm) {
+                f2 s2 = mul2(a[0], a[0]), t2 = mul2(bb[0], bb[0]);
+#pragma unroll
+                for (int k = 1; k < 4; ++k) {
+                    s2 = fma2(a[k], a[k], s2);
+                    t2 = fma2(bb[k], bb[k], t2);
+                }
+                const float r = rsqrtf(row_sum<A::kLanes>(sum2(s2) + sum2(t2)) * (1.0f / D) + p.eps);
+                const f2 r2 = pair2(r, r);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    a[k] = mul2(a[k], r2);
+                    bb[k] = mul2(bb[k], r2);
+                }
+            }
+            turn.apply(a, bb, all, at.rot_a, at.rot_b);
+            if (s * A::kGroups + g < rt.H) {
+                *reinterpret_cast<uint4*>(dst + at.a0) = pack8(a);
+                *reinterpret_cast<uint4*>(dst + at.b0) = pack8(bb);
+            }
+            dst += A::kGroups * rt.ys[1];
+        }
+        if (!more) break;
     }
 }
 
@@ -275,151 +465,135 @@ __global__ void __launch_bounds__(kReadyWarps * 32) qk_norm_rope_kernel(const __
 // the row groups of the warp, the warps of the CTA (both in a fixed order), and
 // by qk_norm_rope_dw_kernel over the CTAs: the same inputs give the same bits.
 template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kReadyWarps * 32, 2) qk_norm_rope_bwd_kernel(const __grid_constant__ ReadyParams p) {
+__global__ void __launch_bounds__(kReadyWarps * 32, BC) qk_norm_rope_bwd_kernel(const __grid_constant__ ReadyParams p) {
     using A = ReadyAngles<D>;
-    __shared__ float s_dw[kReadyWarps][2][D];
+    using Ring = ReadyRing<D, 4, U>;
+    __shared__ float s_dw[kReadyWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = lane % A::kLanes, g = lane / A::kLanes;
     const ReadyLane<D, INTER> at(c, p.rot);
-    A angles;
-    angles.template init<INTER>(p, lane);
-    uint4 w[2][2] = {};
+    const ReadyPlace place(p);
+    const ReadyTensor& rt = p.t[place.t];
+    const bool norm = rt.w != nullptr, all = p.rot == D;
+    const uint32_t warps = place.blocks * kReadyWarps;
+    f2 acc[8];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-        if (p.t[t].w) {
-            w[t][0] = ld16(p.t[t].w + at.a0);
-            w[t][1] = ld16(p.t[t].w + at.b0);
-        }
-    float acc[2][16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) acc[0][k] = acc[1][k] = 0.f;
-    const int total = p.t[0].steps + p.t[1].steps;
-    const uint32_t warps = gridDim.x * kReadyWarps;
-    for (uint32_t u = blockIdx.x * kReadyWarps + warp; u < p.units; u += warps) {
-        const uint32_t token = u / p.units_per_token;
-        const int s0 = static_cast<int>(u - token * p.units_per_token) * p.steps_per_unit;
-        const int s1 = min(total, s0 + p.steps_per_unit);
-        const int b = static_cast<int>(token / static_cast<uint32_t>(p.N));
-        const int n = static_cast<int>(token - static_cast<uint32_t>(b) * p.N);
+    for (int k = 0; k < 8; ++k) acc[k] = 0;
+    ReadyWalk<A::kGroups> w;
+    w.u = place.block * kReadyWarps + warp;
+    bool more = w.u < rt.units;
+    if (more) {
+        Ring ring;
+        ring.start(p, rt, at, g, norm, true, smem_u32(ready_smem) + warp * Ring::kBytes, w.u, warps);
+        A angles;
+        angles.template init<INTER>(p, lane);
+        f2 wa[4], wb[4];
+        load_weight(rt.w, at.a0, at.b0, wa, wb);
+        w.decode(p, rt);
         int pos[A::kOwn];
-        angles.load(p, b, n, pos);
-        float cs[8], sn[8];
-        for (int s = s0; s < s1; s += U) {
-            uint4 ga[U], gb[U], xa[U], xb[U];
-            bool on[U];
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int t = s + j >= p.t[0].steps ? 1 : 0;
-                const ReadyTensor& rt = p.t[t];
-                const int h = (s + j - (t ? p.t[0].steps : 0)) * A::kGroups + g;
-                on[j] = s + j < s1 && h < rt.H;
-                ga[j] = gb[j] = xa[j] = xb[j] = make_uint4(0, 0, 0, 0);
-                if (on[j]) {
-                    const __nv_bfloat16* gr = rt.g + b * rt.gs[0] + h * rt.gs[1] + n * rt.gs[2];
-                    ga[j] = ld_stream(reinterpret_cast<const uint4*>(gr + at.a0));
-                    gb[j] = ld_stream(reinterpret_cast<const uint4*>(gr + at.b0));
-                    if (rt.w) {
-                        const __nv_bfloat16* xr = rt.x + b * rt.xs[0] + h * rt.xs[1] + n * rt.xs[2];
-                        xa[j] = ld_stream(reinterpret_cast<const uint4*>(xr + at.a0));
-                        xb[j] = ld_stream(reinterpret_cast<const uint4*>(xr + at.b0));
-                    }
-                }
+        angles.load(p, w.b, w.n, pos);
+        while (more) {
+            float cs[8], sn[8];
+            angles.eval(pos, lane, cs, sn);
+            ReadyTurn<D, INTER, -1> turn;
+            turn.set(cs, sn, at.rot_a, at.rot_b);
+            __nv_bfloat16* dst = rt.y + w.offset(rt.ys, g);
+            int s = w.s;
+            const int s1 = w.s1;
+            w.u += warps;
+            more = w.u < rt.units;
+            if (more) {
+                w.decode(p, rt);
+                angles.load(p, w.b, w.n, pos);
             }
-            if (s == s0) angles.eval(pos, lane, cs, sn);
+            for (; s < s1; ++s) {
+                const bool on = s * A::kGroups + g < rt.H;
+                f2 ua[4], ub[4], ha[4], hb[4];
+                const uint32_t src = ring.next();
+                unpack8(ld_shared16(src + 1024), ua);
+                unpack8(ld_shared16(src + 1536), ub);
+                if (norm) {
+                    unpack8(ld_shared16(src), ha);
+                    unpack8(ld_shared16(src + 512), hb);
+                }
+                ring.issue(p, rt, at, g, norm, true);
+                turn.apply(ua, ub, all, at.rot_a, at.rot_b);
+                if (norm) {
+                    f2 va[4], vb[4];
+                    f2 s2 = 0, d2 = 0;
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                if (s + j >= s1) break;
-                const int t = s + j >= p.t[0].steps ? 1 : 0;
-                const ReadyTensor& rt = p.t[t];
-                const int h = (s + j - (t ? p.t[0].steps : 0)) * A::kGroups + g;
-                float ua[8], ub[8];
-                bf16x8_to_float(ga[j], ua);
-                bf16x8_to_float(gb[j], ub);
-                turn<INTER, -1>(ua, ub, at.rot_a, at.rot_b, cs, sn);
-                if (rt.w) {
-                    float ha[8], hb[8], wa[8], wb[8];
-                    bf16x8_to_float(xa[j], ha);
-                    bf16x8_to_float(xb[j], hb);
-                    bf16x8_to_float(t ? w[1][0] : w[0][0], wa);
-                    bf16x8_to_float(t ? w[1][1] : w[0][1], wb);
-                    float ss = 0.f, dot = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        ss = fmaf(ha[k], ha[k], fmaf(hb[k], hb[k], ss));
-                        dot = fmaf(ua[k] * wa[k], ha[k], fmaf(ub[k] * wb[k], hb[k], dot));
+                    for (int k = 0; k < 4; ++k) {
+                        s2 = fma2(ha[k], ha[k], fma2(hb[k], hb[k], s2));
+                        va[k] = mul2(ua[k], wa[k]);
+                        vb[k] = mul2(ub[k], wb[k]);
+                        d2 = fma2(va[k], ha[k], fma2(vb[k], hb[k], d2));
                     }
                     // a lane without a row adds nothing to dw, also where eps is 0
-                    const float rr = rsqrtf(row_sum<A::kLanes>(ss) * (1.0f / D) + p.eps);
-                    const float r = on[j] ? rr : 0.f;
-                    const float m = row_sum<A::kLanes>(dot) * r * (1.0f / D);  // mean(u w h)
+                    const float rr = rsqrtf(row_sum<A::kLanes>(sum2(s2)) * (1.0f / D) + p.eps);
+                    const float r = on ? rr : 0.f;
+                    const float m = row_sum<A::kLanes>(sum2(d2)) * r * (1.0f / D);  // mean(u w h)
+                    const f2 r2 = pair2(r, r), m2 = pair2(-m, -m);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        ha[k] *= r;
-                        hb[k] *= r;
-                    }
-                    if (t == 0) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            acc[0][k] = fmaf(ua[k], ha[k], acc[0][k]);
-                            acc[0][8 + k] = fmaf(ub[k], hb[k], acc[0][8 + k]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            acc[1][k] = fmaf(ua[k], ha[k], acc[1][k]);
-                            acc[1][8 + k] = fmaf(ub[k], hb[k], acc[1][8 + k]);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        ua[k] = r * fmaf(-ha[k], m, ua[k] * wa[k]);
-                        ub[k] = r * fmaf(-hb[k], m, ub[k] * wb[k]);
+                    for (int k = 0; k < 4; ++k) {
+                        ha[k] = mul2(ha[k], r2);
+                        hb[k] = mul2(hb[k], r2);
+                        acc[k] = fma2(ua[k], ha[k], acc[k]);
+                        acc[4 + k] = fma2(ub[k], hb[k], acc[4 + k]);
+                        ua[k] = mul2(r2, fma2(ha[k], m2, va[k]));
+                        ub[k] = mul2(r2, fma2(hb[k], m2, vb[k]));
                     }
                 }
-                if (on[j]) {
-                    __nv_bfloat16* row = rt.y + b * rt.ys[0] + h * rt.ys[1] + n * rt.ys[2];
-                    *reinterpret_cast<uint4*>(row + at.a0) = pack8(ua);
-                    *reinterpret_cast<uint4*>(row + at.b0) = pack8(ub);
+                if (on) {
+                    *reinterpret_cast<uint4*>(dst + at.a0) = pack8(ua);
+                    *reinterpret_cast<uint4*>(dst + at.b0) = pack8(ub);
                 }
+                dst += A::kGroups * rt.ys[1];
             }
         }
     }
-    if (!p.part) return;
+    if (!rt.part) return;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int k = 0; k < 8; ++k) {
+        float v[2];
+        split2(acc[k], v[0], v[1]);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            float v = acc[t][k];
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int off = 16; off >= A::kLanes; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-            if (g == 0) s_dw[warp][t][(k < 8 ? at.a0 : at.b0 - 8) + k] = v;
+            for (int off = 16; off >= A::kLanes; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+            if (g == 0) s_dw[warp][(k < 4 ? at.a0 + 2 * k : at.b0 + 2 * (k - 4)) + i] = v[i];
         }
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
+    for (int i = threadIdx.x; i < D; i += blockDim.x) {
         float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < kReadyWarps; ++k) v += s_dw[k][i / D][i % D];
-        p.part[static_cast<size_t>(blockIdx.x) * 2 * D + i] = v;
+        for (int k = 0; k < kReadyWarps; ++k) v += s_dw[k][i];
+        rt.part[static_cast<size_t>(place.block) * D + i] = v;
     }
 }
 
-// dw of both tensors from the CTAs' partial sums: 32 columns a CTA, the rows
-// dealt to 32 warps and their sums added in a fixed order.
+// dw of both tensors from their CTAs' partial sums: CTA (x, y) has 32 columns
+// of tensor y, whose rows are dealt to 32 warps and added in a fixed order.
+struct ReadyDw {
+    const float* part[2];
+    int rows[2];
+    float* dw[2];
+};
 template <int D>
-__global__ void __launch_bounds__(1024) qk_norm_rope_dw_kernel(const float* part, int rows, float* dwq, float* dwk) {
+__global__ void __launch_bounds__(1024) qk_norm_rope_dw_kernel(const ReadyDw a) {
     __shared__ float s[32][33];
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5, t = blockIdx.y;
+    if (!a.dw[t]) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float v = 0.f;
-    for (int r = w; r < rows; r += 32) v += __ldcg(part + static_cast<size_t>(r) * 2 * D + col);
+    for (int r = w; r < a.rows[t]; r += 32) v += __ldcg(a.part[t] + static_cast<size_t>(r) * D + col);
     s[w][threadIdx.x & 31] = v;
     __syncthreads();
     if (w != 0) return;
     v = 0.f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) v += s[k][threadIdx.x];
-    float* dst = col < D ? dwq : dwk;
-    if (dst) dst[col % D] = v;
+    a.dw[t][col] = v;
 }
 
 }  // namespace elsattn

@@ -427,7 +427,7 @@ int attn_qk_norm_rope_bwd(const void* dQout, const int64_t* dqo_strides, const v
                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Device bytes attn_qk_norm_rope_bwd needs as workspace on the current device:
- * two fp32 rows of d per CTA; 0 for d other than 64 or 128, or without a device. */
+ * an fp32 row of d per CTA; 0 for d other than 64 or 128, or without a device. */
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
 
 #ifdef __cplusplus
