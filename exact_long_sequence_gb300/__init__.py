@@ -14,9 +14,11 @@ to FlashAttention - A Memory-Centric Compilation Approach in AICF", section 3.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
+import struct
 
 from . import workloads  # noqa: F401  (seeded synthetic inputs; no attention arithmetic)
 
@@ -172,8 +174,9 @@ def default_scale(d: int) -> float:
 def _stream_handle(stream):
     import torch
 
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # the current device's current stream, without building a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def split_workspace_bytes(B: int, H: int, N: int, d: int, causal: bool) -> int:
@@ -359,13 +362,15 @@ def layernorm_rows(x, gamma, beta, eps: float = 1e-5, out=None, stream=None):
     return out
 
 
+_NOTHING = contextlib.nullcontext()
+_pack3 = struct.Struct("3q").pack
+
+
 def _on_device(device):
     """A context with `device` current: nothing to do where it is already."""
-    import contextlib
-
     import torch
 
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _NOTHING if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _new_for(stream, *tensors):
@@ -375,53 +380,53 @@ def _new_for(stream, *tensors):
             t.record_stream(stream)
 
 
-def _views(named, device):
-    """Checks [B, H, N, d] bf16 views on one device; returns a host array of their strides, three each,
-    and the address of each view's strides in it."""
+def _view(name, t, shape, device):
+    """Checks a [B, H, N, d] bf16 view; returns its address and its three strides as the C call's host array."""
     import torch
 
-    flat = []
-    for name, t, shape in named:
-        if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4 or t.stride(3) != 1:
-            raise ValueError(f"{name} must be a bf16 CUDA tensor [B, H, N, d] with d contiguous, on q's device")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}")
-        flat += t.stride()[:3]
-    arr = (ctypes.c_int64 * len(flat))(*flat)
-    base = ctypes.addressof(arr)
-    return arr, [base + 24 * i for i in range(len(named))]
+    if t.dtype != torch.bfloat16 or t.device != device:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor on q's device")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{name} must have its last axis contiguous")
+    return t.data_ptr(), _pack3(s[0], s[1], s[2])
 
 
 def _rotation(q, k, positions, inv_freq, sections, weights):
     """The checks both directions of qk_norm_rope share.  Returns the sections as a host array, their
-    number, and the positions' axis and batch strides."""
+    number, the positions [axes, B or 1, N], and their axis and batch strides."""
     import torch
 
     if q.dim() != 4 or k.dim() != 4 or not q.is_cuda:
         raise ValueError("q and k must be CUDA tensors [B, H, N, d]")
+    device = q.device
     B, _, N, d = q.shape
-    if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+    kB, _, kN, kd = k.shape
+    if kB != B or kN != N or kd != d:
         raise ValueError("q and k must share B, N and d")
-    if inv_freq.dtype != torch.float64 or inv_freq.device != q.device or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype != torch.float64 or inv_freq.device != device or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 tensor of one axis on q's device")
     if sections is None:
         sections = (inv_freq.shape[0],)
     if sum(sections) != inv_freq.shape[0]:
         raise ValueError("sections must add up to the number of frequencies")
-    if positions.dtype != torch.int32 or positions.device != q.device:
+    if positions.dtype != torch.int32 or positions.device != device:
         raise ValueError("positions must be an int32 tensor on q's device")
-    while positions.dim() < 3 and (positions.dim() < 2 or len(sections) == 1):  # [N] or [B, N]: one axis
-        positions = positions.unsqueeze(0)
     A = len(sections)
+    while positions.dim() < 3 and (positions.dim() < 2 or A == 1):  # [N] or [B, N]: one axis
+        positions = positions.unsqueeze(0)
     if positions.dim() != 3 or positions.shape[0] != A or positions.shape[1] not in (1, B) or positions.shape[2] != N:
         raise ValueError("positions must be [axes, B, N] (B may be 1; [B, N] or [N] for a single axis)")
-    if N > 1 and positions.stride(2) != 1:
+    pa, pb, pn = positions.stride()
+    if N > 1 and pn != 1:
         raise ValueError("positions must be contiguous along the tokens")
     for w in weights:
-        if w is not None and (w.dtype != torch.bfloat16 or w.device != q.device or w.shape != (d,) or
+        if w is not None and (w.dtype != torch.bfloat16 or w.device != device or w.shape != (d,) or
                               not w.is_contiguous()):
             raise ValueError("norm weights must be contiguous bf16 tensors [d] on q's device")
-    return (ctypes.c_int * A)(*sections), A, positions, positions.stride(0), 0 if positions.shape[1] == 1 else positions.stride(1)
+    return (ctypes.c_int * A)(*sections), A, positions, pa, 0 if positions.shape[1] == 1 else pb
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, sections=None, eps: float = 1e-6,
@@ -453,13 +458,15 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, sectio
             k_out = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
             fresh.append(k_out)
         _new_for(stream, *fresh)
-        strides, at = _views((("q", q, q.shape), ("k", k, k.shape), ("q_out", q_out, q.shape), ("k_out", k_out, k.shape)),
-                             q.device)
-        st = lib.attn_qk_norm_rope(q.data_ptr(), at[0], k.data_ptr(), at[1],
-                                   None if q_weight is None else q_weight.data_ptr(),
+        dev = q.device
+        qp, qs = _view("q", q, q.shape, dev)
+        kp, ks = _view("k", k, k.shape, dev)
+        qop, qos = _view("q_out", q_out, q.shape, dev)
+        kop, kos = _view("k_out", k_out, k.shape, dev)
+        st = lib.attn_qk_norm_rope(qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
                                    None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb,
-                                   inv_freq.data_ptr(), sec, A, q_out.data_ptr(), at[2], k_out.data_ptr(), at[3],
-                                   B, Hq, Hk, N, d, eps, int(bool(interleaved)), _stream_handle(stream))
+                                   inv_freq.data_ptr(), sec, A, qop, qos, kop, kos, B, Hq, Hk, N, d, eps,
+                                   1 if interleaved else 0, _stream_handle(stream))
     _check(st, "attn_qk_norm_rope")
     return q_out, k_out
 
@@ -501,14 +508,18 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k
                                       not workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
         _new_for(stream, *fresh)
-        strides, at = _views((("dq_out", dq_out, q.shape), ("dk_out", dk_out, k.shape), ("q", q, q.shape),
-                              ("k", k, k.shape), ("dq", dq, q.shape), ("dk", dk, k.shape)), q.device)
+        dev = q.device
+        gqp, gqs = _view("dq_out", dq_out, q.shape, dev)
+        gkp, gks = _view("dk_out", dk_out, k.shape, dev)
+        qp, qs = _view("q", q, q.shape, dev)
+        kp, ks = _view("k", k, k.shape, dev)
+        dqp, dqs = _view("dq", dq, q.shape, dev)
+        dkp, dks = _view("dk", dk, k.shape, dev)
         st = lib.attn_qk_norm_rope_bwd(
-            dq_out.data_ptr(), at[0], dk_out.data_ptr(), at[1], q.data_ptr(), at[2], k.data_ptr(), at[3],
-            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-            positions.data_ptr(), pa, pb, inv_freq.data_ptr(), sec, A, dq.data_ptr(), at[4], dk.data_ptr(), at[5],
-            None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), B, Hq, Hk, N, d, eps,
-            int(bool(interleaved)), None if workspace is None else workspace.data_ptr(),
+            gqp, gqs, gkp, gks, qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb, inv_freq.data_ptr(), sec, A,
+            dqp, dqs, dkp, dks, None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
+            B, Hq, Hk, N, d, eps, 1 if interleaved else 0, None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel(), _stream_handle(stream))
     _check(st, "attn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk

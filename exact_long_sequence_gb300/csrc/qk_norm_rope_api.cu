@@ -13,9 +13,6 @@
 namespace elsattn {
 namespace {
 
-constexpr int kFwdSteps = FU, kBwdSteps = BU;      // slots of a warp's ring of row steps
-constexpr int kFwdCtasPerSm = FC, kBwdCtasPerSm = BC;
-
 // Sizes, alignment and the axis ranges, shared by both directions.
 int fill_params(ReadyParams& p, const int32_t* positions, int64_t pos_axis, int64_t pos_batch, const double* inv_freq,
                 const int* sections, int num_sections, int B, int Hq, int Hk, int N, int d, float eps) {
@@ -73,7 +70,7 @@ int take_strides(int64_t (&out)[3], const int64_t* s, int B, int H, int N, int d
 // one step more.  A unit is a whole token once there are enough of them to
 // give the tensor's warps one each; below that a token's heads are dealt to
 // more warps.  Returns the grid.
-unsigned deal_units(ReadyParams& p, int num_sms, int per_sm) {
+unsigned deal_units(ReadyParams& p, int num_sms, int per_sm, int cta_warps) {
     const int64_t most = static_cast<int64_t>(num_sms) * per_sm;
     const double cost_q = p.t[0].steps + 1, cost_k = p.t[1].steps + 1;
     int64_t ctas[2];
@@ -83,12 +80,12 @@ unsigned deal_units(ReadyParams& p, int num_sms, int per_sm) {
     ctas[1] = most - ctas[0];
     for (int t = 0; t < 2; ++t) {
         ReadyTensor& r = p.t[t];
-        const int64_t warps = ctas[t] * kReadyWarps;
+        const int64_t warps = ctas[t] * cta_warps;
         const int64_t want = (static_cast<int64_t>(r.steps) * p.tokens + warps - 1) / warps;
         r.steps_per_unit = static_cast<int>(want < 1 ? 1 : want > r.steps ? r.steps : want);
         r.units_per_token = (r.steps + r.steps_per_unit - 1) / r.steps_per_unit;
         r.units = p.tokens * static_cast<uint32_t>(r.units_per_token);  // below 2 * warps + tokens
-        const int64_t need = (static_cast<int64_t>(r.units) + kReadyWarps - 1) / kReadyWarps;
+        const int64_t need = (static_cast<int64_t>(r.units) + cta_warps - 1) / cta_warps;
         if (need < ctas[t]) ctas[t] = need;
         r.part = nullptr;
     }
@@ -96,8 +93,8 @@ unsigned deal_units(ReadyParams& p, int num_sms, int per_sm) {
     return static_cast<unsigned>(ctas[0] + ctas[1]);
 }
 
-constexpr int kFwdSmem = kReadyWarps * ReadyRing<128, 2, kFwdSteps>::kBytes;
-constexpr int kBwdSmem = kReadyWarps * ReadyRing<128, 4, kBwdSteps>::kBytes;
+constexpr int kFwdSmem = kFwdWarps * ReadyRing<128, 2, kFwdSlots>::kBytes;
+constexpr int kBwdSmem = kBwdWarps * ReadyRing<128, 4, kBwdSlots>::kBytes;
 
 // Once per device and kernel (a second call that races with the first sets the same limit again).
 int allow_smem(bool& done, void (*kernel)(ReadyParams), int bytes) {
@@ -146,11 +143,11 @@ extern "C" int attn_qk_norm_rope(const void* Q, const int64_t* q_strides, const 
     }
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != ATTN_OK) return st;
-    const unsigned grid = deal_units(p, dev->num_sms, kFwdCtasPerSm);
-    const auto kernel = d == 64 ? interleaved ? qk_norm_rope_kernel<64, true, kFwdSteps> : qk_norm_rope_kernel<64, false, kFwdSteps>
-                        : interleaved ? qk_norm_rope_kernel<128, true, kFwdSteps> : qk_norm_rope_kernel<128, false, kFwdSteps>;
+    const unsigned grid = deal_units(p, dev->num_sms, kFwdCtasPerSm, kFwdWarps);
+    const auto kernel = d == 64 ? interleaved ? qk_norm_rope_kernel<64, true, kFwdSlots> : qk_norm_rope_kernel<64, false, kFwdSlots>
+                        : interleaved ? qk_norm_rope_kernel<128, true, kFwdSlots> : qk_norm_rope_kernel<128, false, kFwdSlots>;
     if ((st = allow_smem(dev->ready_configured[0][d == 128][interleaved != 0], kernel, kFwdSmem)) != ATTN_OK) return st;
-    kernel<<<grid, kReadyWarps * 32, kFwdSmem, stream>>>(p);
+    kernel<<<grid, kFwdWarps * 32, kFwdSmem, stream>>>(p);
     return launched();
 }
 
@@ -203,7 +200,7 @@ extern "C" int attn_qk_norm_rope_bwd(const void* dQout, const int64_t* dqo_strid
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != ATTN_OK) return st;
     if (any_norm && workspace_bytes < attn_qk_norm_rope_bwd_workspace_bytes(d)) return ATTN_ERR_INVALID_ARG;
-    const unsigned grid = deal_units(p, dev->num_sms, kBwdCtasPerSm);
+    const unsigned grid = deal_units(p, dev->num_sms, kBwdCtasPerSm, kBwdWarps);
     ReadyDw sums;
     const int first[2] = {0, p.first_k}, rows[2] = {p.first_k, static_cast<int>(grid) - p.first_k};
     for (int t = 0; t < 2; ++t) {
@@ -212,10 +209,10 @@ extern "C" int attn_qk_norm_rope_bwd(const void* dQout, const int64_t* dqo_strid
         sums.rows[t] = rows[t];
         sums.dw[t] = dw[t];
     }
-    const auto grad = d == 64 ? interleaved ? qk_norm_rope_bwd_kernel<64, true, kBwdSteps> : qk_norm_rope_bwd_kernel<64, false, kBwdSteps>
-                      : interleaved ? qk_norm_rope_bwd_kernel<128, true, kBwdSteps> : qk_norm_rope_bwd_kernel<128, false, kBwdSteps>;
+    const auto grad = d == 64 ? interleaved ? qk_norm_rope_bwd_kernel<64, true, kBwdSlots> : qk_norm_rope_bwd_kernel<64, false, kBwdSlots>
+                      : interleaved ? qk_norm_rope_bwd_kernel<128, true, kBwdSlots> : qk_norm_rope_bwd_kernel<128, false, kBwdSlots>;
     if ((st = allow_smem(dev->ready_configured[1][d == 128][interleaved != 0], grad, kBwdSmem)) != ATTN_OK) return st;
-    grad<<<grid, kReadyWarps * 32, kBwdSmem, stream>>>(p);
+    grad<<<grid, kBwdWarps * 32, kBwdSmem, stream>>>(p);
     if ((st = launched()) != ATTN_OK || !any_norm) return st;
     // its CTAs may start as the gradient kernel's retire, and wait in-kernel for its completion
     cudaLaunchConfig_t cfg = {};

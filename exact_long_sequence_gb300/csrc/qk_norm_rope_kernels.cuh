@@ -32,16 +32,19 @@
 #include "rowwise_kernels.cuh"
 #include "sm103_ptx.cuh"
 
-#ifndef FU
-#define FU 6
-#define FC 2
-#define BU 4
-#define BC 2
-#endif
 namespace elsattn {
 
 constexpr int kReadyMaxAxes = 4;
-constexpr int kReadyWarps = 8;  // per CTA
+
+// Launch shapes, chosen by measurement on 32768 tokens of 32 + 8 heads of 128
+// (forward 671 MB, backward 1007 MB moved; a plain copy of that size runs at 6.6 TB/s):
+//   forward:  16 warps an SM and 2 steps in flight a warp: 111 us, 6.0 TB/s.  More warps
+//             (20: 115 us, 24: 128 us) or more steps in flight (3: 119 us, 5: 128 us) are slower, one
+//             step in flight too (138 us).
+//   backward: 12 warps an SM, so that a warp's 150-odd registers are held without spills, 2 steps in flight:
+//             165 us, 6.1 TB/s (8 warps: 205 us; 16 warps with spills: 216 us).
+constexpr int kFwdWarps = 4, kFwdCtasPerSm = 4, kFwdSlots = 3;
+constexpr int kBwdWarps = 12, kBwdCtasPerSm = 1, kBwdSlots = 3;
 
 struct ReadyTensor {
     const __nv_bfloat16* x;   // input rows (backward: the forward's input; unused without a norm)
@@ -393,7 +396,7 @@ extern __shared__ __align__(16) uint8_t ready_smem[];
 
 // U: slots of a warp's ring.
 template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kReadyWarps * 32, FC) qk_norm_rope_kernel(const __grid_constant__ ReadyParams p) {
+__global__ void __launch_bounds__(kFwdWarps * 32, kFwdCtasPerSm) qk_norm_rope_kernel(const __grid_constant__ ReadyParams p) {
     using A = ReadyAngles<D>;
     using Ring = ReadyRing<D, 2, U>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -401,16 +404,14 @@ __global__ void __launch_bounds__(kReadyWarps * 32, FC) qk_norm_rope_kernel(cons
     const ReadyLane<D, INTER> at(c, p.rot);
     const ReadyPlace place(p);
     const ReadyTensor& rt = p.t[place.t];
-    const uint32_t warps = place.blocks * kReadyWarps;
+    const uint32_t warps = place.blocks * kFwdWarps;
     ReadyWalk<A::kGroups> w;
-    w.u = place.block * kReadyWarps + warp;
+    w.u = place.block * kFwdWarps + warp;
     if (w.u >= rt.units) return;
     Ring ring;
     ring.start(p, rt, at, g, true, false, smem_u32(ready_smem) + warp * Ring::kBytes, w.u, warps);
     A angles;
     angles.template init<INTER>(p, lane);
-    f2 wa[4], wb[4];
-    load_weight(rt.w, at.a0, at.b0, wa, wb);
     const bool norm = rt.w != nullptr, all = p.rot == D;
     w.decode(p, rt);
     int pos[A::kOwn];
@@ -419,7 +420,11 @@ __global__ void __launch_bounds__(kReadyWarps * 32, FC) qk_norm_rope_kernel(cons
         float cs[8], sn[8];
         angles.eval(pos, lane, cs, sn);
         ReadyTurn<D, INTER, 1> turn;
-        turn.set(cs, sn, at.rot_a, at.rot_b, wa, wb);
+        {  // the weights are read again for each unit (from L1): 16 registers less
+            f2 wa[4], wb[4];
+            load_weight(rt.w, at.a0, at.b0, wa, wb);
+            turn.set(cs, sn, at.rot_a, at.rot_b, wa, wb);
+        }
         __nv_bfloat16* dst = rt.y + w.offset(rt.ys, g);
         int s = w.s;
         const int s1 = w.s1;
@@ -465,22 +470,22 @@ __global__ void __launch_bounds__(kReadyWarps * 32, FC) qk_norm_rope_kernel(cons
 // the row groups of the warp, the warps of the CTA (both in a fixed order), and
 // by qk_norm_rope_dw_kernel over the CTAs: the same inputs give the same bits.
 template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kReadyWarps * 32, BC) qk_norm_rope_bwd_kernel(const __grid_constant__ ReadyParams p) {
+__global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_rope_bwd_kernel(const __grid_constant__ ReadyParams p) {
     using A = ReadyAngles<D>;
     using Ring = ReadyRing<D, 4, U>;
-    __shared__ float s_dw[kReadyWarps][D];
+    __shared__ float s_dw[kBwdWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = lane % A::kLanes, g = lane / A::kLanes;
     const ReadyLane<D, INTER> at(c, p.rot);
     const ReadyPlace place(p);
     const ReadyTensor& rt = p.t[place.t];
     const bool norm = rt.w != nullptr, all = p.rot == D;
-    const uint32_t warps = place.blocks * kReadyWarps;
+    const uint32_t warps = place.blocks * kBwdWarps;
     f2 acc[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = 0;
     ReadyWalk<A::kGroups> w;
-    w.u = place.block * kReadyWarps + warp;
+    w.u = place.block * kBwdWarps + warp;
     bool more = w.u < rt.units;
     if (more) {
         Ring ring;
@@ -567,7 +572,7 @@ __global__ void __launch_bounds__(kReadyWarps * 32, BC) qk_norm_rope_bwd_kernel(
     for (int i = threadIdx.x; i < D; i += blockDim.x) {
         float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < kReadyWarps; ++k) v += s_dw[k][i];
+        for (int k = 0; k < kBwdWarps; ++k) v += s_dw[k][i];
         rt.part[static_cast<size_t>(place.block) * D + i] = v;
     }
 }
