@@ -21,7 +21,7 @@ struct DeviceState {
     uint32_t* error_word = nullptr;  // 256-byte device block, first word = error code
     bool smem_configured[2][2][2] = {};                                   // forward <d == 128><causal><dynamic schedule>
     bool bwd_smem_configured[2][2] = {{false, false}, {false, false}};  // backward <d == 128><causal>
-    bool ready_configured[2][2][2] = {};  // query / key preparation <backward><d == 128><interleaved>
+    bool ready_configured[2][8] = {};  // query / key preparation <backward><variant>
     bool fp8_smem_configured[2][2][2] = {};  // FP8 forward <causal><dynamic schedule><K/V segments>
 };
 

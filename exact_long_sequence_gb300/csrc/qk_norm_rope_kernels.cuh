@@ -17,7 +17,8 @@
 // lane; a warp holds 32 / (d / 16) rows (heads) of one token at a time, so the
 // token's sines and cosines are computed once per warp, each lane evaluating
 // the share of pairs that its row group would otherwise repeat, and are passed
-// around by shuffles.
+// around by shuffles.  A tensor with fewer heads than that can put the rows of
+// several tokens side by side (MULTI).
 //
 // Angles: a position times a frequency loses its fraction of a turn in fp32
 // (position 10^6 at frequency 1 is off by 0.06 rad).  Here the frequency is
@@ -53,9 +54,10 @@ struct ReadyTensor {
     const __nv_bfloat16* w;   // [d] norm weight, or nullptr: no norm
     int64_t xs[3], gs[3], ys[3];  // strides in elements: batch, head, token
     int H;
-    int steps;                // warp steps per token: ceil(H / rows per warp)
+    int hp, tp;               // a warp step holds hp heads (a power of two) of each of tp tokens, hp * tp = rows per warp
+    int steps;                // steps of a token (or of tp tokens): ceil(H / hp)
     int steps_per_unit;       // a work unit: so many steps of one token
-    int units_per_token;
+    int units_per_token;      // of a token, or of tp tokens
     uint32_t units;
     float* part;              // backward: [CTAs of this tensor][d] fp32 partial sums of dw, or nullptr
 };
@@ -70,6 +72,7 @@ struct ReadyParams {
     int rot;                  // rotated elements of a row
     int N;
     uint32_t tokens;          // B * N
+    bool multi;               // a tensor's steps may hold several tokens (tp > 1)
     float eps;
 };
 
@@ -158,11 +161,12 @@ __device__ __forceinline__ uint64_t turn_fraction(double inv_freq) {
 // Cosines and sines of the pairs this lane's elements belong to, for one
 // token.  The rows of a warp share the token, so of the 8 pairs that the lanes
 // with the same c need, each of the kGroups row groups evaluates 8 / kGroups.
-template <int D>
+template <int D, bool MULTI>
 struct ReadyAngles {
     static constexpr int kLanes = D / 16;        // lanes per row
     static constexpr int kGroups = 32 / kLanes;  // rows per warp step
     static constexpr int kOwn = 8 / kGroups;     // pairs evaluated per lane
+    static constexpr int kPos = MULTI ? 8 : kOwn;  // positions held: kOwn for each of a step's tokens
     uint64_t f[kOwn];
     int axis[kOwn];
 
@@ -181,26 +185,41 @@ struct ReadyAngles {
             }
         }
     }
-    // The positions of a token, one per evaluated pair (issued early).
-    __device__ __forceinline__ void load(const ReadyParams& p, int b, int n, int (&pos)[kOwn]) const {
+    // Positions of the pairs this lane evaluates, for each of the step's tp
+    // tokens (issued early).  `at`: where this lane's own token has its positions.
+    __device__ __forceinline__ void load(const ReadyParams& p, const ReadyTensor& rt, int64_t at, int (&pos)[kPos]) const {
 #pragma unroll
-        for (int k = 0; k < kOwn; ++k)
-            pos[k] = p.pos[axis[k] * p.pos_axis + b * p.pos_batch + n];
-    }
-    __device__ __forceinline__ void eval(const int (&pos)[kOwn], int lane, float (&cs)[8], float (&sn)[8]) const {
-        float c0[kOwn], s0[kOwn];
+        for (int t = 0; t < (MULTI ? kGroups : 1); ++t) {
+            if (MULTI && t >= rt.tp) break;
+            const int64_t from = !MULTI || rt.tp == 1 ? at : __shfl_sync(0xffffffffu, at, t * rt.hp * kLanes);
 #pragma unroll
-        for (int k = 0; k < kOwn; ++k) {
-            const uint64_t turn = f[k] * static_cast<uint64_t>(static_cast<int64_t>(pos[k]));
-            // the top 32 bits as a signed fraction of a turn, [-1/2, 1/2); in units of pi: [-1, 1)
-            const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
-            sincospif(x, &s0[k], &c0[k]);
+            for (int k = 0; k < kOwn; ++k) pos[t * kOwn + k] = p.pos[axis[k] * p.pos_axis + from];
         }
+    }
+    // cs, sn: of this lane's own token, the step's gt-th
+    __device__ __forceinline__ void eval(const int (&pos)[kPos], const ReadyTensor& rt, int gt, int lane, float (&cs)[8],
+                                         float (&sn)[8]) const {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int src = (k / kOwn) * kLanes + lane % kLanes;
-            cs[k] = __shfl_sync(0xffffffffu, c0[k % kOwn], src);
-            sn[k] = __shfl_sync(0xffffffffu, s0[k % kOwn], src);
+        for (int t = 0; t < (MULTI ? kGroups : 1); ++t) {
+            if (MULTI && t >= rt.tp) break;
+            float c0[kOwn], s0[kOwn];
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                const uint64_t turn = f[k] * static_cast<uint64_t>(static_cast<int64_t>(pos[t * kOwn + k]));
+                // the top 32 bits as a signed fraction of a turn, [-1/2, 1/2); in units of pi: [-1, 1)
+                const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
+                sincospif(x, &s0[k], &c0[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int src = (k / kOwn) * kLanes + lane % kLanes;
+                const float cv = __shfl_sync(0xffffffffu, c0[k % kOwn], src);
+                const float sv = __shfl_sync(0xffffffffu, s0[k % kOwn], src);
+                if (!MULTI || t == 0 || gt == t) {
+                    cs[k] = cv;
+                    sn[k] = sv;
+                }
+            }
         }
     }
 };
@@ -288,22 +307,35 @@ __device__ __forceinline__ void load_weight(const __nv_bfloat16* w, int a0, int 
     }
 }
 
-// A warp's walk over its units, step by step: where the step's rows are.
-template <int GROUPS>
+// A warp's walk over its units, step by step, seen by one lane: where the
+// step has its row.
+template <int GROUPS, bool MULTI>
 struct ReadyWalk {
     uint32_t u;   // unit (>= units: done)
     int s, s1;    // step within the token, and the unit's end
-    int b, n;     // the token's batch and place
+    int gh, gt;   // this lane's head and token within a step
+    int b, n;     // its token's batch and place
+    bool live;    // the token exists
+    __device__ __forceinline__ void begin(const ReadyTensor& rt, uint32_t unit, int g) {
+        u = unit;
+        gh = MULTI ? g & (rt.hp - 1) : g;
+        gt = MULTI ? g / rt.hp : 0;
+    }
     __device__ __forceinline__ void decode(const ReadyParams& p, const ReadyTensor& rt) {
-        const uint32_t token = u / rt.units_per_token;
-        s = static_cast<int>(u - token * rt.units_per_token) * rt.steps_per_unit;
+        const uint32_t group = u / rt.units_per_token;
+        s = static_cast<int>(u - group * rt.units_per_token) * rt.steps_per_unit;
         s1 = min(rt.steps, s + rt.steps_per_unit);
+        uint32_t token = MULTI ? group * rt.tp + gt : group;
+        live = !MULTI || token < p.tokens;
+        if (!live) token = p.tokens - 1;
         b = static_cast<int>(token / static_cast<uint32_t>(p.N));
         n = static_cast<int>(token - static_cast<uint32_t>(b) * p.N);
     }
-    __device__ __forceinline__ int64_t offset(const int64_t (&st)[3], int g) const {
-        return b * st[0] + (s * GROUPS + g) * st[1] + n * st[2];
+    __device__ __forceinline__ bool on(const ReadyTensor& rt, int step) const { return live && step * GROUPS + gh < rt.H; }
+    __device__ __forceinline__ int64_t offset(const int64_t (&st)[3]) const {
+        return b * st[0] + (s * GROUPS + gh) * st[1] + n * st[2];
     }
+    __device__ __forceinline__ int64_t positions(const ReadyParams& p) const { return b * p.pos_batch + n; }
 };
 
 // 16 bytes from global to shared memory, asynchronously; zeros where !on.
@@ -327,25 +359,25 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
 // U slots, U - 1 steps in flight: a step's copies go to the slot read one step
 // before, whose values have been used (its results are stored) by then.
 // VECS: 16-byte vectors a lane moves per step.
-template <int D, int VECS, int U>
+template <int D, int VECS, int U, bool MULTI>
 struct ReadyRing {
-    using A = ReadyAngles<D>;
+    using A = ReadyAngles<D, MULTI>;
     static constexpr int kBytes = U * VECS * 512;  // per warp
-    ReadyWalk<A::kGroups> w;
+    ReadyWalk<A::kGroups, MULTI> w;
     uint32_t base;       // this lane's place in the warp's ring
     uint32_t warps;
     int fill, slot;      // the ring slots to fill and to read next
     const __nv_bfloat16 *x, *g;   // the next step's rows (g: the second source, where there is one)
 
-    __device__ __forceinline__ void place(const ReadyTensor& rt, int grp, bool first, bool second) {
-        if (first) x = rt.x + w.offset(rt.xs, grp);
-        if (second) g = rt.g + w.offset(rt.gs, grp);
+    __device__ __forceinline__ void place(const ReadyTensor& rt, bool first, bool second) {
+        if (first) x = rt.x + w.offset(rt.xs);
+        if (second) g = rt.g + w.offset(rt.gs);
     }
     template <class Lane>
-    __device__ __forceinline__ void issue(const ReadyParams& p, const ReadyTensor& rt, const Lane& at, int grp, bool first,
+    __device__ __forceinline__ void issue(const ReadyParams& p, const ReadyTensor& rt, const Lane& at, bool first,
                                           bool second) {
         if (w.u < rt.units) {
-            const bool on = w.s * A::kGroups + grp < rt.H;
+            const bool on = w.on(rt, w.s);
             const uint32_t dst = base + fill * (VECS * 512);
             if (first) {
                 copy16(dst, on ? x + at.a0 : rt.x, on);
@@ -361,7 +393,7 @@ struct ReadyRing {
                 w.u += warps;
                 if (w.u < rt.units) {
                     w.decode(p, rt);
-                    place(rt, grp, first, second);
+                    place(rt, first, second);
                 }
             }
         }
@@ -382,31 +414,31 @@ struct ReadyRing {
         warps = n;
         fill = slot = 0;
         x = g = nullptr;
-        w.u = u0;
+        w.begin(rt, u0, grp);
         if (w.u < rt.units) {
             w.decode(p, rt);
-            place(rt, grp, first, second);
+            place(rt, first, second);
         }
 #pragma unroll 1
-        for (int i = 0; i < U - 1; ++i) issue(p, rt, at, grp, first, second);
+        for (int i = 0; i < U - 1; ++i) issue(p, rt, at, first, second);
     }
 };
 
 extern __shared__ __align__(16) uint8_t ready_smem[];
 
 // U: slots of a warp's ring.
-template <int D, bool INTER, int U>
+template <int D, bool INTER, int U, bool MULTI>
 __global__ void __launch_bounds__(kFwdWarps * 32, kFwdCtasPerSm) qk_norm_rope_kernel(const __grid_constant__ ReadyParams p) {
-    using A = ReadyAngles<D>;
-    using Ring = ReadyRing<D, 2, U>;
+    using A = ReadyAngles<D, MULTI>;
+    using Ring = ReadyRing<D, 2, U, MULTI>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = lane % A::kLanes, g = lane / A::kLanes;
     const ReadyLane<D, INTER> at(c, p.rot);
     const ReadyPlace place(p);
     const ReadyTensor& rt = p.t[place.t];
     const uint32_t warps = place.blocks * kFwdWarps;
-    ReadyWalk<A::kGroups> w;
-    w.u = place.block * kFwdWarps + warp;
+    ReadyWalk<A::kGroups, MULTI> w;
+    w.begin(rt, place.block * kFwdWarps + warp, g);
     if (w.u >= rt.units) return;
     Ring ring;
     ring.start(p, rt, at, g, true, false, smem_u32(ready_smem) + warp * Ring::kBytes, w.u, warps);
@@ -414,32 +446,33 @@ __global__ void __launch_bounds__(kFwdWarps * 32, kFwdCtasPerSm) qk_norm_rope_ke
     angles.template init<INTER>(p, lane);
     const bool norm = rt.w != nullptr, all = p.rot == D;
     w.decode(p, rt);
-    int pos[A::kOwn];
-    angles.load(p, w.b, w.n, pos);
+    int pos[A::kPos];
+    angles.load(p, rt, w.positions(p), pos);
     while (true) {
         float cs[8], sn[8];
-        angles.eval(pos, lane, cs, sn);
+        angles.eval(pos, rt, w.gt, lane, cs, sn);
         ReadyTurn<D, INTER, 1> turn;
         {  // the weights are read again for each unit (from L1): 16 registers less
             f2 wa[4], wb[4];
             load_weight(rt.w, at.a0, at.b0, wa, wb);
             turn.set(cs, sn, at.rot_a, at.rot_b, wa, wb);
         }
-        __nv_bfloat16* dst = rt.y + w.offset(rt.ys, g);
+        __nv_bfloat16* dst = rt.y + w.offset(rt.ys);
         int s = w.s;
         const int s1 = w.s1;
+        const bool live = w.live;
         w.u += warps;
         const bool more = w.u < rt.units;
         if (more) {  // the next unit's positions arrive while this one's rows are worked on
             w.decode(p, rt);
-            angles.load(p, w.b, w.n, pos);
+            angles.load(p, rt, w.positions(p), pos);
         }
         for (; s < s1; ++s) {
             f2 a[4], bb[4];
             const uint32_t src = ring.next();
             unpack8(ld_shared16(src), a);
             unpack8(ld_shared16(src + 512), bb);
-            ring.issue(p, rt, at, g, true, false);
+            ring.issue(p, rt, at, true, false);
             if (norm) {
                 f2 s2 = mul2(a[0], a[0]), t2 = mul2(bb[0], bb[0]);
 #pragma unroll
@@ -456,7 +489,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, kFwdCtasPerSm) qk_norm_rope_ke
                 }
             }
             turn.apply(a, bb, all, at.rot_a, at.rot_b);
-            if (s * A::kGroups + g < rt.H) {
+            if (live && s * A::kGroups + w.gh < rt.H) {
                 *reinterpret_cast<uint4*>(dst + at.a0) = pack8(a);
                 *reinterpret_cast<uint4*>(dst + at.b0) = pack8(bb);
             }
@@ -469,10 +502,10 @@ __global__ void __launch_bounds__(kFwdWarps * 32, kFwdCtasPerSm) qk_norm_rope_ke
 // The gradient.  dw is summed per lane in fp32 over the warp's rows, then over
 // the row groups of the warp, the warps of the CTA (both in a fixed order), and
 // by qk_norm_rope_dw_kernel over the CTAs: the same inputs give the same bits.
-template <int D, bool INTER, int U>
+template <int D, bool INTER, int U, bool MULTI>
 __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_rope_bwd_kernel(const __grid_constant__ ReadyParams p) {
-    using A = ReadyAngles<D>;
-    using Ring = ReadyRing<D, 4, U>;
+    using A = ReadyAngles<D, MULTI>;
+    using Ring = ReadyRing<D, 4, U, MULTI>;
     __shared__ float s_dw[kBwdWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = lane % A::kLanes, g = lane / A::kLanes;
@@ -484,8 +517,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_rope_bw
     f2 acc[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = 0;
-    ReadyWalk<A::kGroups> w;
-    w.u = place.block * kBwdWarps + warp;
+    ReadyWalk<A::kGroups, MULTI> w;
+    w.begin(rt, place.block * kBwdWarps + warp, g);
     bool more = w.u < rt.units;
     if (more) {
         Ring ring;
@@ -495,24 +528,25 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_rope_bw
         f2 wa[4], wb[4];
         load_weight(rt.w, at.a0, at.b0, wa, wb);
         w.decode(p, rt);
-        int pos[A::kOwn];
-        angles.load(p, w.b, w.n, pos);
+        int pos[A::kPos];
+        angles.load(p, rt, w.positions(p), pos);
         while (more) {
             float cs[8], sn[8];
-            angles.eval(pos, lane, cs, sn);
+            angles.eval(pos, rt, w.gt, lane, cs, sn);
             ReadyTurn<D, INTER, -1> turn;
             turn.set(cs, sn, at.rot_a, at.rot_b);
-            __nv_bfloat16* dst = rt.y + w.offset(rt.ys, g);
+            __nv_bfloat16* dst = rt.y + w.offset(rt.ys);
             int s = w.s;
             const int s1 = w.s1;
+            const bool live = w.live;
             w.u += warps;
             more = w.u < rt.units;
             if (more) {
                 w.decode(p, rt);
-                angles.load(p, w.b, w.n, pos);
+                angles.load(p, rt, w.positions(p), pos);
             }
             for (; s < s1; ++s) {
-                const bool on = s * A::kGroups + g < rt.H;
+                const bool on = live && s * A::kGroups + w.gh < rt.H;
                 f2 ua[4], ub[4], ha[4], hb[4];
                 const uint32_t src = ring.next();
                 unpack8(ld_shared16(src + 1024), ua);
@@ -521,7 +555,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_rope_bw
                     unpack8(ld_shared16(src), ha);
                     unpack8(ld_shared16(src + 512), hb);
                 }
-                ring.issue(p, rt, at, g, norm, true);
+                ring.issue(p, rt, at, norm, true);
                 turn.apply(ua, ub, all, at.rot_a, at.rot_b);
                 if (norm) {
                     f2 va[4], vb[4];

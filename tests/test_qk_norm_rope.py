@@ -170,6 +170,9 @@ SHAPES = [
     (128, 5, 5, 2, 33, 96, (7, 40, 1), False, 1000, False),
     (128, 6, 2, 2, 9, 80, (10, 10, 10, 10), True, 1000, True),
     (128, 16, 4, 1, 2500, 128, (64,), False, 2500, True),  # whole tokens per warp
+    (128, 2, 1, 3, 333, 128, (20, 20, 24), True, 500, True),  # several tokens per warp step, the last step short
+    (64, 3, 2, 5, 501, 48, (24,), False, 500, False),
+    (64, 1, 4, 2, 4099, 64, (32,), False, 5000, True),
     (128, 40, 8, 64, 1, 64, (32,), False, 100000, True),
 ]
 
