@@ -60,6 +60,8 @@ EXPORTED_SYMBOLS = (
     "attn_qk_norm_rope",
     "attn_qk_norm_rope_bwd",
     "attn_qk_norm_rope_bwd_workspace_bytes",
+    "attn_fwd_prefix",
+    "attn_fwd_prefix_workspace_bytes",
 )
 
 
@@ -154,6 +156,10 @@ def load_library(path: str | None = None):
     lib.attn_qk_norm_rope_bwd.restype = i
     lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i]
     lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_fwd_prefix.argtypes = [vp] * 14 + [i] * 7 + [f, vp, ctypes.c_size_t, vp]
+    lib.attn_fwd_prefix.restype = i
+    lib.attn_fwd_prefix_workspace_bytes.argtypes = [i] * 7
+    lib.attn_fwd_prefix_workspace_bytes.restype = ctypes.c_size_t
     if path is None:
         _lib = lib
     return lib
@@ -169,6 +175,10 @@ def default_scale(d: int) -> float:
     import torch
 
     return float(torch.tensor(1.0 / math.sqrt(d), dtype=torch.float32).item())
+
+
+# default_scale of the two head sizes, as it computes them
+_SCALES = {d: struct.unpack("f", struct.pack("f", 1.0 / math.sqrt(d)))[0] for d in (64, 128)}
 
 
 def _stream_handle(stream):
@@ -523,6 +533,87 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k
             0 if workspace is None else workspace.numel(), _stream_handle(stream))
     _check(st, "attn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
+
+
+def prefix_workspace_bytes(R: int, Hq: int, Hk: int, T: int, P: int, C: int, d: int) -> int:
+    """Device bytes attn_fwd_prefix needs for this shape on the current device (0: invalid shape)."""
+    return int(load_library().attn_fwd_prefix_workspace_bytes(R, Hq, Hk, T, P, C, d))
+
+
+_pack2 = struct.Struct("2q").pack
+
+
+def attn_fwd_prefix(q, k_prefix, v_prefix, k_own=None, v_own=None, own_lens=None, scale: float | None = None, out=None,
+                    lse=None, workspace=None, stream=None):
+    """O, LSE of T new tokens of R requests over a prefix all of them share and each request's own keys.
+
+    q         : bf16 CUDA [R, Hq, T, d], d in {64, 128}
+    k_prefix, v_prefix : bf16 [Hk, P, d], Hk a divisor of Hq; None: no prefix
+    k_own, v_own : bf16 [R, Hk, C, d], caches of capacity C; None: no own keys
+    own_lens  : int32 [R] on the device: own keys of each request, the T new tokens among them as the
+                last; 0: the prefix alone; negative: padding, the request's rows are left as they were.
+                Token t sees the own keys j < own_lens - (T - 1 - t).
+    out, lse  : optional bf16 view like q and fp32 [R, Hq, T] (default: new contiguous tensors)
+    workspace : optional uint8 CUDA tensor of prefix_workspace_bytes() bytes
+    All bf16 tensors are views with d contiguous and other strides positive multiples of 8, so token-major
+    caches may be given transposed.  Returns (out, lse)."""
+    import torch
+
+    lib = load_library()
+    if q.dim() != 4 or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [R, Hq, T, d]")
+    device = q.device
+    R, Hq, T, d = q.shape
+    P = C = 0
+    kp = vp = ko = vo = lens = kps = vps = kos = vos = None
+    if k_prefix is None and k_own is None:
+        raise ValueError("give a prefix, own keys, or both")
+    Hk = k_prefix.shape[0] if k_prefix is not None else k_own.shape[1] if k_own.dim() == 4 else 0
+    if k_prefix is not None:
+        if k_prefix.dim() != 3 or v_prefix is None:
+            raise ValueError("k_prefix and v_prefix must be [Hk, P, d]")
+        P = k_prefix.shape[1]
+        for t in (k_prefix, v_prefix):
+            if t.dtype != torch.bfloat16 or t.device != device or t.shape != (Hk, P, d) or t.stride(2) != 1:
+                raise ValueError("k_prefix and v_prefix must be bf16 [Hk, P, d] on q's device, d contiguous")
+        kp, vp = k_prefix.data_ptr(), v_prefix.data_ptr()
+        kps, vps = _pack2(*k_prefix.stride()[:2]), _pack2(*v_prefix.stride()[:2])
+    if k_own is not None:
+        if k_own.dim() != 4 or v_own is None or own_lens is None:
+            raise ValueError("own keys need k_own and v_own [R, Hk, C, d] and own_lens")
+        C = k_own.shape[2]
+        if own_lens.dtype != torch.int32 or own_lens.device != device or own_lens.shape != (R,) or \
+                not own_lens.is_contiguous():
+            raise ValueError("own_lens must be a contiguous int32 tensor [R] on q's device")
+        shape = (R, Hk, C, d)
+        ko, kos = _view("k_own", k_own, shape, device)
+        vo, vos = _view("v_own", v_own, shape, device)
+        lens = own_lens.data_ptr()
+    if scale is None:
+        scale = _SCALES.get(d) or default_scale(d)
+    with _on_device(device):
+        fresh = []
+        if out is None:
+            out = torch.empty((R, Hq, T, d), dtype=torch.bfloat16, device=device)
+            fresh.append(out)
+        if lse is None:
+            lse = torch.empty((R, Hq, T), dtype=torch.float32, device=device)
+            fresh.append(lse)
+        elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (R, Hq, T) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous fp32 tensor [R, Hq, T] on q's device")
+        if workspace is None:
+            workspace = torch.empty(lib.attn_fwd_prefix_workspace_bytes(R, Hq, Hk, T, P, C, d), dtype=torch.uint8,
+                                    device=device)
+            fresh.append(workspace)
+        elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+        _new_for(stream, *fresh)
+        qp, qs = _view("q", q, q.shape, device)
+        op, os_ = _view("out", out, q.shape, device)
+        st = lib.attn_fwd_prefix(qp, qs, kp, kps, vp, vps, ko, kos, vo, vos, lens, op, os_, lse.data_ptr(), R, Hq, Hk, T,
+                                 P, C, d, scale, workspace.data_ptr() or None, workspace.numel(), _stream_handle(stream))
+    _check(st, "attn_fwd_prefix")
+    return out, lse
 
 
 def attn_fwd_noalloc(q, k, v, out, lse, causal: bool = False, scale: float | None = None, stream=None):

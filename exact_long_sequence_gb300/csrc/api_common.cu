@@ -80,6 +80,18 @@ int encode_rows_map(CUtensorMap* map, const void* base, int BH, int N, int d, in
     return ATTN_OK;
 }
 
+int encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* e, const uint64_t* st, uint32_t box_rows) {
+    cuuint64_t dims[4], strides[3];
+    cuuint32_t box[4] = {64, box_rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) dims[i] = e[i];
+    for (int i = 0; i + 1 < rank; ++i) strides[i] = st[i];
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+    return ATTN_OK;
+}
+
 int encode_f32_rows_map(CUtensorMap* map, void* base, int BH, int N, int d, int box_rows) {
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 4, static_cast<cuuint64_t>(N) * d * 4};

@@ -1,0 +1,870 @@
+// Attention of a batch of requests that share a long prefix, for sm_103a: T new
+// tokens of each of R requests against the prefix's keys and values (stored
+// once) and the request's own.  Queries have Hq = G Hk heads; the G heads that
+// share a key head, the T tokens and, for the prefix, all R requests are rows
+// of one matrix, so the prefix costs one pass over its K/V (and one product
+// with R G T rows), however many requests there are:
+//     rows of key head h:  i = (r G + g) T + t,
+//     O_i = sum_j p_ij V_j over the prefix's and r's own visible keys j.
+// The two ranges (and pieces of them) are independent softmaxes, each giving
+// O over its keys and its log-sum-exp; attn_prefix_combine_kernel merges them,
+//     LSE = log sum_s exp(LSE_s),  O = sum_s exp(LSE_s - LSE) O_s,
+// the combination step of the online softmax applied across pieces.
+//
+// A work item is (key head, up to 256 rows, a run of 128-key tiles of one K/V
+// source).  One persistent CTA per SM runs the items of its share:
+//   warp 0 (one lane)  TMA producer of K_j, V_j into a ring of stages
+//   warp 1             tcgen05.mma issuer; owns the TMEM allocation
+//   warp 2             scheduler: works out the CTA's items (the own lengths are
+//                      device data) and passes them to the others through a ring
+//   warp 3             Q loader: gathers the item's rows into a swizzled tile
+//   warps 4-7, 8-11    softmax warpgroups, one per chain (below)
+// Two chains (S_c, O_c in TMEM, softmax warpgroup c) alternate step by step, so
+// that the tensor core works on one while the softmax of the other runs:
+//   - an item of more than 128 rows has two query tiles, one a chain, that share
+//     every K/V tile;
+//   - an item of at most 128 rows has one query tile, and the chains take turns
+//     with its K/V tiles (even tiles on one, odd on the other); their two
+//     softmaxes are merged when the item ends, each warpgroup writing half of
+//     the columns.
+// The steps of consecutive items form one stream: the next item's first score
+// product is issued before the last output product of this one, and an item of
+// a single tile takes the chain that the previous item left, so short items
+// overlap too.
+//
+// What bounds it: up to about 128 rows a key head, reading K/V from HBM; with
+// 256 and more, the tensor core (4 d operations a row and key).
+#pragma once
+
+#include <cuda.h>
+#include <cstdint>
+
+#include "attn_fwd_kernel.cuh"
+#include "plan.h"
+#include "sm103_ptx.cuh"
+
+namespace elsattn {
+
+// Units of work: a tile of 128 keys is 4, a tail 1 for each 32 keys begun, an
+// item besides its tiles (query rows, pipeline fill, epilogue) kPfxItemCost.
+constexpr int kPfxTileCost = 4;
+constexpr int kPfxItemCost = 2;
+constexpr int kPfxOwnBox = 32;   // keys per TMA box of the own caches
+constexpr int kPfxItemRing = 4;
+
+struct PrefixParams {
+    const __nv_bfloat16* q;
+    int64_t qs[3];          // strides in elements: request, head, token
+    __nv_bfloat16* o;
+    int64_t os[3];
+    float* lse;             // [R, Hq, T]
+    const int32_t* lens;    // [R] own keys, the new tokens among them; nullptr: none
+    int R, T, Hk, G;
+    int GT;                 // rows of a request at one key head
+    int P, C;               // prefix keys; own capacity
+    int pblocks;            // blocks of 256 rows over R GT
+    int ptiles, psegs, seg_tiles;  // prefix tiles; cut into psegs runs of seg_tiles
+    int pitems;             // Hk * psegs * pblocks
+    int oblocks;            // blocks of 256 rows over GT
+    int orows;              // rows of an own slot: min(GT, 256)
+    float* part_o;          // partial rows [.., d] fp32: first [psegs][Hk][R GT], then [own slots][orows]
+    float* part_lse;        // one per partial row
+    int64_t own_first;      // the first own slot's partial row
+    int64_t* own_start;     // [R + 1]: where each request's own work starts, and the total
+    uint32_t* error_word;
+    uint64_t timeout_ns;
+    float scale_log2, max_scale_log2;
+    uint32_t negate_scores;
+};
+
+// Own work is laid on a line: request by request, its (key head, row block)
+// sequences in order, each kPfxItemCost units and then its tiles.  The line is
+// cut into one stretch per CTA: CTAs [0, rem) have one prefix item more than
+// the others and get cap1 units, the others cap0, so that all end together.
+// A tile belongs to the CTA whose stretch holds the tile's first unit.  Caps
+// are 0 or at least a tile, so every CTA between the first and the last of a
+// sequence has a tile of it.
+struct OwnCut {
+    int64_t rem, cap1, cap0;
+    __device__ __forceinline__ OwnCut(const PrefixParams& p, int64_t total, int grid) {
+        rem = p.pitems % grid;
+        const int64_t item = kPfxItemCost + static_cast<int64_t>(p.seg_tiles) * kPfxTileCost;
+        const int64_t level = item * (grid - rem);  // what evens the CTAs out
+        if (rem == 0 || total > level) {
+            const int64_t e = (total - (rem == 0 ? 0 : level) + grid - 1) / grid;
+            cap1 = e;
+            cap0 = rem == 0 ? e : item + e;
+        } else {
+            cap1 = 0;
+            cap0 = (total + grid - rem - 1) / (grid - rem);
+        }
+        if (cap1 > 0 && cap1 < kPfxTileCost) cap1 = kPfxTileCost;
+        if (cap0 < kPfxTileCost) cap0 = kPfxTileCost;
+    }
+    __device__ __forceinline__ int64_t begin(int64_t cta) const {
+        return cta < rem ? cta * cap1 : rem * cap1 + (cta - rem) * cap0;
+    }
+    __device__ __forceinline__ int64_t cta_of(int64_t x) const {
+        return x < rem * cap1 ? x / cap1 : rem + (x - rem * cap1) / cap0;
+    }
+};
+__device__ __forceinline__ int own_len(const PrefixParams& p, int r) { return min(max(__ldg(p.lens + r), 0), p.C); }
+// Units of one sequence of a request with `len` own keys (0: no work), and of the request.
+__device__ __forceinline__ int64_t seq_cost(int len) { return len > 0 ? kPfxItemCost + (len + 31) / 32 : 0; }
+__device__ __forceinline__ int64_t request_cost(const PrefixParams& p, int len) { return seq_cost(len) * (p.Hk * p.oblocks); }
+
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += o;
+    }
+    return v;
+}
+
+struct PrefixItem {
+    int ntiles;      // -1: no more items
+    int tile0;       // first tile
+    int klen;        // keys of the source (the own length, or P)
+    int head;        // key head
+    int req;         // request of an own item; -1: the prefix
+    int row0, nrows; // rows of the key head's matrix
+    int pad;
+    int64_t part;    // partial row of row0
+};
+
+template <int D>
+struct PrefixSmem {
+    static constexpr int kTile = tile_bytes(D);
+    static constexpr int kStages = kv_stages_for(D);
+    static constexpr int kQOff = 0;
+    static constexpr int kRingOff = kQTiles * kTile;
+    static constexpr int kXchgOff = kRingOff + kStages * kTile;   // [128] (m, l) of one chain, then of the other
+    static constexpr int kItemOff = kXchgOff + 128 * 8;           // [kPfxItemRing] PrefixItem
+    static constexpr int kBarOff = kItemOff + kPfxItemRing * static_cast<int>(sizeof(PrefixItem));
+    static constexpr int kKvFull = 0;
+    static constexpr int kKvEmpty = kKvFull + kStages;
+    static constexpr int kQFull = kKvEmpty + kStages;     // [2] by slot
+    static constexpr int kQEmpty = kQFull + 2;            // [2]
+    static constexpr int kSFull = kQEmpty + 2;            // [2] by chain, as all below
+    static constexpr int kPHalf = kSFull + 2;             // [2] first half of P stored, O rescaled
+    static constexpr int kPFull = kPHalf + 2;             // [2]
+    static constexpr int kOFull = kPFull + 2;             // [2]
+    static constexpr int kOEmpty = kOFull + 2;            // [2]
+    static constexpr int kX = kOEmpty + 2;                // [2] the chain's (m, l) are in shared memory
+    static constexpr int kDrain = kX + 2;
+    static constexpr int kItemFull = kDrain + 1;          // [kPfxItemRing]
+    static constexpr int kItemEmpty = kItemFull + kPfxItemRing;
+    static constexpr int kNumBars = kItemEmpty + kPfxItemRing;
+    static constexpr int kFlagsOff = kBarOff + kNumBars * 8;
+    static constexpr int kBytes = kFlagsOff + 16 + kSmemAlign;
+    static_assert(sizeof(PrefixItem) % 8 == 0, "barriers are 8-byte aligned");
+    static_assert(kBytes <= kSmemLimit, "shared memory");
+    static_assert(2 * kBytes > 233472, "one CTA per SM (each allocates all of TMEM)");
+};
+constexpr int kPfxItemReaders = 11;  // producer, MMA, Q loader, eight softmax warps
+
+// 4-D tiled load.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_constant__ CUtensorMap tmap_vp,
+                   const __grid_constant__ CUtensorMap tmap_ko, const __grid_constant__ CUtensorMap tmap_vo,
+                   const __grid_constant__ PrefixParams p) {
+    using L = PrefixSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_base = smem_u32(smem);
+    const uint32_t bar0 = s_base + L::kBarOff;
+    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kFlagsOff);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlagsOff + 4);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const WaitCtx ctx{abort_flag, p.error_word, p.timeout_ns};
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0u;
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(bar(L::kKvFull + s), 1);
+            mbar_init(bar(L::kKvEmpty + s), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(L::kQFull + t), 32);
+            mbar_init(bar(L::kQEmpty + t), 1);
+            mbar_init(bar(L::kSFull + t), 1);
+            mbar_init(bar(L::kPHalf + t), 128);
+            mbar_init(bar(L::kPFull + t), 128);
+            mbar_init(bar(L::kOFull + t), 1);
+            mbar_init(bar(L::kOEmpty + t), 256);  // both warpgroups, or one that counts twice
+            mbar_init(bar(L::kX + t), 128);
+        }
+        mbar_init(bar(L::kDrain), 1);
+        for (int s = 0; s < kPfxItemRing; ++s) {
+            mbar_init(bar(L::kItemFull + s), 1);
+            mbar_init(bar(L::kItemEmpty + s), kPfxItemReaders);
+        }
+        fence_barrier_init();
+        if (p.P > 0) {
+            tma_prefetch_desc(&tmap_kp);
+            tma_prefetch_desc(&tmap_vp);
+        }
+        if (p.lens) {
+            tma_prefetch_desc(&tmap_ko);
+            tma_prefetch_desc(&tmap_vo);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    // The combine kernel may be scheduled onto SMs as this grid's CTAs retire;
+    // it waits for the whole grid before it reads the partial results.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // Reads the next item (ring entry n); `it.ntiles` is -1 after the last.
+    // Called by whole warps, or by one lane (whole = false).
+    auto take_item = [&](uint32_t n, PrefixItem& it, bool whole) -> bool {
+        const uint32_t s = n % kPfxItemRing;
+        bool got = mbar_wait(bar(L::kItemFull + s), (n / kPfxItemRing) & 1u, ctx);
+        if (whole) got = __all_sync(0xffffffffu, got);
+        if (!got) return false;
+        it = *reinterpret_cast<const PrefixItem*>(smem + L::kItemOff + s * sizeof(PrefixItem));
+        if (whole) __syncwarp();
+        if (!whole || lane == 0) mbar_arrive(bar(L::kItemEmpty + s));
+        return it.ntiles >= 0;
+    };
+    // Keys of the item's tile j (1 .. 128).
+    auto tile_keys = [](const PrefixItem& it, int j) -> int { return min(kBc, it.klen - (it.tile0 + j) * kBc); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            RingPos pos{0u, 0u};
+            uint32_t issued = 0;
+            bool ok = true;
+            PrefixItem it;
+            for (uint32_t n = 0; ok && take_item(n, it, false); ++n) {
+                for (int j = 0; j < it.ntiles && ok; ++j) {
+                    const int key = (it.tile0 + j) * kBc;
+                    const int boxes = (tile_keys(it, j) + kPfxOwnBox - 1) / kPfxOwnBox;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = mbar_wait(bar(L::kKvEmpty + pos.stage), pos.phase ^ 1u, ctx);
+                        if (!ok) break;
+                        const uint32_t full = bar(L::kKvFull + pos.stage);
+                        const uint32_t dst = s_base + L::kRingOff + pos.stage * L::kTile;
+                        if (it.req < 0) {
+                            mbar_arrive_expect_tx(full, L::kTile);
+#pragma unroll
+                            for (int b = 0; b < D / 64; ++b)
+                                tma_load_3d(dst + b * (kBc * 128), kv == 0 ? &tmap_kp : &tmap_vp, full, b * 64, key,
+                                            it.head);
+                        } else {
+                            mbar_arrive_expect_tx(full, boxes * kPfxOwnBox * D * 2);
+                            for (int i = 0; i < boxes; ++i)
+#pragma unroll
+                                for (int b = 0; b < D / 64; ++b)
+                                    tma_load_4d(dst + b * (kBc * 128) + i * (kPfxOwnBox * 128),
+                                                kv == 0 ? &tmap_ko : &tmap_vo, full, b * 64, key + i * kPfxOwnBox,
+                                                it.head, it.req);
+                        }
+                        pos = pos.next(L::kStages);
+                        ++issued;
+                    }
+                }
+            }
+            // every issued copy lands before the CTA's shared memory is released (bounded waits)
+            const uint32_t pending = issued < static_cast<uint32_t>(L::kStages) ? issued : L::kStages;
+            RingPos back = pos;
+            for (uint32_t i = 0; i < pending; ++i) {
+                back = back.stage == 0 ? RingPos{L::kStages - 1u, back.phase ^ 1u} : RingPos{back.stage - 1, back.phase};
+                mbar_wait_drain(bar(L::kKvFull + back.stage), back.phase, 50000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t idesc_s = make_idesc_bf16_f32(kBr, kBc, false, false) | (p.negate_scores ? kIdescNegateB : 0u);
+        constexpr uint32_t idesc_o = make_idesc_bf16_f32(kBr, D, false, true);
+        const uint64_t dq0 = make_smem_desc_sw128(s_base + L::kQOff, 16, 1024);
+        const uint64_t dk0 = make_smem_desc_sw128(s_base + L::kRingOff, 16, 1024);
+        const uint64_t dv0 = make_smem_desc_sw128(s_base + L::kRingOff, kBc * 128, 1024);
+        uint32_t p_phase = 0u, o_phase = 3u;  // parities to wait for, bit c of chain c
+        RingPos kpos{0u, 0u};   // K of the current tile
+        uint32_t qpos = 0;      // query tiles taken so far: slot qpos & 1
+        uint32_t par = 0;       // chain of the item's first step
+        bool ok = true;
+        // the output product that is due: of the step before
+        struct { bool due, first, last, first_v, last_v; int chain, ksteps; RingPos v; } pv{};
+        auto run_pv = [&]() -> bool {
+            if (!pv.due) return true;
+            pv.due = false;
+            const int c = pv.chain;
+            bool w = true;
+            if (pv.first_v) w = mbar_wait(bar(L::kKvFull + pv.v.stage), pv.v.phase, ctx);
+            w = w && mbar_wait(bar(L::kPHalf + c), (p_phase >> c) & 1u, ctx);
+            if (pv.first) {
+                w = w && mbar_wait(bar(L::kOEmpty + c), (o_phase >> c) & 1u, ctx);
+                o_phase ^= 1u << c;
+            }
+            if (!__all_sync(0xffffffffu, w)) return false;
+            tc_fence_after_sync();
+            const uint64_t b = dv0 + static_cast<uint64_t>((pv.v.stage * L::kTile) >> 4);
+            auto gemm_o = [&](int k0, int k1) {
+                for (int kk = k0; kk < k1; ++kk)
+                    mma_ts(tmem + 2 * kBc + c * D, tmem + c * kBc + kk * 8, b + static_cast<uint64_t>((kk * 16 * 128) >> 4),
+                           idesc_o, (!pv.first || kk > 0) ? 1u : 0u);
+            };
+            if (elect_one()) gemm_o(0, min(pv.ksteps, 4));
+            __syncwarp();
+            w = mbar_wait(bar(L::kPFull + c), (p_phase >> c) & 1u, ctx);
+            p_phase ^= 1u << c;
+            if (!__all_sync(0xffffffffu, w)) return false;
+            tc_fence_after_sync();
+            if (elect_one()) {
+                gemm_o(4, pv.ksteps);
+                if (pv.last_v) mma_commit(bar(L::kKvEmpty + pv.v.stage));
+                if (pv.last) mma_commit(bar(L::kOFull + c));
+            }
+            __syncwarp();
+            return true;
+        };
+        PrefixItem it;
+        for (uint32_t n = 0; ok && take_item(n, it, true); ++n) {
+            const bool two = it.nrows > kBr;   // two query tiles
+            const int steps = two ? 2 * it.ntiles : it.ntiles;
+            for (int s = 0; s < steps && ok; ++s) {
+                const int j = two ? s >> 1 : s, k = two ? s & 1 : 0;
+                const int c = (par + s) & 1;
+                const uint32_t qslot = (qpos + k) & 1u;
+                bool w = true;
+                if (k == 0) w = mbar_wait(bar(L::kKvFull + kpos.stage), kpos.phase, ctx);
+                if (j == 0) w = w && mbar_wait(bar(L::kQFull + qslot), ((qpos + k) >> 1) & 1u, ctx);
+                if (!(ok = __all_sync(0xffffffffu, w))) break;
+                const bool last_k = !two || k == 1;
+                if (elect_one()) {
+                    const uint64_t a = dq0 + static_cast<uint64_t>((qslot * L::kTile) >> 4);
+                    const uint64_t b = dk0 + static_cast<uint64_t>((kpos.stage * L::kTile) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * (kBr * 128) + (kk & 3) * 32) >> 4);
+                        mma_ss(tmem + c * kBc, a + off, b + off, idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(bar(L::kSFull + c));
+                    if (last_k) mma_commit(bar(L::kKvEmpty + kpos.stage));
+                    if (j == it.ntiles - 1) mma_commit(bar(L::kQEmpty + qslot));
+                }
+                __syncwarp();
+                if (!(ok = run_pv())) break;
+                pv.due = true;
+                pv.chain = c;
+                pv.v = kpos.next(L::kStages);
+                pv.ksteps = (tile_keys(it, j) + 15) / 16;
+                pv.first = two ? j == 0 : s < 2;
+                pv.last = two ? j == it.ntiles - 1 : s + 2 >= steps;
+                pv.first_v = k == 0;
+                pv.last_v = last_k;
+                if (last_k) kpos = kpos.next(L::kStages).next(L::kStages);
+            }
+            qpos += two ? 2 : 1;
+            par = (par + steps) & 1u;
+        }
+        if (ok) run_pv();
+        // Make sure no MMA is still writing TMEM when it is released.
+        if (elect_one()) mma_commit(bar(L::kDrain));
+        __syncwarp();
+        mbar_wait_drain(bar(L::kDrain), 0, 1000000000ull);
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ scheduler
+        uint32_t n = 0;
+        bool ok = true;
+        auto publish = [&](const PrefixItem& it) {
+            const uint32_t s = n % kPfxItemRing;
+            if (n >= kPfxItemRing) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kItemEmpty + s), ((n / kPfxItemRing) - 1) & 1u, ctx));
+            if (!ok) return;
+            if (lane == 0) {
+                *reinterpret_cast<PrefixItem*>(smem + L::kItemOff + s * sizeof(PrefixItem)) = it;
+                mbar_arrive(bar(L::kItemFull + s));
+            }
+            __syncwarp();
+            ++n;
+        };
+        PrefixItem it;
+        it.pad = 0;
+        for (int i = blockIdx.x; i < p.pitems && ok; i += gridDim.x) {
+            const int blk = i % p.pblocks, hs = i / p.pblocks;
+            const int seg = hs % p.psegs;
+            it.head = hs / p.psegs;
+            it.req = -1;
+            it.klen = p.P;
+            it.tile0 = seg * p.seg_tiles;
+            it.ntiles = min(p.seg_tiles, p.ptiles - it.tile0);
+            it.row0 = blk * 2 * kBr;
+            it.nrows = min(2 * kBr, p.R * p.GT - it.row0);
+            it.part = (static_cast<int64_t>(seg) * p.Hk + it.head) * p.R * p.GT + it.row0;
+            publish(it);
+        }
+        if (p.lens && ok) {
+            // The total and the lane whose run of requests holds this CTA's first unit.
+            const int run = (p.R + 31) / 32;
+            int64_t mine = 0;
+            for (int i = 0; i < run; ++i) {
+                const int r = lane * run + i;
+                if (r < p.R) mine += request_cost(p, own_len(p, r));
+            }
+            const int64_t upto = warp_scan(mine, lane);
+            const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+            const OwnCut cut(p, total, gridDim.x);
+            const int64_t x0 = cut.begin(blockIdx.x), x1 = min(cut.begin(blockIdx.x + 1), total);
+            if (x0 < x1) {
+                const int at = __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
+                int64_t start = __shfl_sync(0xffffffffu, upto - mine, at);  // of request r0
+                for (int r0 = at * run; r0 < p.R && start < x1 && ok; r0 += 32) {
+                    const int len_l = r0 + lane < p.R ? own_len(p, r0 + lane) : 0;
+                    for (int i = 0; i < 32 && start < x1 && ok; ++i) {
+                        const int len = __shfl_sync(0xffffffffu, len_l, i);
+                        const int64_t cost = seq_cost(len);
+                        const int seqs = p.Hk * p.oblocks;
+                        if (len > 0 && start + cost * seqs > x0) {
+                            const int nt = (len + kBc - 1) / kBc;
+                            int q = x0 > start ? static_cast<int>((x0 - start) / cost) : 0;
+                            for (; q < seqs && start + q * cost < x1 && ok; ++q) {
+                                const int64_t first = start + q * cost + kPfxItemCost;  // tile 0's unit
+                                const int64_t a = x0 > first ? (x0 - first + kPfxTileCost - 1) / kPfxTileCost : 0;
+                                const int64_t b = x1 > first ? (x1 - first + kPfxTileCost - 1) / kPfxTileCost : 0;
+                                const int t0 = static_cast<int>(min(a, static_cast<int64_t>(nt)));
+                                const int t1 = static_cast<int>(min(b, static_cast<int64_t>(nt)));
+                                if (t0 >= t1) continue;
+                                const int blk = q % p.oblocks;
+                                it.head = q / p.oblocks;
+                                it.req = r0 + i;
+                                it.klen = len;
+                                it.tile0 = t0;
+                                it.ntiles = t1 - t0;
+                                it.row0 = it.req * p.GT + blk * 2 * kBr;
+                                it.nrows = min(2 * kBr, p.GT - blk * 2 * kBr);
+                                const int64_t slot = (static_cast<int64_t>(it.req) * p.Hk * p.oblocks + q) + blockIdx.x;
+                                it.part = p.own_first + slot * p.orows;
+                                publish(it);
+                            }
+                        }
+                        start += cost * seqs;
+                    }
+                }
+            }
+        }
+        it.ntiles = -1;
+        if (ok) publish(it);
+        // One CTA leaves every request's start and the total for the combine kernel.
+        if (p.lens && blockIdx.x == gridDim.x - 1) {
+            int64_t start = 0;
+            for (int r0 = 0; r0 < p.R; r0 += 32) {
+                const int64_t c = r0 + lane < p.R ? request_cost(p, own_len(p, r0 + lane)) : 0;
+                const int64_t upto = warp_scan(c, lane);
+                if (r0 + lane < p.R) p.own_start[r0 + lane] = start + upto - c;
+                start += __shfl_sync(0xffffffffu, upto, 31);
+            }
+            if (lane == 0) p.own_start[p.R] = start;
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ Q loader
+        constexpr int kChunks = D / 8;            // 16-byte chunks of a row
+        constexpr int kRows = 32 / kChunks;       // rows per pass of the warp
+        const int ch = lane % kChunks, sub = lane / kChunks;
+        const uint32_t col = (ch >> 3) * (kBr * 128);
+        uint32_t qpos = 0;
+        bool ok = true;
+        PrefixItem it;
+        for (uint32_t n = 0; ok && take_item(n, it, true); ++n) {
+            for (int k = 0; k < (it.nrows > kBr ? 2 : 1) && ok; ++k, ++qpos) {
+                const uint32_t slot = qpos & 1u;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kQEmpty + slot), ((qpos >> 1) & 1u) ^ 1u, ctx));
+                if (!ok) break;
+                const int rows = min(kBr, it.nrows - k * kBr);
+                const uint32_t dst = s_base + L::kQOff + slot * L::kTile + col;
+                for (int base = 0; base < rows; base += 32) {
+                    // lane l works out where row base + l is
+                    const int row = it.row0 + k * kBr + min(base + lane, rows - 1);
+                    const int r = row / p.GT, x = row - r * p.GT;
+                    const int g = x / p.T, t = x - g * p.T;
+                    const int64_t at = r * p.qs[0] + (static_cast<int64_t>(it.head) * p.G + g) * p.qs[1] + t * p.qs[2];
+                    const int here = min(32, rows - base);
+                    for (int i = 0; i < here; i += kRows) {
+                        const int64_t from = __shfl_sync(0xffffffffu, at, i + sub);
+                        const int rr = base + i + sub;
+                        if (i + sub < here)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                             dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)),
+                                         "l"(p.q + from + ch * 8)
+                                         : "memory");
+                    }
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async_smem();
+                mbar_arrive(bar(L::kQFull + slot));
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax warpgroups
+        const int t = (warp - 4) >> 2;          // chain
+        const int quad = warp & 3;              // TMEM lane quadrant
+        const int rloc = quad * 32 + lane;      // row within the tile
+        const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t t_s = tmem + lane_addr + t * kBc;
+        const uint32_t t_o = tmem + lane_addr + 2 * kBc;  // O_0; O_1 is D columns further
+        float2* xchg = reinterpret_cast<float2*>(smem + L::kXchgOff);
+        const float sl2 = p.scale_log2;
+        uint32_t s_cnt = 0, x_cnt = 0, ring = 0;  // ring: K/V fills before this item
+        uint32_t o_phase = 0u;                    // parity of each chain's next finished item, bit c
+        uint32_t par = 0;
+        bool ok = true;
+        PrefixItem it;
+        for (uint32_t n = 0; ok && take_item(n, it, true); ++n) {
+            const bool two = it.nrows > kBr;
+            const int steps = two ? 2 * it.ntiles : it.ntiles;
+            const int mine = t ^ static_cast<int>(par);       // this chain's first step
+            const int k = two ? mine : 0;                     // its query tile
+            const int nrow = min(kBr, it.nrows - k * kBr);
+            const bool warp_on = quad * 32 < nrow;            // the warp has rows
+            const bool row_on = rloc < nrow;
+            const bool both = two || it.ntiles >= 2;          // both chains work on the item
+            const bool used = both || mine == 0;
+            float m_ref = -INFINITY;
+            float l = 0.f;
+            if (used) {
+                // keys this row sees: all of the source, but for later tokens of its own request
+                int lim = it.klen;
+                if (it.req >= 0 && p.T > 1) {
+                    const int x = it.row0 + k * kBr + min(rloc, nrow - 1) - it.req * p.GT;
+                    lim -= p.T - 1 - x % p.T;
+                }
+                const int all_see = it.klen - (it.req >= 0 ? p.T - 1 : 0);  // keys below this are seen by every row
+                bool first = true;
+                for (int j = two ? 0 : mine; j < it.ntiles; j += two ? 1 : 2) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kSFull + t), s_cnt & 1u, ctx));
+                    ++s_cnt;
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const int key0 = (it.tile0 + j) * kBc;
+                    const int keys = tile_keys(it, j);
+                    // The output product sums over keys in steps of 16.  Own-cache rows past the
+                    // last key may hold anything (a NaN times a zero weight is a NaN): zero them.
+                    if (it.req >= 0 && k == 0 && (keys & 15) != 0) {
+                        const uint32_t at = ring + 2 * j + 1;  // V_j's fill
+                        const uint32_t stage = at % L::kStages;
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvFull + stage), (at / L::kStages) & 1u, ctx));
+                        if (!ok) break;
+                        const int pad = ((keys + 15) & ~15) - keys;
+                        uint8_t* v = smem + L::kRingOff + stage * L::kTile;
+                        for (int i = rloc; i < pad * (D / 8); i += 128) {
+                            const int row = keys + i / (D / 8), c8 = i % (D / 8);
+                            *reinterpret_cast<uint4*>(v + (c8 >> 3) * (kBc * 128) + row * 128 + (c8 & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    if (!warp_on) {  // none of this warp's rows exist: only keep the barriers' counts
+                        mbar_arrive(bar(L::kPHalf + t));
+                        mbar_arrive(bar(L::kPFull + t));
+                        continue;
+                    }
+                    // Chunks of 32 scores past the tile's last key are left out: the output
+                    // product stops at the step of 16 that holds it.
+                    const int nch = (keys + 31) >> 5;
+                    uint32_t r0[32], r1[32], r2[32], r3[32];
+                    tmem_ld32(t_s + 0, r0);
+                    if (nch > 1) tmem_ld32(t_s + 32, r1);
+                    tmem_wait_ld(r0);
+                    tmem_wait_ld(r1);
+                    if (nch > 2) tmem_ld32(t_s + 64, r2);
+                    if (nch > 3) tmem_ld32(t_s + 96, r3);
+                    float* s0 = reinterpret_cast<float*>(r0);
+                    float* s1 = reinterpret_cast<float*>(r1);
+                    float* s2 = reinterpret_cast<float*>(r2);
+                    float* s3 = reinterpret_cast<float*>(r3);
+                    const bool need_mask = key0 + kBc > all_see;
+                    if (need_mask) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            if (key0 + c >= lim) s0[c] = -INFINITY;
+                            if (key0 + 32 + c >= lim) s1[c] = -INFINITY;
+                        }
+                    }
+                    float mx0 = fmax3(s0[0], s0[1], s0[2]), mx1 = fmax3(s1[0], s1[1], s1[2]);
+#pragma unroll
+                    for (int c = 3; c < 31; c += 2) {
+                        mx0 = fmax3(mx0, s0[c], s0[c + 1]);
+                        mx1 = fmax3(mx1, s1[c], s1[c + 1]);
+                    }
+                    mx0 = fmax3(mx0, s0[31], fmaxf(mx1, s1[31]));
+                    tmem_wait_ld(r2);
+                    tmem_wait_ld(r3);
+                    if (need_mask) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            if (key0 + 64 + c >= lim) s2[c] = -INFINITY;
+                            if (key0 + 96 + c >= lim) s3[c] = -INFINITY;
+                        }
+                    }
+                    float mx2 = fmax3(s2[0], s2[1], s2[2]), mx3 = fmax3(s3[0], s3[1], s3[2]);
+#pragma unroll
+                    for (int c = 3; c < 31; c += 2) {
+                        mx2 = fmax3(mx2, s2[c], s2[c + 1]);
+                        mx3 = fmax3(mx3, s3[c], s3[c + 1]);
+                    }
+                    mx0 = fmax3(mx0, fmax3(mx2, s2[31], mx3), s3[31]);
+                    // a row that sees no key of the tile keeps its reference (0 * -inf would be a NaN)
+                    const float m_tile = mx0 == -INFINITY ? -INFINITY : mx0 * p.max_scale_log2;
+                    const bool grow = row_on && m_tile > m_ref + kRescaleLog2Bf16;
+                    float alpha = 1.f;
+                    if (grow) {
+                        alpha = ex2_approx(m_ref - m_tile);  // 0 the first time
+                        m_ref = m_tile;
+                    }
+                    const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+                    l *= alpha;
+                    float acc0 = 0.f, acc1 = 0.f, acc2 = 0.f, acc3 = 0.f;
+                    auto exp_chunk = [&](const float* sc, uint32_t col) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) {
+                            float x0, x1, x2, x3;
+                            ffma2(x0, x1, sc[2 * c], sc[2 * c + 1], sl2, -m_use);
+                            ffma2(x2, x3, sc[2 * c + 2], sc[2 * c + 3], sl2, -m_use);
+                            const float a0 = ex2_approx(x0), b0 = ex2_approx(x1);
+                            const float a1 = ex2_approx(x2), b1 = ex2_approx(x3);
+                            fadd2(acc0, acc1, a0, b0);
+                            fadd2(acc2, acc3, a1, b1);
+                            pk[c] = pack_bf16x2(a0, b0);
+                            pk[c + 1] = pack_bf16x2(a1, b1);
+                        }
+                        tmem_st16(t_s + col, pk);
+                    };
+                    exp_chunk(s0, 0);
+                    if (nch > 1) exp_chunk(s1, 16);
+                    // Rescale O when a reference moved, before the first half of P is released.
+                    // O's previous product has completed: it was issued before this S.
+                    if (__any_sync(0xffffffffu, grow && !first)) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + t * D + c, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(t_o + t * D + c, o);
+                        }
+                    }
+                    first = false;
+                    tmem_wait_st();
+                    tc_fence_before_sync();
+                    mbar_arrive(bar(L::kPHalf + t));
+                    if (nch > 2) exp_chunk(s2, 32);
+                    if (nch > 3) exp_chunk(s3, 48);
+                    l += (acc0 + acc1) + (acc2 + acc3);
+                    tmem_wait_st();
+                    tc_fence_before_sync();
+                    mbar_arrive(bar(L::kPFull + t));
+                }
+                if (!ok) break;
+                // Epilogue: this piece's O / l (fp32) and log-sum-exp, for the combine kernel.
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kOFull + t), (o_phase >> t) & 1u, ctx));
+                if (!ok) break;
+                const bool merge = both && !two;
+                float w_own = 1.f, w_other = 0.f;  // of this chain's O and the other's
+                float m = m_ref, sum = l;
+                if (merge) {
+                    // chain 1's (m, l) through shared memory, then chain 0's through the same place
+                    if (t == 1) {
+                        xchg[rloc] = make_float2(m_ref, l);
+                        mbar_arrive(bar(L::kX + 1));
+                    }
+                    ok = mbar_wait(bar(L::kX + (t ^ 1)), x_cnt & 1u, ctx) &&
+                         mbar_wait(bar(L::kOFull + (t ^ 1)), (o_phase >> (t ^ 1)) & 1u, ctx);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    const float2 other = xchg[rloc];
+                    if (t == 0) {
+                        xchg[rloc] = make_float2(m_ref, l);
+                        mbar_arrive(bar(L::kX + 0));
+                    }
+                    m = fmaxf(m_ref, other.x);
+                    w_own = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
+                    w_other = other.x == -INFINITY ? 0.f : ex2_approx(other.x - m);
+                    // a chain whose reference never moved has l = 0, or a NaN to pass on
+                    sum = (m_ref == -INFINITY ? l : l * w_own) + (other.x == -INFINITY ? other.y : other.y * w_other);
+                }
+                tc_fence_after_sync();
+                // a row that sees no key of this piece: O = 0, LSE = -inf
+                const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+                if (warp_on) {
+                    const int64_t idx = it.part + k * kBr + rloc;
+                    float* orow = p.part_o + idx * D;
+                    const int c0 = merge ? t * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
+                    const float wa = w_own * inv, wb = w_other * inv;
+                    // evict-last: read back right after this grid
+                    const uint64_t keep = l2_policy_evict_last();
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t oa[32];
+                        if (merge) {
+                            uint32_t ob[32];
+                            tmem_ld32(t_o + t * D + c, oa);
+                            tmem_ld32(t_o + (t ^ 1) * D + c, ob);
+                            tmem_wait_ld(oa);
+                            tmem_wait_ld(ob);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                // a chain without a visible key for the row has weight 0 and finite O
+                                const float v = __uint_as_float(oa[i]) * wa + __uint_as_float(ob[i]) * wb;
+                                oa[i] = __float_as_uint(v);
+                            }
+                        } else {
+                            tmem_ld32(t_o + t * D + c, oa);
+                            tmem_wait_ld(oa);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) oa[i] = __float_as_uint(__uint_as_float(oa[i]) * wa);
+                        }
+                        if (row_on) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                st_global_v4_hint(orow + c + 4 * i, __uint_as_float(oa[4 * i]),
+                                                  __uint_as_float(oa[4 * i + 1]), __uint_as_float(oa[4 * i + 2]),
+                                                  __uint_as_float(oa[4 * i + 3]), keep);
+                        }
+                    }
+                    if (row_on && (!merge || t == 0))
+                        st_global_hint(p.part_lse + idx, sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2, keep);
+                }
+                tc_fence_before_sync();
+                if (merge) {
+                    mbar_arrive(bar(L::kOEmpty + 0));
+                    mbar_arrive(bar(L::kOEmpty + 1));
+                    ++x_cnt;
+                } else {
+                    mbar_arrive_n(bar(L::kOEmpty + t), 2);
+                }
+            }
+            o_phase ^= both ? 3u : 1u << par;
+            ring += 2 * it.ntiles;
+            par = (par + steps) & 1u;
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Merge each row's pieces: prefix segments, then own pieces, in that fixed
+// order.  WARPS warps per row (pieces dealt to them, then added in order);
+// lane l holds columns [kPer l, kPer l + kPer).  Requests with a negative own
+// length are padding: their rows are left as they were.
+template <int D, int WARPS>
+__global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_constant__ PrefixParams p, int grid) {
+    constexpr int kPer = D / 32;
+    constexpr int kRows = 8 / WARPS;  // rows per CTA
+    __shared__ float s_acc[8][D];
+    __shared__ float s_sum[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = warp % WARPS;
+    const int64_t rows = static_cast<int64_t>(p.R) * p.Hk * p.GT;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / WARPS;  // (r, hq, t)
+    const int hgt = p.Hk * p.GT;
+    const int r = row < rows ? static_cast<int>(row / hgt) : 0;
+    const int rem = static_cast<int>(row - static_cast<int64_t>(r) * hgt);
+    const int h = rem / p.GT, x = rem - h * p.GT;  // key head, row within the request
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int raw_len = p.lens ? __ldg(p.lens + r) : 0;
+    const bool on = row < rows && raw_len >= 0;
+    const int segs = p.P > 0 ? p.psegs : 0;
+    const int64_t pstep = static_cast<int64_t>(p.Hk) * p.R * p.GT;
+    const int64_t pfirst = (static_cast<int64_t>(h) * p.R + r) * p.GT + x;
+    int64_t ofirst = 0;
+    int pieces = 0;
+    if (on) {
+        pieces = segs;
+        const int len = min(raw_len, p.C);
+        if (len > 0) {
+            const OwnCut cut(p, __ldcg(p.own_start + p.R), grid);
+            const int q = h * p.oblocks + x / (2 * kBr);
+            const int64_t first = __ldcg(p.own_start + r) + q * seq_cost(len) + kPfxItemCost;
+            const int64_t a = cut.cta_of(first), b = cut.cta_of(first + static_cast<int64_t>((len - 1) / kBc) * kPfxTileCost);
+            ofirst = p.own_first + (static_cast<int64_t>(r) * p.Hk * p.oblocks + q + a) * p.orows + x % (2 * kBr);
+            pieces += static_cast<int>(b - a) + 1;
+        }
+    }
+    auto at = [&](int i) -> int64_t { return i < segs ? pfirst + i * pstep : ofirst + static_cast<int64_t>(i - segs) * p.orows; };
+    // the largest log-sum-exp, then every weight relative to it
+    float mx = -INFINITY;
+    for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, __ldcg(p.part_lse + at(i)));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    float acc[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+    float sum = 0.f;
+    constexpr int kUnroll = 4;
+    for (int i0 = part; i0 < pieces; i0 += WARPS * kUnroll) {
+        float v[kUnroll][kPer], ls[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * WARPS;
+            ls[u] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) v[u][c] = 0.f;
+            if (i < pieces) {
+                const int64_t idx = at(i);
+                ls[u] = __ldcg(p.part_lse + idx);
+                CombineVec<D>::load(p.part_o + idx * D + lane * kPer, v[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const float w = ls[u] == -INFINITY ? 0.f : expf(ls[u] - mx);
+            sum += w;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) acc[c] = fmaf(w, v[u][c], acc[c]);
+        }
+    }
+    if (WARPS > 1) {
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) s_acc[warp][lane * kPer + c] = acc[c];
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        if (part != 0) return;
+        for (int k = 1; k < WARPS; ++k) {
+            sum += s_sum[warp + k];
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) acc[c] += s_acc[warp + k][lane * kPer + c];
+        }
+    }
+    if (!on) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no visible key at all: O = 0, LSE = -inf
+    const int g = x / p.T, t = x - g * p.T;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + r * p.os[0] + (static_cast<int64_t>(h) * p.G + g) * p.os[1] + t * p.os[2] +
+                                                lane * kPer);
+#pragma unroll
+    for (int c = 0; c < kPer; c += 2) dst[c / 2] = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+    if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : mx + logf(sum);
+}
+
+}  // namespace elsattn

@@ -430,6 +430,53 @@ int attn_qk_norm_rope_bwd(const void* dQout, const int64_t* dqo_strides, const v
  * an fp32 row of d per CTA; 0 for d other than 64 or 128, or without a device. */
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
 
+/*
+ * attn_fwd_prefix - attention of a batch of requests that share a long prefix
+ * (one prompt or document and many continuations): T new tokens of each of R
+ * requests against the prefix's keys and values, stored once for all, and the
+ * request's own,
+ *     O = softmax(scale * q [Kp; Ko_r]^T) [Vp; Vo_r]  and its log-sum-exp.
+ * The rows of all requests and of the Hq / Hk query heads that share a key head
+ * form one tall matrix against the prefix (the tall-and-skinny product of the
+ * AttenIO abstract), so the prefix is read once, not once per request.  Both key ranges run as the
+ * streaming pass of attn_fwd in pieces, merged like attn_fwd_split's segments.
+ *   Q, O    : bf16 [R, Hq, T, d] device views; Hq a multiple of Hk, query head h
+ *             reads key head h / (Hq / Hk)
+ *   Kp, Vp  : bf16 [Hk, P, d] device views; P = 0: no prefix (then they may be NULL)
+ *   Ko, Vo  : bf16 [R, Hk, C, d] device views, caches of capacity C; C = 0: no own
+ *             keys (then they and own_lens may be NULL).  P and C are not both 0.
+ *   own_lens: int32 [R] device: the request's own keys, its T new tokens (the
+ *             last of them) among them; more than C counts as C.  0: none: the rows see
+ *             the prefix alone (without one: O = 0, LSE = -inf).  Negative: the
+ *             request is padding and its rows of O and LSE stay as they were.
+ *             Read on the device, so a captured graph may be replayed with other lengths.
+ *   Masking : every token sees the whole prefix; token t of T sees the own keys
+ *             j < own_lens - (T - 1 - t).  Cache rows at and past own_lens are not
+ *             used and may hold anything, NaN included.  A NaN or infinity in the K or V of
+ *             a new token reaches every token of that request, also those that do not see it.
+ *   LSE     : fp32 [R, Hq, T] device, contiguous (natural log)
+ *   *_strides : host arrays in elements, outermost axis first, d contiguous (Q,
+ *             O: request, head, token; Kp, Vp: head, key; Ko, Vo: request, head, key);
+ *             NULL: contiguous.  Positive multiples of 8 below 2^39 for axes longer than 1.
+ *   d       : 64 or 128;  scale : any finite value;  R, Hq, Hk, T >= 1, R*Hq*T < 2^31
+ *   workspace : device buffer of at least attn_fwd_prefix_workspace_bytes(), 16-byte
+ *             aligned, owned by the caller, not used by other work while this call runs
+ *             (calls that may overlap, captured graphs among them, need one each)
+ * Arithmetic as attn_fwd (fp32 scores and sums, P rounded to bf16); pieces are
+ * kept in fp32, O is rounded once.  The cut into pieces depends on the own
+ * lengths, so bits may differ between batches, not between equal calls.
+ * Two launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
+ */
+int attn_fwd_prefix(const void* Q, const int64_t* q_strides, const void* Kp, const int64_t* kp_strides, const void* Vp,
+                    const int64_t* vp_strides, const void* Ko, const int64_t* ko_strides, const void* Vo,
+                    const int64_t* vo_strides, const int32_t* own_lens, void* O, const int64_t* o_strides, float* LSE,
+                    int R, int Hq, int Hk, int T, int P, int C, int d, float scale, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream);
+
+/* Device bytes attn_fwd_prefix needs as workspace on the current device (its
+ * partial rows); 0 for an invalid shape or without a device. */
+size_t attn_fwd_prefix_workspace_bytes(int R, int Hq, int Hk, int T, int P, int C, int d);
+
 #ifdef __cplusplus
 }
 #endif
