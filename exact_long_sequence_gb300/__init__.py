@@ -543,7 +543,7 @@ def prefix_workspace_bytes(R: int, Hq: int, Hk: int, T: int, P: int, C: int, d: 
 _pack2 = struct.Struct("2q").pack
 
 
-def attn_fwd_prefix(q, k_prefix, v_prefix, k_own=None, v_own=None, own_lens=None, scale: float | None = None, out=None,
+def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own_lens=None, scale: float | None = None, out=None,
                     lse=None, workspace=None, stream=None):
     """O, LSE of T new tokens of R requests over a prefix all of them share and each request's own keys.
 

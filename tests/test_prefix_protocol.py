@@ -1,0 +1,423 @@
+"""Models of the shared-prefix attention's host-free parts, on the CPU.
+
+1. The cut of the work (csrc/attn_prefix_kernel.cuh: the scheduler warp, OwnCut; csrc/attn_prefix_api.cu:
+   lay_out, the workspace): every tile of every row block is taken exactly once, every piece
+   has partial rows of its own inside the workspace, and the combine kernel reads exactly the pieces
+   that were written.
+2. The barrier protocol of the roles of one CTA, replayed under many random interleavings with the
+   kernel's arrival counts and issue order, as the forward kernel's model does: no deadlock, no barrier
+   two phases ahead of a waiter, and every buffer (K/V stages, query slots, score and output
+   accumulators, the exchanged statistics) holds what its reader expects when it is read.
+   An asynchronous operation completes at once here, the most permissive timing for run-ahead.
+Like the kernel's own documentation, the models state it; when the kernel changes, they change with it.
+"""
+import random
+
+import pytest
+
+TILE, ITEM, BC, BR = 4, 2, 128, 128
+STAGES, RING = 5, 4
+
+
+# ------------------------------------------------------------------ 1. the cut
+def cdiv(a, b):
+    return -(-a // b)
+
+
+class Layout:
+    def __init__(self, R, Hk, G, T, P, C, grid):
+        self.R, self.Hk, self.GT, self.T, self.P, self.C, self.grid = R, Hk, G * T, T, P, C, grid
+        self.ptiles = cdiv(P, BC)
+        self.pblocks, self.oblocks = cdiv(R * self.GT, 256), cdiv(self.GT, 256)
+        self.orows = min(self.GT, 256)
+        self.psegs, self.seg_tiles, self.pitems = 0, 1, 0
+        if self.ptiles:
+            units = Hk * self.pblocks
+            most = min(max(2 * grid // units, 8), self.ptiles)
+            best = None
+            for n in range(1, most + 1):
+                tiles = cdiv(self.ptiles, n)
+                cost = cdiv(units * n, grid) * (ITEM + tiles * TILE) + 0.25 * n
+                if best is None or cost < best:
+                    best, self.seg_tiles = cost, tiles
+            self.psegs = cdiv(self.ptiles, self.seg_tiles)
+            self.pitems = units * self.psegs
+        self.own_first = self.psegs * Hk * R * self.GT
+        self.rows = self.own_first + ((R * Hk * self.oblocks + grid) * self.orows if C else 0)
+
+    def seq_cost(self, n):
+        return ITEM + cdiv(n, 32) if n > 0 else 0
+
+
+class Cut:
+    def __init__(self, L, total):
+        g = L.grid
+        self.rem = L.pitems % g
+        item = ITEM + L.seg_tiles * TILE
+        level = item * (g - self.rem)
+        if self.rem == 0 or total > level:
+            e = cdiv(total - (0 if self.rem == 0 else level), g)
+            self.cap1, self.cap0 = e, e if self.rem == 0 else item + e
+        else:
+            self.cap1, self.cap0 = 0, cdiv(total, g - self.rem)
+        if 0 < self.cap1 < TILE:
+            self.cap1 = TILE
+        self.cap0 = max(self.cap0, TILE)
+
+    def begin(self, b):
+        return b * self.cap1 if b < self.rem else self.rem * self.cap1 + (b - self.rem) * self.cap0
+
+    def cta_of(self, x):
+        return x // self.cap1 if x < self.rem * self.cap1 else self.rem + (x - self.rem * self.cap1) // self.cap0
+
+
+def schedule(L, lens, cta):
+    """The items of one CTA: (req, head, row0, nrows, tile0, ntiles, first partial row)."""
+    out = []
+    for i in range(cta, L.pitems, L.grid):
+        blk, hs = i % L.pblocks, i // L.pblocks
+        seg, head = hs % L.psegs, hs // L.psegs
+        t0 = seg * L.seg_tiles
+        row0 = blk * 256
+        out.append((-1, head, row0, min(256, L.R * L.GT - row0), t0, min(L.seg_tiles, L.ptiles - t0),
+                    (seg * L.Hk + head) * L.R * L.GT + row0))
+    if not L.C:
+        return out
+    lens = [min(max(n, 0), L.C) for n in lens]
+    seqs = L.Hk * L.oblocks
+    run = cdiv(L.R, 32)
+    mine = [sum(L.seq_cost(n) * seqs for n in lens[k * run:(k + 1) * run]) for k in range(32)]
+    upto = [sum(mine[:k + 1]) for k in range(32)]
+    cut = Cut(L, upto[31])
+    x0, x1 = cut.begin(cta), min(cut.begin(cta + 1), upto[31])
+    if x0 >= x1:
+        return out
+    at = next(k for k in range(32) if upto[k] > x0)
+    start = upto[at] - mine[at]
+    for r in range(at * run, L.R):
+        if start >= x1:
+            break
+        cost = L.seq_cost(lens[r])
+        if lens[r] > 0 and start + cost * seqs > x0:
+            nt = cdiv(lens[r], BC)
+            for q in range((x0 - start) // cost if x0 > start else 0, seqs):
+                if start + q * cost >= x1:
+                    break
+                first = start + q * cost + ITEM
+                t0 = min(cdiv(x0 - first, TILE) if x0 > first else 0, nt)
+                t1 = min(cdiv(x1 - first, TILE) if x1 > first else 0, nt)
+                if t0 >= t1:
+                    continue
+                blk = q % L.oblocks
+                out.append((r, q // L.oblocks, r * L.GT + blk * 256, min(256, L.GT - blk * 256), t0, t1 - t0,
+                            L.own_first + (r * seqs + q + cta) * L.orows))
+        start += cost * seqs
+    return out
+
+
+def combine_rows(L, lens, r, h, x):
+    """The partial rows the combine kernel merges for row x of request r at key head h."""
+    rows = [(s * L.Hk + h) * L.R * L.GT + r * L.GT + x for s in range(L.psegs)]
+    n = min(lens[r], L.C) if L.C else 0
+    if n > 0:
+        seqs = L.Hk * L.oblocks
+        starts = [0]
+        for v in lens:
+            starts.append(starts[-1] + L.seq_cost(min(max(v, 0), L.C)) * seqs)
+        cut = Cut(L, starts[-1])
+        q = h * L.oblocks + x // 256
+        first = starts[r] + q * L.seq_cost(n) + ITEM
+        a, b = cut.cta_of(first), cut.cta_of(first + (n - 1) // BC * TILE)
+        rows += [L.own_first + (r * seqs + q + c) * L.orows + x % 256 for c in range(a, b + 1)]
+    return rows
+
+
+def own_lengths(kind, R, C, rng):
+    return {"zero": lambda: 0, "full": lambda: C, "one": lambda: 1, "padding": lambda: rng.choice([-1, 0, 1, C]),
+            "any": lambda: rng.randint(-1, C + 5), "few": lambda: rng.choice([0] * 9 + [C])}[kind]()
+
+
+@pytest.mark.parametrize("kind", ["zero", "full", "one", "padding", "any", "few"])
+@pytest.mark.parametrize("R,Hk,G,T,P,C,grid", [
+    (1, 1, 1, 1, 1, 0, 152), (1, 1, 1, 1, 0, 5, 152), (3, 2, 4, 1, 1000, 700, 152), (5, 1, 3, 100, 300, 900, 8),
+    (70, 2, 2, 1, 0, 4000, 152), (33, 8, 4, 2, 5000, 257, 152), (2, 4, 1, 300, 129, 400, 11), (100, 3, 1, 1, 128, 31, 13),
+    (1, 1, 64, 1, 70000, 50000, 152), (40, 1, 16, 1, 2048, 129, 7),
+])
+def test_every_tile_once_and_every_piece_found(R, Hk, G, T, P, C, grid, kind):
+    rng = random.Random(R * 31 + P)
+    L = Layout(R, Hk, G, T, P, C, grid)
+    lens = [own_lengths(kind, R, C, rng) for _ in range(R)]
+    tiles, written = {}, set()
+    for cta in range(grid):
+        for req, head, row0, nrows, t0, nt, part in schedule(L, lens, cta):
+            assert nt >= 1 and 1 <= nrows <= 256
+            for j in range(t0, t0 + nt):
+                key = (req, head, row0, j)
+                assert key not in tiles
+                tiles[key] = cta
+            span = set(range(part, part + nrows))
+            assert not span & written and 0 <= part and part + nrows <= L.rows
+            written |= span
+    want = {(-1, h, b * 256, j) for h in range(Hk) for b in range(L.pblocks) for j in range(L.ptiles)}
+    for r in range(R):
+        for h in range(Hk):
+            for b in range(L.oblocks):
+                want |= {(r, h, r * L.GT + b * 256, j) for j in range(cdiv(min(max(lens[r], 0), C), BC))}
+    assert set(tiles) == want
+    read = set()
+    for r in range(R):
+        for h in range(Hk):
+            for x in range(L.GT):
+                rows = combine_rows(L, lens, r, h, x)
+                assert len(set(rows)) == len(rows) and not read & set(rows) and set(rows) <= written
+                read |= set(rows)
+    assert read == written  # nothing computed for nothing, padding's prefix rows included
+
+
+# ------------------------------------------------------------------ 2. the barriers
+class Barrier:
+    def __init__(self, name, count):
+        self.name, self.count, self.pending, self.done = name, count, count, 0
+
+    def arrive(self, n=1):
+        self.pending -= n
+        assert self.pending >= 0, f"{self.name}: more arrivals than the count"
+        if self.pending == 0:
+            self.done += 1
+            self.pending = self.count
+
+
+def run(items, seed, stages=STAGES, o_empty_twice=True):
+    """One CTA over items (two query tiles?, K/V tiles, zeroed tail?).  None, or what went wrong."""
+    rng = random.Random(seed)
+    B = {}
+
+    def mk(name, count=1):
+        B[name] = Barrier(name, count)
+
+    for s in range(stages):
+        mk(("KvFull", s)), mk(("KvEmpty", s))
+    for t in (0, 1):
+        for n in ("QFull", "QEmpty", "SFull", "OFull"):
+            mk((n, t))
+        mk(("PHalf", t), 128), mk(("PFull", t), 128), mk(("OEmpty", t), 256), mk(("X", t), 128)
+    for s in range(RING):
+        mk(("ItemFull", s)), mk(("ItemEmpty", s), 11)
+    stage, qslot, S, O = [None] * stages, [None] * 2, [None] * 2, [None] * 2
+    xchg = [None]
+    entries = items + [None]
+    slot_item = [None] * RING
+
+    def need(got, want, what):
+        if got != want:
+            raise AssertionError(f"{what}: {got}, wanted {want}")
+
+    def take(n):
+        yield ("ItemFull", n % RING), n // RING
+        need(slot_item[n % RING], n, "item")
+
+    def scheduler():
+        for n in range(len(entries)):
+            if n >= RING:
+                yield ("ItemEmpty", n % RING), n // RING - 1
+            slot_item[n % RING] = n
+            B[("ItemFull", n % RING)].arrive()
+
+    def producer():
+        pos = 0
+        for n, it in enumerate(entries):
+            yield from take(n)
+            B[("ItemEmpty", n % RING)].arrive()
+            if it is None:
+                return
+            for j in range(it[1]):
+                for kv in "KV":
+                    st, use = pos % stages, pos // stages
+                    if use:
+                        yield ("KvEmpty", st), use - 1
+                    stage[st] = (n, kv, j)
+                    B[("KvFull", st)].arrive()
+                    pos += 1
+
+    def qloader():
+        qpos = 0
+        for n, it in enumerate(entries):
+            yield from take(n)
+            B[("ItemEmpty", n % RING)].arrive()
+            if it is None:
+                return
+            for k in range(2 if it[0] else 1):
+                if qpos >= 2:
+                    yield ("QEmpty", qpos & 1), (qpos >> 1) - 1
+                qslot[qpos & 1] = (n, k)
+                B[("QFull", qpos & 1)].arrive()
+                qpos += 1
+
+    def mma():
+        kpos = qpos = par = 0
+        pph, oph = [0, 0], [0, 0]
+        due = []
+
+        def run_pv():
+            if not due:
+                return
+            n, j, c, k, v, first, last, first_v, last_v = due.pop()
+            if first_v:
+                yield ("KvFull", v % stages), v // stages
+            yield ("PHalf", c), pph[c]
+            if first:
+                if oph[c]:
+                    yield ("OEmpty", c), oph[c] - 1
+                oph[c] += 1
+                O[c] = [n, k, []]
+            need(S[c], ("P", n, j, k), "P half")
+            yield ("PFull", c), pph[c]
+            pph[c] += 1
+            need(S[c], ("P", n, j, k), "P")
+            need(stage[v % stages], (n, "V", j), "V")
+            need(O[c][:2], [n, k], "O")
+            O[c][2].append(j)
+            if last_v:
+                B[("KvEmpty", v % stages)].arrive()
+            if last:
+                B[("OFull", c)].arrive()
+
+        for n, it in enumerate(entries):
+            yield from take(n)
+            B[("ItemEmpty", n % RING)].arrive()
+            if it is None:
+                break
+            two, nt, _ = it
+            steps = 2 * nt if two else nt
+            for s in range(steps):
+                j, k = (s >> 1, s & 1) if two else (s, 0)
+                c = (par + s) & 1
+                if k == 0:
+                    yield ("KvFull", kpos % stages), kpos // stages
+                if j == 0:
+                    yield ("QFull", (qpos + k) & 1), (qpos + k) >> 1
+                need(stage[kpos % stages], (n, "K", j), "K")
+                need(qslot[(qpos + k) & 1], (n, k), "Q")
+                last_k = not two or k == 1
+                if S[c] is not None:
+                    need(S[c][0], "free", "score buffer still in use")
+                S[c] = ("S", n, j, k)
+                B[("SFull", c)].arrive()
+                if last_k:
+                    B[("KvEmpty", kpos % stages)].arrive()
+                if j == nt - 1:
+                    B[("QEmpty", (qpos + k) & 1)].arrive()
+                prev = due[0][2] if due else None
+                yield from run_pv()
+                if prev is not None:
+                    S[prev] = ("free",) if prev != c else S[prev]
+                due.append((n, j, c, k, kpos + 1, j == 0 if two else s < 2, j == nt - 1 if two else s + 2 >= steps,
+                            k == 0, last_k))
+                if last_k:
+                    kpos += 2
+            qpos += 2 if two else 1
+            par = (par + steps) & 1
+        yield from run_pv()
+
+    def softmax(t):
+        s_cnt = x_cnt = ring = par = 0
+        o_cnt = [0, 0]
+        for n, it in enumerate(entries):
+            yield from take(n)
+            B[("ItemEmpty", n % RING)].arrive(4)
+            if it is None:
+                return
+            two, nt, tail = it
+            steps = 2 * nt if two else nt
+            mine = t ^ par
+            k = mine if two else 0
+            both = two or nt >= 2
+            if both or mine == 0:
+                js = range(nt) if two else range(mine, nt, 2)
+                for j in js:
+                    yield ("SFull", t), s_cnt
+                    s_cnt += 1
+                    need(S[t], ("S", n, j, k), "S")
+                    if tail and k == 0 and j == nt - 1:
+                        at = ring + 2 * j + 1
+                        yield ("KvFull", at % stages), at // stages
+                        need(stage[at % stages], (n, "V", j), "V to be zeroed")
+                    S[t] = ("P", n, j, k)
+                    B[("PHalf", t)].arrive(128)
+                    yield None
+                    B[("PFull", t)].arrive(128)
+                yield ("OFull", t), o_cnt[t]
+                need(O[t], [n, k, list(js)], "finished O")
+                if both and not two:
+                    if t == 1:
+                        xchg[0] = (n, 1)
+                        B[("X", 1)].arrive(128)
+                    yield ("X", t ^ 1), x_cnt
+                    yield ("OFull", t ^ 1), o_cnt[t ^ 1]
+                    need(xchg[0], (n, t ^ 1), "other chain's statistics")
+                    if t == 0:
+                        xchg[0] = (n, 0)
+                        B[("X", 0)].arrive(128)
+                    x_cnt += 1
+                    need(O[t ^ 1], [n, 0, list(range(1 - mine, nt, 2))], "other chain's O")
+                    yield None
+                    need(O[t ^ 1], [n, 0, list(range(1 - mine, nt, 2))], "other chain's O after the readout")
+                    B[("OEmpty", 0)].arrive(128)
+                    B[("OEmpty", 1)].arrive(128)
+                else:
+                    B[("OEmpty", t)].arrive(256 if o_empty_twice else 128)
+            for c in (0, 1):
+                if both or par == c:
+                    o_cnt[c] += 1
+            ring += 2 * nt
+            par = (par + steps) & 1
+
+    roles = {"scheduler": scheduler(), "producer": producer(), "qloader": qloader(), "mma": mma(), "softmax0": softmax(0),
+             "softmax1": softmax(1)}
+    waiting = {k: None for k in roles}
+    alive = set(roles)
+    while alive:
+        runnable = []
+        for k in sorted(alive):
+            w = waiting[k]
+            if w is None:
+                runnable.append(k)
+                continue
+            done = B[w[0]].done
+            if done >= w[1] + 2:
+                return f"phase overrun: {k} waits {w[0]} phase {w[1]}, barrier already completed {done}"
+            if done >= w[1] + 1:
+                runnable.append(k)
+        if not runnable:
+            return f"deadlock: { {k: waiting[k] for k in sorted(alive)} }"
+        k = rng.choice(runnable)
+        waiting[k] = None
+        try:
+            waiting[k] = next(roles[k])
+        except StopIteration:
+            alive.discard(k)
+        except AssertionError as e:
+            return f"{k}: {e}"
+    return None
+
+
+ITEMS = [
+    [(False, 1, False)], [(True, 1, True)], [],
+    [(False, 1, True)] * 9,
+    [(False, 7, False), (False, 2, True), (False, 1, True), (False, 1, False), (False, 3, True)],
+    [(True, 5, False), (False, 4, False), (True, 1, False), (False, 1, True), (True, 2, True)],
+    [(False, 2, True)] * 7, [(True, 3, False)] * 4 + [(False, 1, True)] * 6,
+]
+
+
+@pytest.mark.parametrize("items", ITEMS + [[(random.Random(k).random() < 0.3, random.Random(k + i).randint(1, 4),
+                                             random.Random(k * i).random() < 0.5) for i in range(12)] for k in range(8)])
+def test_protocol(items):
+    for seed in range(25):
+        assert run(items, seed) is None
+        assert run(items, seed, stages=8) is None
+
+
+def test_checker_finds_an_accumulator_that_is_never_released():
+    found = [run([(False, 1, False)] * 6, seed, o_empty_twice=False) for seed in range(5)]
+    assert all(f and f.startswith("deadlock") for f in found)
