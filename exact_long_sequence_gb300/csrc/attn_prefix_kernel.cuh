@@ -29,8 +29,8 @@
 //     the columns.
 // The steps of consecutive items form one stream: the next item's first score
 // product is issued before the last output product of this one, and an item of
-// a single tile takes the chain that the previous item left, so short items
-// overlap too.
+// one query tile starts on the chain that the previous step left, so short
+// items overlap too.
 //
 // What bounds it: up to about 128 rows a key head, reading K/V from HBM; with
 // 256 and more, the tensor core (4 d operations a row and key).
@@ -38,6 +38,7 @@
 
 #include <cuda.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_fwd_kernel.cuh"
 #include "plan.h"
@@ -174,6 +175,33 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
 }
+// 16 TMEM lanes x 32 columns: thread i of the warp gets, for each block of 8
+// columns b, columns 2 (i % 4), 2 (i % 4) + 1 of lane i / 4 in r[4 b], r[4 b + 1]
+// and of lane i / 4 + 8 in r[4 b + 2], r[4 b + 3]; four threads hold 32
+// neighbouring bytes of a row, so a store fills whole sectors.
+__device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void st_global_v2_hint(float* p, float a, float b, uint64_t pol) {
+    asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(p), "f"(a), "f"(b), "l"(pol) : "memory");
+}
+// Whether the phase with the given parity has completed; never waits.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
@@ -191,7 +219,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
     auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kFlagsOff);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlagsOff + 4);
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int lane = threadIdx.x & 31;
     const WaitCtx ctx{abort_flag, p.error_word, p.timeout_ns};
 
@@ -245,8 +273,23 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         bool got = mbar_wait(bar(L::kItemFull + s), (n / kPfxItemRing) & 1u, ctx);
         if (whole) got = __all_sync(0xffffffffu, got);
         if (!got) return false;
-        it = *reinterpret_cast<const PrefixItem*>(smem + L::kItemOff + s * sizeof(PrefixItem));
-        if (whole) __syncwarp();
+        const int* from = reinterpret_cast<const int*>(smem + L::kItemOff + s * sizeof(PrefixItem));
+        if (whole) {
+            // one word a lane, handed round by shuffles: the compiler then knows the fields to be the
+            // same for the whole warp and keeps what follows from them in uniform registers
+            const int word = from[lane < static_cast<int>(sizeof(PrefixItem) / 4) ? lane : 0];
+            it.ntiles = __shfl_sync(0xffffffffu, word, 0);
+            it.tile0 = __shfl_sync(0xffffffffu, word, 1);
+            it.klen = __shfl_sync(0xffffffffu, word, 2);
+            it.head = __shfl_sync(0xffffffffu, word, 3);
+            it.req = __shfl_sync(0xffffffffu, word, 4);
+            it.row0 = __shfl_sync(0xffffffffu, word, 5);
+            it.nrows = __shfl_sync(0xffffffffu, word, 6);
+            const uint32_t lo = __shfl_sync(0xffffffffu, word, 8), hi = __shfl_sync(0xffffffffu, word, 9);
+            it.part = static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+        } else {
+            it = *reinterpret_cast<const PrefixItem*>(from);
+        }
         if (!whole || lane == 0) mbar_arrive(bar(L::kItemEmpty + s));
         return it.ntiles >= 0;
     };
@@ -310,6 +353,14 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         uint32_t qpos = 0;      // query tiles taken so far: slot qpos & 1
         uint32_t par = 0;       // chain of the item's first step
         bool ok = true;
+        // S_c = Q K^T, the operands' descriptors given
+        auto gemm_s = [&](int c, uint64_t a, uint64_t b) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = static_cast<uint64_t>(((kk >> 2) * (kBr * 128) + (kk & 3) * 32) >> 4);
+                mma_ss(tmem + c * kBc, a + off, b + off, idesc_s, kk > 0 ? 1u : 0u);
+            }
+        };
         // the output product that is due: of the step before
         struct { bool due, first, last, first_v, last_v; int chain, ksteps; RingPos v; } pv{};
         auto run_pv = [&]() -> bool {
@@ -326,49 +377,139 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             if (!__all_sync(0xffffffffu, w)) return false;
             tc_fence_after_sync();
             const uint64_t b = dv0 + static_cast<uint64_t>((pv.v.stage * L::kTile) >> 4);
-            auto gemm_o = [&](int k0, int k1) {
-                for (int kk = k0; kk < k1; ++kk)
-                    mma_ts(tmem + 2 * kBc + c * D, tmem + c * kBc + kk * 8, b + static_cast<uint64_t>((kk * 16 * 128) >> 4),
-                           idesc_o, (!pv.first || kk > 0) ? 1u : 0u);
+            // products over keys [64 half, 64 half + 64), in steps of 16 up to the tile's last key
+            auto gemm_o = [&](int half) {
+#pragma unroll
+                for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                    if (kk < pv.ksteps)
+                        mma_ts(tmem + 2 * kBc + c * D, tmem + c * kBc + kk * 8,
+                               b + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_o, (!pv.first || kk > 0) ? 1u : 0u);
             };
-            if (elect_one()) gemm_o(0, min(pv.ksteps, 4));
+            if (elect_one()) gemm_o(0);
             __syncwarp();
             w = mbar_wait(bar(L::kPFull + c), (p_phase >> c) & 1u, ctx);
             p_phase ^= 1u << c;
             if (!__all_sync(0xffffffffu, w)) return false;
             tc_fence_after_sync();
             if (elect_one()) {
-                gemm_o(4, pv.ksteps);
+                gemm_o(1);
                 if (pv.last_v) mma_commit(bar(L::kKvEmpty + pv.v.stage));
                 if (pv.last) mma_commit(bar(L::kOFull + c));
             }
             __syncwarp();
             return true;
         };
+        // The next score product goes first where its operands are there already: the tensor core
+        // works on it while the softmax of the step before runs.  Where they are not (short items,
+        // the ends of a CTA's share), the product that is due does not wait for them.
+        auto there = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_test(b, parity)); };
         PrefixItem it;
-        for (uint32_t n = 0; ok && take_item(n, it, true); ++n) {
-            const bool two = it.nrows > kBr;   // two query tiles
-            const int steps = two ? 2 * it.ntiles : it.ntiles;
-            for (int s = 0; s < steps && ok; ++s) {
-                const int j = two ? s >> 1 : s, k = two ? s & 1 : 0;
-                const int c = (par + s) & 1;
-                const uint32_t qslot = (qpos + k) & 1u;
-                bool w = true;
-                if (k == 0) w = mbar_wait(bar(L::kKvFull + kpos.stage), kpos.phase, ctx);
-                if (j == 0) w = w && mbar_wait(bar(L::kQFull + qslot), ((qpos + k) >> 1) & 1u, ctx);
-                if (!(ok = __all_sync(0xffffffffu, w))) break;
-                const bool last_k = !two || k == 1;
-                if (elect_one()) {
-                    const uint64_t a = dq0 + static_cast<uint64_t>((qslot * L::kTile) >> 4);
-                    const uint64_t b = dk0 + static_cast<uint64_t>((kpos.stage * L::kTile) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * (kBr * 128) + (kk & 3) * 32) >> 4);
-                        mma_ss(tmem + c * kBc, a + off, b + off, idesc_s, kk > 0 ? 1u : 0u);
+        for (uint32_t n = 0; ok; ++n) {
+            if (pv.due && !there(bar(L::kItemFull + n % kPfxItemRing), (n / kPfxItemRing) & 1u) && !(ok = run_pv())) break;
+            if (!take_item(n, it, true)) break;
+            const int nt = it.ntiles;
+            if (it.nrows > kBr) {
+                // Two query tiles, chain = tile: S0_j; O1 += P1_{j-1} V_{j-1}; S1_j; O0 += P0_j V_j.
+                // The chains are literal in this loop, which is what bounds it: the issue of
+                // a step's products and its waits, with generic steps, took 1.2 us.
+                const uint32_t q0 = qpos & 1u, q1 = q0 ^ 1u;
+                if (pv.due && (pv.chain == 0 || !there(bar(L::kKvFull + kpos.stage), kpos.phase) ||
+                               !there(bar(L::kQFull + q0), (qpos >> 1) & 1u)) && !(ok = run_pv()))
+                    break;
+                const uint64_t a0 = dq0 + static_cast<uint64_t>((q0 * L::kTile) >> 4);
+                const uint64_t a1 = dq0 + static_cast<uint64_t>((q1 * L::kTile) >> 4);
+                const int last_steps = (tile_keys(it, nt - 1) + 15) / 16;
+                // O_c (+)= P_c V_j, V_j at ring position v
+                auto pv_two = [&](auto chain, int j, RingPos v) -> bool {
+                    constexpr int c = decltype(chain)::value;
+                    bool w = true;
+                    if (c == 0) w = mbar_wait(bar(L::kKvFull + v.stage), v.phase, ctx);
+                    w = w && mbar_wait(bar(L::kPHalf + c), (p_phase >> c) & 1u, ctx);
+                    if (j == 0) {
+                        w = w && mbar_wait(bar(L::kOEmpty + c), (o_phase >> c) & 1u, ctx);
+                        o_phase ^= 1u << c;
                     }
+                    if (!__all_sync(0xffffffffu, w)) return false;
+                    tc_fence_after_sync();
+                    const uint64_t b = dv0 + static_cast<uint64_t>((v.stage * L::kTile) >> 4);
+                    const int ks = j == nt - 1 ? last_steps : kBc / 16;
+                    auto gemm = [&](int half) {
+#pragma unroll
+                        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                            if (kk < ks)
+                                mma_ts(tmem + 2 * kBc + c * D, tmem + c * kBc + kk * 8,
+                                       b + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                    };
+                    if (elect_one()) gemm(0);
+                    __syncwarp();
+                    w = mbar_wait(bar(L::kPFull + c), (p_phase >> c) & 1u, ctx);
+                    p_phase ^= 1u << c;
+                    if (!__all_sync(0xffffffffu, w)) return false;
+                    tc_fence_after_sync();
+                    if (elect_one()) {
+                        gemm(1);
+                        if (c == 1) mma_commit(bar(L::kKvEmpty + v.stage));
+                        if (j == nt - 1) mma_commit(bar(L::kOFull + c));
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                RingPos vprev{0u, 0u};
+                for (int j = 0; j < nt && ok; ++j) {
+                    bool w = mbar_wait(bar(L::kKvFull + kpos.stage), kpos.phase, ctx);
+                    if (j == 0)
+                        w = w && mbar_wait(bar(L::kQFull + q0), (qpos >> 1) & 1u, ctx) &&
+                            mbar_wait(bar(L::kQFull + q1), ((qpos + 1) >> 1) & 1u, ctx);
+                    if (!(ok = __all_sync(0xffffffffu, w))) break;
+                    const uint64_t b = dk0 + static_cast<uint64_t>((kpos.stage * L::kTile) >> 4);
+                    if (elect_one()) {
+                        gemm_s(0, a0, b);
+                        mma_commit(bar(L::kSFull + 0));
+                        if (j == nt - 1) mma_commit(bar(L::kQEmpty + q0));
+                    }
+                    __syncwarp();
+                    ok = j == 0 ? run_pv() : pv_two(std::integral_constant<int, 1>{}, j - 1, vprev);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        gemm_s(1, a1, b);
+                        mma_commit(bar(L::kSFull + 1));
+                        mma_commit(bar(L::kKvEmpty + kpos.stage));
+                        if (j == nt - 1) mma_commit(bar(L::kQEmpty + q1));
+                    }
+                    __syncwarp();
+                    vprev = kpos.next(L::kStages);
+                    if (!(ok = pv_two(std::integral_constant<int, 0>{}, j, vprev))) break;
+                    kpos = vprev.next(L::kStages);
+                }
+                if (!ok) break;
+                pv.due = true;
+                pv.chain = 1;
+                pv.v = vprev;
+                pv.ksteps = last_steps;
+                pv.first = nt == 1;
+                pv.last = true;
+                pv.first_v = false;
+                pv.last_v = true;
+                qpos += 2;
+                par = 0;
+                continue;
+            }
+            // One query tile; the chains take turns with the K/V tiles.
+            const uint32_t qslot = qpos & 1u;
+            for (int j = 0; j < nt && ok; ++j) {
+                const int c = (par + j) & 1;
+                if (pv.due && (!there(bar(L::kKvFull + kpos.stage), kpos.phase) ||
+                               (j == 0 && !there(bar(L::kQFull + qslot), (qpos >> 1) & 1u))) && !(ok = run_pv()))
+                    break;
+                bool w = mbar_wait(bar(L::kKvFull + kpos.stage), kpos.phase, ctx);
+                if (j == 0) w = w && mbar_wait(bar(L::kQFull + qslot), (qpos >> 1) & 1u, ctx);
+                if (!(ok = __all_sync(0xffffffffu, w))) break;
+                if (elect_one()) {
+                    gemm_s(c, dq0 + static_cast<uint64_t>((qslot * L::kTile) >> 4),
+                           dk0 + static_cast<uint64_t>((kpos.stage * L::kTile) >> 4));
                     mma_commit(bar(L::kSFull + c));
-                    if (last_k) mma_commit(bar(L::kKvEmpty + kpos.stage));
-                    if (j == it.ntiles - 1) mma_commit(bar(L::kQEmpty + qslot));
+                    mma_commit(bar(L::kKvEmpty + kpos.stage));
+                    if (j == nt - 1) mma_commit(bar(L::kQEmpty + qslot));
                 }
                 __syncwarp();
                 if (!(ok = run_pv())) break;
@@ -376,14 +517,14 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                 pv.chain = c;
                 pv.v = kpos.next(L::kStages);
                 pv.ksteps = (tile_keys(it, j) + 15) / 16;
-                pv.first = two ? j == 0 : s < 2;
-                pv.last = two ? j == it.ntiles - 1 : s + 2 >= steps;
-                pv.first_v = k == 0;
-                pv.last_v = last_k;
-                if (last_k) kpos = kpos.next(L::kStages).next(L::kStages);
+                pv.first = j < 2;
+                pv.last = j + 2 >= nt;
+                pv.first_v = true;
+                pv.last_v = true;
+                kpos = pv.v.next(L::kStages);
             }
-            qpos += two ? 2 : 1;
-            par = (par + steps) & 1u;
+            ++qpos;
+            par = (par + nt) & 1u;
         }
         if (ok) run_pv();
         // Make sure no MMA is still writing TMEM when it is released.
@@ -504,15 +645,18 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                     const int r = row / p.GT, x = row - r * p.GT;
                     const int g = x / p.T, t = x - g * p.T;
                     const int64_t at = r * p.qs[0] + (static_cast<int64_t>(it.head) * p.G + g) * p.qs[1] + t * p.qs[2];
-                    const int here = min(32, rows - base);
-                    for (int i = 0; i < here; i += kRows) {
-                        const int64_t from = __shfl_sync(0xffffffffu, at, i + sub);
-                        const int rr = base + i + sub;
-                        if (i + sub < here)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                             dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)),
-                                         "l"(p.q + from + ch * 8)
-                                         : "memory");
+                    for (int i0 = 0; i0 < 32 && base + i0 < rows; i0 += 4 * kRows) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int i = i0 + u * kRows + sub;
+                            const int64_t from = __shfl_sync(0xffffffffu, at, i);
+                            const int rr = base + i;
+                            if (rr < rows)
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                                 dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)),
+                                             "l"(p.q + from + ch * 8)
+                                             : "memory");
+                        }
                     }
                 }
                 asm volatile("cp.async.wait_all;" ::: "memory");
@@ -537,8 +681,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         PrefixItem it;
         for (uint32_t n = 0; ok && take_item(n, it, true); ++n) {
             const bool two = it.nrows > kBr;
-            const int steps = two ? 2 * it.ntiles : it.ntiles;
-            const int mine = t ^ static_cast<int>(par);       // this chain's first step
+            const int mine = two ? t : t ^ static_cast<int>(par);  // this chain's query tile, or its first K/V tile
             const int k = two ? mine : 0;                     // its query tile
             const int nrow = min(kBr, it.nrows - k * kBr);
             const bool warp_on = quad * 32 < nrow;            // the warp has rows
@@ -584,63 +727,39 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                         mbar_arrive(bar(L::kPFull + t));
                         continue;
                     }
-                    // Chunks of 32 scores past the tile's last key are left out: the output
-                    // product stops at the step of 16 that holds it.
-                    const int nch = (keys + 31) >> 5;
-                    uint32_t r0[32], r1[32], r2[32], r3[32];
-                    tmem_ld32(t_s + 0, r0);
-                    if (nch > 1) tmem_ld32(t_s + 32, r1);
-                    tmem_wait_ld(r0);
-                    tmem_wait_ld(r1);
-                    if (nch > 2) tmem_ld32(t_s + 64, r2);
-                    if (nch > 3) tmem_ld32(t_s + 96, r3);
-                    float* s0 = reinterpret_cast<float*>(r0);
-                    float* s1 = reinterpret_cast<float*>(r1);
-                    float* s2 = reinterpret_cast<float*>(r2);
-                    float* s3 = reinterpret_cast<float*>(r3);
-                    const bool need_mask = key0 + kBc > all_see;
-                    if (need_mask) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            if (key0 + c >= lim) s0[c] = -INFINITY;
-                            if (key0 + 32 + c >= lim) s1[c] = -INFINITY;
-                        }
-                    }
-                    float mx0 = fmax3(s0[0], s0[1], s0[2]), mx1 = fmax3(s1[0], s1[1], s1[2]);
-#pragma unroll
-                    for (int c = 3; c < 31; c += 2) {
-                        mx0 = fmax3(mx0, s0[c], s0[c + 1]);
-                        mx1 = fmax3(mx1, s1[c], s1[c + 1]);
-                    }
-                    mx0 = fmax3(mx0, s0[31], fmaxf(mx1, s1[31]));
-                    tmem_wait_ld(r2);
-                    tmem_wait_ld(r3);
-                    if (need_mask) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            if (key0 + 64 + c >= lim) s2[c] = -INFINITY;
-                            if (key0 + 96 + c >= lim) s3[c] = -INFINITY;
-                        }
-                    }
-                    float mx2 = fmax3(s2[0], s2[1], s2[2]), mx3 = fmax3(s3[0], s3[1], s3[2]);
-#pragma unroll
-                    for (int c = 3; c < 31; c += 2) {
-                        mx2 = fmax3(mx2, s2[c], s2[c + 1]);
-                        mx3 = fmax3(mx3, s3[c], s3[c + 1]);
-                    }
-                    mx0 = fmax3(mx0, fmax3(mx2, s2[31], mx3), s3[31]);
-                    // a row that sees no key of the tile keeps its reference (0 * -inf would be a NaN)
-                    const float m_tile = mx0 == -INFINITY ? -INFINITY : mx0 * p.max_scale_log2;
-                    const bool grow = row_on && m_tile > m_ref + kRescaleLog2Bf16;
+                    const float m_old = m_ref;
+                    bool grow = false;
                     float alpha = 1.f;
-                    if (grow) {
-                        alpha = ex2_approx(m_ref - m_tile);  // 0 the first time
-                        m_ref = m_tile;
-                    }
-                    const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-                    l *= alpha;
+                    // moves the reference maximum and l where a tile's maximum asks for it
+                    auto refer = [&](float mx) {
+                        // a row that sees no key of the tile keeps its reference (0 * -inf would be a NaN)
+                        const float m_tile = mx == -INFINITY ? -INFINITY : mx * p.max_scale_log2;
+                        grow = row_on && m_tile > m_old + kRescaleLog2Bf16;
+                        if (grow) {
+                            alpha = ex2_approx(m_old - m_tile);  // 0 the first time
+                            m_ref = m_tile;
+                        }
+                        l *= alpha;
+                    };
+                    // Rescales O when a reference moved, before the first half of P is released.
+                    // O's previous product has completed: it was issued before this S.
+                    auto rescale = [&]() {
+                        if (__any_sync(0xffffffffu, grow && !first)) {
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(t_o + t * D + c, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                tmem_st32(t_o + t * D + c, o);
+                            }
+                        }
+                        first = false;
+                    };
                     float acc0 = 0.f, acc1 = 0.f, acc2 = 0.f, acc3 = 0.f;
                     auto exp_chunk = [&](const float* sc, uint32_t col) {
+                        const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
                         uint32_t pk[16];
 #pragma unroll
                         for (int c = 0; c < 16; c += 2) {
@@ -656,27 +775,75 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                         }
                         tmem_st16(t_s + col, pk);
                     };
-                    exp_chunk(s0, 0);
-                    if (nch > 1) exp_chunk(s1, 16);
-                    // Rescale O when a reference moved, before the first half of P is released.
-                    // O's previous product has completed: it was issued before this S.
-                    if (__any_sync(0xffffffffu, grow && !first)) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(t_o + t * D + c, o);
-                            tmem_wait_ld(o);
+                    if (key0 + kBc <= all_see) {  // every row sees all 128 keys
+                        uint32_t r0[32], r1[32], r2[32], r3[32];
+                        tmem_ld32(t_s + 0, r0);
+                        tmem_ld32(t_s + 32, r1);
+                        tmem_wait_ld(r0);
+                        tmem_wait_ld(r1);
+                        tmem_ld32(t_s + 64, r2);
+                        tmem_ld32(t_s + 96, r3);
+                        float* s0 = reinterpret_cast<float*>(r0);
+                        float* s1 = reinterpret_cast<float*>(r1);
+                        float* s2 = reinterpret_cast<float*>(r2);
+                        float* s3 = reinterpret_cast<float*>(r3);
+                        float mx0 = fmax3(s0[0], s0[1], s0[2]), mx1 = fmax3(s1[0], s1[1], s1[2]);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tmem_st32(t_o + t * D + c, o);
+                        for (int c = 3; c < 31; c += 2) {
+                            mx0 = fmax3(mx0, s0[c], s0[c + 1]);
+                            mx1 = fmax3(mx1, s1[c], s1[c + 1]);
                         }
+                        mx0 = fmax3(mx0, s0[31], fmaxf(mx1, s1[31]));
+                        tmem_wait_ld(r2);
+                        tmem_wait_ld(r3);
+                        float mx2 = fmax3(s2[0], s2[1], s2[2]), mx3 = fmax3(s3[0], s3[1], s3[2]);
+#pragma unroll
+                        for (int c = 3; c < 31; c += 2) {
+                            mx2 = fmax3(mx2, s2[c], s2[c + 1]);
+                            mx3 = fmax3(mx3, s3[c], s3[c + 1]);
+                        }
+                        refer(fmax3(mx0, fmax3(mx2, s2[31], mx3), s3[31]));
+                        exp_chunk(s0, 0);
+                        exp_chunk(s1, 16);
+                        rescale();
+                        tmem_wait_st();
+                        tc_fence_before_sync();
+                        mbar_arrive(bar(L::kPHalf + t));
+                        exp_chunk(s2, 32);
+                        exp_chunk(s3, 48);
+                    } else {
+                        // A tail, or later tokens' keys: chunk by chunk in little code, reading the
+                        // scores twice.  Chunks past the last key are left out (the output product
+                        // stops at the step of 16 that holds it).  P of chunk i overwrites scores of
+                        // chunk i / 2, which has been read.
+                        const int nch = (keys + 31) >> 5;
+                        uint32_t r[32];
+                        float* sc = reinterpret_cast<float*>(r);
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int i = 0; i < nch; ++i) {
+                            tmem_ld32(t_s + 32 * i, r);
+                            tmem_wait_ld(r);
+                            const int left = lim - key0 - 32 * i;  // visible keys from here on
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) mx = fmaxf(mx, c < left ? sc[c] : -INFINITY);
+                        }
+                        refer(mx);
+                        rescale();
+#pragma unroll 1
+                        for (int i = 0; i < nch; ++i) {
+                            tmem_ld32(t_s + 32 * i, r);
+                            tmem_wait_ld(r);
+                            const int left = lim - key0 - 32 * i;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (c >= left) sc[c] = -INFINITY;
+                            exp_chunk(sc, 16 * i);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before_sync();
+                        mbar_arrive(bar(L::kPHalf + t));
                     }
-                    first = false;
-                    tmem_wait_st();
-                    tc_fence_before_sync();
-                    mbar_arrive(bar(L::kPHalf + t));
-                    if (nch > 2) exp_chunk(s2, 32);
-                    if (nch > 3) exp_chunk(s3, 48);
                     l += (acc0 + acc1) + (acc2 + acc3);
                     tmem_wait_st();
                     tc_fence_before_sync();
@@ -713,43 +880,53 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                 // a row that sees no key of this piece: O = 0, LSE = -inf
                 const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
                 if (warp_on) {
-                    const int64_t idx = it.part + k * kBr + rloc;
-                    float* orow = p.part_o + idx * D;
                     const int c0 = merge ? t * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
                     const float wa = w_own * inv, wb = w_other * inv;
                     // evict-last: read back right after this grid
                     const uint64_t keep = l2_policy_evict_last();
+                    const int here = nrow - quad * 32;  // rows of this warp
+                    float* out = p.part_o + (it.part + k * kBr + quad * 32 + (lane >> 2)) * D + (lane & 3) * 2;
 #pragma unroll 1
-                    for (int c = c0; c < c1; c += 32) {
-                        uint32_t oa[32];
-                        if (merge) {
-                            uint32_t ob[32];
-                            tmem_ld32(t_o + t * D + c, oa);
-                            tmem_ld32(t_o + (t ^ 1) * D + c, ob);
-                            tmem_wait_ld(oa);
-                            tmem_wait_ld(ob);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
+                    for (int half = 0; half < 32 && half < here; half += 16) {
+                        // the weights of this thread's two rows
+                        const int ra = half + (lane >> 2);
+                        const float wa0 = __shfl_sync(0xffffffffu, wa, ra), wa1 = __shfl_sync(0xffffffffu, wa, ra + 8);
+                        const float wb0 = __shfl_sync(0xffffffffu, wb, ra), wb1 = __shfl_sync(0xffffffffu, wb, ra + 8);
+                        const uint32_t lanes = static_cast<uint32_t>(half) << 16;
+#pragma unroll 1
+                        for (int c = c0; c < c1; c += 32) {
+                            uint32_t oa[16];
+                            tmem_ld16x256(t_o + lanes + t * D + c, oa);
+                            if (merge) {
+                                uint32_t ob[16];
+                                tmem_ld16x256(t_o + lanes + (t ^ 1) * D + c, ob);
+                                tmem_wait_ld16(oa);
+                                tmem_wait_ld16(ob);
                                 // a chain without a visible key for the row has weight 0 and finite O
-                                const float v = __uint_as_float(oa[i]) * wa + __uint_as_float(ob[i]) * wb;
-                                oa[i] = __float_as_uint(v);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    oa[i] = __float_as_uint(__uint_as_float(oa[i]) * ((i & 2) ? wa1 : wa0) +
+                                                            __uint_as_float(ob[i]) * ((i & 2) ? wb1 : wb0));
+                            } else {
+                                tmem_wait_ld16(oa);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    oa[i] = __float_as_uint(__uint_as_float(oa[i]) * ((i & 2) ? wa1 : wa0));
                             }
-                        } else {
-                            tmem_ld32(t_o + t * D + c, oa);
-                            tmem_wait_ld(oa);
+                            float* o0 = out + half * D + c;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) oa[i] = __float_as_uint(__uint_as_float(oa[i]) * wa);
-                        }
-                        if (row_on) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                st_global_v4_hint(orow + c + 4 * i, __uint_as_float(oa[4 * i]),
-                                                  __uint_as_float(oa[4 * i + 1]), __uint_as_float(oa[4 * i + 2]),
-                                                  __uint_as_float(oa[4 * i + 3]), keep);
+                            for (int i = 0; i < 16; i += 4) {
+                                if (ra < here)
+                                    st_global_v2_hint(o0 + 2 * i, __uint_as_float(oa[i]), __uint_as_float(oa[i + 1]), keep);
+                                if (ra + 8 < here)
+                                    st_global_v2_hint(o0 + 8 * D + 2 * i, __uint_as_float(oa[i + 2]),
+                                                      __uint_as_float(oa[i + 3]), keep);
+                            }
                         }
                     }
                     if (row_on && (!merge || t == 0))
-                        st_global_hint(p.part_lse + idx, sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2, keep);
+                        st_global_hint(p.part_lse + it.part + k * kBr + rloc,
+                                       sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2, keep);
                 }
                 tc_fence_before_sync();
                 if (merge) {
@@ -762,7 +939,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             }
             o_phase ^= both ? 3u : 1u << par;
             ring += 2 * it.ntiles;
-            par = (par + steps) & 1u;
+            par = two ? 0u : (par + it.ntiles) & 1u;
         }
     }
 

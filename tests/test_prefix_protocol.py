@@ -282,16 +282,32 @@ def run(items, seed, stages=STAGES, o_empty_twice=True):
             if last:
                 B[("OFull", c)].arrive()
 
+        def free(c):  # the score buffer of the product that ran (unless the next scores already went into it)
+            if S[c][0] == "P":
+                S[c] = ("free",)
+
+        def pv_now():
+            if due:
+                c = due[0][2]
+                yield from run_pv()
+                free(c)
+
         for n, it in enumerate(entries):
+            if rng.random() < 0.3:  # the next item is not known yet: the due product goes first
+                yield from pv_now()
             yield from take(n)
             B[("ItemEmpty", n % RING)].arrive()
             if it is None:
                 break
             two, nt, _ = it
             steps = 2 * nt if two else nt
+            par = 0 if two else par
             for s in range(steps):
                 j, k = (s >> 1, s & 1) if two else (s, 0)
                 c = (par + s) & 1
+                if due and (due[0][2] == c or ((s == 0 or not two) and rng.random() < 0.3)):
+                    assert due[0][2] != c or (two and s == 0)  # the same chain again: only at a two-tile item's start
+                    yield from pv_now()  # or its operands are not there yet
                 if k == 0:
                     yield ("KvFull", kpos % stages), kpos // stages
                 if j == 0:
@@ -307,16 +323,13 @@ def run(items, seed, stages=STAGES, o_empty_twice=True):
                     B[("KvEmpty", kpos % stages)].arrive()
                 if j == nt - 1:
                     B[("QEmpty", (qpos + k) & 1)].arrive()
-                prev = due[0][2] if due else None
-                yield from run_pv()
-                if prev is not None:
-                    S[prev] = ("free",) if prev != c else S[prev]
+                yield from pv_now()
                 due.append((n, j, c, k, kpos + 1, j == 0 if two else s < 2, j == nt - 1 if two else s + 2 >= steps,
                             k == 0, last_k))
                 if last_k:
                     kpos += 2
             qpos += 2 if two else 1
-            par = (par + steps) & 1
+            par = 0 if two else (par + steps) & 1
         yield from run_pv()
 
     def softmax(t):
@@ -329,7 +342,7 @@ def run(items, seed, stages=STAGES, o_empty_twice=True):
                 return
             two, nt, tail = it
             steps = 2 * nt if two else nt
-            mine = t ^ par
+            mine = t if two else t ^ par
             k = mine if two else 0
             both = two or nt >= 2
             if both or mine == 0:
@@ -370,7 +383,7 @@ def run(items, seed, stages=STAGES, o_empty_twice=True):
                 if both or par == c:
                     o_cnt[c] += 1
             ring += 2 * nt
-            par = (par + steps) & 1
+            par = 0 if two else (par + steps) & 1
 
     roles = {"scheduler": scheduler(), "producer": producer(), "qloader": qloader(), "mma": mma(), "softmax0": softmax(0),
              "softmax1": softmax(1)}
