@@ -80,9 +80,9 @@ int encode_rows_map(CUtensorMap* map, const void* base, int BH, int N, int d, in
     return ATTN_OK;
 }
 
-int encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* e, const uint64_t* st, uint32_t box_rows) {
-    cuuint64_t dims[4], strides[3];
-    cuuint32_t box[4] = {64, box_rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+int encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* e, const uint64_t* st, const uint32_t* box) {
+    cuuint64_t dims[5], strides[4];
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) dims[i] = e[i];
     for (int i = 0; i + 1 < rank; ++i) strides[i] = st[i];
     CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims,

@@ -21,7 +21,7 @@ struct DeviceState {
     uint32_t* error_word = nullptr;  // 256-byte device block, first word = error code
     bool smem_configured[2][2][2] = {};                                   // forward <d == 128><causal><dynamic schedule>
     bool bwd_smem_configured[2][2] = {{false, false}, {false, false}};  // backward <d == 128><causal>
-    bool prefix_smem_configured[2] = {};  // shared-prefix forward <d == 128>
+    bool prefix_smem_configured[2][2] = {};  // shared-prefix forward <own-keys kernel><d == 128>
     bool ready_configured[2][8] = {};  // query / key preparation <backward><variant>
     bool fp8_smem_configured[2][2][2] = {};  // FP8 forward <causal><dynamic schedule><K/V segments>
 };
@@ -44,10 +44,10 @@ int device_state(DeviceState** out);
 // descriptors expect.  Rows past N read as zero.
 int encode_rows_map(CUtensorMap* map, const void* base, int BH, int N, int d, int box_rows);
 
-// A bf16 tensor of rank 3 or 4 with extents e (e[0] = d innermost) and byte
-// strides st of the outer axes (multiples of 16), read by TMA in boxes of 64
-// columns x box_rows rows (axis 1), 128-byte swizzle.  Rows past e[1] read as zero.
-int encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* e, const uint64_t* st, uint32_t box_rows);
+// A bf16 tensor of rank 3 to 5 with extents e (e[0] = d innermost) and byte
+// strides st of the outer axes (multiples of 16), read by TMA in boxes `box`
+// (box[0] = 64 columns), 128-byte swizzle.  What lies past an extent reads as zero.
+int encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* e, const uint64_t* st, const uint32_t* box);
 
 // An fp32 tensor viewed as [BH][N][d], written by TMA (reduce-add) in boxes of
 // d columns x box_rows rows, unswizzled.  Rows past N are dropped.

@@ -42,9 +42,18 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
     p.P = s.P;
     p.C = s.C;
     p.ptiles = (s.P + kBc - 1) / kBc;
-    p.pblocks = static_cast<int>((static_cast<int64_t>(s.R) * p.GT + 2 * kBr - 1) / (2 * kBr));
-    p.oblocks = (p.GT + 2 * kBr - 1) / (2 * kBr);
-    p.orows = p.GT < 2 * kBr ? p.GT : 2 * kBr;
+    p.qrows = p.GT <= kBr ? kBr / p.GT * p.GT : kBr;
+    p.pblocks = static_cast<int>((static_cast<int64_t>(s.R) * p.GT + 2 * p.qrows - 1) / (2 * p.qrows));
+    p.oblocks = (p.GT + 2 * p.qrows - 1) / (2 * p.qrows);
+    p.orows = p.GT < 2 * p.qrows ? p.GT : 2 * p.qrows;
+    // Own keys of up to 16 rows a request and key head: a kernel of their own (see there).  Its
+    // warps: as many as there can be steps for, up to kOwnWarps an SM.
+    p.workers = 0;
+    if (s.C > 0 && p.GT <= kOwnRows) {
+        const int64_t steps = static_cast<int64_t>(s.R) * s.Hk * ((s.C + kOwnStep - 1) / kOwnStep);
+        const int64_t ctas = (steps + kOwnWarps - 1) / kOwnWarps;
+        p.workers = static_cast<int>(ctas < num_sms ? ctas : num_sms) * kOwnWarps;
+    }
     p.psegs = 0;
     p.seg_tiles = 1;
     p.pitems = 0;
@@ -74,7 +83,8 @@ size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 struct PrefixSpace {
     size_t start, lse, rows, bytes;
     int64_t own_first;
-    PrefixSpace(const PrefixParams& p, int d, int grid) {
+    PrefixSpace(const PrefixParams& p, int d, int num_sms) {
+        const int grid = p.workers > 0 ? p.workers : num_sms;  // who may have a piece of a sequence
         own_first = static_cast<int64_t>(p.psegs) * p.Hk * p.R * p.GT;
         const int64_t own = p.C > 0 ? (static_cast<int64_t>(p.R) * p.Hk * p.oblocks + grid) * p.orows : 0;
         start = 0;
@@ -94,7 +104,7 @@ int take_view(int64_t (&out)[N], const int64_t* given, const int64_t (&dims)[N],
         if (given && dims[i] > 1) {
             out[i] = given[i];
             if (out[i] % 8 != 0) return ATTN_ERR_MISALIGNED;
-            if (out[i] <= 0 || out[i] >= (1LL << 39)) return ATTN_ERR_INVALID_ARG;
+            if (out[i] <= 0 || out[i] >= (1LL << 39) || out[i] > (1LL << 39) / dims[i]) return ATTN_ERR_INVALID_ARG;
         }
         dense *= dims[i];
     }
@@ -102,31 +112,57 @@ int take_view(int64_t (&out)[N], const int64_t* given, const int64_t (&dims)[N],
 }
 
 template <int D>
-int launch(DeviceState& dev, const CUtensorMap (&maps)[4], const PrefixParams& p, cudaStream_t stream) {
+int launch(DeviceState& dev, const CUtensorMap (&maps)[6], const PrefixParams& p, cudaStream_t stream) {
     auto kernel = attn_prefix_kernel<D>;
     constexpr int smem = PrefixSmem<D>::kBytes;
-    bool& configured = dev.prefix_smem_configured[D == 128];
+    bool& configured = dev.prefix_smem_configured[0][D == 128];
     cudaError_t e;
     if (!configured) {
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
             return cuda_fail(e);
         configured = true;
     }
-    kernel<<<dev.num_sms, kThreads, smem, stream>>>(maps[0], maps[1], maps[2], maps[3], p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
-    // one warp a row, or eight where there are few rows and many pieces to merge
-    const int64_t rows = static_cast<int64_t>(p.R) * p.Hk * p.GT;
-    const bool wide = rows < 8 * static_cast<int64_t>(dev.num_sms);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    if (p.workers > 0) {
+        auto own = attn_prefix_own_kernel<D>;
+        constexpr int own_smem = OwnSmem<D>::kBytes;
+        bool& own_configured = dev.prefix_smem_configured[1][D == 128];
+        if (!own_configured) {
+            if ((e = cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, own_smem)) != cudaSuccess)
+                return cuda_fail(e);
+            own_configured = true;
+        }
+        own<<<p.workers / kOwnWarps, kOwnWarps * 32, own_smem, stream>>>(maps[1], maps[4], maps[5], p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+        // the prefix kernel is a programmatic dependent: its CTAs start as the SMs become free
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    if (p.workers == 0 || p.pitems > 0) {
+        const int grid = p.workers > 0 && p.pitems < dev.num_sms ? p.pitems : dev.num_sms;
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        if ((e = cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p)) != cudaSuccess)
+            return cuda_fail(e);
+    }
+    // a row's pieces are dealt to as many warps (1, 2, 4, 8) as there are pieces for and as
+    // the SMs hold at once (32 each)
+    const int64_t rows = static_cast<int64_t>(p.R) * p.Hk * p.GT;
+    const int pieces = p.psegs + (p.C > 0 ? 1 : 0);
+    int warps = 1;
+    while (warps < 8 && warps < pieces && rows * warps * 2 <= 32ll * dev.num_sms) warps *= 2;
+    cfg.gridDim = dim3(static_cast<unsigned>((rows * warps + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto combine = wide ? attn_prefix_combine_kernel<D, 8> : attn_prefix_combine_kernel<D, 1>;
+    auto combine = warps == 8 ? attn_prefix_combine_kernel<D, 8> : warps == 4 ? attn_prefix_combine_kernel<D, 4>
+                   : warps == 2 ? attn_prefix_combine_kernel<D, 2> : attn_prefix_combine_kernel<D, 1>;
     if ((e = cudaLaunchKernelEx(&cfg, combine, p, dev.num_sms)) != cudaSuccess) return cuda_fail(e);
     return ATTN_OK;
 }
@@ -177,7 +213,7 @@ extern "C" int attn_fwd_prefix(const void* Q, const int64_t* q_strides, const vo
     lay_out(p, s, dev->num_sms);
     const PrefixSpace space(p, d, dev->num_sms);
     if (workspace_bytes < space.bytes) return ATTN_ERR_INVALID_ARG;
-    CUtensorMap maps[4] = {};
+    CUtensorMap maps[6] = {};  // Q by tiles of the prefix, Q by requests; Kp, Vp; Ko, Vo
     const void* pre[2] = {Kp, Vp};
     const void* own[2] = {Ko, Vo};
     const int64_t *pre_st[2] = {kp, vp}, *own_st[2] = {ko, vo};
@@ -185,15 +221,29 @@ extern "C" int attn_fwd_prefix(const void* Q, const int64_t* q_strides, const vo
         if (P > 0) {
             const uint64_t e[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(P), static_cast<uint64_t>(Hk)};
             const uint64_t b[2] = {static_cast<uint64_t>(pre_st[i][1]) * 2, static_cast<uint64_t>(pre_st[i][0]) * 2};
-            if ((st = encode_bf16_map(&maps[i], pre[i], 3, e, b, kBc)) != ATTN_OK) return st;
+            const uint32_t box[3] = {64, kBc, 1};
+            if ((st = encode_bf16_map(&maps[2 + i], pre[i], 3, e, b, box)) != ATTN_OK) return st;
         }
         if (C > 0) {
             const uint64_t e[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(C), static_cast<uint64_t>(Hk),
                                    static_cast<uint64_t>(R)};
             const uint64_t b[3] = {static_cast<uint64_t>(own_st[i][2]) * 2, static_cast<uint64_t>(own_st[i][1]) * 2,
                                    static_cast<uint64_t>(own_st[i][0]) * 2};
-            if ((st = encode_bf16_map(&maps[2 + i], own[i], 4, e, b, kPfxOwnBox)) != ATTN_OK) return st;
+            const uint32_t box[4] = {64, static_cast<uint32_t>(p.workers > 0 ? kOwnStep : kPfxOwnBox), 1, 1};
+            if ((st = encode_bf16_map(&maps[4 + i], own[i], 4, e, b, box)) != ATTN_OK) return st;
         }
+    }
+    if (p.GT <= kBr) {
+        const uint64_t e[5] = {static_cast<uint64_t>(d), static_cast<uint64_t>(T), static_cast<uint64_t>(p.G),
+                               static_cast<uint64_t>(Hk), static_cast<uint64_t>(R)};
+        const uint64_t b[4] = {static_cast<uint64_t>(p.qs[2]) * 2, static_cast<uint64_t>(p.qs[1]) * 2,
+                               static_cast<uint64_t>(p.qs[1]) * p.G * 2, static_cast<uint64_t>(p.qs[0]) * 2};
+        const uint32_t tile[5] = {64, static_cast<uint32_t>(T), static_cast<uint32_t>(p.G), 1,
+                                  static_cast<uint32_t>(p.qrows / p.GT)};
+        const uint32_t one[5] = {64, static_cast<uint32_t>(T), static_cast<uint32_t>(p.G), 1, 1};
+        if ((P > 0 && (st = encode_bf16_map(&maps[0], Q, 5, e, b, tile)) != ATTN_OK) ||
+            (C > 0 && (st = encode_bf16_map(&maps[1], Q, 5, e, b, one)) != ATTN_OK))
+            return st;
     }
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.q = static_cast<const __nv_bfloat16*>(Q);

@@ -17,7 +17,8 @@
 //   warp 1             tcgen05.mma issuer; owns the TMEM allocation
 //   warp 2             scheduler: works out the CTA's items (the own lengths are
 //                      device data) and passes them to the others through a ring
-//   warp 3             Q loader: gathers the item's rows into a swizzled tile
+//   warp 3             Q loader: the rows of whole requests by TMA (a box of T x G x
+//                      requests lands in row order), or row by row where a request has more than 128
 //   warps 4-7, 8-11    softmax warpgroups, one per chain (below)
 // Two chains (S_c, O_c in TMEM, softmax warpgroup c) alternate step by step, so
 // that the tensor core works on one while the softmax of the other runs:
@@ -51,7 +52,7 @@ namespace elsattn {
 constexpr int kPfxTileCost = 4;
 constexpr int kPfxItemCost = 2;
 constexpr int kPfxOwnBox = 32;   // keys per TMA box of the own caches
-constexpr int kPfxItemRing = 4;
+constexpr int kPfxItemRing = 8;
 
 struct PrefixParams {
     const __nv_bfloat16* q;
@@ -63,15 +64,17 @@ struct PrefixParams {
     int R, T, Hk, G;
     int GT;                 // rows of a request at one key head
     int P, C;               // prefix keys; own capacity
-    int pblocks;            // blocks of 256 rows over R GT
+    int qrows;              // rows of a query tile: the whole requests that fit 128 rows, or 128 if one does not
+    int pblocks;            // blocks of two query tiles over R GT
     int ptiles, psegs, seg_tiles;  // prefix tiles; cut into psegs runs of seg_tiles
     int pitems;             // Hk * psegs * pblocks
-    int oblocks;            // blocks of 256 rows over GT
-    int orows;              // rows of an own slot: min(GT, 256)
+    int oblocks;            // blocks of two query tiles over GT
+    int orows;              // rows of an own slot: min(GT, 2 qrows)
     float* part_o;          // partial rows [.., d] fp32: first [psegs][Hk][R GT], then [own slots][orows]
     float* part_lse;        // one per partial row
     int64_t own_first;      // the first own slot's partial row
     int64_t* own_start;     // [R + 1]: where each request's own work starts, and the total
+    int workers;            // warps of attn_prefix_own_kernel, which then does the own work; 0: it is items of the prefix kernel
     uint32_t* error_word;
     uint64_t timeout_ns;
     float scale_log2, max_scale_log2;
@@ -166,7 +169,15 @@ struct PrefixSmem {
 };
 constexpr int kPfxItemReaders = 11;  // producer, MMA, Q loader, eight softmax warps
 
-// 4-D tiled load.
+// 4-D and 5-D tiled loads.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3, int32_t c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1,
                                             int32_t c2, int32_t c3) {
     asm volatile(
@@ -208,7 +219,8 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_constant__ CUtensorMap tmap_vp,
+attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_constant__ CUtensorMap tmap_qo,
+                   const __grid_constant__ CUtensorMap tmap_kp, const __grid_constant__ CUtensorMap tmap_vp,
                    const __grid_constant__ CUtensorMap tmap_ko, const __grid_constant__ CUtensorMap tmap_vo,
                    const __grid_constant__ PrefixParams p) {
     using L = PrefixSmem<D>;
@@ -245,11 +257,14 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             mbar_init(bar(L::kItemEmpty + s), kPfxItemReaders);
         }
         fence_barrier_init();
+        if (p.GT <= kBr) {
+            tma_prefetch_desc(p.P > 0 ? &tmap_qp : &tmap_qo);
+        }
         if (p.P > 0) {
             tma_prefetch_desc(&tmap_kp);
             tma_prefetch_desc(&tmap_vp);
         }
-        if (p.lens) {
+        if (p.lens && p.workers == 0) {
             tma_prefetch_desc(&tmap_ko);
             tma_prefetch_desc(&tmap_vo);
         }
@@ -408,7 +423,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             if (pv.due && !there(bar(L::kItemFull + n % kPfxItemRing), (n / kPfxItemRing) & 1u) && !(ok = run_pv())) break;
             if (!take_item(n, it, true)) break;
             const int nt = it.ntiles;
-            if (it.nrows > kBr) {
+            if (it.nrows > p.qrows) {
                 // Two query tiles, chain = tile: S0_j; O1 += P1_{j-1} V_{j-1}; S1_j; O0 += P0_j V_j.
                 // The chains are literal in this loop, which is what bounds it: the issue of
                 // a step's products and its waits, with generic steps, took 1.2 us.
@@ -556,19 +571,21 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
             it.klen = p.P;
             it.tile0 = seg * p.seg_tiles;
             it.ntiles = min(p.seg_tiles, p.ptiles - it.tile0);
-            it.row0 = blk * 2 * kBr;
-            it.nrows = min(2 * kBr, p.R * p.GT - it.row0);
+            it.row0 = blk * 2 * p.qrows;
+            it.nrows = min(2 * p.qrows, p.R * p.GT - it.row0);
             it.part = (static_cast<int64_t>(seg) * p.Hk + it.head) * p.R * p.GT + it.row0;
             publish(it);
         }
-        if (p.lens && ok) {
+        if (p.lens && p.workers == 0 && ok) {
             // The total and the lane whose run of requests holds this CTA's first unit.
             const int run = (p.R + 31) / 32;
             int64_t mine = 0;
+#pragma unroll 8
             for (int i = 0; i < run; ++i) {
                 const int r = lane * run + i;
-                if (r < p.R) mine += request_cost(p, own_len(p, r));
+                mine += seq_cost(r < p.R ? own_len(p, r) : 0);
             }
+            mine *= p.Hk * p.oblocks;
             const int64_t upto = warp_scan(mine, lane);
             const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
             const OwnCut cut(p, total, gridDim.x);
@@ -598,8 +615,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                                 it.klen = len;
                                 it.tile0 = t0;
                                 it.ntiles = t1 - t0;
-                                it.row0 = it.req * p.GT + blk * 2 * kBr;
-                                it.nrows = min(2 * kBr, p.GT - blk * 2 * kBr);
+                                it.row0 = it.req * p.GT + blk * 2 * p.qrows;
+                                it.nrows = min(2 * p.qrows, p.GT - blk * 2 * p.qrows);
                                 const int64_t slot = (static_cast<int64_t>(it.req) * p.Hk * p.oblocks + q) + blockIdx.x;
                                 it.part = p.own_first + slot * p.orows;
                                 publish(it);
@@ -613,7 +630,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         it.ntiles = -1;
         if (ok) publish(it);
         // One CTA leaves every request's start and the total for the combine kernel.
-        if (p.lens && blockIdx.x == gridDim.x - 1) {
+        if (p.lens && p.workers == 0 && blockIdx.x == gridDim.x - 1) {
             int64_t start = 0;
             for (int r0 = 0; r0 < p.R; r0 += 32) {
                 const int64_t c = r0 + lane < p.R ? request_cost(p, own_len(p, r0 + lane)) : 0;
@@ -630,13 +647,33 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         const int ch = lane % kChunks, sub = lane / kChunks;
         const uint32_t col = (ch >> 3) * (kBr * 128);
         uint32_t qpos = 0;
+        uint32_t q_slots = 0, q_parity = 0;  // slots that a TMA copy was issued to, and the parity it completes
         bool ok = true;
         PrefixItem it;
         for (uint32_t n = 0; ok && take_item(n, it, true); ++n) {
-            for (int k = 0; k < (it.nrows > kBr ? 2 : 1) && ok; ++k, ++qpos) {
+            for (int k = 0; k < (it.nrows > p.qrows ? 2 : 1) && ok; ++k, ++qpos) {
                 const uint32_t slot = qpos & 1u;
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kQEmpty + slot), ((qpos >> 1) & 1u) ^ 1u, ctx));
                 if (!ok) break;
+                if (p.GT <= kBr) {
+                    // whole requests: those of the tile (past the last they read as zero), or the item's own
+                    const uint32_t full = bar(L::kQFull + slot);
+                    if (lane == 0) {
+                        const int rows = it.req < 0 ? p.qrows : p.GT;
+                        mbar_arrive_expect_tx(full, rows * D * 2);
+#pragma unroll
+                        for (int b = 0; b < D / 64; ++b)
+                            tma_load_5d(s_base + L::kQOff + slot * L::kTile + b * (kBr * 128),
+                                        it.req < 0 ? &tmap_qp : &tmap_qo, full, b * 64, 0, 0, it.head,
+                                        (it.row0 + k * p.qrows) / p.GT);
+                        q_slots |= 1u << slot;
+                        q_parity = (q_parity & ~(1u << slot)) | (((qpos >> 1) & 1u) << slot);
+                    } else {
+                        mbar_arrive(full);
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 const int rows = min(kBr, it.nrows - k * kBr);
                 const uint32_t dst = s_base + L::kQOff + slot * L::kTile + col;
                 for (int base = 0; base < rows; base += 32) {
@@ -664,6 +701,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                 mbar_arrive(bar(L::kQFull + slot));
             }
         }
+        for (uint32_t s = 0; s < 2; ++s)  // the copies land before the shared memory is released
+            if (q_slots & (1u << s)) mbar_wait_drain(bar(L::kQFull + s), (q_parity >> s) & 1u, 50000000ull);
     } else {
         // ------------------------------------------------------------ softmax warpgroups
         const int t = (warp - 4) >> 2;          // chain
@@ -680,10 +719,10 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         bool ok = true;
         PrefixItem it;
         for (uint32_t n = 0; ok && take_item(n, it, true); ++n) {
-            const bool two = it.nrows > kBr;
+            const bool two = it.nrows > p.qrows;
             const int mine = two ? t : t ^ static_cast<int>(par);  // this chain's query tile, or its first K/V tile
             const int k = two ? mine : 0;                     // its query tile
-            const int nrow = min(kBr, it.nrows - k * kBr);
+            const int nrow = min(p.qrows, it.nrows - k * p.qrows);
             const bool warp_on = quad * 32 < nrow;            // the warp has rows
             const bool row_on = rloc < nrow;
             const bool both = two || it.ntiles >= 2;          // both chains work on the item
@@ -694,7 +733,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                 // keys this row sees: all of the source, but for later tokens of its own request
                 int lim = it.klen;
                 if (it.req >= 0 && p.T > 1) {
-                    const int x = it.row0 + k * kBr + min(rloc, nrow - 1) - it.req * p.GT;
+                    const int x = it.row0 + k * p.qrows + min(rloc, nrow - 1) - it.req * p.GT;
                     lim -= p.T - 1 - x % p.T;
                 }
                 const int all_see = it.klen - (it.req >= 0 ? p.T - 1 : 0);  // keys below this are seen by every row
@@ -885,7 +924,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                     // evict-last: read back right after this grid
                     const uint64_t keep = l2_policy_evict_last();
                     const int here = nrow - quad * 32;  // rows of this warp
-                    float* out = p.part_o + (it.part + k * kBr + quad * 32 + (lane >> 2)) * D + (lane & 3) * 2;
+                    float* out = p.part_o + (it.part + k * p.qrows + quad * 32 + (lane >> 2)) * D + (lane & 3) * 2;
 #pragma unroll 1
                     for (int half = 0; half < 32 && half < here; half += 16) {
                         // the weights of this thread's two rows
@@ -925,7 +964,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
                         }
                     }
                     if (row_on && (!merge || t == 0))
-                        st_global_hint(p.part_lse + it.part + k * kBr + rloc,
+                        st_global_hint(p.part_lse + it.part + k * p.qrows + rloc,
                                        sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2, keep);
                 }
                 tc_fence_before_sync();
@@ -949,18 +988,375 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kp, const __grid_con
         tc_fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
+    // The own kernel may still run (this grid does not read what it writes): it has ended when this
+    // grid has, so that the combine kernel, which waits for this grid, finds both kernels' pieces.
+    if (p.workers > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Merge each row's pieces: prefix segments, then own pieces, in that fixed
-// order.  WARPS warps per row (pieces dealt to them, then added in order);
-// lane l holds columns [kPer l, kPer l + kPer).  Requests with a negative own
-// length are padding: their rows are left as they were.
+// ---------------------------------------------------------------------------
+// Own keys of requests with at most 16 rows a key head (the usual decoding
+// step).  A piece of one request at one key head is then a product of 16 rows
+// (most of them padding at small groups), bound by reading K and V once: a
+// warp is enough for it, and many warps with a piece each hide the latency that
+// the roles of the kernel above hand from one to the next (2048 pieces of 16 keys: 47 us
+// there, 18 us here).  Each warp streams K and V in steps of 16 keys through a ring of its own,
+// filled by TMA some steps ahead, across the ends of pieces; Q comes with a
+// piece's first step.  S = Q K^T and O += P V as mma.sync m16n8k16 on
+// registers: the tensor work is a few percent of a step's time, so the rate of
+// these instructions does not matter, and a 128-row tcgen05 tile would be
+// seven eighths empty.
+// ---------------------------------------------------------------------------
+constexpr int kOwnWarps = 6;
+constexpr int kOwnStep = 16;
+constexpr int kOwnRows = 16;
+
+template <int D>
+struct OwnSmem {
+    static constexpr int kPart = kOwnStep * D * 2;         // K, V or Q of a step
+    static constexpr int kStage = 3 * kPart;
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kWarp = kStages * kStage;
+    static constexpr int kStepOff = kOwnWarps * kWarp;     // [warps][stages] OwnStep
+    static constexpr int kBarOff = kStepOff + kOwnWarps * kStages * 32;
+    static constexpr int kFlagOff = kBarOff + kOwnWarps * kStages * 8;
+    static constexpr int kBytes = kFlagOff + 16 + kSmemAlign;
+    static_assert(kPart % 1024 == 0, "swizzle atoms");
+    static_assert(kBytes <= kSmemLimit, "shared memory");
+};
+struct OwnStep {
+    int req, head, key0, len;
+    int first, last;      // of its piece
+    int64_t part;         // the piece's partial rows
+};
+static_assert(sizeof(OwnStep) == 32, "OwnSmem");
+
+// The line of own work as this kernel cuts it: a sequence (request, key head)
+// is one unit and then its steps; every worker (warp) has `cap` units.
+struct WarpCut {
+    int64_t cap;
+    __device__ __forceinline__ WarpCut(int64_t total, int workers) {
+        cap = (total + workers - 1) / workers;
+        if (cap < 1) cap = 1;
+    }
+};
+__device__ __forceinline__ int64_t warp_seq_cost(int len) { return len > 0 ? 1 + (len + kOwnStep - 1) / kOwnStep : 0; }
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 with fp32 accumulation
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kOwnWarps * 32, 1)
+attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PrefixParams p) {
+    using L = OwnSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int lane = threadIdx.x & 31;
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlagOff);
+    const WaitCtx ctx{abort_flag, p.error_word, p.timeout_ns};
+    const uint32_t bars = smem_u32(smem) + L::kBarOff + warp * L::kStages * 8;
+    const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
+    OwnStep* steps = reinterpret_cast<OwnStep*>(smem + L::kStepOff) + warp * L::kStages;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) *abort_flag = 0u;
+    if (lane == 0) {
+        for (int s = 0; s < L::kStages; ++s) mbar_init(bars + 8 * s, 1);
+        fence_barrier_init();
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+    }
+    __syncthreads();
+
+    // ---- this warp's stretch of the line
+    const int worker = blockIdx.x * kOwnWarps + warp;
+    const int run = (p.R + 31) / 32;
+    int64_t mine = 0;
+#pragma unroll 8
+    for (int i = 0; i < run; ++i) {
+        const int r = lane * run + i;
+        mine += warp_seq_cost(r < p.R ? own_len(p, r) : 0);
+    }
+    mine *= p.Hk;
+    const int64_t upto = warp_scan(mine, lane);
+    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+    const WarpCut cut(total, p.workers);
+    const int64_t x0 = worker * cut.cap, x1 = min(x0 + cut.cap, total);
+
+    // ---- the walk of the issuing side (the same in every lane): request r, key head h, steps [s, s1)
+    int r = 0, h = 0, s = 0, s1 = 0, s_first = 0, len = 0;
+    int window = 0, len_l = 0;       // lens of requests [window, window + 32), one a lane
+    int64_t start = 0;               // of the sequence (r, h)
+    bool more = x0 < x1;
+    auto len_of = [&](int i) -> int {
+        if (i >= window + 32) {
+            window = i;
+            len_l = window + lane < p.R ? own_len(p, window + lane) : 0;
+        }
+        return __shfl_sync(0xffffffffu, len_l, i - window);
+    };
+    // the steps of sequence (r, h) in the stretch; moves on over sequences that have none
+    auto settle = [&]() {
+        while (more) {
+            if (start >= x1 || r >= p.R) {
+                more = false;
+                break;
+            }
+            const int64_t cost = warp_seq_cost(len);
+            if (len > 0 && start + cost > x0) {
+                const int64_t f = start + 1;  // step 0's unit
+                s = static_cast<int>(x0 > f ? x0 - f : 0);
+                s1 = static_cast<int>(min(x1 - f, cost - 1));
+                s_first = s;
+                if (s < s1) break;
+            }
+            start += cost;
+            if (len == 0 || ++h == p.Hk) {
+                h = 0;
+                if (++r < p.R) len = len_of(r);
+            }
+        }
+    };
+    if (more) {
+        const int at = __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
+        r = at * run;
+        start = __shfl_sync(0xffffffffu, upto - mine, at);
+        window = r - 32;
+        len = len_of(r);
+        // skip whole requests before the stretch, then whole sequences
+        while (r < p.R && start + warp_seq_cost(len) * p.Hk <= x0) {
+            start += warp_seq_cost(len) * p.Hk;
+            if (++r < p.R) len = len_of(r);
+        }
+        const int64_t cost = warp_seq_cost(len);
+        if (cost > 0) {
+            h = static_cast<int>((x0 - start) / cost);
+            start += h * cost;
+        }
+        settle();
+    }
+    uint32_t filled = 0, used = 0;
+    auto issue = [&]() {
+        if (!more) return;
+        const uint32_t st = filled % L::kStages;
+        if (lane == 0) {
+            OwnStep d;
+            d.req = r;
+            d.head = h;
+            d.key0 = s * kOwnStep;
+            d.len = len;
+            d.first = s == s_first;
+            d.last = s + 1 == s1;
+            d.part = p.own_first + (static_cast<int64_t>(r) * p.Hk + h + worker) * p.orows;
+            steps[st] = d;
+            const uint32_t full = bars + 8 * st;
+            const uint32_t dst = ring + st * L::kStage;
+            mbar_arrive_expect_tx(full, 2 * L::kPart + (d.first ? p.GT * D * 2 : 0));
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b) {
+                const uint32_t o = dst + b * (kOwnStep * 128);
+                if (d.first) tma_load_5d(o + 2 * L::kPart, &tmap_q, full, b * 64, 0, 0, h, r);
+                tma_load_4d(o, &tmap_k, full, b * 64, d.key0, h, r);
+                tma_load_4d(o + L::kPart, &tmap_v, full, b * 64, d.key0, h, r);
+            }
+        }
+        __syncwarp();
+        ++filled;
+        if (++s == s1) {
+            start += warp_seq_cost(len);
+            if (++h == p.Hk) {
+                h = 0;
+                if (++r < p.R) len = len_of(r);
+            }
+            settle();
+        }
+    };
+    for (int i = 0; i < L::kStages; ++i) issue();
+
+    // ---- the consuming side
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4];
+    float m[2], l[2];             // rows lane / 4 and lane / 4 + 8
+    int hide[2];                  // the last keys these rows do not see
+    const int row0 = lane >> 2;
+    const bool valid[2] = {row0 < p.GT, row0 + 8 < p.GT};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        hide[i] = valid[i] ? p.T - 1 - (row0 + 8 * i) % p.T : 0;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    const uint32_t lo8 = lane & 7;
+    // ldmatrix row addresses: Q and V take rows (lane & 15), K rows (lane & 7) + 8 (lane / 16)
+    const uint32_t qv_row = lane & 15, qv_ch = lane >> 4;
+    const uint32_t k_row = (lane & 7) + ((lane >> 4) << 3), k_ch = (lane >> 3) & 1;
+    const float sign = p.negate_scores ? -1.f : 1.f;
+    bool ok = true;
+    for (; used < filled; ++used) {
+        const uint32_t st = used % L::kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * st, (used / L::kStages) & 1u, ctx));
+        if (!ok) break;
+        const uint32_t kb = ring + st * L::kStage, vb = kb + L::kPart, qb = vb + L::kPart;
+        const OwnStep d = steps[st];
+        if (d.first) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t c = 2 * kk + qv_ch;
+                ldmatrix4(qb + (c >> 3) * (kOwnStep * 128) + qv_row * 128 + (((c & 7) ^ lo8) << 4), qf[kk]);
+            }
+        }
+        // Cache rows past the last key may hold anything; a zero weight does not undo a NaN in V.
+        const int keys = d.len - d.key0;
+        if (keys < kOwnStep) {
+            for (int i = lane; i < (kOwnStep - keys) * (D / 8); i += 32) {
+                const int row = keys + i / (D / 8), c8 = i % (D / 8);
+                *reinterpret_cast<uint4*>(smem + (vb - smem_u32(smem)) + (c8 >> 3) * (kOwnStep * 128) + row * 128 +
+                                          (c8 & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();  // before the copy that fills this place next
+            __syncwarp();
+        }
+        float sc[2][2][4] = {};  // two chains of products for each of two groups of 8 keys
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t c = 2 * kk + k_ch;
+            uint32_t kf[4];
+            ldmatrix4(kb + (c >> 3) * (kOwnStep * 128) + k_row * 128 + (((c & 7) ^ lo8) << 4), kf);
+            mma_16816(sc[kk & 1][0], qf[kk], kf[0], kf[1]);
+            mma_16816(sc[kk & 1][1], qf[kk], kf[2], kf[3]);
+        }
+        float x[2][4];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[g][i] = (sc[0][g][i] + sc[1][g][i]) * sign;
+        if (keys < kOwnStep + p.T - 1) {
+            const int c = d.key0 + (lane & 3) * 2;
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + 8 * g + (i & 1) >= d.len - hide[i >> 1]) x[g][i] = -INFINITY;
+        }
+        bool grow = false;
+        float alpha[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float mx = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float m_tile = mx == -INFINITY ? -INFINITY : mx * p.max_scale_log2;
+            alpha[i] = 1.f;
+            if (valid[i] && m_tile > m[i] + kRescaleLog2Bf16) {
+                alpha[i] = ex2_approx(m[i] - m_tile);
+                m[i] = m_tile;
+                grow = true;
+            }
+        }
+        if (__any_sync(0xffffffffu, grow) && !d.first) {
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                o[j][0] *= alpha[0];
+                o[j][1] *= alpha[0];
+                o[j][2] *= alpha[1];
+                o[j][3] *= alpha[1];
+            }
+            l[0] *= alpha[0];
+            l[1] *= alpha[1];
+        }
+        uint32_t pf[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float mu = m[i] == -INFINITY ? 0.f : m[i];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const float a = ex2_approx(fmaf(x[g][2 * i], p.scale_log2, -mu));
+                const float b = ex2_approx(fmaf(x[g][2 * i + 1], p.scale_log2, -mu));
+                l[i] += a + b;
+                pf[2 * g + i] = pack_bf16x2(a, b);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            const uint32_t c = 2 * j + qv_ch;
+            uint32_t vf[4];
+            ldmatrix4_trans(vb + (c >> 3) * (kOwnStep * 128) + qv_row * 128 + (((c & 7) ^ lo8) << 4), vf);
+            mma_16816(o[2 * j], pf, vf[0], vf[1]);
+            mma_16816(o[2 * j + 1], pf, vf[2], vf[3]);
+        }
+        __syncwarp();  // every lane has read the step
+        issue();
+        if (d.last) {
+            const uint64_t keep = l2_policy_evict_last();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float sum = l[i];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                // a row that sees no key of this piece: O = 0, LSE = -inf
+                const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+                if (valid[i]) {
+                    const int64_t row = d.part + row0 + 8 * i;
+                    float* dst = p.part_o + row * D + (lane & 3) * 2;
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j)
+                        st_global_v2_hint(dst + 8 * j, o[j][2 * i] * inv, o[j][2 * i + 1] * inv, keep);
+                    if ((lane & 3) == 0)
+                        st_global_hint(p.part_lse + row, sum == 0.f ? -INFINITY : (m[i] + lg2_approx(sum)) * kLn2, keep);
+                }
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        }
+    }
+    // after an abort, the copies in flight land before the shared memory is released
+    for (; used < filled; ++used)
+        mbar_wait_drain(bars + 8 * (used % L::kStages), (used / L::kStages) & 1u, 50000000ull);
+    // One warp leaves every request's start and the total for the combine kernel.
+    if (worker == p.workers - 1) {
+        int64_t at = 0;
+        for (int r0 = 0; r0 < p.R; r0 += 32) {
+            const int64_t c = r0 + lane < p.R ? warp_seq_cost(own_len(p, r0 + lane)) * p.Hk : 0;
+            const int64_t sum = warp_scan(c, lane);
+            if (r0 + lane < p.R) p.own_start[r0 + lane] = at + sum - c;
+            at += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) p.own_start[p.R] = at;
+    }
+}
+
+// Merge each row's pieces: prefix segments, then own pieces.  WARPS warps per
+// row (pieces dealt to them in order, each with a running maximum, then merged
+// in a fixed order); lane l holds columns [kPer l, kPer l + kPer).  Requests
+// with a negative own length are padding: their rows are left as they were.
 template <int D, int WARPS>
 __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_constant__ PrefixParams p, int grid) {
     constexpr int kPer = D / 32;
     constexpr int kRows = 8 / WARPS;  // rows per CTA
     __shared__ float s_acc[8][D];
-    __shared__ float s_sum[8];
+    __shared__ float2 s_stat[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = warp % WARPS;
     const int64_t rows = static_cast<int64_t>(p.R) * p.Hk * p.GT;
@@ -969,37 +1365,41 @@ __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_c
     const int r = row < rows ? static_cast<int>(row / hgt) : 0;
     const int rem = static_cast<int>(row - static_cast<int64_t>(r) * hgt);
     const int h = rem / p.GT, x = rem - h * p.GT;  // key head, row within the request
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int raw_len = p.lens ? __ldg(p.lens + r) : 0;
+    const int raw_len = p.lens ? __ldg(p.lens + r) : 0;  // an input: no need to wait for it
     const bool on = row < rows && raw_len >= 0;
     const int segs = p.P > 0 ? p.psegs : 0;
     const int64_t pstep = static_cast<int64_t>(p.Hk) * p.R * p.GT;
     const int64_t pfirst = (static_cast<int64_t>(h) * p.R + r) * p.GT + x;
     int64_t ofirst = 0;
-    int pieces = 0;
-    if (on) {
-        pieces = segs;
-        const int len = min(raw_len, p.C);
-        if (len > 0) {
-            const OwnCut cut(p, __ldcg(p.own_start + p.R), grid);
-            const int q = h * p.oblocks + x / (2 * kBr);
+    int pieces = on ? segs : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int len = min(raw_len, p.C);
+    if (on && len > 0) {
+        const int64_t total = __ldcg(p.own_start + p.R);
+        int64_t a, b, seq;
+        if (p.workers > 0) {
+            const WarpCut cut(total, p.workers);
+            const int64_t first = __ldcg(p.own_start + r) + h * warp_seq_cost(len) + 1;
+            a = first / cut.cap;
+            b = (first + (len - 1) / kOwnStep) / cut.cap;
+            seq = static_cast<int64_t>(r) * p.Hk + h;
+        } else {
+            const OwnCut cut(p, total, grid);
+            const int q = h * p.oblocks + x / (2 * p.qrows);
             const int64_t first = __ldcg(p.own_start + r) + q * seq_cost(len) + kPfxItemCost;
-            const int64_t a = cut.cta_of(first), b = cut.cta_of(first + static_cast<int64_t>((len - 1) / kBc) * kPfxTileCost);
-            ofirst = p.own_first + (static_cast<int64_t>(r) * p.Hk * p.oblocks + q + a) * p.orows + x % (2 * kBr);
-            pieces += static_cast<int>(b - a) + 1;
+            a = cut.cta_of(first);
+            b = cut.cta_of(first + static_cast<int64_t>((len - 1) / kBc) * kPfxTileCost);
+            seq = static_cast<int64_t>(r) * p.Hk * p.oblocks + q;
         }
+        ofirst = p.own_first + (seq + a) * p.orows + x % (2 * p.qrows);
+        pieces += static_cast<int>(b - a) + 1;
     }
     auto at = [&](int i) -> int64_t { return i < segs ? pfirst + i * pstep : ofirst + static_cast<int64_t>(i - segs) * p.orows; };
-    // the largest log-sum-exp, then every weight relative to it
-    float mx = -INFINITY;
-    for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, __ldcg(p.part_lse + at(i)));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     float acc[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
-    float sum = 0.f;
-    constexpr int kUnroll = 4;
+    float sum = 0.f, mx = -INFINITY;
+    constexpr int kUnroll = 6;
     for (int i0 = part; i0 < pieces; i0 += WARPS * kUnroll) {
         float v[kUnroll][kPer], ls[kUnroll];
 #pragma unroll
@@ -1014,6 +1414,14 @@ __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_c
                 CombineVec<D>::load(p.part_o + idx * D + lane * kPer, v[u]);
             }
         }
+        float m = mx;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) m = fmaxf(m, ls[u]);
+        const float keep = mx == -INFINITY ? 0.f : expf(mx - m);
+        mx = m;
+        sum *= keep;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) acc[c] *= keep;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const float w = ls[u] == -INFINITY ? 0.f : expf(ls[u] - mx);
@@ -1025,14 +1433,23 @@ __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_c
     if (WARPS > 1) {
 #pragma unroll
         for (int c = 0; c < kPer; ++c) s_acc[warp][lane * kPer + c] = acc[c];
-        if (lane == 0) s_sum[warp] = sum;
+        if (lane == 0) s_stat[warp] = make_float2(mx, sum);
         __syncthreads();
         if (part != 0) return;
-        for (int k = 1; k < WARPS; ++k) {
-            sum += s_sum[warp + k];
+        float m = mx;
+        for (int k = 1; k < WARPS; ++k) m = fmaxf(m, s_stat[warp + k].x);
+        const float keep = mx == -INFINITY ? 0.f : expf(mx - m);
+        sum = mx == -INFINITY ? sum : sum * keep;  // (a NaN stays)
 #pragma unroll
-            for (int c = 0; c < kPer; ++c) acc[c] += s_acc[warp + k][lane * kPer + c];
+        for (int c = 0; c < kPer; ++c) acc[c] *= keep;
+        for (int k = 1; k < WARPS; ++k) {
+            const float2 o = s_stat[warp + k];
+            const float w = o.x == -INFINITY ? 0.f : expf(o.x - m);
+            sum += o.x == -INFINITY ? o.y : o.y * w;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) acc[c] = fmaf(w, s_acc[warp + k][lane * kPer + c], acc[c]);
         }
+        mx = m;
     }
     if (!on) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no visible key at all: O = 0, LSE = -inf

@@ -457,7 +457,8 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
  *   LSE     : fp32 [R, Hq, T] device, contiguous (natural log)
  *   *_strides : host arrays in elements, outermost axis first, d contiguous (Q,
  *             O: request, head, token; Kp, Vp: head, key; Ko, Vo: request, head, key);
- *             NULL: contiguous.  Positive multiples of 8 below 2^39 for axes longer than 1.
+ *             NULL: contiguous.  Positive multiples of 8 for axes longer than 1, and
+ *             stride times extent at most 2^39.
  *   d       : 64 or 128;  scale : any finite value;  R, Hq, Hk, T >= 1, R*Hq*T < 2^31
  *   workspace : device buffer of at least attn_fwd_prefix_workspace_bytes(), 16-byte
  *             aligned, owned by the caller, not used by other work while this call runs

@@ -45,7 +45,7 @@ def cdll_call(lib, **over):
     (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(d=96), 2), (dict(Q=0x1004), 3),
     (dict(Vp=0x3008), 3), (dict(Ko=0x4002), 3), (dict(O=0x7008), 3), (dict(LSE=0x8002), 3), (dict(lens=0x6001), 3),
     (dict(ws=0x9008), 3), (dict(qs=(512, 68, 64)), 3), (dict(kps=(6400, 0)), 1), (dict(vos=(6400, -64, 64)), 1),
-    (dict(kps=(1 << 39, 64)), 1),
+    (dict(kps=(1 << 39, 64)), 1), (dict(qs=(1 << 38, 64, 64)), 1),
 ])
 def test_refusals(lib, over, status):
     assert cdll_call(lib, **over) == status
@@ -154,6 +154,9 @@ SHAPES = [
     (2, 8, 2, 4, 64, 0, 130, [4, 130], True),
     (2, 2, 1, 3, 128, 50, 9, [1, 2], False),                        # fewer own keys than new tokens
     (2, 8, 1, 33, 128, 260, 400, [33, 400], False),                 # 264 rows of a request: two own blocks
+    (50, 12, 2, 3, 128, 700, 40, [(3 * i) % 41 for i in range(50)], True),  # 18 rows a request: tiles of 126 rows
+    (9, 33, 1, 2, 64, 300, 20, [20] * 9, False),                    # 66 rows a request: one a tile
+    (3, 16, 2, 17, 64, 200, 50, [50, 17, 20], False),               # 136 rows a request: rows fetched one by one
     (1, 64, 1, 1, 128, 0, 5000, [4999], False),                     # a long own part alone, cut over many CTAs
     (1, 8, 8, 1, 64, 40000, 0, [], False),
     (3, 3, 3, 1, 128, 200, 64, [70, 64, 1 << 30], False),           # lengths past the capacity

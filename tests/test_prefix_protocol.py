@@ -16,7 +16,7 @@ import random
 import pytest
 
 TILE, ITEM, BC, BR = 4, 2, 128, 128
-STAGES, RING = 5, 4
+STAGES, RING = 5, 8
 
 
 # ------------------------------------------------------------------ 1. the cut
@@ -28,8 +28,9 @@ class Layout:
     def __init__(self, R, Hk, G, T, P, C, grid):
         self.R, self.Hk, self.GT, self.T, self.P, self.C, self.grid = R, Hk, G * T, T, P, C, grid
         self.ptiles = cdiv(P, BC)
-        self.pblocks, self.oblocks = cdiv(R * self.GT, 256), cdiv(self.GT, 256)
-        self.orows = min(self.GT, 256)
+        self.two = 2 * (128 // self.GT * self.GT if self.GT <= 128 else 128)  # rows of two query tiles
+        self.pblocks, self.oblocks = cdiv(R * self.GT, self.two), cdiv(self.GT, self.two)
+        self.orows = min(self.GT, self.two)
         self.psegs, self.seg_tiles, self.pitems = 0, 1, 0
         if self.ptiles:
             units = Hk * self.pblocks
@@ -78,8 +79,8 @@ def schedule(L, lens, cta):
         blk, hs = i % L.pblocks, i // L.pblocks
         seg, head = hs % L.psegs, hs // L.psegs
         t0 = seg * L.seg_tiles
-        row0 = blk * 256
-        out.append((-1, head, row0, min(256, L.R * L.GT - row0), t0, min(L.seg_tiles, L.ptiles - t0),
+        row0 = blk * L.two
+        out.append((-1, head, row0, min(L.two, L.R * L.GT - row0), t0, min(L.seg_tiles, L.ptiles - t0),
                     (seg * L.Hk + head) * L.R * L.GT + row0))
     if not L.C:
         return out
@@ -109,7 +110,7 @@ def schedule(L, lens, cta):
                 if t0 >= t1:
                     continue
                 blk = q % L.oblocks
-                out.append((r, q // L.oblocks, r * L.GT + blk * 256, min(256, L.GT - blk * 256), t0, t1 - t0,
+                out.append((r, q // L.oblocks, r * L.GT + blk * L.two, min(L.two, L.GT - blk * L.two), t0, t1 - t0,
                             L.own_first + (r * seqs + q + cta) * L.orows))
         start += cost * seqs
     return out
@@ -125,10 +126,10 @@ def combine_rows(L, lens, r, h, x):
         for v in lens:
             starts.append(starts[-1] + L.seq_cost(min(max(v, 0), L.C)) * seqs)
         cut = Cut(L, starts[-1])
-        q = h * L.oblocks + x // 256
+        q = h * L.oblocks + x // L.two
         first = starts[r] + q * L.seq_cost(n) + ITEM
         a, b = cut.cta_of(first), cut.cta_of(first + (n - 1) // BC * TILE)
-        rows += [L.own_first + (r * seqs + q + c) * L.orows + x % 256 for c in range(a, b + 1)]
+        rows += [L.own_first + (r * seqs + q + c) * L.orows + x % L.two for c in range(a, b + 1)]
     return rows
 
 
@@ -158,11 +159,11 @@ def test_every_tile_once_and_every_piece_found(R, Hk, G, T, P, C, grid, kind):
             span = set(range(part, part + nrows))
             assert not span & written and 0 <= part and part + nrows <= L.rows
             written |= span
-    want = {(-1, h, b * 256, j) for h in range(Hk) for b in range(L.pblocks) for j in range(L.ptiles)}
+    want = {(-1, h, b * L.two, j) for h in range(Hk) for b in range(L.pblocks) for j in range(L.ptiles)}
     for r in range(R):
         for h in range(Hk):
             for b in range(L.oblocks):
-                want |= {(r, h, r * L.GT + b * 256, j) for j in range(cdiv(min(max(lens[r], 0), C), BC))}
+                want |= {(r, h, r * L.GT + b * L.two, j) for j in range(cdiv(min(max(lens[r], 0), C), BC))}
     assert set(tiles) == want
     read = set()
     for r in range(R):
@@ -172,6 +173,71 @@ def test_every_tile_once_and_every_piece_found(R, Hk, G, T, P, C, grid, kind):
                 assert len(set(rows)) == len(rows) and not read & set(rows) and set(rows) <= written
                 read |= set(rows)
     assert read == written  # nothing computed for nothing, padding's prefix rows included
+
+
+# The own-keys kernel's cut (requests of at most 16 rows a key head): steps of 16 keys, one stretch a warp.
+def warp_seq_cost(n):
+    return 1 + cdiv(n, 16) if n > 0 else 0
+
+
+def warp_walk(R, Hk, lens, total, upto, mine, run, worker, workers):
+    """(request, key head, first step, end) of every piece of a warp, by the kernel's walk."""
+    cap = max(1, cdiv(total, workers))
+    x0, x1 = worker * cap, min(worker * cap + cap, total)
+    out = []
+    if x0 >= x1:
+        return out
+    at = next(k for k in range(32) if upto[k] > x0)
+    r, start, h = at * run, upto[at] - mine[at], 0
+    while r < R and start + warp_seq_cost(lens[r]) * Hk <= x0:
+        start += warp_seq_cost(lens[r]) * Hk
+        r += 1
+    cost = warp_seq_cost(lens[r]) if r < R else 0
+    if cost:
+        h = (x0 - start) // cost
+        start += h * cost
+    while start < x1 and r < R:
+        cost = warp_seq_cost(lens[r])
+        if lens[r] > 0 and start + cost > x0:
+            s, s1 = max(0, x0 - start - 1), min(x1 - start - 1, cost - 1)
+            if s < s1:
+                out.append((r, h, s, s1))
+        start += cost
+        h += 1
+        if lens[r] == 0 or h == Hk:
+            r, h = r + 1, 0
+    return out
+
+
+@pytest.mark.parametrize("kind", ["zero", "full", "one", "padding", "any", "few"])
+@pytest.mark.parametrize("R,Hk,C,workers", [(1, 1, 1, 6), (1, 8, 5000, 912), (3, 2, 700, 912), (70, 2, 400, 60), (33, 8, 33, 912),
+                                            (200, 1, 17, 912), (100, 3, 31, 18), (40, 4, 129, 912)])
+def test_every_own_step_once_and_every_piece_found(R, Hk, C, workers, kind):
+    rng = random.Random(R * 31 + C)
+    lens = [min(max(own_lengths(kind, R, C, rng), 0), C) for _ in range(R)]
+    run = cdiv(R, 32)
+    mine = [Hk * sum(warp_seq_cost(n) for n in lens[k * run:(k + 1) * run]) for k in range(32)]
+    upto = [sum(mine[:k + 1]) for k in range(32)]
+    total = upto[31]
+    steps, slots = set(), set()
+    for w in range(workers):
+        for r, h, s, s1 in warp_walk(R, Hk, lens, total, upto, mine, run, w, workers):
+            assert s < s1
+            for j in range(s, s1):
+                assert (r, h, j) not in steps
+                steps.add((r, h, j))
+            slot = r * Hk + h + w
+            assert slot not in slots and slot < R * Hk + workers
+            slots.add(slot)
+    assert steps == {(r, h, j) for r in range(R) for h in range(Hk) for j in range(cdiv(lens[r], 16))}
+    cap, at, read = max(1, cdiv(total, workers)), 0, set()
+    for r in range(R):
+        for h in range(Hk):
+            if lens[r] > 0:
+                first = at + h * warp_seq_cost(lens[r]) + 1
+                read |= {r * Hk + h + w for w in range(first // cap, (first + (lens[r] - 1) // 16) // cap + 1)}
+        at += warp_seq_cost(lens[r]) * Hk
+    assert read == slots
 
 
 # ------------------------------------------------------------------ 2. the barriers
