@@ -14,11 +14,13 @@ to FlashAttention - A Memory-Centric Compilation Approach in AICF", section 3.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 import struct
+
+import torch
 
 from . import workloads  # noqa: F401  (seeded synthetic inputs; no attention arithmetic)
 
@@ -372,15 +374,18 @@ def layernorm_rows(x, gamma, beta, eps: float = 1e-5, out=None, stream=None):
     return out
 
 
-_NOTHING = contextlib.nullcontext()
-_pack3 = struct.Struct("3q").pack
+_BF16 = torch.bfloat16
+_pack2, _pack3 = struct.Struct("2q").pack, struct.Struct("3q").pack
 
 
-def _on_device(device):
-    """A context with `device` current: nothing to do where it is already."""
-    import torch
+def _elsewhere(device) -> bool:
+    """Whether another device than `device` is current (the library works on the current one)."""
+    return torch.cuda.current_device() != device.index
 
-    return _NOTHING if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+def _raw_stream(stream, device):
+    """The handle of `stream`, or of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _new_for(stream, *tensors):
@@ -392,23 +397,17 @@ def _new_for(stream, *tensors):
 
 def _view(name, t, shape, device):
     """Checks a [B, H, N, d] bf16 view; returns its address and its three strides as the C call's host array."""
-    import torch
-
-    if t.dtype != torch.bfloat16 or t.device != device:
-        raise ValueError(f"{name} must be a bf16 CUDA tensor on q's device")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    s = t.stride()
-    if s[3] != 1:
+    if t.dtype is not _BF16 or t.device != device or t.shape != shape:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on q's device")
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1:
         raise ValueError(f"{name} must have its last axis contiguous")
-    return t.data_ptr(), _pack3(s[0], s[1], s[2])
+    return t.data_ptr(), _pack3(s0, s1, s2)
 
 
 def _rotation(q, k, positions, inv_freq, sections, weights):
     """The checks both directions of qk_norm_rope share.  Returns the sections as a host array, their
     number, the positions [axes, B or 1, N], and their axis and batch strides."""
-    import torch
-
     if q.dim() != 4 or k.dim() != 4 or not q.is_cuda:
         raise ValueError("q and k must be CUDA tensors [B, H, N, d]")
     device = q.device
@@ -453,36 +452,42 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, sectio
     q_out, k_out : optional bf16 views of the outputs' shapes (a cache's rows, or q and k themselves);
                  default: new contiguous tensors, the layout attn_fwd reads
     Returns (q_out, k_out)."""
-    import torch
-
     lib = load_library()
     sec, A, positions, pa, pb = _rotation(q, k, positions, inv_freq, sections, (q_weight, k_weight))
     B, Hq, N, d = q.shape
     Hk = k.shape[1]
-    with _on_device(q.device):
-        fresh = []
-        if q_out is None:
-            q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
-            fresh.append(q_out)
-        if k_out is None:
-            k_out = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
-            fresh.append(k_out)
-        _new_for(stream, *fresh)
-        dev = q.device
-        qp, qs = _view("q", q, q.shape, dev)
-        kp, ks = _view("k", k, k.shape, dev)
-        qop, qos = _view("q_out", q_out, q.shape, dev)
-        kop, kos = _view("k_out", k_out, k.shape, dev)
-        st = lib.attn_qk_norm_rope(qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
-                                   None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb,
-                                   inv_freq.data_ptr(), sec, A, qop, qos, kop, kos, B, Hq, Hk, N, d, eps,
-                                   1 if interleaved else 0, _stream_handle(stream))
+    if _elsewhere(q.device):
+        with torch.cuda.device(q.device):
+            return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, sections, eps, interleaved, q_out, k_out,
+                                stream)
+    fresh = []
+    if q_out is None:
+        q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+        fresh.append(q_out)
+    if k_out is None:
+        k_out = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
+        fresh.append(k_out)
+    _new_for(stream, *fresh)
+    dev = q.device
+    qp, qs = _view("q", q, q.shape, dev)
+    kp, ks = _view("k", k, k.shape, dev)
+    qop, qos = _view("q_out", q_out, q.shape, dev)
+    kop, kos = _view("k_out", k_out, k.shape, dev)
+    st = lib.attn_qk_norm_rope(qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
+                               None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb,
+                               inv_freq.data_ptr(), sec, A, qop, qos, kop, kos, B, Hq, Hk, N, d, eps,
+                               1 if interleaved else 0, _raw_stream(stream, q.device))
     _check(st, "attn_qk_norm_rope")
     return q_out, k_out
 
 
 def qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
     """Device bytes qk_norm_rope_bwd needs with a norm, on the current device."""
+    return int(load_library().attn_qk_norm_rope_bwd_workspace_bytes(d))
+
+
+@functools.lru_cache(maxsize=16)
+def _bwd_workspace_bytes(index, d) -> int:
     return int(load_library().attn_qk_norm_rope_bwd_workspace_bytes(d))
 
 
@@ -494,43 +499,44 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k
     dq, dk     : optional bf16 views for the gradients of q and k (default: new contiguous tensors)
     workspace  : optional uint8 CUDA tensor of qk_norm_rope_bwd_workspace_bytes(d) bytes
     Returns (dq, dk, dq_weight, dk_weight), the weights' gradients fp32 [d], None without a weight."""
-    import torch
-
     lib = load_library()
     sec, A, positions, pa, pb = _rotation(q, k, positions, inv_freq, sections, (q_weight, k_weight))
     B, Hq, N, d = q.shape
     Hk = k.shape[1]
-    with _on_device(q.device):
-        fresh = []
-        if dq is None:
-            dq = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
-            fresh.append(dq)
-        if dk is None:
-            dk = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
-            fresh.append(dk)
-        dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
-        dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
-        fresh += [t for t in (dwq, dwk) if t is not None]
-        if workspace is None and (dwq is not None or dwk is not None):
-            workspace = torch.empty(lib.attn_qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8, device=q.device)
-            fresh.append(workspace)
-        if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != q.device or
-                                      not workspace.is_contiguous()):
-            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-        _new_for(stream, *fresh)
-        dev = q.device
-        gqp, gqs = _view("dq_out", dq_out, q.shape, dev)
-        gkp, gks = _view("dk_out", dk_out, k.shape, dev)
-        qp, qs = _view("q", q, q.shape, dev)
-        kp, ks = _view("k", k, k.shape, dev)
-        dqp, dqs = _view("dq", dq, q.shape, dev)
-        dkp, dks = _view("dk", dk, k.shape, dev)
-        st = lib.attn_qk_norm_rope_bwd(
-            gqp, gqs, gkp, gks, qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb, inv_freq.data_ptr(), sec, A,
-            dqp, dqs, dkp, dks, None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
-            B, Hq, Hk, N, d, eps, 1 if interleaved else 0, None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel(), _stream_handle(stream))
+    if _elsewhere(q.device):
+        with torch.cuda.device(q.device):
+            return qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight, sections, eps,
+                                    interleaved, dq, dk, workspace, stream)
+    fresh = []
+    if dq is None:
+        dq = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+        fresh.append(dq)
+    if dk is None:
+        dk = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
+        fresh.append(dk)
+    dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+    dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+    fresh += [t for t in (dwq, dwk) if t is not None]
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = torch.empty(_bwd_workspace_bytes(q.device.index, d), dtype=torch.uint8, device=q.device)
+        fresh.append(workspace)
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != q.device or
+                                  not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    _new_for(stream, *fresh)
+    dev = q.device
+    gqp, gqs = _view("dq_out", dq_out, q.shape, dev)
+    gkp, gks = _view("dk_out", dk_out, k.shape, dev)
+    qp, qs = _view("q", q, q.shape, dev)
+    kp, ks = _view("k", k, k.shape, dev)
+    dqp, dqs = _view("dq", dq, q.shape, dev)
+    dkp, dks = _view("dk", dk, k.shape, dev)
+    st = lib.attn_qk_norm_rope_bwd(
+        gqp, gqs, gkp, gks, qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
+        None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb, inv_freq.data_ptr(), sec, A,
+        dqp, dqs, dkp, dks, None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
+        B, Hq, Hk, N, d, eps, 1 if interleaved else 0, None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), _raw_stream(stream, q.device))
     _check(st, "attn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -540,11 +546,14 @@ def prefix_workspace_bytes(R: int, Hq: int, Hk: int, T: int, P: int, C: int, d: 
     return int(load_library().attn_fwd_prefix_workspace_bytes(R, Hq, Hk, T, P, C, d))
 
 
-_pack2 = struct.Struct("2q").pack
+@functools.lru_cache(maxsize=256)
+def _prefix_workspace_bytes(index, *shape) -> int:
+    """The query's answer for a device (the current one) and a shape."""
+    return int(load_library().attn_fwd_prefix_workspace_bytes(*shape))
 
 
-def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own_lens=None, scale: float | None = None, out=None,
-                    lse=None, workspace=None, stream=None):
+def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own_lens=None, scale: float | None = None,
+                    out=None, lse=None, workspace=None, stream=None):
     """O, LSE of T new tokens of R requests over a prefix all of them share and each request's own keys.
 
     q         : bf16 CUDA [R, Hq, T, d], d in {64, 128}
@@ -557,8 +566,6 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
     workspace : optional uint8 CUDA tensor of prefix_workspace_bytes() bytes
     All bf16 tensors are views with d contiguous and other strides positive multiples of 8, so token-major
     caches may be given transposed.  Returns (out, lse)."""
-    import torch
-
     lib = load_library()
     if q.dim() != 4 or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [R, Hq, T, d]")
@@ -591,27 +598,29 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
         lens = own_lens.data_ptr()
     if scale is None:
         scale = _SCALES.get(d) or default_scale(d)
-    with _on_device(device):
-        fresh = []
-        if out is None:
-            out = torch.empty((R, Hq, T, d), dtype=torch.bfloat16, device=device)
-            fresh.append(out)
-        if lse is None:
-            lse = torch.empty((R, Hq, T), dtype=torch.float32, device=device)
-            fresh.append(lse)
-        elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (R, Hq, T) or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous fp32 tensor [R, Hq, T] on q's device")
-        if workspace is None:
-            workspace = torch.empty(lib.attn_fwd_prefix_workspace_bytes(R, Hq, Hk, T, P, C, d), dtype=torch.uint8,
-                                    device=device)
-            fresh.append(workspace)
-        elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-        _new_for(stream, *fresh)
-        qp, qs = _view("q", q, q.shape, device)
-        op, os_ = _view("out", out, q.shape, device)
-        st = lib.attn_fwd_prefix(qp, qs, kp, kps, vp, vps, ko, kos, vo, vos, lens, op, os_, lse.data_ptr(), R, Hq, Hk, T,
-                                 P, C, d, scale, workspace.data_ptr() or None, workspace.numel(), _stream_handle(stream))
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return attn_fwd_prefix(q, k_prefix, v_prefix, k_own, v_own, own_lens, scale, out, lse, workspace, stream)
+    fresh = []
+    if out is None:
+        out = torch.empty((R, Hq, T, d), dtype=torch.bfloat16, device=device)
+        fresh.append(out)
+    if lse is None:
+        lse = torch.empty((R, Hq, T), dtype=torch.float32, device=device)
+        fresh.append(lse)
+    elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (R, Hq, T) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 tensor [R, Hq, T] on q's device")
+    if workspace is None:
+        workspace = torch.empty(_prefix_workspace_bytes(device.index, R, Hq, Hk, T, P, C, d), dtype=torch.uint8,
+                                device=device)
+        fresh.append(workspace)
+    elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    _new_for(stream, *fresh)
+    qp, qs = _view("q", q, q.shape, device)
+    op, os_ = _view("out", out, q.shape, device)
+    st = lib.attn_fwd_prefix(qp, qs, kp, kps, vp, vps, ko, kos, vo, vos, lens, op, os_, lse.data_ptr(), R, Hq, Hk, T,
+                             P, C, d, scale, workspace.data_ptr() or None, workspace.numel(), _raw_stream(stream, q.device))
     _check(st, "attn_fwd_prefix")
     return out, lse
 

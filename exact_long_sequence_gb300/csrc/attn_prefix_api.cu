@@ -29,10 +29,16 @@ int check_shape(const PrefixShape& s) {
     return ATTN_OK;
 }
 
-// Sizes that follow from the shape, and the cut of the prefix: the number of
-// segments with the least estimated time, in the units of the kernel's own
-// work (items in whole waves, each its tiles and a constant), plus what a
-// further segment costs the combine kernel.
+// What the cut of the prefix costs besides its tiles, in the kernel's units of
+// work (a tile of 128 keys is 4, about 1.6 us with two query tiles): a piece's
+// start and end (3 us: its rows, the pipeline's fill, O out), and a partial row
+// written and read back (1 KB at 6 TB/s).
+constexpr double kPlanPiece = 8.0;
+constexpr double kPlanRow = 4.2e-4;
+
+// Sizes that follow from the shape, and the cut of the prefix into the number
+// of stretches with the least estimated time: items in whole waves, each its
+// tiles and its pieces, and the partial rows.
 void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
     p.R = s.R;
     p.T = s.T;
@@ -55,25 +61,25 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
         p.workers = static_cast<int>(ctas < num_sms ? ctas : num_sms) * kOwnWarps;
     }
     p.psegs = 0;
-    p.seg_tiles = 1;
     p.pitems = 0;
     if (p.ptiles > 0) {
-        const int64_t units = static_cast<int64_t>(s.Hk) * p.pblocks;
-        int64_t most = 2 * num_sms / units;
+        const int64_t line = static_cast<int64_t>(s.Hk) * p.ptiles;
+        int64_t most = 2 * num_sms / p.pblocks;
         if (most < 8) most = 8;
-        if (most > p.ptiles) most = p.ptiles;
+        if (most > line) most = line;
+        const double row = kPlanRow * s.R * p.GT;
         double best = 0;
         for (int64_t n = 1; n <= most; ++n) {
-            const int64_t tiles = (p.ptiles + n - 1) / n;
-            const int64_t waves = (units * n + num_sms - 1) / num_sms;
-            const double cost = static_cast<double>(waves) * (kPfxItemCost + tiles * kPfxTileCost) + 0.25 * n;
+            const double waves = static_cast<double>((p.pblocks * n + num_sms - 1) / num_sms);
+            // the most pieces of a stretch: key heads' borders fall on stretches' where they can
+            const double pieces = n % s.Hk == 0 ? 1.0 : static_cast<double>((s.Hk + n - 1) / n + 1);
+            const double cost = waves * (static_cast<double>((line + n - 1) / n) * kPfxTileCost + pieces * kPlanPiece) + row * (n + s.Hk);
             if (n == 1 || cost < best) {
                 best = cost;
-                p.seg_tiles = static_cast<int>(tiles);
+                p.psegs = static_cast<int>(n);
             }
         }
-        p.psegs = (p.ptiles + p.seg_tiles - 1) / p.seg_tiles;
-        p.pitems = static_cast<int>(units * p.psegs);
+        p.pitems = static_cast<int>(p.pblocks * p.psegs);
     }
 }
 
@@ -85,7 +91,7 @@ struct PrefixSpace {
     int64_t own_first;
     PrefixSpace(const PrefixParams& p, int d, int num_sms) {
         const int grid = p.workers > 0 ? p.workers : num_sms;  // who may have a piece of a sequence
-        own_first = static_cast<int64_t>(p.psegs) * p.Hk * p.R * p.GT;
+        own_first = p.psegs == 0 ? 0 : static_cast<int64_t>(p.psegs + p.Hk - 1) * p.R * p.GT;
         const int64_t own = p.C > 0 ? (static_cast<int64_t>(p.R) * p.Hk * p.oblocks + grid) * p.orows : 0;
         start = 0;
         lse = align256(static_cast<size_t>(p.R + 1) * sizeof(int64_t));
@@ -153,7 +159,7 @@ int launch(DeviceState& dev, const CUtensorMap (&maps)[6], const PrefixParams& p
     // a row's pieces are dealt to as many warps (1, 2, 4, 8) as there are pieces for and as
     // the SMs hold at once (32 each)
     const int64_t rows = static_cast<int64_t>(p.R) * p.Hk * p.GT;
-    const int pieces = p.psegs + (p.C > 0 ? 1 : 0);
+    const int pieces = (p.psegs + p.Hk - 1) / p.Hk + (p.C > 0 ? 1 : 0);  // about
     int warps = 1;
     while (warps < 8 && warps < pieces && rows * warps * 2 <= 32ll * dev.num_sms) warps *= 2;
     cfg.gridDim = dim3(static_cast<unsigned>((rows * warps + 7) / 8));

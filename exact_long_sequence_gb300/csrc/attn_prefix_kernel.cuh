@@ -66,11 +66,12 @@ struct PrefixParams {
     int P, C;               // prefix keys; own capacity
     int qrows;              // rows of a query tile: the whole requests that fit 128 rows, or 128 if one does not
     int pblocks;            // blocks of two query tiles over R GT
-    int ptiles, psegs, seg_tiles;  // prefix tiles; cut into psegs runs of seg_tiles
-    int pitems;             // Hk * psegs * pblocks
+    int ptiles;             // prefix tiles of a key head
+    int psegs;              // the line of all key heads' tiles is cut into so many even stretches
+    int pitems;             // psegs * pblocks (a stretch at one row block, at one or more key heads)
     int oblocks;            // blocks of two query tiles over GT
     int orows;              // rows of an own slot: min(GT, 2 qrows)
-    float* part_o;          // partial rows [.., d] fp32: first [psegs][Hk][R GT], then [own slots][orows]
+    float* part_o;          // partial rows [.., d] fp32: first [psegs + Hk - 1][R GT], then [own slots][orows]
     float* part_lse;        // one per partial row
     int64_t own_first;      // the first own slot's partial row
     int64_t* own_start;     // [R + 1]: where each request's own work starts, and the total
@@ -92,7 +93,7 @@ struct OwnCut {
     int64_t rem, cap1, cap0;
     __device__ __forceinline__ OwnCut(const PrefixParams& p, int64_t total, int grid) {
         rem = p.pitems % grid;
-        const int64_t item = kPfxItemCost + static_cast<int64_t>(p.seg_tiles) * kPfxTileCost;
+        const int64_t item = p.psegs == 0 ? 0 : kPfxItemCost + (static_cast<int64_t>(p.Hk) * p.ptiles + p.psegs - 1) / p.psegs * kPfxTileCost;
         const int64_t level = item * (grid - rem);  // what evens the CTAs out
         if (rem == 0 || total > level) {
             const int64_t e = (total - (rem == 0 ? 0 : level) + grid - 1) / grid;
@@ -125,6 +126,21 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
         if (lane >= off) v += o;
     }
     return v;
+}
+
+// The prefix: one line of Hk * ptiles tiles, stretch k holding the tiles
+// [k W / psegs, (k + 1) W / psegs).  A stretch's tiles at one key head are a
+// piece; pieces in order step either to the next stretch or to the next head
+// (or both), so stretch + head numbers them apart.  The row blocks of a
+// stretch are neighbouring items, which run at the same time and share its K/V in L2.
+__device__ __forceinline__ int64_t stretch_begin(const PrefixParams& p, int k) {
+    return static_cast<int64_t>(k) * p.Hk * p.ptiles / p.psegs;
+}
+__device__ __forceinline__ int stretch_of(const PrefixParams& p, int64_t tile) {
+    return static_cast<int>(((tile + 1) * p.psegs - 1) / (static_cast<int64_t>(p.Hk) * p.ptiles));
+}
+__device__ __forceinline__ int64_t prefix_part(const PrefixParams& p, int k, int head) {
+    return static_cast<int64_t>(k + head) * p.R * p.GT;
 }
 
 struct PrefixItem {
@@ -564,17 +580,19 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
         PrefixItem it;
         it.pad = 0;
         for (int i = blockIdx.x; i < p.pitems && ok; i += gridDim.x) {
-            const int blk = i % p.pblocks, hs = i / p.pblocks;
-            const int seg = hs % p.psegs;
-            it.head = hs / p.psegs;
+            const int blk = i % p.pblocks, k = i / p.pblocks;
             it.req = -1;
             it.klen = p.P;
-            it.tile0 = seg * p.seg_tiles;
-            it.ntiles = min(p.seg_tiles, p.ptiles - it.tile0);
             it.row0 = blk * 2 * p.qrows;
             it.nrows = min(2 * p.qrows, p.R * p.GT - it.row0);
-            it.part = (static_cast<int64_t>(seg) * p.Hk + it.head) * p.R * p.GT + it.row0;
-            publish(it);
+            const int64_t end = stretch_begin(p, k + 1);
+            for (int64_t x = stretch_begin(p, k); x < end && ok; x += it.ntiles) {
+                it.head = static_cast<int>(x / p.ptiles);
+                it.tile0 = static_cast<int>(x - static_cast<int64_t>(it.head) * p.ptiles);
+                it.ntiles = static_cast<int>(min(end - x, static_cast<int64_t>(p.ptiles - it.tile0)));
+                it.part = prefix_part(p, k, it.head) + it.row0;
+                publish(it);
+            }
         }
         if (p.lens && p.workers == 0 && ok) {
             // The total and the lane whose run of requests holds this CTA's first unit.
@@ -1367,9 +1385,15 @@ __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_c
     const int h = rem / p.GT, x = rem - h * p.GT;  // key head, row within the request
     const int raw_len = p.lens ? __ldg(p.lens + r) : 0;  // an input: no need to wait for it
     const bool on = row < rows && raw_len >= 0;
-    const int segs = p.P > 0 ? p.psegs : 0;
-    const int64_t pstep = static_cast<int64_t>(p.Hk) * p.R * p.GT;
-    const int64_t pfirst = (static_cast<int64_t>(h) * p.R + r) * p.GT + x;
+    const int64_t pstep = static_cast<int64_t>(p.R) * p.GT;
+    int segs = 0;
+    int64_t pfirst = 0;
+    if (p.P > 0) {
+        const int64_t tile = static_cast<int64_t>(h) * p.ptiles;
+        const int k0 = stretch_of(p, tile);
+        segs = stretch_of(p, tile + p.ptiles - 1) - k0 + 1;
+        pfirst = prefix_part(p, k0, h) + static_cast<int64_t>(r) * p.GT + x;
+    }
     int64_t ofirst = 0;
     int pieces = on ? segs : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");

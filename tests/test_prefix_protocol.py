@@ -31,19 +31,19 @@ class Layout:
         self.two = 2 * (128 // self.GT * self.GT if self.GT <= 128 else 128)  # rows of two query tiles
         self.pblocks, self.oblocks = cdiv(R * self.GT, self.two), cdiv(self.GT, self.two)
         self.orows = min(self.GT, self.two)
-        self.psegs, self.seg_tiles, self.pitems = 0, 1, 0
+        self.psegs, self.pitems = 0, 0
+        self.line = Hk * self.ptiles
         if self.ptiles:
-            units = Hk * self.pblocks
-            most = min(max(2 * grid // units, 8), self.ptiles)
+            most = min(max(2 * grid // self.pblocks, 8), self.line)
             best = None
             for n in range(1, most + 1):
-                tiles = cdiv(self.ptiles, n)
-                cost = cdiv(units * n, grid) * (ITEM + tiles * TILE) + 0.25 * n
+                pieces = 1 if n % Hk == 0 else cdiv(Hk, n) + 1
+                cost = (cdiv(self.pblocks * n, grid) * (cdiv(self.line, n) * TILE + pieces * 8.0) +
+                        4.2e-4 * R * self.GT * (n + Hk))
                 if best is None or cost < best:
-                    best, self.seg_tiles = cost, tiles
-            self.psegs = cdiv(self.ptiles, self.seg_tiles)
-            self.pitems = units * self.psegs
-        self.own_first = self.psegs * Hk * R * self.GT
+                    best, self.psegs = cost, n
+            self.pitems = self.pblocks * self.psegs
+        self.own_first = (self.psegs + Hk - 1) * R * self.GT if self.psegs else 0
         self.rows = self.own_first + ((R * Hk * self.oblocks + grid) * self.orows if C else 0)
 
     def seq_cost(self, n):
@@ -54,7 +54,7 @@ class Cut:
     def __init__(self, L, total):
         g = L.grid
         self.rem = L.pitems % g
-        item = ITEM + L.seg_tiles * TILE
+        item = ITEM + cdiv(L.line, L.psegs) * TILE if L.psegs else 0
         level = item * (g - self.rem)
         if self.rem == 0 or total > level:
             e = cdiv(total - (0 if self.rem == 0 else level), g)
@@ -76,12 +76,15 @@ def schedule(L, lens, cta):
     """The items of one CTA: (req, head, row0, nrows, tile0, ntiles, first partial row)."""
     out = []
     for i in range(cta, L.pitems, L.grid):
-        blk, hs = i % L.pblocks, i // L.pblocks
-        seg, head = hs % L.psegs, hs // L.psegs
-        t0 = seg * L.seg_tiles
+        blk, k = i % L.pblocks, i // L.pblocks
         row0 = blk * L.two
-        out.append((-1, head, row0, min(L.two, L.R * L.GT - row0), t0, min(L.seg_tiles, L.ptiles - t0),
-                    (seg * L.Hk + head) * L.R * L.GT + row0))
+        x, end = k * L.line // L.psegs, (k + 1) * L.line // L.psegs
+        while x < end:
+            head = x // L.ptiles
+            t0 = x - head * L.ptiles
+            n = min(end - x, L.ptiles - t0)
+            out.append((-1, head, row0, min(L.two, L.R * L.GT - row0), t0, n, (k + head) * L.R * L.GT + row0))
+            x += n
     if not L.C:
         return out
     lens = [min(max(n, 0), L.C) for n in lens]
@@ -118,7 +121,10 @@ def schedule(L, lens, cta):
 
 def combine_rows(L, lens, r, h, x):
     """The partial rows the combine kernel merges for row x of request r at key head h."""
-    rows = [(s * L.Hk + h) * L.R * L.GT + r * L.GT + x for s in range(L.psegs)]
+    rows = []
+    if L.ptiles:
+        first, last = (((t + 1) * L.psegs - 1) // L.line for t in (h * L.ptiles, (h + 1) * L.ptiles - 1))
+        rows = [(k + h) * L.R * L.GT + r * L.GT + x for k in range(first, last + 1)]
     n = min(lens[r], L.C) if L.C else 0
     if n > 0:
         seqs = L.Hk * L.oblocks
