@@ -63,20 +63,20 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
     p.psegs = 0;
     p.pitems = 0;
     if (p.ptiles > 0) {
-        const int64_t line = static_cast<int64_t>(s.Hk) * p.ptiles;
-        int64_t most = 2 * num_sms / p.pblocks;
-        if (most < 8) most = 8;
-        if (most > line) most = line;
+        // (in floating point: the quotients are small and this is on every call's path)
+        const double line = static_cast<double>(s.Hk) * p.ptiles, blocks = p.pblocks, sms = num_sms, heads = s.Hk;
+        const int most = static_cast<int>(std::fmin(line, std::fmax(8.0, std::floor(2.0 * sms / blocks))));
         const double row = kPlanRow * s.R * p.GT;
         double best = 0;
-        for (int64_t n = 1; n <= most; ++n) {
-            const double waves = static_cast<double>((p.pblocks * n + num_sms - 1) / num_sms);
+        int rest = 0;  // n modulo the key heads
+        for (int n = 1; n <= most; ++n) {
+            rest = rest + 1 == s.Hk ? 0 : rest + 1;
             // the most pieces of a stretch: key heads' borders fall on stretches' where they can
-            const double pieces = n % s.Hk == 0 ? 1.0 : static_cast<double>((s.Hk + n - 1) / n + 1);
-            const double cost = waves * (static_cast<double>((line + n - 1) / n) * kPfxTileCost + pieces * kPlanPiece) + row * (n + s.Hk);
+            const double pieces = rest == 0 ? 1.0 : std::ceil(heads / n) + 1.0;
+            const double cost = std::ceil(blocks * n / sms) * (std::ceil(line / n) * kPfxTileCost + pieces * kPlanPiece) + row * (n + heads);
             if (n == 1 || cost < best) {
                 best = cost;
-                p.psegs = static_cast<int>(n);
+                p.psegs = n;
             }
         }
         p.pitems = static_cast<int>(p.pblocks * p.psegs);
