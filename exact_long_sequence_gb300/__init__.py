@@ -378,14 +378,14 @@ _BF16 = torch.bfloat16
 _pack2, _pack3 = struct.Struct("2q").pack, struct.Struct("3q").pack
 
 
-def _elsewhere(device) -> bool:
-    """Whether another device than `device` is current (the library works on the current one)."""
-    return torch.cuda.current_device() != device.index
+def _elsewhere(index) -> bool:
+    """Whether another device than `index` is current (the library works on the current one)."""
+    return torch.cuda.current_device() != index
 
 
-def _raw_stream(stream, device):
+def _raw_stream(stream, index):
     """The handle of `stream`, or of the device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _new_for(stream, *tensors):
@@ -395,14 +395,17 @@ def _new_for(stream, *tensors):
             t.record_stream(stream)
 
 
-def _view(name, t, shape, device):
-    """Checks a [B, H, N, d] bf16 view; returns its address and its three strides as the C call's host array."""
-    if t.dtype is not _BF16 or t.device != device or t.shape != shape:
+def _view(name, t, shape, index):
+    """Checks a bf16 view with its last axis contiguous; returns its address and the other axes' strides
+    as the C call's host array (None: contiguous)."""
+    if t.dtype is not _BF16 or t.get_device() != index or t.shape != shape:
         raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on q's device")
-    s0, s1, s2, s3 = t.stride()
-    if s3 != 1:
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    s = t.stride()
+    if s[-1] != 1:
         raise ValueError(f"{name} must have its last axis contiguous")
-    return t.data_ptr(), _pack3(s0, s1, s2)
+    return t.data_ptr(), _pack3(*s[:3]) if len(s) == 4 else _pack2(*s[:2])
 
 
 def _rotation(q, k, positions, inv_freq, sections, weights):
@@ -410,18 +413,18 @@ def _rotation(q, k, positions, inv_freq, sections, weights):
     number, the positions [axes, B or 1, N], and their axis and batch strides."""
     if q.dim() != 4 or k.dim() != 4 or not q.is_cuda:
         raise ValueError("q and k must be CUDA tensors [B, H, N, d]")
-    device = q.device
+    index = q.get_device()
     B, _, N, d = q.shape
     kB, _, kN, kd = k.shape
     if kB != B or kN != N or kd != d:
         raise ValueError("q and k must share B, N and d")
-    if inv_freq.dtype != torch.float64 or inv_freq.device != device or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype != torch.float64 or inv_freq.get_device() != index or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 tensor of one axis on q's device")
     if sections is None:
         sections = (inv_freq.shape[0],)
     if sum(sections) != inv_freq.shape[0]:
         raise ValueError("sections must add up to the number of frequencies")
-    if positions.dtype != torch.int32 or positions.device != device:
+    if positions.dtype != torch.int32 or positions.get_device() != index:
         raise ValueError("positions must be an int32 tensor on q's device")
     A = len(sections)
     while positions.dim() < 3 and (positions.dim() < 2 or A == 1):  # [N] or [B, N]: one axis
@@ -432,7 +435,7 @@ def _rotation(q, k, positions, inv_freq, sections, weights):
     if N > 1 and pn != 1:
         raise ValueError("positions must be contiguous along the tokens")
     for w in weights:
-        if w is not None and (w.dtype != torch.bfloat16 or w.device != device or w.shape != (d,) or
+        if w is not None and (w.dtype != torch.bfloat16 or w.get_device() != index or w.shape != (d,) or
                               not w.is_contiguous()):
             raise ValueError("norm weights must be contiguous bf16 tensors [d] on q's device")
     return (ctypes.c_int * A)(*sections), A, positions, pa, 0 if positions.shape[1] == 1 else pb
@@ -456,8 +459,9 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, sectio
     sec, A, positions, pa, pb = _rotation(q, k, positions, inv_freq, sections, (q_weight, k_weight))
     B, Hq, N, d = q.shape
     Hk = k.shape[1]
-    if _elsewhere(q.device):
-        with torch.cuda.device(q.device):
+    index = q.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
             return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, sections, eps, interleaved, q_out, k_out,
                                 stream)
     fresh = []
@@ -468,15 +472,14 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, sectio
         k_out = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
         fresh.append(k_out)
     _new_for(stream, *fresh)
-    dev = q.device
-    qp, qs = _view("q", q, q.shape, dev)
-    kp, ks = _view("k", k, k.shape, dev)
-    qop, qos = _view("q_out", q_out, q.shape, dev)
-    kop, kos = _view("k_out", k_out, k.shape, dev)
+    qp, qs = _view("q", q, q.shape, index)
+    kp, ks = _view("k", k, k.shape, index)
+    qop, qos = _view("q_out", q_out, q.shape, index)
+    kop, kos = _view("k_out", k_out, k.shape, index)
     st = lib.attn_qk_norm_rope(qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
                                None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb,
                                inv_freq.data_ptr(), sec, A, qop, qos, kop, kos, B, Hq, Hk, N, d, eps,
-                               1 if interleaved else 0, _raw_stream(stream, q.device))
+                               1 if interleaved else 0, _raw_stream(stream, index))
     _check(st, "attn_qk_norm_rope")
     return q_out, k_out
 
@@ -503,8 +506,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k
     sec, A, positions, pa, pb = _rotation(q, k, positions, inv_freq, sections, (q_weight, k_weight))
     B, Hq, N, d = q.shape
     Hk = k.shape[1]
-    if _elsewhere(q.device):
-        with torch.cuda.device(q.device):
+    index = q.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
             return qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight, sections, eps,
                                     interleaved, dq, dk, workspace, stream)
     fresh = []
@@ -518,25 +522,24 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k
     dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
     fresh += [t for t in (dwq, dwk) if t is not None]
     if workspace is None and (dwq is not None or dwk is not None):
-        workspace = torch.empty(_bwd_workspace_bytes(q.device.index, d), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(_bwd_workspace_bytes(index, d), dtype=torch.uint8, device=q.device)
         fresh.append(workspace)
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != q.device or
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.get_device() != index or
                                   not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     _new_for(stream, *fresh)
-    dev = q.device
-    gqp, gqs = _view("dq_out", dq_out, q.shape, dev)
-    gkp, gks = _view("dk_out", dk_out, k.shape, dev)
-    qp, qs = _view("q", q, q.shape, dev)
-    kp, ks = _view("k", k, k.shape, dev)
-    dqp, dqs = _view("dq", dq, q.shape, dev)
-    dkp, dks = _view("dk", dk, k.shape, dev)
+    gqp, gqs = _view("dq_out", dq_out, q.shape, index)
+    gkp, gks = _view("dk_out", dk_out, k.shape, index)
+    qp, qs = _view("q", q, q.shape, index)
+    kp, ks = _view("k", k, k.shape, index)
+    dqp, dqs = _view("dq", dq, q.shape, index)
+    dkp, dks = _view("dk", dk, k.shape, index)
     st = lib.attn_qk_norm_rope_bwd(
         gqp, gqs, gkp, gks, qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
         None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb, inv_freq.data_ptr(), sec, A,
         dqp, dqs, dkp, dks, None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
         B, Hq, Hk, N, d, eps, 1 if interleaved else 0, None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _raw_stream(stream, q.device))
+        0 if workspace is None else workspace.numel(), _raw_stream(stream, index))
     _check(st, "attn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -569,7 +572,7 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
     lib = load_library()
     if q.dim() != 4 or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [R, Hq, T, d]")
-    device = q.device
+    index = q.get_device()
     R, Hq, T, d = q.shape
     P = C = 0
     kp = vp = ko = vo = lens = kps = vps = kos = vos = None
@@ -580,47 +583,44 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
         if k_prefix.dim() != 3 or v_prefix is None:
             raise ValueError("k_prefix and v_prefix must be [Hk, P, d]")
         P = k_prefix.shape[1]
-        for t in (k_prefix, v_prefix):
-            if t.dtype != torch.bfloat16 or t.device != device or t.shape != (Hk, P, d) or t.stride(2) != 1:
-                raise ValueError("k_prefix and v_prefix must be bf16 [Hk, P, d] on q's device, d contiguous")
-        kp, vp = k_prefix.data_ptr(), v_prefix.data_ptr()
-        kps, vps = _pack2(*k_prefix.stride()[:2]), _pack2(*v_prefix.stride()[:2])
+        kp, kps = _view("k_prefix", k_prefix, (Hk, P, d), index)
+        vp, vps = _view("v_prefix", v_prefix, (Hk, P, d), index)
     if k_own is not None:
         if k_own.dim() != 4 or v_own is None or own_lens is None:
             raise ValueError("own keys need k_own and v_own [R, Hk, C, d] and own_lens")
         C = k_own.shape[2]
-        if own_lens.dtype != torch.int32 or own_lens.device != device or own_lens.shape != (R,) or \
+        if own_lens.dtype != torch.int32 or own_lens.get_device() != index or own_lens.shape != (R,) or \
                 not own_lens.is_contiguous():
             raise ValueError("own_lens must be a contiguous int32 tensor [R] on q's device")
         shape = (R, Hk, C, d)
-        ko, kos = _view("k_own", k_own, shape, device)
-        vo, vos = _view("v_own", v_own, shape, device)
+        ko, kos = _view("k_own", k_own, shape, index)
+        vo, vos = _view("v_own", v_own, shape, index)
         lens = own_lens.data_ptr()
     if scale is None:
         scale = _SCALES.get(d) or default_scale(d)
-    if _elsewhere(device):
-        with torch.cuda.device(device):
+    if _elsewhere(index):
+        with torch.cuda.device(index):
             return attn_fwd_prefix(q, k_prefix, v_prefix, k_own, v_own, own_lens, scale, out, lse, workspace, stream)
     fresh = []
     if out is None:
-        out = torch.empty((R, Hq, T, d), dtype=torch.bfloat16, device=device)
+        out = torch.empty((R, Hq, T, d), dtype=torch.bfloat16, device=q.device)
         fresh.append(out)
     if lse is None:
-        lse = torch.empty((R, Hq, T), dtype=torch.float32, device=device)
+        lse = torch.empty((R, Hq, T), dtype=torch.float32, device=q.device)
         fresh.append(lse)
-    elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (R, Hq, T) or not lse.is_contiguous():
+    elif lse.dtype != torch.float32 or lse.get_device() != index or lse.shape != (R, Hq, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [R, Hq, T] on q's device")
     if workspace is None:
-        workspace = torch.empty(_prefix_workspace_bytes(device.index, R, Hq, Hk, T, P, C, d), dtype=torch.uint8,
-                                device=device)
+        workspace = torch.empty(_prefix_workspace_bytes(index, R, Hq, Hk, T, P, C, d), dtype=torch.uint8,
+                                device=q.device)
         fresh.append(workspace)
-    elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+    elif workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     _new_for(stream, *fresh)
-    qp, qs = _view("q", q, q.shape, device)
-    op, os_ = _view("out", out, q.shape, device)
+    qp, qs = _view("q", q, q.shape, index)
+    op, os_ = _view("out", out, q.shape, index)
     st = lib.attn_fwd_prefix(qp, qs, kp, kps, vp, vps, ko, kos, vo, vos, lens, op, os_, lse.data_ptr(), R, Hq, Hk, T,
-                             P, C, d, scale, workspace.data_ptr() or None, workspace.numel(), _raw_stream(stream, q.device))
+                             P, C, d, scale, workspace.data_ptr() or None, workspace.numel(), _raw_stream(stream, index))
     _check(st, "attn_fwd_prefix")
     return out, lse
 
