@@ -589,12 +589,13 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
         if k_own.dim() != 4 or v_own is None or own_lens is None:
             raise ValueError("own keys need k_own and v_own [R, Hk, C, d] and own_lens")
         C = k_own.shape[2]
-        if own_lens.dtype != torch.int32 or own_lens.get_device() != index or own_lens.shape != (R,) or \
-                not own_lens.is_contiguous():
-            raise ValueError("own_lens must be a contiguous int32 tensor [R] on q's device")
         shape = (R, Hk, C, d)
         ko, kos = _view("k_own", k_own, shape, index)
         vo, vos = _view("v_own", v_own, shape, index)
+    if own_lens is not None:
+        if own_lens.dtype != torch.int32 or own_lens.get_device() != index or own_lens.shape != (R,) or \
+                not own_lens.is_contiguous():
+            raise ValueError("own_lens must be a contiguous int32 tensor [R] on q's device")
         lens = own_lens.data_ptr()
     if scale is None:
         scale = _SCALES.get(d) or default_scale(d)

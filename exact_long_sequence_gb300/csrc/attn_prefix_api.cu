@@ -26,6 +26,11 @@ int check_shape(const PrefixShape& s) {
     if (static_cast<long long>(s.R) * s.Hq >= (1LL << 31) || static_cast<long long>(s.R) * s.Hq * s.T >= (1LL << 31))
         return ATTN_ERR_INVALID_ARG;
     if (s.d != 64 && s.d != 128) return ATTN_ERR_UNSUPPORTED;
+    // the kernels count tiles and steps of work in 32 bits (2^31 of them would not fit device memory)
+    const double heads = s.Hk, blocks = std::ceil(static_cast<double>(s.Hq / s.Hk) * s.T / kBr);
+    if (heads * (static_cast<double>(s.P) / kBc + 1) >= 1073741824.0 ||
+        s.R * heads * blocks * (static_cast<double>(s.C) / kOwnStep + kPfxItemCost + 1) >= 1073741824.0)
+        return ATTN_ERR_INVALID_ARG;
     return ATTN_OK;
 }
 
@@ -62,6 +67,8 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
     }
     p.psegs = 0;
     p.pitems = 0;
+    p.cut_len = p.cut_per = p.cut_base = 1;
+    p.cut_rem = 0;
     if (p.ptiles > 0) {
         // (in floating point: the quotients are small and this is on every call's path)
         const double line = static_cast<double>(s.Hk) * p.ptiles, blocks = p.pblocks, sms = num_sms, heads = s.Hk;
@@ -79,13 +86,18 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
                 p.psegs = n;
             }
         }
-        p.pitems = static_cast<int>(p.pblocks * p.psegs);
+        p.pitems = p.pblocks * p.psegs;
+        const bool by_head = p.psegs % s.Hk == 0;
+        p.cut_len = by_head ? p.ptiles : p.ptiles * s.Hk;
+        p.cut_per = by_head ? p.psegs / s.Hk : p.psegs;
+        p.cut_base = p.cut_len / p.cut_per;
+        p.cut_rem = p.cut_len % p.cut_per;
     }
 }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// Workspace: [R + 1 int64][log-sum-exp of the partial rows][partial rows].
+// Workspace: [R + 1 int][log-sum-exp of the partial rows][partial rows].
 struct PrefixSpace {
     size_t start, lse, rows, bytes;
     int64_t own_first;
@@ -94,7 +106,7 @@ struct PrefixSpace {
         own_first = p.psegs == 0 ? 0 : static_cast<int64_t>(p.psegs + p.Hk - 1) * p.R * p.GT;
         const int64_t own = p.C > 0 ? (static_cast<int64_t>(p.R) * p.Hk * p.oblocks + grid) * p.orows : 0;
         start = 0;
-        lse = align256(static_cast<size_t>(p.R + 1) * sizeof(int64_t));
+        lse = align256((static_cast<size_t>(p.R) + 1) * sizeof(int));
         rows = lse + align256(static_cast<size_t>(own_first + own) * sizeof(float));
         bytes = rows + static_cast<size_t>(own_first + own) * d * sizeof(float);
     }
@@ -149,7 +161,9 @@ int launch(DeviceState& dev, const CUtensorMap (&maps)[6], const PrefixParams& p
         cfg.numAttrs = 1;
     }
     if (p.workers == 0 || p.pitems > 0) {
-        const int grid = p.workers > 0 && p.pitems < dev.num_sms ? p.pitems : dev.num_sms;
+        // with own items, a CTA per SM (their cut counts on it); else no more than there are items
+        const bool own_items = p.C > 0 && p.workers == 0;
+        const int grid = !own_items && p.pitems < dev.num_sms ? p.pitems : dev.num_sms;
         cfg.gridDim = dim3(static_cast<unsigned>(grid));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = smem;
@@ -200,7 +214,7 @@ extern "C" int attn_fwd_prefix(const void* Q, const int64_t* q_strides, const vo
     if ((P > 0 && (!Kp || !Vp)) || (C > 0 && (!Ko || !Vo || !own_lens))) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(Q) || !aligned16(O) || (reinterpret_cast<uintptr_t>(LSE) & 3u) != 0 ||
         (P > 0 && (!aligned16(Kp) || !aligned16(Vp))) ||
-        (C > 0 && (!aligned16(Ko) || !aligned16(Vo) || (reinterpret_cast<uintptr_t>(own_lens) & 3u) != 0)))
+        (reinterpret_cast<uintptr_t>(own_lens) & 3u) != 0 || (C > 0 && (!aligned16(Ko) || !aligned16(Vo))))
         return ATTN_ERR_MISALIGNED;
     if (!workspace) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
@@ -255,8 +269,8 @@ extern "C" int attn_fwd_prefix(const void* Q, const int64_t* q_strides, const vo
     p.q = static_cast<const __nv_bfloat16*>(Q);
     p.o = static_cast<__nv_bfloat16*>(O);
     p.lse = LSE;
-    p.lens = C > 0 ? own_lens : nullptr;
-    p.own_start = reinterpret_cast<int64_t*>(ws + space.start);
+    p.lens = own_lens;
+    p.own_start = reinterpret_cast<int*>(ws + space.start);
     p.part_lse = reinterpret_cast<float*>(ws + space.lse);
     p.part_o = reinterpret_cast<float*>(ws + space.rows);
     p.own_first = space.own_first;

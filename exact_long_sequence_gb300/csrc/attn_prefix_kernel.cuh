@@ -60,21 +60,23 @@ struct PrefixParams {
     __nv_bfloat16* o;
     int64_t os[3];
     float* lse;             // [R, Hq, T]
-    const int32_t* lens;    // [R] own keys, the new tokens among them; nullptr: none
+    const int32_t* lens;    // [R] own keys, the new tokens among them (negative: padding); nullptr: none
     int R, T, Hk, G;
     int GT;                 // rows of a request at one key head
     int P, C;               // prefix keys; own capacity
     int qrows;              // rows of a query tile: the whole requests that fit 128 rows, or 128 if one does not
     int pblocks;            // blocks of two query tiles over R GT
     int ptiles;             // prefix tiles of a key head
-    int psegs;              // the line of all key heads' tiles is cut into so many even stretches
+    int psegs;              // the line of all key heads' tiles is cut into so many even stretches:
+    int cut_len, cut_per;   // ... each run of cut_len tiles (a head's, or the whole line) into cut_per of them,
+    int cut_base, cut_rem;  // ... the first cut_rem of cut_base + 1 tiles, the others of cut_base
     int pitems;             // psegs * pblocks (a stretch at one row block, at one or more key heads)
     int oblocks;            // blocks of two query tiles over GT
     int orows;              // rows of an own slot: min(GT, 2 qrows)
     float* part_o;          // partial rows [.., d] fp32: first [psegs + Hk - 1][R GT], then [own slots][orows]
     float* part_lse;        // one per partial row
     int64_t own_first;      // the first own slot's partial row
-    int64_t* own_start;     // [R + 1]: where each request's own work starts, and the total
+    int* own_start;         // [R + 1]: where each request's own work starts, and the total
     int workers;            // warps of attn_prefix_own_kernel, which then does the own work; 0: it is items of the prefix kernel
     uint32_t* error_word;
     uint64_t timeout_ns;
@@ -89,14 +91,15 @@ struct PrefixParams {
 // A tile belongs to the CTA whose stretch holds the tile's first unit.  Caps
 // are 0 or at least a tile, so every CTA between the first and the last of a
 // sequence has a tile of it.
+// (All counts of work fit 32 bits: the host refuses shapes whose do not.)
 struct OwnCut {
-    int64_t rem, cap1, cap0;
-    __device__ __forceinline__ OwnCut(const PrefixParams& p, int64_t total, int grid) {
+    int rem, cap1, cap0;
+    __device__ __forceinline__ OwnCut(const PrefixParams& p, int total, int grid) {
         rem = p.pitems % grid;
-        const int64_t item = p.psegs == 0 ? 0 : kPfxItemCost + (static_cast<int64_t>(p.Hk) * p.ptiles + p.psegs - 1) / p.psegs * kPfxTileCost;
-        const int64_t level = item * (grid - rem);  // what evens the CTAs out
+        const int item = p.psegs == 0 ? 0 : kPfxItemCost + (p.cut_base + (p.cut_rem > 0 ? 1 : 0)) * kPfxTileCost;
+        const int64_t level = static_cast<int64_t>(item) * (grid - rem);  // what evens the CTAs out
         if (rem == 0 || total > level) {
-            const int64_t e = (total - (rem == 0 ? 0 : level) + grid - 1) / grid;
+            const int e = (total - (rem == 0 ? 0 : static_cast<int>(level)) + grid - 1) / grid;
             cap1 = e;
             cap0 = rem == 0 ? e : item + e;
         } else {
@@ -106,38 +109,44 @@ struct OwnCut {
         if (cap1 > 0 && cap1 < kPfxTileCost) cap1 = kPfxTileCost;
         if (cap0 < kPfxTileCost) cap0 = kPfxTileCost;
     }
-    __device__ __forceinline__ int64_t begin(int64_t cta) const {
-        return cta < rem ? cta * cap1 : rem * cap1 + (cta - rem) * cap0;
+    // (the last stretches may begin past the line's end, and past 32 bits)
+    __device__ __forceinline__ int64_t begin(int cta) const {
+        return cta < rem ? static_cast<int64_t>(cta) * cap1
+                         : static_cast<int64_t>(rem) * cap1 + static_cast<int64_t>(cta - rem) * cap0;
     }
-    __device__ __forceinline__ int64_t cta_of(int64_t x) const {
+    __device__ __forceinline__ int cta_of(int x) const {
         return x < rem * cap1 ? x / cap1 : rem + (x - rem * cap1) / cap0;
     }
 };
 __device__ __forceinline__ int own_len(const PrefixParams& p, int r) { return min(max(__ldg(p.lens + r), 0), p.C); }
 // Units of one sequence of a request with `len` own keys (0: no work), and of the request.
-__device__ __forceinline__ int64_t seq_cost(int len) { return len > 0 ? kPfxItemCost + (len + 31) / 32 : 0; }
-__device__ __forceinline__ int64_t request_cost(const PrefixParams& p, int len) { return seq_cost(len) * (p.Hk * p.oblocks); }
+__device__ __forceinline__ int seq_cost(int len) { return len > 0 ? kPfxItemCost + (len + 31) / 32 : 0; }
+__device__ __forceinline__ int request_cost(const PrefixParams& p, int len) { return seq_cost(len) * (p.Hk * p.oblocks); }
 
 // Inclusive sum over the warp's lanes.
-__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+__device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
+        const int o = __shfl_up_sync(0xffffffffu, v, off);
         if (lane >= off) v += o;
     }
     return v;
 }
 
-// The prefix: one line of Hk * ptiles tiles, stretch k holding the tiles
-// [k W / psegs, (k + 1) W / psegs).  A stretch's tiles at one key head are a
-// piece; pieces in order step either to the next stretch or to the next head
-// (or both), so stretch + head numbers them apart.  The row blocks of a
-// stretch are neighbouring items, which run at the same time and share its K/V in L2.
-__device__ __forceinline__ int64_t stretch_begin(const PrefixParams& p, int k) {
-    return static_cast<int64_t>(k) * p.Hk * p.ptiles / p.psegs;
+// The prefix: one line of Hk * ptiles tiles, cut into even stretches (within
+// each head where their number allows it, so that no stretch crosses heads).  A
+// stretch's tiles at one key head are a piece; pieces in order step either to
+// the next stretch or to the next head (or both), so stretch + head numbers
+// them apart.  The row blocks of a stretch are neighbouring items, which run at
+// the same time and share its K/V in L2.
+__device__ __forceinline__ int stretch_begin(const PrefixParams& p, int k) {
+    const int run = k / p.cut_per, i = k - run * p.cut_per;
+    return run * p.cut_len + i * p.cut_base + min(i, p.cut_rem);
 }
-__device__ __forceinline__ int stretch_of(const PrefixParams& p, int64_t tile) {
-    return static_cast<int>(((tile + 1) * p.psegs - 1) / (static_cast<int64_t>(p.Hk) * p.ptiles));
+__device__ __forceinline__ int stretch_of(const PrefixParams& p, int tile) {
+    const int run = tile / p.cut_len, y = tile - run * p.cut_len;
+    const int longer = p.cut_rem * (p.cut_base + 1);  // tiles of the longer stretches
+    return run * p.cut_per + (y < longer ? y / (p.cut_base + 1) : p.cut_rem + (y - longer) / p.cut_base);
 }
 __device__ __forceinline__ int64_t prefix_part(const PrefixParams& p, int k, int head) {
     return static_cast<int64_t>(k + head) * p.R * p.GT;
@@ -280,7 +289,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
             tma_prefetch_desc(&tmap_kp);
             tma_prefetch_desc(&tmap_vp);
         }
-        if (p.lens && p.workers == 0) {
+        if (p.C > 0 && p.workers == 0) {
             tma_prefetch_desc(&tmap_ko);
             tma_prefetch_desc(&tmap_vo);
         }
@@ -585,47 +594,48 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
             it.klen = p.P;
             it.row0 = blk * 2 * p.qrows;
             it.nrows = min(2 * p.qrows, p.R * p.GT - it.row0);
-            const int64_t end = stretch_begin(p, k + 1);
-            for (int64_t x = stretch_begin(p, k); x < end && ok; x += it.ntiles) {
-                it.head = static_cast<int>(x / p.ptiles);
-                it.tile0 = static_cast<int>(x - static_cast<int64_t>(it.head) * p.ptiles);
-                it.ntiles = static_cast<int>(min(end - x, static_cast<int64_t>(p.ptiles - it.tile0)));
+            const int end = stretch_begin(p, k + 1);
+            for (int x = stretch_begin(p, k); x < end && ok; x += it.ntiles) {
+                it.head = x / p.ptiles;
+                it.tile0 = x - it.head * p.ptiles;
+                it.ntiles = min(end - x, p.ptiles - it.tile0);
                 it.part = prefix_part(p, k, it.head) + it.row0;
                 publish(it);
             }
         }
-        if (p.lens && p.workers == 0 && ok) {
+        if (p.C > 0 && p.workers == 0 && ok) {
             // The total and the lane whose run of requests holds this CTA's first unit.
             const int run = (p.R + 31) / 32;
-            int64_t mine = 0;
+            int mine = 0;
 #pragma unroll 8
             for (int i = 0; i < run; ++i) {
                 const int r = lane * run + i;
                 mine += seq_cost(r < p.R ? own_len(p, r) : 0);
             }
             mine *= p.Hk * p.oblocks;
-            const int64_t upto = warp_scan(mine, lane);
-            const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+            const int upto = warp_scan(mine, lane);
+            const int total = __shfl_sync(0xffffffffu, upto, 31);
             const OwnCut cut(p, total, gridDim.x);
-            const int64_t x0 = cut.begin(blockIdx.x), x1 = min(cut.begin(blockIdx.x + 1), total);
+            const int x0 = static_cast<int>(min(cut.begin(blockIdx.x), static_cast<int64_t>(total)));
+            const int x1 = static_cast<int>(min(cut.begin(blockIdx.x + 1), static_cast<int64_t>(total)));
             if (x0 < x1) {
                 const int at = __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
-                int64_t start = __shfl_sync(0xffffffffu, upto - mine, at);  // of request r0
+                int start = __shfl_sync(0xffffffffu, upto - mine, at);  // of request r0
                 for (int r0 = at * run; r0 < p.R && start < x1 && ok; r0 += 32) {
                     const int len_l = r0 + lane < p.R ? own_len(p, r0 + lane) : 0;
                     for (int i = 0; i < 32 && start < x1 && ok; ++i) {
                         const int len = __shfl_sync(0xffffffffu, len_l, i);
-                        const int64_t cost = seq_cost(len);
+                        const int cost = seq_cost(len);
                         const int seqs = p.Hk * p.oblocks;
                         if (len > 0 && start + cost * seqs > x0) {
                             const int nt = (len + kBc - 1) / kBc;
-                            int q = x0 > start ? static_cast<int>((x0 - start) / cost) : 0;
+                            int q = x0 > start ? (x0 - start) / cost : 0;
                             for (; q < seqs && start + q * cost < x1 && ok; ++q) {
-                                const int64_t first = start + q * cost + kPfxItemCost;  // tile 0's unit
-                                const int64_t a = x0 > first ? (x0 - first + kPfxTileCost - 1) / kPfxTileCost : 0;
-                                const int64_t b = x1 > first ? (x1 - first + kPfxTileCost - 1) / kPfxTileCost : 0;
-                                const int t0 = static_cast<int>(min(a, static_cast<int64_t>(nt)));
-                                const int t1 = static_cast<int>(min(b, static_cast<int64_t>(nt)));
+                                const int first = start + q * cost + kPfxItemCost;  // tile 0's unit
+                                const int a = x0 > first ? (x0 - first + kPfxTileCost - 1) / kPfxTileCost : 0;
+                                const int b = x1 > first ? (x1 - first + kPfxTileCost - 1) / kPfxTileCost : 0;
+                                const int t0 = min(a, nt);
+                                const int t1 = min(b, nt);
                                 if (t0 >= t1) continue;
                                 const int blk = q % p.oblocks;
                                 it.head = q / p.oblocks;
@@ -648,11 +658,11 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
         it.ntiles = -1;
         if (ok) publish(it);
         // One CTA leaves every request's start and the total for the combine kernel.
-        if (p.lens && p.workers == 0 && blockIdx.x == gridDim.x - 1) {
-            int64_t start = 0;
+        if (p.C > 0 && p.workers == 0 && blockIdx.x == gridDim.x - 1) {
+            int start = 0;
             for (int r0 = 0; r0 < p.R; r0 += 32) {
-                const int64_t c = r0 + lane < p.R ? request_cost(p, own_len(p, r0 + lane)) : 0;
-                const int64_t upto = warp_scan(c, lane);
+                const int c = r0 + lane < p.R ? request_cost(p, own_len(p, r0 + lane)) : 0;
+                const int upto = warp_scan(c, lane);
                 if (r0 + lane < p.R) p.own_start[r0 + lane] = start + upto - c;
                 start += __shfl_sync(0xffffffffu, upto, 31);
             }
@@ -1053,13 +1063,13 @@ static_assert(sizeof(OwnStep) == 32, "OwnSmem");
 // The line of own work as this kernel cuts it: a sequence (request, key head)
 // is one unit and then its steps; every worker (warp) has `cap` units.
 struct WarpCut {
-    int64_t cap;
-    __device__ __forceinline__ WarpCut(int64_t total, int workers) {
+    int cap;
+    __device__ __forceinline__ WarpCut(int total, int workers) {
         cap = (total + workers - 1) / workers;
         if (cap < 1) cap = 1;
     }
 };
-__device__ __forceinline__ int64_t warp_seq_cost(int len) { return len > 0 ? 1 + (len + kOwnStep - 1) / kOwnStep : 0; }
+__device__ __forceinline__ int warp_seq_cost(int len) { return len > 0 ? 1 + (len + kOwnStep - 1) / kOwnStep : 0; }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -1109,22 +1119,23 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
     // ---- this warp's stretch of the line
     const int worker = blockIdx.x * kOwnWarps + warp;
     const int run = (p.R + 31) / 32;
-    int64_t mine = 0;
+    int mine = 0;
 #pragma unroll 8
     for (int i = 0; i < run; ++i) {
         const int r = lane * run + i;
         mine += warp_seq_cost(r < p.R ? own_len(p, r) : 0);
     }
     mine *= p.Hk;
-    const int64_t upto = warp_scan(mine, lane);
-    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+    const int upto = warp_scan(mine, lane);
+    const int total = __shfl_sync(0xffffffffu, upto, 31);
     const WarpCut cut(total, p.workers);
-    const int64_t x0 = worker * cut.cap, x1 = min(x0 + cut.cap, total);
+    const int x0 = static_cast<int>(min(static_cast<int64_t>(worker) * cut.cap, static_cast<int64_t>(total)));
+    const int x1 = min(cut.cap, total - x0) + x0;
 
     // ---- the walk of the issuing side (the same in every lane): request r, key head h, steps [s, s1)
     int r = 0, h = 0, s = 0, s1 = 0, s_first = 0, len = 0;
     int window = 0, len_l = 0;       // lens of requests [window, window + 32), one a lane
-    int64_t start = 0;               // of the sequence (r, h)
+    int start = 0;                   // of the sequence (r, h)
     bool more = x0 < x1;
     auto len_of = [&](int i) -> int {
         if (i >= window + 32) {
@@ -1140,11 +1151,11 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                 more = false;
                 break;
             }
-            const int64_t cost = warp_seq_cost(len);
+            const int cost = warp_seq_cost(len);
             if (len > 0 && start + cost > x0) {
-                const int64_t f = start + 1;  // step 0's unit
-                s = static_cast<int>(x0 > f ? x0 - f : 0);
-                s1 = static_cast<int>(min(x1 - f, cost - 1));
+                const int f = start + 1;  // step 0's unit
+                s = x0 > f ? x0 - f : 0;
+                s1 = min(x1 - f, cost - 1);
                 s_first = s;
                 if (s < s1) break;
             }
@@ -1166,9 +1177,9 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
             start += warp_seq_cost(len) * p.Hk;
             if (++r < p.R) len = len_of(r);
         }
-        const int64_t cost = warp_seq_cost(len);
+        const int cost = warp_seq_cost(len);
         if (cost > 0) {
-            h = static_cast<int>((x0 - start) / cost);
+            h = (x0 - start) / cost;
             start += h * cost;
         }
         settle();
@@ -1356,10 +1367,10 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         mbar_wait_drain(bars + 8 * (used % L::kStages), (used / L::kStages) & 1u, 50000000ull);
     // One warp leaves every request's start and the total for the combine kernel.
     if (worker == p.workers - 1) {
-        int64_t at = 0;
+        int at = 0;
         for (int r0 = 0; r0 < p.R; r0 += 32) {
-            const int64_t c = r0 + lane < p.R ? warp_seq_cost(own_len(p, r0 + lane)) * p.Hk : 0;
-            const int64_t sum = warp_scan(c, lane);
+            const int c = r0 + lane < p.R ? warp_seq_cost(own_len(p, r0 + lane)) * p.Hk : 0;
+            const int sum = warp_scan(c, lane);
             if (r0 + lane < p.R) p.own_start[r0 + lane] = at + sum - c;
             at += __shfl_sync(0xffffffffu, sum, 31);
         }
@@ -1379,11 +1390,11 @@ __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_c
     __shared__ float2 s_stat[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = warp % WARPS;
-    const int64_t rows = static_cast<int64_t>(p.R) * p.Hk * p.GT;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / WARPS;  // (r, hq, t)
-    const int hgt = p.Hk * p.GT;
+    const uint32_t rows = static_cast<uint32_t>(p.R) * p.Hk * p.GT;  // below 2^31
+    const uint32_t row = blockIdx.x * kRows + warp / WARPS;          // (r, hq, t)
+    const uint32_t hgt = p.Hk * p.GT;
     const int r = row < rows ? static_cast<int>(row / hgt) : 0;
-    const int rem = static_cast<int>(row - static_cast<int64_t>(r) * hgt);
+    const int rem = static_cast<int>(row - r * hgt);
     const int h = rem / p.GT, x = rem - h * p.GT;  // key head, row within the request
     const int raw_len = p.lens ? __ldg(p.lens + r) : 0;  // an input: no need to wait for it
     const bool on = row < rows && raw_len >= 0;
@@ -1391,7 +1402,7 @@ __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_c
     int segs = 0;
     int64_t pfirst = 0;
     if (p.P > 0) {
-        const int64_t tile = static_cast<int64_t>(h) * p.ptiles;
+        const int tile = h * p.ptiles;
         const int k0 = stretch_of(p, tile);
         segs = stretch_of(p, tile + p.ptiles - 1) - k0 + 1;
         pfirst = prefix_part(p, k0, h) + static_cast<int64_t>(r) * p.GT + x;
@@ -1401,24 +1412,25 @@ __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = min(raw_len, p.C);
     if (on && len > 0) {
-        const int64_t total = __ldcg(p.own_start + p.R);
-        int64_t a, b, seq;
+        const int total = __ldcg(p.own_start + p.R);
+        int a, b;
+        int64_t seq;
         if (p.workers > 0) {
             const WarpCut cut(total, p.workers);
-            const int64_t first = __ldcg(p.own_start + r) + h * warp_seq_cost(len) + 1;
+            const int first = __ldcg(p.own_start + r) + h * warp_seq_cost(len) + 1;
             a = first / cut.cap;
             b = (first + (len - 1) / kOwnStep) / cut.cap;
             seq = static_cast<int64_t>(r) * p.Hk + h;
         } else {
             const OwnCut cut(p, total, grid);
             const int q = h * p.oblocks + x / (2 * p.qrows);
-            const int64_t first = __ldcg(p.own_start + r) + q * seq_cost(len) + kPfxItemCost;
+            const int first = __ldcg(p.own_start + r) + q * seq_cost(len) + kPfxItemCost;
             a = cut.cta_of(first);
-            b = cut.cta_of(first + static_cast<int64_t>((len - 1) / kBc) * kPfxTileCost);
+            b = cut.cta_of(first + (len - 1) / kBc * kPfxTileCost);
             seq = static_cast<int64_t>(r) * p.Hk * p.oblocks + q;
         }
         ofirst = p.own_first + (seq + a) * p.orows + x % (2 * p.qrows);
-        pieces += static_cast<int>(b - a) + 1;
+        pieces += b - a + 1;
     }
     auto at = [&](int i) -> int64_t { return i < segs ? pfirst + i * pstep : ofirst + static_cast<int64_t>(i - segs) * p.orows; };
     float acc[kPer];

@@ -444,7 +444,8 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
  *             reads key head h / (Hq / Hk)
  *   Kp, Vp  : bf16 [Hk, P, d] device views; P = 0: no prefix (then they may be NULL)
  *   Ko, Vo  : bf16 [R, Hk, C, d] device views, caches of capacity C; C = 0: no own
- *             keys (then they and own_lens may be NULL).  P and C are not both 0.
+ *             keys (then they, and own_lens where no request is padding, may be NULL).
+ *             P and C are not both 0.
  *   own_lens: int32 [R] device: the request's own keys, its T new tokens (the
  *             last of them) among them; more than C counts as C.  0: none: the rows see
  *             the prefix alone (without one: O = 0, LSE = -inf).  Negative: the
@@ -459,7 +460,8 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
  *             O: request, head, token; Kp, Vp: head, key; Ko, Vo: request, head, key);
  *             NULL: contiguous.  Positive multiples of 8 for axes longer than 1, and
  *             stride times extent at most 2^39.
- *   d       : 64 or 128;  scale : any finite value;  R, Hq, Hk, T >= 1, R*Hq*T < 2^31
+ *   d       : 64 or 128;  scale : any finite value;  R, Hq, Hk, T >= 1, R*Hq*T < 2^31,
+ *             and less than 2^30 tiles of work (Hk * P / 128; R * Hk * C / 16)
  *   workspace : device buffer of at least attn_fwd_prefix_workspace_bytes(), 16-byte
  *             aligned, owned by the caller, not used by other work while this call runs
  *             (calls that may overlap, captured graphs among them, need one each)

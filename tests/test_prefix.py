@@ -45,7 +45,7 @@ def cdll_call(lib, **over):
     (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(d=96), 2), (dict(Q=0x1004), 3),
     (dict(Vp=0x3008), 3), (dict(Ko=0x4002), 3), (dict(O=0x7008), 3), (dict(LSE=0x8002), 3), (dict(lens=0x6001), 3),
     (dict(ws=0x9008), 3), (dict(qs=(512, 68, 64)), 3), (dict(kps=(6400, 0)), 1), (dict(vos=(6400, -64, 64)), 1),
-    (dict(kps=(1 << 39, 64)), 1), (dict(qs=(1 << 38, 64, 64)), 1),
+    (dict(kps=(1 << 39, 64)), 1), (dict(R=1 << 20, C=1 << 14), 1), (dict(qs=(1 << 38, 64, 64)), 1),
 ])
 def test_refusals(lib, over, status):
     assert cdll_call(lib, **over) == status
@@ -156,6 +156,7 @@ SHAPES = [
     (2, 8, 1, 33, 128, 260, 400, [33, 400], False),                 # 264 rows of a request: two own blocks
     (50, 12, 2, 3, 128, 700, 40, [(3 * i) % 41 for i in range(50)], True),  # 18 rows a request: tiles of 126 rows
     (9, 33, 1, 2, 64, 300, 20, [20] * 9, False),                    # 66 rows a request: one a tile
+    (3, 128, 1, 1, 128, 300, 33, [33, 0, 7], False),                # 128 rows a request: one a tile
     (3, 16, 2, 17, 64, 200, 50, [50, 17, 20], False),               # 136 rows a request: rows fetched one by one
     (1, 64, 1, 1, 128, 0, 5000, [4999], False),                     # a long own part alone, cut over many CTAs
     (1, 8, 8, 1, 64, 40000, 0, [], False),
@@ -193,6 +194,23 @@ def test_padding_requests_are_left_as_they_were(lib):
     check(s, out, lse)
     for r in (1, 3):
         assert (out[r] == 7.0).all() and (lse[r] == 7.0).all()
+
+
+@gpu
+def test_padding_without_own_keys(lib):
+    s = make(4, 4, 2, 1, 64, 150, 0, [], seed=13)
+    out = torch.full((4, 4, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, 4, 1), 7.0, device="cuda")
+    ela.attn_fwd_prefix(**s, own_lens=torch.tensor([0, -1, 5, -1], dtype=torch.int32, device="cuda"), out=out, lse=lse)
+    for r in (1, 3):
+        assert (out[r] == 7.0).all() and (lse[r] == 7.0).all()
+    keep = [0, 2]
+    check(dict(s, q=s["q"][keep]), out[keep], lse[keep])
+    # an empty cache is the same as none
+    empty = torch.empty(4, 2, 0, 64, dtype=torch.bfloat16, device="cuda")
+    a = ela.attn_fwd_prefix(**s, k_own=empty, v_own=empty, own_lens=torch.zeros(4, dtype=torch.int32, device="cuda"))
+    b = ela.attn_fwd_prefix(**s)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 @gpu

@@ -43,8 +43,22 @@ class Layout:
                 if best is None or cost < best:
                     best, self.psegs = cost, n
             self.pitems = self.pblocks * self.psegs
+            by_head = self.psegs % Hk == 0
+            self.cut_len = self.ptiles if by_head else self.line
+            self.cut_per = self.psegs // Hk if by_head else self.psegs
+            self.cut_base, self.cut_rem = divmod(self.cut_len, self.cut_per)
+            assert self.cut_base >= 1
         self.own_first = (self.psegs + Hk - 1) * R * self.GT if self.psegs else 0
         self.rows = self.own_first + ((R * Hk * self.oblocks + grid) * self.orows if C else 0)
+
+    def stretch_begin(self, k):
+        run, i = divmod(k, self.cut_per)
+        return run * self.cut_len + i * self.cut_base + min(i, self.cut_rem)
+
+    def stretch_of(self, tile):
+        run, y = divmod(tile, self.cut_len)
+        longer = self.cut_rem * (self.cut_base + 1)
+        return run * self.cut_per + (y // (self.cut_base + 1) if y < longer else self.cut_rem + (y - longer) // self.cut_base)
 
     def seq_cost(self, n):
         return ITEM + cdiv(n, 32) if n > 0 else 0
@@ -54,7 +68,7 @@ class Cut:
     def __init__(self, L, total):
         g = L.grid
         self.rem = L.pitems % g
-        item = ITEM + cdiv(L.line, L.psegs) * TILE if L.psegs else 0
+        item = ITEM + (L.cut_base + (L.cut_rem > 0)) * TILE if L.psegs else 0
         level = item * (g - self.rem)
         if self.rem == 0 or total > level:
             e = cdiv(total - (0 if self.rem == 0 else level), g)
@@ -78,7 +92,8 @@ def schedule(L, lens, cta):
     for i in range(cta, L.pitems, L.grid):
         blk, k = i % L.pblocks, i // L.pblocks
         row0 = blk * L.two
-        x, end = k * L.line // L.psegs, (k + 1) * L.line // L.psegs
+        x, end = L.stretch_begin(k), L.stretch_begin(k + 1)
+        assert x < end and all(L.stretch_of(t) == k for t in (x, end - 1))
         while x < end:
             head = x // L.ptiles
             t0 = x - head * L.ptiles
@@ -123,7 +138,7 @@ def combine_rows(L, lens, r, h, x):
     """The partial rows the combine kernel merges for row x of request r at key head h."""
     rows = []
     if L.ptiles:
-        first, last = (((t + 1) * L.psegs - 1) // L.line for t in (h * L.ptiles, (h + 1) * L.ptiles - 1))
+        first, last = (L.stretch_of(t) for t in (h * L.ptiles, (h + 1) * L.ptiles - 1))
         rows = [(k + h) * L.R * L.GT + r * L.GT + x for k in range(first, last + 1)]
     n = min(lens[r], L.C) if L.C else 0
     if n > 0:
