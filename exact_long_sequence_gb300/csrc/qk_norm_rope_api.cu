@@ -41,7 +41,7 @@ int fill_params(ReadyParams& p, const int32_t* positions, int64_t pos_axis, int6
     p.pos_batch = pos_batch;
     p.inv_freq = inv_freq;
     p.rot = 2 * pairs;
-    p.N = N;
+    p.N.set(N);
     p.tokens = static_cast<uint32_t>(B) * static_cast<uint32_t>(N);
     p.eps = eps;
     const int group = 32 / (d / 16);
@@ -103,8 +103,10 @@ unsigned deal_units(ReadyParams& p, int num_sms, int per_sm, int cta_warps) {
         const uint32_t groups = (p.tokens + r.tp - 1) / r.tp;
         const int64_t want = (static_cast<int64_t>(r.steps) * groups + warps - 1) / warps;
         r.steps_per_unit = static_cast<int>(want < 1 ? 1 : want > r.steps ? r.steps : want);
-        r.units_per_token = (r.steps + r.steps_per_unit - 1) / r.steps_per_unit;
-        r.units = groups * static_cast<uint32_t>(r.units_per_token);  // below 2 * warps + tokens
+        const int per_token = (r.steps + r.steps_per_unit - 1) / r.steps_per_unit;
+        r.units_per_token.set(per_token);
+        // more than one a token only while there are fewer units than warps: below 2^31
+        r.units = groups * static_cast<uint32_t>(per_token);
         const int64_t need = (static_cast<int64_t>(r.units) + cta_warps - 1) / cta_warps;
         if (need < ctas[t]) ctas[t] = need;
         r.part = nullptr;

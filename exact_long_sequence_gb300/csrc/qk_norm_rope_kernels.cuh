@@ -47,6 +47,24 @@ constexpr int kReadyMaxAxes = 4;
 constexpr int kFwdWarps = 4, kFwdCtasPerSm = 4, kFwdSlots = 3;
 constexpr int kBwdWarps = 12, kBwdCtasPerSm = 1, kBwdSlots = 3;
 
+// Quotients of numbers below 2^31 by a divisor that the host knows: with
+// 2^(s - 1) < d <= 2^s and m = ceil(2^(31 + s) / d), n / d = (n m) >> (31 + s)
+// for every such n (Granlund and Montgomery, division by invariant integers).
+// Two instructions; a division takes twenty.
+struct Quotient {
+    uint32_t m = 0;
+    int shift = 0;  // 31 + s - 32
+    int d = 1;
+    __host__ void set(int divisor) {
+        d = divisor;
+        int s = 0;
+        while ((1ll << s) < divisor) ++s;
+        m = s == 0 ? 0u : static_cast<uint32_t>(((1ull << (31 + s)) + divisor - 1) / divisor);
+        shift = s - 1;
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t n) const { return d == 1 ? n : __umulhi(n, m) >> shift; }
+};
+
 struct ReadyTensor {
     const __nv_bfloat16* x;   // input rows (backward: the forward's input; unused without a norm)
     const __nv_bfloat16* g;   // backward: gradient of the output rows
@@ -57,7 +75,7 @@ struct ReadyTensor {
     int hp, tp;               // a warp step holds hp heads (a power of two) of each of tp tokens, hp * tp = rows per warp
     int steps;                // steps of a token (or of tp tokens): ceil(H / hp)
     int steps_per_unit;       // a work unit: so many steps of one token
-    int units_per_token;      // of a token, or of tp tokens
+    Quotient units_per_token; // of a token, or of tp tokens
     uint32_t units;
     float* part;              // backward: [CTAs of this tensor][d] fp32 partial sums of dw, or nullptr
 };
@@ -70,7 +88,7 @@ struct ReadyParams {
     const double* inv_freq;   // [rot / 2]
     int axis_end[kReadyMaxAxes];  // pairs [axis_end[a - 1], axis_end[a]) turn by axis a
     int rot;                  // rotated elements of a row
-    int N;
+    Quotient N;
     uint32_t tokens;          // B * N
     bool multi;               // a tensor's steps may hold several tokens (tp > 1)
     float eps;
@@ -170,20 +188,25 @@ struct ReadyAngles {
     uint64_t f[kOwn];
     int axis[kOwn];
 
+    // Which pairs, their axes, and their frequencies' loads; finish() converts what arrived.
     template <bool INTER>
-    __device__ __forceinline__ void init(const ReadyParams& p, int lane) {
+    __device__ __forceinline__ void start(const ReadyParams& p, int lane, double (&freq)[kOwn]) {
         const int c = lane % kLanes, g = lane / kLanes;
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
             const int i = ReadyLane<D, INTER>::pair(c, g * kOwn + k);
-            f[k] = 0;
             axis[k] = 0;
+            freq[k] = 0.0;
             if (i < (p.rot >> 1)) {
-                f[k] = turn_fraction(p.inv_freq[i]);
+                freq[k] = __ldg(p.inv_freq + i);
 #pragma unroll
                 for (int a = 0; a < kReadyMaxAxes - 1; ++a) axis[k] += i >= p.axis_end[a] ? 1 : 0;
             }
         }
+    }
+    __device__ __forceinline__ void finish(const double (&freq)[kOwn]) {
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) f[k] = turn_fraction(freq[k]);
     }
     // Positions of the pairs this lane evaluates, for each of the step's tp
     // tokens (issued early).  `at`: where this lane's own token has its positions.
@@ -322,14 +345,14 @@ struct ReadyWalk {
         gt = MULTI ? g / rt.hp : 0;
     }
     __device__ __forceinline__ void decode(const ReadyParams& p, const ReadyTensor& rt) {
-        const uint32_t group = u / rt.units_per_token;
-        s = static_cast<int>(u - group * rt.units_per_token) * rt.steps_per_unit;
+        const uint32_t group = rt.units_per_token.of(u);
+        s = static_cast<int>(u - group * rt.units_per_token.d) * rt.steps_per_unit;
         s1 = min(rt.steps, s + rt.steps_per_unit);
         uint32_t token = MULTI ? group * rt.tp + gt : group;
         live = !MULTI || token < p.tokens;
         if (!live) token = p.tokens - 1;
-        b = static_cast<int>(token / static_cast<uint32_t>(p.N));
-        n = static_cast<int>(token - static_cast<uint32_t>(b) * p.N);
+        b = static_cast<int>(p.N.of(token));
+        n = static_cast<int>(token - static_cast<uint32_t>(b) * p.N.d);
     }
     __device__ __forceinline__ bool on(const ReadyTensor& rt, int step) const { return live && step * GROUPS + gh < rt.H; }
     __device__ __forceinline__ int64_t offset(const int64_t (&st)[3]) const {
@@ -440,14 +463,17 @@ __global__ void __launch_bounds__(kFwdWarps * 32, kFwdCtasPerSm) qk_norm_rope_ke
     ReadyWalk<A::kGroups, MULTI> w;
     w.begin(rt, place.block * kFwdWarps + warp, g);
     if (w.u >= rt.units) return;
-    Ring ring;
-    ring.start(p, rt, at, g, true, false, smem_u32(ready_smem) + warp * Ring::kBytes, w.u, warps);
+    // every load that the first rows wait for is under way before any of it is used
     A angles;
-    angles.template init<INTER>(p, lane);
-    const bool norm = rt.w != nullptr, all = p.rot == D;
+    double freq[A::kOwn];
+    angles.template start<INTER>(p, lane, freq);
     w.decode(p, rt);
     int pos[A::kPos];
     angles.load(p, rt, w.positions(p), pos);
+    Ring ring;
+    ring.start(p, rt, at, g, true, false, smem_u32(ready_smem) + warp * Ring::kBytes, w.u, warps);
+    angles.finish(freq);
+    const bool norm = rt.w != nullptr, all = p.rot == D;
     while (true) {
         float cs[8], sn[8];
         angles.eval(pos, rt, w.gt, lane, cs, sn);
@@ -521,15 +547,17 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_rope_bw
     w.begin(rt, place.block * kBwdWarps + warp, g);
     bool more = w.u < rt.units;
     if (more) {
-        Ring ring;
-        ring.start(p, rt, at, g, norm, true, smem_u32(ready_smem) + warp * Ring::kBytes, w.u, warps);
         A angles;
-        angles.template init<INTER>(p, lane);
-        f2 wa[4], wb[4];
-        load_weight(rt.w, at.a0, at.b0, wa, wb);
+        double freq[A::kOwn];
+        angles.template start<INTER>(p, lane, freq);
         w.decode(p, rt);
         int pos[A::kPos];
         angles.load(p, rt, w.positions(p), pos);
+        f2 wa[4], wb[4];
+        load_weight(rt.w, at.a0, at.b0, wa, wb);
+        Ring ring;
+        ring.start(p, rt, at, g, norm, true, smem_u32(ready_smem) + warp * Ring::kBytes, w.u, warps);
+        angles.finish(freq);
         while (more) {
             float cs[8], sn[8];
             angles.eval(pos, rt, w.gt, lane, cs, sn);

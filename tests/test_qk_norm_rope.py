@@ -92,6 +92,19 @@ def test_binding_refuses_on_the_host():
         ela.qk_norm_rope(q, q, torch.zeros(4, dtype=torch.int32), torch.ones(32, dtype=torch.float64))
 
 
+def test_quotients_by_multiplication():
+    """The rule the kernels divide token numbers by (struct Quotient), over its whole range of numbers."""
+    rng = np.random.default_rng(3)
+    divisors = [*range(1, 400), *(2 ** k + e for k in range(9, 31) for e in (-1, 0, 1)), 2 ** 31 - 1]
+    for d in divisors + rng.integers(1, 2 ** 31, 300).tolist():
+        s = (d - 1).bit_length()
+        m = -(-(1 << (31 + s)) // d) if d > 1 else 0
+        assert m < 2 ** 32
+        ns = np.concatenate([rng.integers(0, 2 ** 31, 50), rng.integers(0, 2 ** 31, 50) // d * d, [0, 2 ** 31 - 1]])
+        for n in {int(n) + e for n in ns for e in (-1, 0) if 0 <= n + e < 2 ** 31}:
+            assert (n if d == 1 else n * m >> 32 >> (s - 1)) == n // d
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_reference_gradient_against_differences(interleaved):
     rng = np.random.default_rng(5)
