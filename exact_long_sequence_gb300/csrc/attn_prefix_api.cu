@@ -27,7 +27,7 @@ int check_shape(const PrefixShape& s) {
         return ATTN_ERR_INVALID_ARG;
     if (s.d != 64 && s.d != 128) return ATTN_ERR_UNSUPPORTED;
     // the kernels count tiles and steps of work in 32 bits (2^31 of them would not fit device memory)
-    const double heads = s.Hk, blocks = std::ceil(static_cast<double>(s.Hq / s.Hk) * s.T / kBr);
+    const double heads = s.Hk, blocks = std::ceil(static_cast<double>(s.Hq / s.Hk) * s.T / 8);
     if (heads * (static_cast<double>(s.P) / kBc + 1) >= 1073741824.0 ||
         s.R * heads * blocks * (static_cast<double>(s.C) / kOwnStep + kPfxItemCost + 1) >= 1073741824.0)
         return ATTN_ERR_INVALID_ARG;
@@ -57,11 +57,14 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
     p.pblocks = static_cast<int>((static_cast<int64_t>(s.R) * p.GT + 2 * p.qrows - 1) / (2 * p.qrows));
     p.oblocks = (p.GT + 2 * p.qrows - 1) / (2 * p.qrows);
     p.orows = p.GT < 2 * p.qrows ? p.GT : 2 * p.qrows;
-    // Own keys of up to 16 rows a request and key head: a kernel of their own (see there).  Its
-    // warps: as many as there can be steps for, up to kOwnWarps an SM.
+    // Own keys of few rows a request and key head: a kernel of their own (see there), with row
+    // blocks of whole heads of the group.  Its warps: as many as there can be steps for, up to kOwnWarps an SM.
     p.workers = 0;
-    if (s.C > 0 && p.GT <= kOwnRows) {
-        const int64_t steps = static_cast<int64_t>(s.R) * s.Hk * ((s.C + kOwnStep - 1) / kOwnStep);
+    if (s.C > 0 && s.T <= kOwnRows && (p.GT <= kOwnRows || (p.GT <= kOwnMostRows && s.C <= kOwnMostKeys))) {
+        const int heads = kOwnRows / s.T < p.G ? kOwnRows / s.T : p.G;
+        p.oblocks = (p.G + heads - 1) / heads;
+        p.orows = heads * s.T;
+        const int64_t steps = static_cast<int64_t>(s.R) * s.Hk * p.oblocks * ((s.C + kOwnStep - 1) / kOwnStep);
         const int64_t ctas = (steps + kOwnWarps - 1) / kOwnWarps;
         p.workers = static_cast<int>(ctas < num_sms ? ctas : num_sms) * kOwnWarps;
     }
@@ -260,7 +263,7 @@ extern "C" int attn_fwd_prefix(const void* Q, const int64_t* q_strides, const vo
                                static_cast<uint64_t>(p.qs[1]) * p.G * 2, static_cast<uint64_t>(p.qs[0]) * 2};
         const uint32_t tile[5] = {64, static_cast<uint32_t>(T), static_cast<uint32_t>(p.G), 1,
                                   static_cast<uint32_t>(p.qrows / p.GT)};
-        const uint32_t one[5] = {64, static_cast<uint32_t>(T), static_cast<uint32_t>(p.G), 1, 1};
+        const uint32_t one[5] = {64, static_cast<uint32_t>(T), static_cast<uint32_t>(p.workers > 0 ? p.orows / T : p.G), 1, 1};
         if ((P > 0 && (st = encode_bf16_map(&maps[0], Q, 5, e, b, tile)) != ATTN_OK) ||
             (C > 0 && (st = encode_bf16_map(&maps[1], Q, 5, e, b, one)) != ATTN_OK))
             return st;

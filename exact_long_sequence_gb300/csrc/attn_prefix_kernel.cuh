@@ -71,8 +71,8 @@ struct PrefixParams {
     int cut_len, cut_per;   // ... each run of cut_len tiles (a head's, or the whole line) into cut_per of them,
     int cut_base, cut_rem;  // ... the first cut_rem of cut_base + 1 tiles, the others of cut_base
     int pitems;             // psegs * pblocks (a stretch at one row block, at one or more key heads)
-    int oblocks;            // blocks of two query tiles over GT
-    int orows;              // rows of an own slot: min(GT, 2 qrows)
+    int oblocks;            // row blocks of a request at a key head, for its own keys,
+    int orows;              // ... of so many rows: two query tiles, or up to 16 in the own-keys kernel (at most GT)
     float* part_o;          // partial rows [.., d] fp32: first [psegs + Hk - 1][R GT], then [own slots][orows]
     float* part_lse;        // one per partial row
     int64_t own_first;      // the first own slot's partial row
@@ -1022,10 +1022,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
 }
 
 // ---------------------------------------------------------------------------
-// Own keys of requests with at most 16 rows a key head (the usual decoding
-// step).  A piece of one request at one key head is then a product of 16 rows
-// (most of them padding at small groups), bound by reading K and V once: a
-// warp is enough for it, and many warps with a piece each hide the latency that
+// Own keys of requests with few rows a key head (the usual decoding step).  A
+// piece of one request at one key head and up to 16 rows (whole heads of the group) is bound by
+// reading K and V: a warp is enough for it, and many warps with a piece each hide the latency that
 // the roles of the kernel above hand from one to the next (2048 pieces of 16 keys: 47 us
 // there, 18 us here).  Each warp streams K and V in steps of 16 keys through a ring of its own,
 // filled by TMA some steps ahead, across the ends of pieces; Q comes with a
@@ -1039,6 +1038,12 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
 constexpr int kOwnWarps = 8;
 constexpr int kOwnStep = 16;
 constexpr int kOwnRows = 16;
+// Requests with more rows take several row blocks, whose K/V come from L2 for all but the first.
+// That pays up to kOwnMostRows rows (four blocks) on short caches: 64 requests x 8 heads of 20 rows, 64 keys
+// 18.5 us (26.8 us as items of the prefix kernel), 600 keys 51 (60) us; on 8 requests of
+// 8192 keys it does not: 88 (61) us.
+constexpr int kOwnMostRows = 64;
+constexpr int kOwnMostKeys = 1024;   // of a cache, for requests of more than one block
 
 template <int D>
 struct OwnSmem {
@@ -1055,13 +1060,14 @@ struct OwnSmem {
 };
 struct OwnStep {
     int req, head, key0, len;
-    int first, last;      // of its piece
+    int rows;             // of its piece, whose
+    int edge;             // ... first step this is (bit 0), or last (bit 1)
     int64_t part;         // the piece's partial rows
 };
 static_assert(sizeof(OwnStep) == 32, "OwnSmem");
 
-// The line of own work as this kernel cuts it: a sequence (request, key head)
-// is one unit and then its steps; every worker (warp) has `cap` units.
+// The line of own work as this kernel cuts it: a sequence (request, key head,
+// row block) is one unit and then its steps; every worker (warp) has `cap` units.
 struct WarpCut {
     int cap;
     __device__ __forceinline__ WarpCut(int total, int workers) {
@@ -1125,14 +1131,15 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         const int r = lane * run + i;
         mine += warp_seq_cost(r < p.R ? own_len(p, r) : 0);
     }
-    mine *= p.Hk;
+    const int seqs = p.Hk * p.oblocks;
+    mine *= seqs;
     const int upto = warp_scan(mine, lane);
     const int total = __shfl_sync(0xffffffffu, upto, 31);
     const WarpCut cut(total, p.workers);
     const int x0 = static_cast<int>(min(static_cast<int64_t>(worker) * cut.cap, static_cast<int64_t>(total)));
     const int x1 = min(cut.cap, total - x0) + x0;
 
-    // ---- the walk of the issuing side (the same in every lane): request r, key head h, steps [s, s1)
+    // ---- the walk of the issuing side (the same in every lane): request r, its sequence h, steps [s, s1)
     int r = 0, h = 0, s = 0, s1 = 0, s_first = 0, len = 0;
     int window = 0, len_l = 0;       // lens of requests [window, window + 32), one a lane
     int start = 0;                   // of the sequence (r, h)
@@ -1160,7 +1167,7 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                 if (s < s1) break;
             }
             start += cost;
-            if (len == 0 || ++h == p.Hk) {
+            if (len == 0 || ++h == seqs) {
                 h = 0;
                 if (++r < p.R) len = len_of(r);
             }
@@ -1173,8 +1180,8 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         window = r - 32;
         len = len_of(r);
         // skip whole requests before the stretch, then whole sequences
-        while (r < p.R && start + warp_seq_cost(len) * p.Hk <= x0) {
-            start += warp_seq_cost(len) * p.Hk;
+        while (r < p.R && start + warp_seq_cost(len) * seqs <= x0) {
+            start += warp_seq_cost(len) * seqs;
             if (++r < p.R) len = len_of(r);
         }
         const int cost = warp_seq_cost(len);
@@ -1190,30 +1197,31 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         const uint32_t st = filled % L::kStages;
         if (lane == 0) {
             OwnStep d;
+            const int blk = h % p.oblocks;
             d.req = r;
-            d.head = h;
+            d.head = h / p.oblocks;
             d.key0 = s * kOwnStep;
             d.len = len;
-            d.first = s == s_first;
-            d.last = s + 1 == s1;
-            d.part = p.own_first + (static_cast<int64_t>(r) * p.Hk + h + worker) * p.orows;
+            d.rows = min(p.orows, p.GT - blk * p.orows);
+            d.edge = (s == s_first ? 1 : 0) | (s + 1 == s1 ? 2 : 0);
+            d.part = p.own_first + (static_cast<int64_t>(r) * seqs + h + worker) * p.orows;
             steps[st] = d;
             const uint32_t full = bars + 8 * st;
             const uint32_t dst = ring + st * L::kStage;
-            mbar_arrive_expect_tx(full, 2 * L::kPart + (d.first ? p.GT * D * 2 : 0));
+            mbar_arrive_expect_tx(full, 2 * L::kPart + (d.edge & 1 ? p.orows * D * 2 : 0));
 #pragma unroll
             for (int b = 0; b < D / 64; ++b) {
                 const uint32_t o = dst + b * (kOwnStep * 128);
-                if (d.first) tma_load_5d(o + 2 * L::kPart, &tmap_q, full, b * 64, 0, 0, h, r);
-                tma_load_4d(o, &tmap_k, full, b * 64, d.key0, h, r);
-                tma_load_4d(o + L::kPart, &tmap_v, full, b * 64, d.key0, h, r);
+                if (d.edge & 1) tma_load_5d(o + 2 * L::kPart, &tmap_q, full, b * 64, 0, blk * p.orows / p.T, d.head, r);
+                tma_load_4d(o, &tmap_k, full, b * 64, d.key0, d.head, r);
+                tma_load_4d(o + L::kPart, &tmap_v, full, b * 64, d.key0, d.head, r);
             }
         }
         __syncwarp();
         ++filled;
         if (++s == s1) {
             start += warp_seq_cost(len);
-            if (++h == p.Hk) {
+            if (++h == seqs) {
                 h = 0;
                 if (++r < p.R) len = len_of(r);
             }
@@ -1228,10 +1236,10 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
     float m[2], l[2];             // rows lane / 4 and lane / 4 + 8
     int hide[2];                  // the last keys these rows do not see
     const int row0 = lane >> 2;
-    const bool valid[2] = {row0 < p.GT, row0 + 8 < p.GT};
+    bool valid[2] = {false, false};   // whether the piece has them
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        hide[i] = valid[i] ? p.T - 1 - (row0 + 8 * i) % p.T : 0;
+        hide[i] = p.T - 1 - (row0 + 8 * i) % p.T;  // (a block begins with a head)
         m[i] = -INFINITY;
         l[i] = 0.f;
     }
@@ -1249,7 +1257,9 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         if (!ok) break;
         const uint32_t kb = ring + st * L::kStage, vb = kb + L::kPart, qb = vb + L::kPart;
         const OwnStep d = steps[st];
-        if (d.first) {
+        if (d.edge & 1) {
+            valid[0] = row0 < d.rows;
+            valid[1] = row0 + 8 < d.rows;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t c = 2 * kk + qv_ch;
@@ -1304,7 +1314,7 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                 grow = true;
             }
         }
-        if (__any_sync(0xffffffffu, grow) && !d.first) {
+        if (__any_sync(0xffffffffu, grow) && !(d.edge & 1)) {
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {
                 o[j][0] *= alpha[0];
@@ -1337,7 +1347,7 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         }
         __syncwarp();  // every lane has read the step
         issue();
-        if (d.last) {
+        if (d.edge & 2) {
             const uint64_t keep = l2_policy_evict_last();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -1369,7 +1379,7 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
     if (worker == p.workers - 1) {
         int at = 0;
         for (int r0 = 0; r0 < p.R; r0 += 32) {
-            const int c = r0 + lane < p.R ? warp_seq_cost(own_len(p, r0 + lane)) * p.Hk : 0;
+            const int c = r0 + lane < p.R ? warp_seq_cost(own_len(p, r0 + lane)) * seqs : 0;
             const int sum = warp_scan(c, lane);
             if (r0 + lane < p.R) p.own_start[r0 + lane] = at + sum - c;
             at += __shfl_sync(0xffffffffu, sum, 31);
@@ -1414,22 +1424,19 @@ __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_c
     if (on && len > 0) {
         const int total = __ldcg(p.own_start + p.R);
         int a, b;
-        int64_t seq;
+        const int q = h * p.oblocks + x / p.orows;
         if (p.workers > 0) {
             const WarpCut cut(total, p.workers);
-            const int first = __ldcg(p.own_start + r) + h * warp_seq_cost(len) + 1;
+            const int first = __ldcg(p.own_start + r) + q * warp_seq_cost(len) + 1;
             a = first / cut.cap;
             b = (first + (len - 1) / kOwnStep) / cut.cap;
-            seq = static_cast<int64_t>(r) * p.Hk + h;
         } else {
             const OwnCut cut(p, total, grid);
-            const int q = h * p.oblocks + x / (2 * p.qrows);
             const int first = __ldcg(p.own_start + r) + q * seq_cost(len) + kPfxItemCost;
             a = cut.cta_of(first);
             b = cut.cta_of(first + (len - 1) / kBc * kPfxTileCost);
-            seq = static_cast<int64_t>(r) * p.Hk * p.oblocks + q;
         }
-        ofirst = p.own_first + (seq + a) * p.orows + x % (2 * p.qrows);
+        ofirst = p.own_first + (static_cast<int64_t>(r) * p.Hk * p.oblocks + q + a) * p.orows + x % p.orows;
         pieces += b - a + 1;
     }
     auto at = [&](int i) -> int64_t { return i < segs ? pfirst + i * pstep : ofirst + static_cast<int64_t>(i - segs) * p.orows; };

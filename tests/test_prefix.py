@@ -155,6 +155,9 @@ SHAPES = [
     (2, 2, 1, 3, 128, 50, 9, [1, 2], False),                        # fewer own keys than new tokens
     (2, 8, 1, 33, 128, 260, 400, [33, 400], False),                 # 264 rows of a request: two own blocks
     (50, 12, 2, 3, 128, 700, 40, [(3 * i) % 41 for i in range(50)], True),  # 18 rows a request: tiles of 126 rows
+    (5, 20, 2, 3, 128, 100, 1100, [1100, 0, 2, 700, 129], False),   # 30 rows, caches too long for row blocks
+    (5, 20, 2, 3, 64, 100, 700, [700, 0, 2, 16, 129], True),        # 30 rows in blocks of 15
+    (3, 44, 4, 4, 128, 60, 64, [64, 17, 5], False),                 # 44 rows in blocks of 16, the last of 12
     (9, 33, 1, 2, 64, 300, 20, [20] * 9, False),                    # 66 rows a request: one a tile
     (3, 128, 1, 1, 128, 300, 33, [33, 0, 7], False),                # 128 rows a request: one a tile
     (3, 16, 2, 17, 64, 200, 50, [50, 17, 20], False),               # 136 rows a request: rows fetched one by one

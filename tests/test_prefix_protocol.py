@@ -196,7 +196,8 @@ def test_every_tile_once_and_every_piece_found(R, Hk, G, T, P, C, grid, kind):
     assert read == written  # nothing computed for nothing, padding's prefix rows included
 
 
-# The own-keys kernel's cut (requests of at most 16 rows a key head): steps of 16 keys, one stretch a warp.
+# The own-keys kernel's cut (requests with few rows a key head): steps of 16 keys, one stretch a warp.
+# Hk stands for a request's sequences: key heads times row blocks.
 def warp_seq_cost(n):
     return 1 + cdiv(n, 16) if n > 0 else 0
 
