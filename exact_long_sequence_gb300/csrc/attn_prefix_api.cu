@@ -41,6 +41,18 @@ int check_shape(const PrefixShape& s) {
 constexpr double kPlanPiece = 8.0;
 constexpr double kPlanRow = 4.2e-4;
 
+// The own-keys kernel is bound by HBM and the prefix, with many rows, by the
+// tensor core.  The former runs at 5 of its 5.9 TB/s on 88 SMs, so that is what it gets
+// where there is a prefix to run beside it; a step of 16 keys of 128 then takes
+// 1 / 976 of a prefix tile's time.  Measured, own kernel on all SMs -> on 88: 64 requests on
+// 16384 keys, up to 1024 own 60.4 -> 53.7 us (96 SMs 57.4, 80 52.1, 72 55.4 us), with 1024 own each 78.9 -> 77.3
+// (72.0, 80.9, 88.3) us, 256 on 65536 246.6 -> 239 us.  Not where the own keys could take
+// more than about five times the prefix's time (the capacity is what the host knows).
+constexpr int kBesideSms = 88;
+constexpr int kBesideLead = 1074;          // 2^20 / 976
+constexpr double kBesideLeast = 4096.0;    // own steps (6 us)
+constexpr double kBesideMost = 5750.0;     // own steps for a prefix tile of every SM: 5 x 1150
+
 // Sizes that follow from the shape, and the cut of the prefix into the number
 // of stretches with the least estimated time: items in whole waves, each its
 // tiles and its pieces, and the partial rows.
@@ -70,8 +82,9 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
     }
     p.psegs = 0;
     p.pitems = 0;
-    p.cut_len = p.cut_per = p.cut_base = 1;
-    p.cut_rem = 0;
+    p.by_head = p.run_per = 1;
+    p.run_len = p.even_base = p.even_rem = 0;
+    p.early = p.lead = 0;
     if (p.ptiles > 0) {
         // (in floating point: the quotients are small and this is on every call's path)
         const double line = static_cast<double>(s.Hk) * p.ptiles, blocks = p.pblocks, sms = num_sms, heads = s.Hk;
@@ -90,11 +103,21 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
             }
         }
         p.pitems = p.pblocks * p.psegs;
-        const bool by_head = p.psegs % s.Hk == 0;
-        p.cut_len = by_head ? p.ptiles : p.ptiles * s.Hk;
-        p.cut_per = by_head ? p.psegs / s.Hk : p.psegs;
-        p.cut_base = p.cut_len / p.cut_per;
-        p.cut_rem = p.cut_len % p.cut_per;
+        p.by_head = p.psegs % s.Hk == 0;
+        p.run_len = p.by_head ? p.ptiles : p.ptiles * s.Hk;
+        p.run_per = p.by_head ? p.psegs / s.Hk : p.psegs;
+        p.even_base = p.run_len / p.run_per;
+        p.even_rem = p.run_len % p.run_per;
+        // Side by side: the own-keys kernel leaves SMs to the prefix, whose first stretches start at once and are longer.
+        const double own_steps = p.workers == 0 ? 0.0 : static_cast<double>(s.R) * s.Hk * p.oblocks * ((s.C + kOwnStep - 1) / kOwnStep);
+        if (p.pitems <= num_sms && p.workers > kBesideSms * kOwnWarps && own_steps >= kBesideLeast && line >= 3.0 * p.psegs &&
+            own_steps <= kBesideMost * line * blocks / sms) {
+            p.workers = kBesideSms * kOwnWarps;
+            const int beside = (num_sms - kBesideSms) / p.pblocks;  // stretches whose CTAs start at once
+            p.early = p.by_head ? beside / s.Hk : beside;
+            if (p.early >= p.run_per) p.early = p.run_per - 1;
+            p.lead = s.d == 128 ? kBesideLead : kBesideLead * 3 / 4;
+        }
     }
 }
 
@@ -106,7 +129,7 @@ struct PrefixSpace {
     int64_t own_first;
     PrefixSpace(const PrefixParams& p, int d, int num_sms) {
         const int grid = p.workers > 0 ? p.workers : num_sms;  // who may have a piece of a sequence
-        own_first = p.psegs == 0 ? 0 : static_cast<int64_t>(p.psegs + p.Hk - 1) * p.R * p.GT;
+        own_first = p.psegs == 0 ? 0 : static_cast<int64_t>(p.psegs + (p.by_head ? 0 : p.Hk - 1)) * p.R * p.GT;
         const int64_t own = p.C > 0 ? (static_cast<int64_t>(p.R) * p.Hk * p.oblocks + grid) * p.orows : 0;
         start = 0;
         lse = align256((static_cast<size_t>(p.R) + 1) * sizeof(int));

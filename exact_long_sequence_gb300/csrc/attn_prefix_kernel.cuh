@@ -53,6 +53,7 @@ constexpr int kPfxTileCost = 4;
 constexpr int kPfxItemCost = 2;
 constexpr int kPfxOwnBox = 32;   // keys per TMA box of the own caches
 constexpr int kPfxItemRing = 8;
+constexpr int kOwnStep = 16;     // keys per step of the own-keys kernel
 
 struct PrefixParams {
     const __nv_bfloat16* q;
@@ -67,10 +68,14 @@ struct PrefixParams {
     int qrows;              // rows of a query tile: the whole requests that fit 128 rows, or 128 if one does not
     int pblocks;            // blocks of two query tiles over R GT
     int ptiles;             // prefix tiles of a key head
-    int psegs;              // the line of all key heads' tiles is cut into so many even stretches:
-    int cut_len, cut_per;   // ... each run of cut_len tiles (a head's, or the whole line) into cut_per of them,
-    int cut_base, cut_rem;  // ... the first cut_rem of cut_base + 1 tiles, the others of cut_base
-    int pitems;             // psegs * pblocks (a stretch at one row block, at one or more key heads)
+    int psegs;              // stretches that the tiles are cut into (PrefixCut)
+    int by_head;            // whether each head is cut by itself
+    int run_len, run_per;   // tiles of a run (a head, or the line) and its stretches
+    int even_base, even_rem;  // an even cut: run_per stretches of even_base tiles, the first even_rem one more
+    int early;              // ... into psegs / Hk stretches, or the line of all heads into psegs; the first
+    int lead;               // `early` of them are longer by what their CTAs can do before the others start:
+                            // lead / 2^20 tiles for each step of own work
+    int pitems;             // psegs * pblocks (a stretch at one row block)
     int oblocks;            // row blocks of a request at a key head, for its own keys,
     int orows;              // ... of so many rows: two query tiles, or up to 16 in the own-keys kernel (at most GT)
     float* part_o;          // partial rows [.., d] fp32: first [psegs + Hk - 1][R GT], then [own slots][orows]
@@ -96,7 +101,8 @@ struct OwnCut {
     int rem, cap1, cap0;
     __device__ __forceinline__ OwnCut(const PrefixParams& p, int total, int grid) {
         rem = p.pitems % grid;
-        const int item = p.psegs == 0 ? 0 : kPfxItemCost + (p.cut_base + (p.cut_rem > 0 ? 1 : 0)) * kPfxTileCost;
+        // (with own items the stretches are even: at most this many tiles)
+        const int item = p.psegs == 0 ? 0 : kPfxItemCost + (p.Hk * p.ptiles + p.psegs - 1) / p.psegs * kPfxTileCost;
         const int64_t level = static_cast<int64_t>(item) * (grid - rem);  // what evens the CTAs out
         if (rem == 0 || total > level) {
             const int e = (total - (rem == 0 ? 0 : static_cast<int>(level)) + grid - 1) / grid;
@@ -123,6 +129,9 @@ __device__ __forceinline__ int own_len(const PrefixParams& p, int r) { return mi
 __device__ __forceinline__ int seq_cost(int len) { return len > 0 ? kPfxItemCost + (len + 31) / 32 : 0; }
 __device__ __forceinline__ int request_cost(const PrefixParams& p, int len) { return seq_cost(len) * (p.Hk * p.oblocks); }
 
+// Units of one sequence in the own-keys kernel (WarpCut).
+__device__ __forceinline__ int warp_seq_cost(int len) { return len > 0 ? 1 + (len + kOwnStep - 1) / kOwnStep : 0; }
+
 // Inclusive sum over the warp's lanes.
 __device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
@@ -133,24 +142,60 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {
     return v;
 }
 
-// The prefix: one line of Hk * ptiles tiles, cut into even stretches (within
-// each head where their number allows it, so that no stretch crosses heads).  A
-// stretch's tiles at one key head are a piece; pieces in order step either to
-// the next stretch or to the next head (or both), so stretch + head numbers
-// them apart.  The row blocks of a stretch are neighbouring items, which run at
-// the same time and share its K/V in L2.
-__device__ __forceinline__ int stretch_begin(const PrefixParams& p, int k) {
-    const int run = k / p.cut_per, i = k - run * p.cut_per;
-    return run * p.cut_len + i * p.cut_base + min(i, p.cut_rem);
-}
-__device__ __forceinline__ int stretch_of(const PrefixParams& p, int tile) {
-    const int run = tile / p.cut_len, y = tile - run * p.cut_len;
-    const int longer = p.cut_rem * (p.cut_base + 1);  // tiles of the longer stretches
-    return run * p.cut_per + (y < longer ? y / (p.cut_base + 1) : p.cut_rem + (y - longer) / p.cut_base);
-}
-__device__ __forceinline__ int64_t prefix_part(const PrefixParams& p, int k, int head) {
-    return static_cast<int64_t>(k + head) * p.R * p.GT;
-}
+// The cut of the prefix's tiles.  Where the number of stretches allows it each
+// key head is cut by itself (the stretches go head by head, first all early
+// ones, then the others); otherwise the line of all heads' tiles is, and a
+// stretch may cross heads.  A stretch's tiles at one head are a piece.  The row blocks of a stretch are
+// neighbouring items, which run at the same time and share its K/V in L2.
+// The stretches are even, but where the own keys' kernel holds many SMs: the
+// CTAs of the first stretches start beside it, the others after it, so the
+// first are longer by its time in tiles.
+struct PrefixCut {
+    int len, per;           // tiles of a run (a head, or the line), and its stretches
+    int etiles, ebase, erem;  // the early stretches' tiles; each has ebase, the first erem one more
+    int lbase, lrem;        // the others'
+    __device__ __forceinline__ PrefixCut(const PrefixParams& p, int own_total)
+        : len(p.run_len), per(p.run_per), etiles(0), ebase(0), erem(0), lbase(p.even_base), lrem(p.even_rem) {
+        if (p.early == 0) return;
+        // early ones `delta` longer: per * late + early * delta = len, late >= 0  (0 < early < per <= len)
+        const int64_t delta = (static_cast<int64_t>(own_total) * p.lead) >> 20;
+        const int64_t ahead = min(static_cast<int64_t>(len), p.early * delta);
+        const int late = (len - static_cast<int>(ahead)) / per;
+        etiles = len - late * (per - p.early);
+        ebase = etiles / p.early;
+        erem = etiles - ebase * p.early;
+        lbase = late;  // what is left over is the early ones'
+        lrem = 0;
+    }
+    __device__ __forceinline__ int run_begin(const PrefixParams& p, int i) const {
+        return i < p.early ? i * ebase + min(i, erem) : etiles + (i - p.early) * lbase + min(i - p.early, lrem);
+    }
+    // Stretch k as the i-th of a run (of head `run`, or of the line).
+    __device__ __forceinline__ void place(const PrefixParams& p, int k, int& run, int& i) const {
+        run = 0;
+        i = k;
+        if (!p.by_head) return;
+        const int first = p.early * p.Hk, n = k < first ? p.early : per - p.early;
+        const int y = k < first ? k : k - first;
+        run = y / n;
+        i = y - run * n + (k < first ? 0 : p.early);
+    }
+    // The stretch of a run that tile y of it is in.
+    __device__ __forceinline__ int run_of(const PrefixParams& p, int y) const {
+        if (y < etiles) {
+            const int longer = erem * (ebase + 1);
+            return y < longer ? y / (ebase + 1) : erem + (y - longer) / ebase;
+        }
+        y -= etiles;
+        const int longer = lrem * (lbase + 1);
+        return p.early + (y < longer ? y / (lbase + 1) : lrem + (y - longer) / lbase);
+    }
+    // Partial rows of the piece of a run's i-th stretch at a head (the row blocks are parts of them).  In the
+    // line, pieces in order step to the next stretch or to the next head, so that their sum numbers them apart.
+    __device__ __forceinline__ int64_t part(const PrefixParams& p, int i, int head) const {
+        return static_cast<int64_t>(p.by_head ? head * per + i : i + head) * p.R * p.GT;
+    }
+};
 
 struct PrefixItem {
     int ntiles;      // -1: no more items
@@ -588,18 +633,27 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
         };
         PrefixItem it;
         it.pad = 0;
+        int own_total = 0;
+        if (p.early > 0) {  // (with the own-keys kernel)
+#pragma unroll 4
+            for (int r = lane; r < p.R; r += 32) own_total += warp_seq_cost(own_len(p, r));
+            own_total = __reduce_add_sync(0xffffffffu, own_total) * (p.Hk * p.oblocks);
+        }
+        const PrefixCut cut(p, own_total);
         for (int i = blockIdx.x; i < p.pitems && ok; i += gridDim.x) {
             const int blk = i % p.pblocks, k = i / p.pblocks;
             it.req = -1;
             it.klen = p.P;
             it.row0 = blk * 2 * p.qrows;
             it.nrows = min(2 * p.qrows, p.R * p.GT - it.row0);
-            const int end = stretch_begin(p, k + 1);
-            for (int x = stretch_begin(p, k); x < end && ok; x += it.ntiles) {
+            int run, nth;
+            cut.place(p, k, run, nth);
+            const int base = run * cut.len, end = base + cut.run_begin(p, nth + 1);
+            for (int x = base + cut.run_begin(p, nth); x < end && ok; x += it.ntiles) {
                 it.head = x / p.ptiles;
                 it.tile0 = x - it.head * p.ptiles;
                 it.ntiles = min(end - x, p.ptiles - it.tile0);
-                it.part = prefix_part(p, k, it.head) + it.row0;
+                it.part = cut.part(p, nth, it.head) + it.row0;
                 publish(it);
             }
         }
@@ -615,9 +669,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
             mine *= p.Hk * p.oblocks;
             const int upto = warp_scan(mine, lane);
             const int total = __shfl_sync(0xffffffffu, upto, 31);
-            const OwnCut cut(p, total, gridDim.x);
-            const int x0 = static_cast<int>(min(cut.begin(blockIdx.x), static_cast<int64_t>(total)));
-            const int x1 = static_cast<int>(min(cut.begin(blockIdx.x + 1), static_cast<int64_t>(total)));
+            const OwnCut own(p, total, gridDim.x);
+            const int x0 = static_cast<int>(min(own.begin(blockIdx.x), static_cast<int64_t>(total)));
+            const int x1 = static_cast<int>(min(own.begin(blockIdx.x + 1), static_cast<int64_t>(total)));
             if (x0 < x1) {
                 const int at = __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
                 int start = __shfl_sync(0xffffffffu, upto - mine, at);  // of request r0
@@ -1033,10 +1087,11 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
 // these instructions does not matter, and a 128-row tcgen05 tile would be
 // seven eighths empty.
 // ---------------------------------------------------------------------------
-// Eight warps with two steps of 16 keys in flight each (128 KB an SM): 64 pieces of 16384 keys in 92 us
-// (5.8 TB/s), 2048 of 256 in 55 us; six with three: 97 and 57 us, four with four: 91 and 58 us, three with five: 115 and 71 us.
+// Eight warps with two steps of 16 keys in flight each (128 KB an SM): 64 pieces of 16384 keys in 91 us
+// (5.9 TB/s), 2048 of 256 in 54 us.  A warp's own chain (wait, products, softmax, next copies) is
+// about 1 us a step, so warps count and depth does not: seven with three steps 94 and 56 us, six with
+// four 101 and 59 us, five with four 121 and 66 us.
 constexpr int kOwnWarps = 8;
-constexpr int kOwnStep = 16;
 constexpr int kOwnRows = 16;
 // Requests with more rows take several row blocks, whose K/V come from L2 for all but the first.
 // That pays up to kOwnMostRows rows (four blocks) on short caches: 64 requests x 8 heads of 20 rows, 64 keys
@@ -1047,10 +1102,12 @@ constexpr int kOwnMostKeys = 1024;   // of a cache, for requests of more than on
 
 template <int D>
 struct OwnSmem {
-    static constexpr int kPart = kOwnStep * D * 2;         // K, V or Q of a step
-    static constexpr int kStage = 3 * kPart;
+    static constexpr int kPart = kOwnStep * D * 2;         // K or V of a step, or Q of a piece
+    static constexpr int kStage = 2 * kPart;
     static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr int kWarp = kStages * kStage;
+    static constexpr int kQSlots = 2;                      // pieces whose Q may be in flight or waiting
+    static constexpr int kQOff = kStages * kStage;
+    static constexpr int kWarp = kQOff + kQSlots * kPart;
     static constexpr int kStepOff = kOwnWarps * kWarp;     // [warps][stages] OwnStep
     static constexpr int kBarOff = kStepOff + kOwnWarps * kStages * 32;
     static constexpr int kFlagOff = kBarOff + kOwnWarps * kStages * 8;
@@ -1075,7 +1132,6 @@ struct WarpCut {
         if (cap < 1) cap = 1;
     }
 };
-__device__ __forceinline__ int warp_seq_cost(int len) { return len > 0 ? 1 + (len + kOwnStep - 1) / kOwnStep : 0; }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -1192,8 +1248,10 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         settle();
     }
     uint32_t filled = 0, used = 0;
-    auto issue = [&]() {
-        if (!more) return;
+    uint32_t q_filled = 0, q_used = 0;   // pieces whose Q was asked for, and read
+    // Asks for the next step while there is a stage for it, and a place for its Q if it begins a piece.
+    auto issue = [&]() -> bool {
+        if (!more || filled - used == L::kStages || (s == s_first && q_filled - q_used == L::kQSlots)) return false;
         const uint32_t st = filled % L::kStages;
         if (lane == 0) {
             OwnStep d;
@@ -1212,13 +1270,16 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
 #pragma unroll
             for (int b = 0; b < D / 64; ++b) {
                 const uint32_t o = dst + b * (kOwnStep * 128);
-                if (d.edge & 1) tma_load_5d(o + 2 * L::kPart, &tmap_q, full, b * 64, 0, blk * p.orows / p.T, d.head, r);
+                if (d.edge & 1)
+                    tma_load_5d(ring + L::kQOff + (q_filled % L::kQSlots) * L::kPart + b * (kOwnStep * 128), &tmap_q, full, b * 64,
+                                0, blk * p.orows / p.T, d.head, r);
                 tma_load_4d(o, &tmap_k, full, b * 64, d.key0, d.head, r);
                 tma_load_4d(o + L::kPart, &tmap_v, full, b * 64, d.key0, d.head, r);
             }
         }
         __syncwarp();
         ++filled;
+        if (s == s_first) ++q_filled;
         if (++s == s1) {
             start += warp_seq_cost(len);
             if (++h == seqs) {
@@ -1227,8 +1288,10 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
             }
             settle();
         }
+        return true;
     };
-    for (int i = 0; i < L::kStages; ++i) issue();
+    while (issue()) {
+    }
 
     // ---- the consuming side
     uint32_t qf[D / 16][4];
@@ -1251,15 +1314,17 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
     const uint32_t k_row = (lane & 7) + ((lane >> 4) << 3), k_ch = (lane >> 3) & 1;
     const float sign = p.negate_scores ? -1.f : 1.f;
     bool ok = true;
-    for (; used < filled; ++used) {
+    while (used < filled) {
         const uint32_t st = used % L::kStages;
         ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * st, (used / L::kStages) & 1u, ctx));
         if (!ok) break;
-        const uint32_t kb = ring + st * L::kStage, vb = kb + L::kPart, qb = vb + L::kPart;
+        const uint32_t kb = ring + st * L::kStage, vb = kb + L::kPart;
         const OwnStep d = steps[st];
         if (d.edge & 1) {
             valid[0] = row0 < d.rows;
             valid[1] = row0 + 8 < d.rows;
+            const uint32_t qb = ring + L::kQOff + (q_used % L::kQSlots) * L::kPart;
+            ++q_used;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t c = 2 * kk + qv_ch;
@@ -1346,7 +1411,9 @@ attn_prefix_own_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
             mma_16816(o[2 * j + 1], pf, vf[2], vf[3]);
         }
         __syncwarp();  // every lane has read the step
-        issue();
+        ++used;
+        while (issue()) {
+        }
         if (d.edge & 2) {
             const uint64_t keep = l2_policy_evict_last();
 #pragma unroll
@@ -1408,21 +1475,25 @@ __global__ void __launch_bounds__(256) attn_prefix_combine_kernel(const __grid_c
     const int h = rem / p.GT, x = rem - h * p.GT;  // key head, row within the request
     const int raw_len = p.lens ? __ldg(p.lens + r) : 0;  // an input: no need to wait for it
     const bool on = row < rows && raw_len >= 0;
-    const int64_t pstep = static_cast<int64_t>(p.R) * p.GT;
+    int64_t pstep = 0, pfirst = 0;
     int segs = 0;
-    int64_t pfirst = 0;
-    if (p.P > 0) {
-        const int tile = h * p.ptiles;
-        const int k0 = stretch_of(p, tile);
-        segs = stretch_of(p, tile + p.ptiles - 1) - k0 + 1;
-        pfirst = prefix_part(p, k0, h) + static_cast<int64_t>(r) * p.GT + x;
-    }
     int64_t ofirst = 0;
-    int pieces = on ? segs : 0;
+    auto find_prefix = [&](int own_total) {
+        if (!on || p.P == 0) return;
+        const PrefixCut cut(p, own_total);
+        const int base = p.by_head ? 0 : h * p.ptiles;  // the head's first tile in its run
+        const int i0 = cut.run_of(p, base);
+        segs = cut.run_of(p, base + p.ptiles - 1) - i0 + 1;
+        pfirst = cut.part(p, i0, h) + static_cast<int64_t>(r) * p.GT + x;
+        pstep = static_cast<int64_t>(p.R) * p.GT;
+    };
+    if (p.early == 0) find_prefix(0);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = min(raw_len, p.C);
+    const int total = p.C > 0 ? __ldcg(p.own_start + p.R) : 0;
+    if (p.early > 0) find_prefix(total);
+    int pieces = segs;
     if (on && len > 0) {
-        const int total = __ldcg(p.own_start + p.R);
         int a, b;
         const int q = h * p.oblocks + x / p.orows;
         if (p.workers > 0) {

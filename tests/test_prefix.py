@@ -180,6 +180,22 @@ def test_parity(lib, shape):
 
 
 @gpu
+@pytest.mark.parametrize("lens", ["zero", "short", "full", "one", "any"])
+@pytest.mark.parametrize("R,Hq,Hk,d,P,C", [(40, 16, 8, 64, 16384, 500), (256, 32, 8, 128, 5000, 100), (120, 3, 3, 128, 20001, 400)])
+def test_prefix_beside_the_own_keys(lib, R, Hq, Hk, d, P, C, lens):
+    """Shapes whose prefix starts beside the own-keys kernel, on stretches that follow from the lengths."""
+    n = {"zero": lambda i: 0, "short": lambda i: 1 + i % 7, "full": lambda i: C, "one": lambda i: C if i == 3 else 0,
+         "any": lambda i: (i * 37) % (C + 1) - (i % 11 == 0)}[lens]
+    s = make(R, Hq, Hk, 1, d, P, C, [n(i) for i in range(R)], seed=R)
+    out = torch.full((R, Hq, 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((R, Hq, 1), 7.0, device="cuda")
+    ela.attn_fwd_prefix(**s, out=out, lse=lse)
+    check(s, out, lse, requests=range(0, R, 5))
+    pad = s["own_lens"] < 0
+    assert (out[pad] == 7.0).all() and torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+@gpu
 def test_rows_without_any_key(lib):
     """No prefix and no own keys for a request, or for its first tokens: O = 0, LSE = -inf."""
     s = make(4, 4, 2, 3, 64, 0, 50, [0, 1, 2, 50], seed=1)

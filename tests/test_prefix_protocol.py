@@ -24,6 +24,88 @@ def cdiv(a, b):
     return -(-a // b)
 
 
+class PrefixCut:
+    """The cut of the prefix's tiles into stretches, the first `early` of a run longer."""
+
+    def __init__(self, Hk, ptiles, psegs, early, lead, own_total):
+        self.Hk, self.ptiles, self.psegs, self.early = Hk, ptiles, psegs, early
+        self.by_head = psegs % Hk == 0
+        self.len = ptiles if self.by_head else ptiles * Hk
+        self.per = psegs // Hk if self.by_head else psegs
+        assert 0 <= early < self.per <= self.len
+        self.etiles = self.ebase = self.erem = 0
+        self.lbase, self.lrem = divmod(self.len, self.per)
+        if early:
+            ahead = min(self.len, early * (own_total * lead >> 20))
+            late = (self.len - ahead) // self.per
+            self.etiles = self.len - late * (self.per - early)
+            self.ebase, self.erem = divmod(self.etiles, early)
+            self.lbase, self.lrem = late, 0
+
+    def run_begin(self, i):
+        if i < self.early:
+            return i * self.ebase + min(i, self.erem)
+        return self.etiles + (i - self.early) * self.lbase + min(i - self.early, self.lrem)
+
+    def place(self, k):
+        if not self.by_head:
+            return 0, k
+        first = self.early * self.Hk
+        n, y = (self.early, k) if k < first else (self.per - self.early, k - first)
+        return y // n, y % n + (0 if k < first else self.early)
+
+    def begin(self, k, past):
+        run, i = self.place(k)
+        return run * self.len + self.run_begin(i + past)
+
+    def run_of(self, y):
+        if y < self.etiles:
+            longer = self.erem * (self.ebase + 1)
+            return y // (self.ebase + 1) if y < longer else self.erem + (y - longer) // self.ebase
+        y -= self.etiles
+        longer = self.lrem * (self.lbase + 1)
+        return self.early + (y // (self.lbase + 1) if y < longer else self.lrem + (y - longer) // self.lbase)
+
+    def slot(self, k, head):
+        return head * self.per + self.place(k)[1] if self.by_head else k + head
+
+    def head_slots(self, h):
+        """Where the combine kernel looks for a head's pieces."""
+        base = 0 if self.by_head else h * self.ptiles
+        i0 = self.run_of(base)
+        n = self.run_of(base + self.ptiles - 1) - i0 + 1
+        return [(h * self.per if self.by_head else h) + i0 + i for i in range(n)]
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_the_cut_of_the_prefix(seed):
+    """Every tile once, every piece in a slot of its own, and the slots that are read are those written."""
+    rng = random.Random(seed)
+    for _ in range(60):
+        Hk, ptiles = rng.choice([1, 2, 3, 4, 8]), rng.choice([1, 2, 3, 7, 19, 64, 200])
+        psegs = rng.choice([n for n in (1, 2, 3, 5, 8, 16, 19, 24, 38, 64, 152) if n <= Hk * ptiles])
+        per = psegs // Hk if psegs % Hk == 0 else psegs
+        early = rng.randrange(per)
+        c = PrefixCut(Hk, ptiles, psegs, early, rng.choice([0, 891, 1 << 20]), rng.choice([0, 1, 500, 20000, 1 << 29]))
+        seen, slots = set(), {}
+        for k in range(psegs):
+            x, end = c.begin(k, 0), c.begin(k, 1)
+            assert x <= end
+            while x < end:
+                head = x // ptiles
+                n = min(end - x, (head + 1) * ptiles - x)
+                tiles = set(range(x, x + n))
+                assert not tiles & seen and c.slot(k, head) not in slots
+                assert 0 <= c.slot(k, head) < psegs + (0 if c.by_head else Hk - 1)
+                seen |= tiles
+                slots[c.slot(k, head)] = head
+                x += n
+        assert seen == set(range(Hk * ptiles))
+        for h in range(Hk):
+            read = c.head_slots(h)
+            assert len(set(read)) == len(read) and set(read) == {s for s, head in slots.items() if head == h}
+
+
 class Layout:
     def __init__(self, R, Hk, G, T, P, C, grid):
         self.R, self.Hk, self.GT, self.T, self.P, self.C, self.grid = R, Hk, G * T, T, P, C, grid
@@ -43,22 +125,10 @@ class Layout:
                 if best is None or cost < best:
                     best, self.psegs = cost, n
             self.pitems = self.pblocks * self.psegs
-            by_head = self.psegs % Hk == 0
-            self.cut_len = self.ptiles if by_head else self.line
-            self.cut_per = self.psegs // Hk if by_head else self.psegs
-            self.cut_base, self.cut_rem = divmod(self.cut_len, self.cut_per)
-            assert self.cut_base >= 1
-        self.own_first = (self.psegs + Hk - 1) * R * self.GT if self.psegs else 0
+            self.cut = PrefixCut(Hk, self.ptiles, self.psegs, 0, 0, 0)
+        by_head = self.psegs % Hk == 0
+        self.own_first = (self.psegs + (0 if by_head else Hk - 1)) * R * self.GT if self.psegs else 0
         self.rows = self.own_first + ((R * Hk * self.oblocks + grid) * self.orows if C else 0)
-
-    def stretch_begin(self, k):
-        run, i = divmod(k, self.cut_per)
-        return run * self.cut_len + i * self.cut_base + min(i, self.cut_rem)
-
-    def stretch_of(self, tile):
-        run, y = divmod(tile, self.cut_len)
-        longer = self.cut_rem * (self.cut_base + 1)
-        return run * self.cut_per + (y // (self.cut_base + 1) if y < longer else self.cut_rem + (y - longer) // self.cut_base)
 
     def seq_cost(self, n):
         return ITEM + cdiv(n, 32) if n > 0 else 0
@@ -68,7 +138,7 @@ class Cut:
     def __init__(self, L, total):
         g = L.grid
         self.rem = L.pitems % g
-        item = ITEM + (L.cut_base + (L.cut_rem > 0)) * TILE if L.psegs else 0
+        item = ITEM + cdiv(L.line, L.psegs) * TILE if L.psegs else 0
         level = item * (g - self.rem)
         if self.rem == 0 or total > level:
             e = cdiv(total - (0 if self.rem == 0 else level), g)
@@ -92,13 +162,14 @@ def schedule(L, lens, cta):
     for i in range(cta, L.pitems, L.grid):
         blk, k = i % L.pblocks, i // L.pblocks
         row0 = blk * L.two
-        x, end = L.stretch_begin(k), L.stretch_begin(k + 1)
-        assert x < end and all(L.stretch_of(t) == k for t in (x, end - 1))
+        x, end = L.cut.begin(k, 0), L.cut.begin(k, 1)
+        assert x < end
         while x < end:
             head = x // L.ptiles
             t0 = x - head * L.ptiles
             n = min(end - x, L.ptiles - t0)
-            out.append((-1, head, row0, min(L.two, L.R * L.GT - row0), t0, n, (k + head) * L.R * L.GT + row0))
+            out.append((-1, head, row0, min(L.two, L.R * L.GT - row0), t0, n,
+                        L.cut.slot(k, head) * L.R * L.GT + row0))
             x += n
     if not L.C:
         return out
@@ -138,8 +209,7 @@ def combine_rows(L, lens, r, h, x):
     """The partial rows the combine kernel merges for row x of request r at key head h."""
     rows = []
     if L.ptiles:
-        first, last = (L.stretch_of(t) for t in (h * L.ptiles, (h + 1) * L.ptiles - 1))
-        rows = [(k + h) * L.R * L.GT + r * L.GT + x for k in range(first, last + 1)]
+        rows = [slot * L.R * L.GT + r * L.GT + x for slot in L.cut.head_slots(h)]
     n = min(lens[r], L.C) if L.C else 0
     if n > 0:
         seqs = L.Hk * L.oblocks
