@@ -352,8 +352,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // Reads the next item (ring entry n); `it.ntiles` is -1 after the last.
-    // Called by whole warps, or by one lane (whole = false).
-    auto take_item = [&](uint32_t n, PrefixItem& it, bool whole) -> bool {
+    // Called by whole warps, or by one lane (whole = false).  keep: the caller
+    // gives the ring entry back itself (the softmax warps read it again at the item's end).
+    auto take_item = [&](uint32_t n, PrefixItem& it, bool whole, bool keep = false) -> bool {
         const uint32_t s = n % kPfxItemRing;
         bool got = mbar_wait(bar(L::kItemFull + s), (n / kPfxItemRing) & 1u, ctx);
         if (whole) got = __all_sync(0xffffffffu, got);
@@ -375,7 +376,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
         } else {
             it = *reinterpret_cast<const PrefixItem*>(from);
         }
-        if (!whole || lane == 0) mbar_arrive(bar(L::kItemEmpty + s));
+        if (!keep && (!whole || lane == 0)) mbar_arrive(bar(L::kItemEmpty + s));
         return it.ntiles >= 0;
     };
     // Keys of the item's tile j (1 .. 128).
@@ -800,36 +801,40 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
         uint32_t par = 0;
         bool ok = true;
         PrefixItem it;
-        for (uint32_t n = 0; ok && take_item(n, it, true); ++n) {
+        for (uint32_t n = 0; ok && take_item(n, it, true, true); ++n) {
             const bool two = it.nrows > p.qrows;
+            const int nt = it.ntiles;
+            const bool own = it.req >= 0;
             const int mine = two ? t : t ^ static_cast<int>(par);  // this chain's query tile, or its first K/V tile
             const int k = two ? mine : 0;                     // its query tile
             const int nrow = min(p.qrows, it.nrows - k * p.qrows);
             const bool warp_on = quad * 32 < nrow;            // the warp has rows
             const bool row_on = rloc < nrow;
-            const bool both = two || it.ntiles >= 2;          // both chains work on the item
+            const bool both = two || nt >= 2;                 // both chains work on the item
             const bool used = both || mine == 0;
             float m_ref = -INFINITY;
             float l = 0.f;
             if (used) {
-                // keys this row sees: all of the source, but for later tokens of its own request
-                int lim = it.klen;
-                if (it.req >= 0 && p.T > 1) {
+                // Key counts from the item's first tile on: all of the source's, and those that this row
+                // sees (not the later tokens' of its own request) and every row does.
+                const int left = it.klen - it.tile0 * kBc;
+                int lim = left;
+                if (own && p.T > 1) {
                     const int x = it.row0 + k * p.qrows + min(rloc, nrow - 1) - it.req * p.GT;
                     lim -= p.T - 1 - x % p.T;
                 }
-                const int all_see = it.klen - (it.req >= 0 ? p.T - 1 : 0);  // keys below this are seen by every row
+                const int all_see = left - (own ? p.T - 1 : 0);
                 bool first = true;
-                for (int j = two ? 0 : mine; j < it.ntiles; j += two ? 1 : 2) {
+                for (int j = two ? 0 : mine; j < nt; j += two ? 1 : 2) {
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kSFull + t), s_cnt & 1u, ctx));
                     ++s_cnt;
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const int key0 = (it.tile0 + j) * kBc;
-                    const int keys = tile_keys(it, j);
+                    const int key0 = j * kBc;
+                    const int keys = min(kBc, left - key0);
                     // The output product sums over keys in steps of 16.  Own-cache rows past the
                     // last key may hold anything (a NaN times a zero weight is a NaN): zero them.
-                    if (it.req >= 0 && k == 0 && (keys & 15) != 0) {
+                    if (own && k == 0 && (keys & 15) != 0) {
                         const uint32_t at = ring + 2 * j + 1;  // V_j's fill
                         const uint32_t stage = at % L::kStages;
                         ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvFull + stage), (at / L::kStages) & 1u, ctx));
@@ -945,9 +950,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
                         for (int i = 0; i < nch; ++i) {
                             tmem_ld32(t_s + 32 * i, r);
                             tmem_wait_ld(r);
-                            const int left = lim - key0 - 32 * i;  // visible keys from here on
+                            const int seen = lim - key0 - 32 * i;  // visible keys from here on
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) mx = fmaxf(mx, c < left ? sc[c] : -INFINITY);
+                            for (int c = 0; c < 32; ++c) mx = fmaxf(mx, c < seen ? sc[c] : -INFINITY);
                         }
                         refer(mx);
                         rescale();
@@ -955,10 +960,10 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
                         for (int i = 0; i < nch; ++i) {
                             tmem_ld32(t_s + 32 * i, r);
                             tmem_wait_ld(r);
-                            const int left = lim - key0 - 32 * i;
+                            const int seen = lim - key0 - 32 * i;
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                if (c >= left) sc[c] = -INFINITY;
+                                if (c >= seen) sc[c] = -INFINITY;
                             exp_chunk(sc, 16 * i);
                         }
                         tmem_wait_st();
@@ -1001,12 +1006,14 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
                 // a row that sees no key of this piece: O = 0, LSE = -inf
                 const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
                 if (warp_on) {
+                    const int64_t part = reinterpret_cast<const volatile PrefixItem*>(
+                                             smem + L::kItemOff + (n % kPfxItemRing) * sizeof(PrefixItem))->part + k * p.qrows;
                     const int c0 = merge ? t * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
                     const float wa = w_own * inv, wb = w_other * inv;
                     // evict-last: read back right after this grid
                     const uint64_t keep = l2_policy_evict_last();
                     const int here = nrow - quad * 32;  // rows of this warp
-                    float* out = p.part_o + (it.part + k * p.qrows + quad * 32 + (lane >> 2)) * D + (lane & 3) * 2;
+                    float* out = p.part_o + (part + quad * 32 + (lane >> 2)) * D + (lane & 3) * 2;
 #pragma unroll 1
                     for (int half = 0; half < 32 && half < here; half += 16) {
                         // the weights of this thread's two rows
@@ -1046,7 +1053,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
                         }
                     }
                     if (row_on && (!merge || t == 0))
-                        st_global_hint(p.part_lse + it.part + k * p.qrows + rloc,
+                        st_global_hint(p.part_lse + part + rloc,
                                        sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2, keep);
                 }
                 tc_fence_before_sync();
@@ -1059,8 +1066,10 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tmap_qp, const __grid_con
                 }
             }
             o_phase ^= both ? 3u : 1u << par;
-            ring += 2 * it.ntiles;
-            par = two ? 0u : (par + it.ntiles) & 1u;
+            ring += 2 * nt;
+            par = two ? 0u : (par + nt) & 1u;
+            __syncwarp();  // every lane has read the ring entry
+            if (lane == 0) mbar_arrive(bar(L::kItemEmpty + n % kPfxItemRing));
         }
     }
 

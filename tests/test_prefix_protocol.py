@@ -495,7 +495,6 @@ def run(items, seed, stages=STAGES, o_empty_twice=True):
         o_cnt = [0, 0]
         for n, it in enumerate(entries):
             yield from take(n)
-            B[("ItemEmpty", n % RING)].arrive(4)
             if it is None:
                 return
             two, nt, tail = it
@@ -542,6 +541,8 @@ def run(items, seed, stages=STAGES, o_empty_twice=True):
                     o_cnt[c] += 1
             ring += 2 * nt
             par = 0 if two else (par + steps) & 1
+            need(slot_item[n % RING], n, "the item at its end")
+            B[("ItemEmpty", n % RING)].arrive(4)
 
     roles = {"scheduler": scheduler(), "producer": producer(), "qloader": qloader(), "mma": mma(), "softmax0": softmax(0),
              "softmax1": softmax(1)}
