@@ -157,6 +157,10 @@ SHAPES = [
     (50, 12, 2, 3, 128, 700, 40, [(3 * i) % 41 for i in range(50)], True),  # 18 rows a request: tiles of 126 rows
     (5, 20, 2, 3, 128, 100, 1100, [1100, 0, 2, 700, 129], False),   # 30 rows, caches too long for row blocks
     (5, 20, 2, 3, 64, 100, 700, [700, 0, 2, 16, 129], True),        # 30 rows in blocks of 15
+    (5, 20, 2, 3, 64, 0, 700, [700, 0, 2, 16, 129], True),          # ... without a prefix: the own-keys kernel
+    (3, 44, 4, 4, 128, 0, 64, [64, 17, 5], False),
+    (60, 21, 3, 3, 128, 100, 90, [(7 * i) % 91 for i in range(60)], True),  # 180 sequences beside a prefix
+    (200, 4, 1, 1, 64, 300, 50, [(3 * i) % 51 for i in range(200)], False),
     (3, 44, 4, 4, 128, 60, 64, [64, 17, 5], False),                 # 44 rows in blocks of 16, the last of 12
     (9, 33, 1, 2, 64, 300, 20, [20] * 9, False),                    # 66 rows a request: one a tile
     (3, 128, 1, 1, 128, 300, 33, [33, 0, 7], False),                # 128 rows a request: one a tile
@@ -284,8 +288,9 @@ def test_views_workspace_and_outputs_stay_inside_their_buffers(lib):
 
 
 @gpu
-def test_streams_graphs_and_repeated_calls(lib):
-    R, Hq, Hk, T, d, P, C = 30, 8, 2, 1, 128, 2000, 300
+@pytest.mark.parametrize("R", [30, 100])  # own keys as items of the prefix kernel, and in a kernel of their own
+def test_streams_graphs_and_repeated_calls(lib, R):
+    Hq, Hk, T, d, P, C = 8, 2, 1, 128, 2000, 300
     lens = [(13 * i) % 301 for i in range(R)]
     s = make(R, Hq, Hk, T, d, P, C, [C] * R, seed=7)
     s["own_lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -300,7 +305,8 @@ def test_streams_graphs_and_repeated_calls(lib):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         g = ela.attn_fwd_prefix(**s)
-    for shift in (0, 1, 100):  # other lengths and queries in the same buffers
+    # other lengths and queries in the same buffers (the caches hold numbers up to their capacity)
+    for shift in (0, 1, 100):
         s["own_lens"].copy_(torch.tensor([(n + shift) % 301 for n in lens], dtype=torch.int32))
         s["q"].copy_(s["q"].roll(shift, 0))
         graph.replay()
@@ -311,7 +317,7 @@ def test_streams_graphs_and_repeated_calls(lib):
 
 @gpu
 def test_two_calls_at_once_with_a_workspace_each(lib):
-    s = make(16, 8, 2, 1, 128, 3000, 200, [12 * i for i in range(16)], seed=8)
+    s = make(100, 8, 2, 1, 128, 3000, 200, [2 * i for i in range(100)], seed=8)
     t = make(16, 8, 2, 1, 128, 3000, 200, [200 - 12 * i for i in range(16)], seed=9)
     want = ela.attn_fwd_prefix(**s), ela.attn_fwd_prefix(**t)
     torch.cuda.synchronize()
@@ -325,8 +331,9 @@ def test_two_calls_at_once_with_a_workspace_each(lib):
 
 
 @gpu
-def test_a_nonfinite_request_stays_alone(lib):
-    s = make(5, 8, 2, 1, 64, 300, 60, [60, 60, 30, 7, 60], seed=10)
+@pytest.mark.parametrize("P", [300, 0])
+def test_a_nonfinite_request_stays_alone(lib, P):
+    s = make(5, 8, 2, 1, 64, P, 60, [60, 60, 30, 7, 60], seed=10)
     clean = ela.attn_fwd_prefix(**s)
     s["k_own"][1, 0, 3, 5] = float("nan")
     s["v_own"][3, 1, 2, 9] = float("inf")
