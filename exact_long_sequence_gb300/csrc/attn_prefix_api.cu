@@ -42,7 +42,7 @@ constexpr double kPlanPiece = 8.0;
 constexpr double kPlanRow = 4.2e-4;
 
 // The own-keys kernel is bound by HBM and the prefix, with many rows, by the
-// tensor core.  The former runs at 5 of its 5.9 TB/s on 88 SMs, so that is what it gets
+// tensor core.  The former reads 5.9 TB/s on all SMs, 5.3 on 96 and 4.4 on 76, so about 5 on 88, which is what it gets
 // where there is a prefix to run beside it; a step of 16 keys of 128 then takes
 // 1 / 976 of a prefix tile's time.  Measured, own kernel on all SMs -> on 88: 64 requests on
 // 16384 keys, up to 1024 own 60.4 -> 53.7 us (96 SMs 57.4, 80 52.1, 72 55.4 us), with 1024 own each 78.9 -> 77.3
@@ -74,6 +74,7 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
     // Beside a prefix, up to one sequence an SM are items of the prefix kernel: that takes the GPU as
     // long and saves the host a launch (8 requests x 8 heads on 1000 keys: 15.6 us, 16.5 us with the own kernel, a call
     // from the host 19 and 25 us; 128 x 1 on 8192: 24.7 and 26.4 us; but 128 sequences of 40 keys 18.6 and 16.6 us).
+    // On long caches the two meet at the boundary (8 heads, 8192 own keys: 19 requests 112.3 us, 20 with the own kernel 111.3).
     p.workers = 0;
     const bool few = s.P > 0 && static_cast<int64_t>(s.R) * s.Hk <= num_sms;
     if (s.C > 0 && !few && s.T <= kOwnRows && (p.GT <= kOwnRows || (p.GT <= kOwnMostRows && s.C <= kOwnMostKeys))) {

@@ -468,7 +468,7 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
  * Arithmetic as attn_fwd (fp32 scores and sums, P rounded to bf16); pieces are
  * kept in fp32, O is rounded once.  The cut into pieces depends on the own
  * lengths, so bits may differ between batches, not between equal calls.
- * Two launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
+ * Two or three launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
  */
 int attn_fwd_prefix(const void* Q, const int64_t* q_strides, const void* Kp, const int64_t* kp_strides, const void* Vp,
                     const int64_t* vp_strides, const void* Ko, const int64_t* ko_strides, const void* Vo,
