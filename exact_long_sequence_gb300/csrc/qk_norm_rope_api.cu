@@ -49,9 +49,9 @@ int fill_params(ReadyParams& p, const int32_t* positions, int64_t pos_axis, int6
     p.t[1].H = Hk;
     // Several tokens side by side in a warp step, for tensors with few heads.
     // That walk costs about a fifth more per step (32768 tokens of 32 + 8 heads
-    // of 128, backward: 201 us against 165 us) and saves steps where a tensor's
+    // of 128, backward: 191 us against 163 us) and saves steps where a tensor's
     // heads fill less than a step (65536 tokens of 1 + 1 heads of 64,
-    // backward: 36 us against 109 us).
+    // backward: 33 us against 96 us).
     double one = 0, several = 0;
     int hp[2], tp[2];
     for (int i = 0; i < 2; ++i) {
