@@ -191,6 +191,21 @@ def _stream_handle(stream):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream, returned=True):
+    """An uninitialised tensor for a call on `stream` (None: the current one), from that stream's memory: a
+    block of the current stream may be one that its earlier work, still running, uses.  returned: the
+    caller gets the tensor, and may free it while its own stream still reads it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream must be a stream of the tensors' device {device}")
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def split_workspace_bytes(B: int, H: int, N: int, d: int, causal: bool) -> int:
     """Device bytes attn_fwd_split needs for this shape on the current device (0: none)."""
     return int(load_library().attn_fwd_split_workspace_bytes(B, H, N, d, int(bool(causal))))
@@ -388,13 +403,6 @@ def _raw_stream(stream, index):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _new_for(stream, *tensors):
-    """Tensors allocated here on the current stream and used on `stream`."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
-
-
 def _view(name, t, shape, index):
     """Checks a bf16 view with its last axis contiguous; returns its address and the other axes' strides
     as the C call's host array (None: contiguous)."""
@@ -464,14 +472,10 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, sectio
         with torch.cuda.device(index):
             return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, sections, eps, interleaved, q_out, k_out,
                                 stream)
-    fresh = []
     if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
-        fresh.append(q_out)
+        q_out = _empty((B, Hq, N, d), torch.bfloat16, q.device, stream)
     if k_out is None:
-        k_out = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
-        fresh.append(k_out)
-    _new_for(stream, *fresh)
+        k_out = _empty((B, Hk, N, d), torch.bfloat16, q.device, stream)
     qp, qs = _view("q", q, q.shape, index)
     kp, ks = _view("k", k, k.shape, index)
     qop, qos = _view("q_out", q_out, q.shape, index)
@@ -511,23 +515,17 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k
         with torch.cuda.device(index):
             return qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight, sections, eps,
                                     interleaved, dq, dk, workspace, stream)
-    fresh = []
     if dq is None:
-        dq = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
-        fresh.append(dq)
+        dq = _empty((B, Hq, N, d), torch.bfloat16, q.device, stream)
     if dk is None:
-        dk = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
-        fresh.append(dk)
-    dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
-    dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
-    fresh += [t for t in (dwq, dwk) if t is not None]
+        dk = _empty((B, Hk, N, d), torch.bfloat16, q.device, stream)
+    dwq = None if q_weight is None else _empty((d,), torch.float32, q.device, stream)
+    dwk = None if k_weight is None else _empty((d,), torch.float32, q.device, stream)
     if workspace is None and (dwq is not None or dwk is not None):
-        workspace = torch.empty(_bwd_workspace_bytes(index, d), dtype=torch.uint8, device=q.device)
-        fresh.append(workspace)
+        workspace = _empty((_bwd_workspace_bytes(index, d),), torch.uint8, q.device, stream, returned=False)
     if workspace is not None and (workspace.dtype != torch.uint8 or workspace.get_device() != index or
                                   not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    _new_for(stream, *fresh)
     gqp, gqs = _view("dq_out", dq_out, q.shape, index)
     gkp, gks = _view("dk_out", dk_out, k.shape, index)
     qp, qs = _view("q", q, q.shape, index)
@@ -602,22 +600,17 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
     if _elsewhere(index):
         with torch.cuda.device(index):
             return attn_fwd_prefix(q, k_prefix, v_prefix, k_own, v_own, own_lens, scale, out, lse, workspace, stream)
-    fresh = []
     if out is None:
-        out = torch.empty((R, Hq, T, d), dtype=torch.bfloat16, device=q.device)
-        fresh.append(out)
+        out = _empty((R, Hq, T, d), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((R, Hq, T), dtype=torch.float32, device=q.device)
-        fresh.append(lse)
+        lse = _empty((R, Hq, T), torch.float32, q.device, stream)
     elif lse.dtype != torch.float32 or lse.get_device() != index or lse.shape != (R, Hq, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [R, Hq, T] on q's device")
     if workspace is None:
-        workspace = torch.empty(_prefix_workspace_bytes(index, R, Hq, Hk, T, P, C, d), dtype=torch.uint8,
-                                device=q.device)
-        fresh.append(workspace)
+        workspace = _empty((_prefix_workspace_bytes(index, R, Hq, Hk, T, P, C, d),), torch.uint8, q.device, stream,
+                           returned=False)
     elif workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    _new_for(stream, *fresh)
     qp, qs = _view("q", q, q.shape, index)
     op, os_ = _view("out", out, q.shape, index)
     st = lib.attn_fwd_prefix(qp, qs, kp, kps, vp, vps, ko, kos, vo, vos, lens, op, os_, lse.data_ptr(), R, Hq, Hk, T,
