@@ -260,9 +260,9 @@ def attn_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None
     if scale is None:
         scale = default_scale(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H, N), torch.float32, q.device, stream)
     if out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if lse.shape != (B, H, N) or lse.dtype != torch.float32 or not lse.is_contiguous():
@@ -275,9 +275,7 @@ def attn_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None
             _check(st, "attn_fwd")
             return out, lse
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            workspace = _empty((need,), torch.uint8, q.device, stream, returned=False)
         if workspace.dtype != torch.uint8 or not workspace.is_cuda or workspace.numel() < need:
             raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
         st = lib.attn_fwd_split(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
@@ -304,10 +302,10 @@ def attn_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None = No
         raise ValueError("lse must be a contiguous fp32 [B, H, N] tensor")
     if scale is None:
         scale = default_scale(d)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+    dq, dk, dv = (_empty(q.shape, q.dtype, q.device, stream) for _ in range(3))
     need = lib.attn_bwd_workspace_bytes(B, H, N, d)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty((need,), torch.uint8, q.device, stream, returned=False)
     with torch.cuda.device(q.device):
         st = lib.attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
                           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, N, d, int(bool(causal)), float(scale),
@@ -332,12 +330,12 @@ def attn_fwd_fp8(q8, k8, v8, scales, causal: bool = False, scale: float | None =
     if scale is None:
         scale = default_scale(d)
     if out is None:
-        out = torch.empty(q8.shape, dtype=torch.bfloat16, device=q8.device)
+        out = _empty(q8.shape, torch.bfloat16, q8.device, stream)
     if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q8.device)
+        lse = _empty((B, H, N), torch.float32, q8.device, stream)
     need = lib.attn_fwd_fp8_workspace_bytes(B, H, N, d)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q8.device)
+        workspace = _empty((max(need, 16),), torch.uint8, q8.device, stream, returned=False)
     sq, sk, sv = (float(x) for x in scales)
     with torch.cuda.device(q8.device):
         st = lib.attn_fwd_fp8(q8.data_ptr(), k8.data_ptr(), v8.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, N, d,
@@ -357,10 +355,10 @@ def softmax_rows(x, out=None, workspace=None, stream=None):
     N = x.shape[-1]
     R = x.numel() // N
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     need = lib.attn_softmax_rows_workspace_bytes(R, N)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty((need,), torch.uint8, x.device, stream, returned=False)
     with torch.cuda.device(x.device):
         st = lib.attn_softmax_rows(x.data_ptr(), out.data_ptr(), R, N,
                                    workspace.data_ptr() if workspace is not None else None,
@@ -381,7 +379,7 @@ def layernorm_rows(x, gamma, beta, eps: float = 1e-5, out=None, stream=None):
     if gamma.shape != (N,) or beta.shape != (N,):
         raise ValueError("gamma and beta must have the row length")
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     with torch.cuda.device(x.device):
         st = lib.attn_layernorm_rows(x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), out.data_ptr(),
                                      x.numel() // N, N, float(eps), _stream_handle(stream))
@@ -661,7 +659,7 @@ def attn_fwd_host(q_h, k_h, v_h, causal: bool = False, scale: float | None = Non
         lse_h = torch.empty((B, H, N), dtype=torch.float32, pin_memory=q_h.is_pinned())
     need = lib.attn_fwd_host_workspace_bytes(B, H, N, d)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+        workspace = _empty((need,), torch.uint8, torch.device("cuda", torch.cuda.current_device()), stream, returned=False)
     st = lib.attn_fwd_host(q_h.data_ptr(), k_h.data_ptr(), v_h.data_ptr(), out_h.data_ptr(), lse_h.data_ptr(),
                            B, H, N, d, int(bool(causal)), float(scale), workspace.data_ptr(),
                            workspace.numel() * workspace.element_size(), _stream_handle(stream))

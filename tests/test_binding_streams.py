@@ -137,7 +137,34 @@ def prefix(**kw):
                                Tensor((3,), torch.int32), **kw)
 
 
-CALLS = {"qk_norm_rope": (ready, 2), "qk_norm_rope_bwd": (ready_bwd, 5), "attn_fwd_prefix": (prefix, 3)}
+def qkv(n=3, dtype=torch.bfloat16):
+    return [Tensor((1, 2, 300, 128), dtype) for _ in range(n)]
+
+
+def forward(**kw):
+    return ela.attn_fwd(*qkv(), **kw)
+
+
+def backward(**kw):
+    return ela.attn_bwd(*qkv(4), Tensor((1, 2, 300), torch.float32), *qkv(1), **kw)
+
+
+def forward_fp8(**kw):
+    return ela.attn_fwd_fp8(*qkv(dtype=torch.uint8), (1.0, 1.0, 1.0), **kw)
+
+
+def softmax(**kw):
+    return ela.softmax_rows(bf16(4, 70000), **kw)
+
+
+def layernorm(**kw):
+    return ela.layernorm_rows(bf16(4, 64), bf16(64), bf16(64), **kw)
+
+
+# the call, and how many buffers it allocates
+CALLS = {"qk_norm_rope": (ready, 2), "qk_norm_rope_bwd": (ready_bwd, 5), "attn_fwd_prefix": (prefix, 3),
+         "attn_fwd": (forward, 3), "attn_bwd": (backward, 4), "attn_fwd_fp8": (forward_fp8, 3), "softmax_rows": (softmax, 2),
+         "layernorm_rows": (layernorm, 1)}
 
 
 @pytest.mark.parametrize("name", CALLS)
@@ -157,6 +184,12 @@ def test_buffers_come_from_the_memory_of_the_stream_that_uses_them(machine, name
     call()
     assert len(machine.made) == buffers and all(t.made_on is caller and not t.used_on for t in machine.made)
     assert machine.lib.calls[-1][1] == 10
+
+
+def test_the_host_entry_takes_its_workspace_from_the_memory_of_the_stream(machine):
+    side = types.SimpleNamespace(cuda_stream=20, device=DEVICE)
+    ela.attn_fwd_host(*qkv(), out_h=bf16(1, 2, 300, 128), lse_h=Tensor((1, 2, 300), torch.float32), stream=side)
+    assert [t.made_on for t in machine.made] == [side] and not machine.made[0].used_on
 
 
 @pytest.mark.parametrize("name", CALLS)
@@ -189,7 +222,23 @@ def gpu_ready_bwd(seed):
     return lambda stream: ela.qk_norm_rope_bwd(g, gk, q, k, pos, inv, wq, wk, stream=stream)
 
 
-GPU_CALLS = {"attn_fwd_prefix": gpu_prefix, "qk_norm_rope_bwd": gpu_ready_bwd}
+def gpu_forward(seed):
+    q, k, v = (_draw(seed + i, 1, 1, 16000, 128) for i in range(3))  # few units: the K/V split and its workspace
+    return lambda stream: ela.attn_fwd(q, k, v, causal=True, stream=stream)
+
+
+def gpu_fp8(seed):
+    q, k, v = ((_draw(seed + i, 1, 4, 4096, 128).view(torch.uint8)[..., ::2] & 0x3f).contiguous() for i in range(3))
+    return lambda stream: ela.attn_fwd_fp8(q, k, v, (0.1, 0.1, 0.1), stream=stream)
+
+
+def gpu_softmax(seed):
+    x = _draw(seed, 60, 300000)  # rows in segments, with a workspace
+    return lambda stream: (ela.softmax_rows(x, stream=stream),)
+
+
+GPU_CALLS = {"attn_fwd_prefix": gpu_prefix, "qk_norm_rope_bwd": gpu_ready_bwd, "attn_fwd": gpu_forward,
+             "attn_fwd_fp8": gpu_fp8, "softmax_rows": gpu_softmax}
 
 
 @gpu
