@@ -401,6 +401,26 @@ def _raw_stream(stream, index):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+class _NoSize(Exception):
+    pass
+
+
+def _found(size) -> int:
+    """A workspace query's answer, to be kept; raises for 0 (an invalid shape, or no device state: device memory
+    may be full just now), which is not."""
+    if size == 0:
+        raise _NoSize
+    return int(size)
+
+
+def _size(query, *key) -> int:
+    """The answer of a query that keeps its answers; 0: none, and the call is then refused."""
+    try:
+        return query(*key)
+    except _NoSize:
+        return 0
+
+
 def _view(name, t, shape, index):
     """Checks a bf16 view with its last axis contiguous; returns its address and the other axes' strides
     as the C call's host array (None: contiguous)."""
@@ -493,7 +513,7 @@ def qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
 
 @functools.lru_cache(maxsize=16)
 def _bwd_workspace_bytes(index, d) -> int:
-    return int(load_library().attn_qk_norm_rope_bwd_workspace_bytes(d))
+    return _found(load_library().attn_qk_norm_rope_bwd_workspace_bytes(d))
 
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k_weight=None, sections=None,
@@ -520,7 +540,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k
     dwq = None if q_weight is None else _empty((d,), torch.float32, q.device, stream)
     dwk = None if k_weight is None else _empty((d,), torch.float32, q.device, stream)
     if workspace is None and (dwq is not None or dwk is not None):
-        workspace = _empty((_bwd_workspace_bytes(index, d),), torch.uint8, q.device, stream, returned=False)
+        workspace = _empty((_size(_bwd_workspace_bytes, index, d),), torch.uint8, q.device, stream, returned=False)
     if workspace is not None and (workspace.dtype != torch.uint8 or workspace.get_device() != index or
                                   not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
@@ -548,7 +568,7 @@ def prefix_workspace_bytes(R: int, Hq: int, Hk: int, T: int, P: int, C: int, d: 
 @functools.lru_cache(maxsize=256)
 def _prefix_workspace_bytes(index, *shape) -> int:
     """The query's answer for a device (the current one) and a shape."""
-    return int(load_library().attn_fwd_prefix_workspace_bytes(*shape))
+    return _found(load_library().attn_fwd_prefix_workspace_bytes(*shape))
 
 
 def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own_lens=None, scale: float | None = None,
@@ -605,7 +625,7 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
     elif lse.dtype != torch.float32 or lse.get_device() != index or lse.shape != (R, Hq, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [R, Hq, T] on q's device")
     if workspace is None:
-        workspace = _empty((_prefix_workspace_bytes(index, R, Hq, Hk, T, P, C, d),), torch.uint8, q.device, stream,
+        workspace = _empty((_size(_prefix_workspace_bytes, index, R, Hq, Hk, T, P, C, d),), torch.uint8, q.device, stream,
                            returned=False)
     elif workspace.dtype != torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
