@@ -594,6 +594,8 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
     kp = vp = ko = vo = lens = kps = vps = kos = vos = None
     if k_prefix is None and k_own is None:
         raise ValueError("give a prefix, own keys, or both")
+    if (k_prefix is None and v_prefix is not None) or (k_own is None and v_own is not None):
+        raise ValueError("values need their keys")
     Hk = k_prefix.shape[0] if k_prefix is not None else k_own.shape[1] if k_own.dim() == 4 else 0
     if k_prefix is not None:
         if k_prefix.dim() != 3 or v_prefix is None:
