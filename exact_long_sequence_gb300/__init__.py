@@ -500,8 +500,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, sectio
     kop, kos = _view("k_out", k_out, k.shape, index)
     st = lib.attn_qk_norm_rope(qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
                                None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb,
-                               inv_freq.data_ptr(), sec, A, qop, qos, kop, kos, B, Hq, Hk, N, d, eps,
-                               1 if interleaved else 0, _raw_stream(stream, index))
+                               inv_freq.data_ptr(), sec, A, qop, qos, kop, kos, B, Hq, Hk, N, d,
+                               float(eps), 1 if interleaved else 0, _raw_stream(stream, index))
     _check(st, "attn_qk_norm_rope")
     return q_out, k_out
 
@@ -554,7 +554,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k
         gqp, gqs, gkp, gks, qp, qs, kp, ks, None if q_weight is None else q_weight.data_ptr(),
         None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), pa, pb, inv_freq.data_ptr(), sec, A,
         dqp, dqs, dkp, dks, None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
-        B, Hq, Hk, N, d, eps, 1 if interleaved else 0, None if workspace is None else workspace.data_ptr(),
+        B, Hq, Hk, N, d, float(eps), 1 if interleaved else 0, None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel(), _raw_stream(stream, index))
     _check(st, "attn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
@@ -634,7 +634,8 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
     qp, qs = _view("q", q, q.shape, index)
     op, os_ = _view("out", out, q.shape, index)
     st = lib.attn_fwd_prefix(qp, qs, kp, kps, vp, vps, ko, kos, vo, vos, lens, op, os_, lse.data_ptr(), R, Hq, Hk, T,
-                             P, C, d, scale, workspace.data_ptr() or None, workspace.numel(), _raw_stream(stream, index))
+                             P, C, d, float(scale), workspace.data_ptr() or None, workspace.numel(),
+                             _raw_stream(stream, index))
     _check(st, "attn_fwd_prefix")
     return out, lse
 

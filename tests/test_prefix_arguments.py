@@ -27,3 +27,16 @@ def test_each_part_may_be_left_out_whole(machine):  # noqa: F811
     call(k_own=None, v_own=None)
     call(k_own=None, v_own=None, own_lens=None)
     assert len(machine.lib.calls) == 3
+
+
+def test_numbers_of_other_types_are_taken_as_the_other_entries_take_them(machine, monkeypatch):  # noqa: F811
+    """scale and eps may be anything float() takes, as attn_fwd's scale and layernorm_rows' eps."""
+    for number in (np.float32(0.25), torch.tensor(0.25), np.array(0.25)):
+        calls = []
+        for name in ("attn_fwd_prefix", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd"):
+            monkeypatch.setattr(machine.lib, name, lambda *a: calls.append(a) or ela.ATTN_OK, raising=False)
+        call(scale=number)
+        ela.qk_norm_rope(*ready_args(), eps=number)
+        ela.qk_norm_rope_bwd(bf16(2, 4, 6, 64), bf16(2, 2, 6, 64), *ready_args(), eps=number)
+        assert len(calls) == 3
+        assert all(any(type(x) is float and x == 0.25 for x in a) for a in calls)
