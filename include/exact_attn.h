@@ -453,8 +453,9 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
  *             Read on the device, so a captured graph may be replayed with other lengths.
  *   Masking : every token sees the whole prefix; token t of T sees the own keys
  *             j < own_lens - (T - 1 - t).  Cache rows at and past own_lens are not
- *             used and may hold anything, NaN included.  A NaN or infinity in the K or V of
- *             a new token reaches every token of that request, also those that do not see it.
+ *             used and may hold anything, NaN included.  A NaN or infinity in a new token's K
+ *             reaches only the tokens that see it; in its V it reaches every token of that
+ *             request (its weight for the others is 0, and 0 times it is a NaN).
  *   LSE     : fp32 [R, Hq, T] device, contiguous (natural log)
  *   *_strides : host arrays in elements, outermost axis first, d contiguous (Q,
  *             O: request, head, token; Kp, Vp: head, key; Ko, Vo: request, head, key);

@@ -59,3 +59,24 @@ def test_scores_that_rise_move_the_reference_maximum(path):
         s["k_own"][r, :, s["own_lens"][r]:] = float("nan")
     out, lse = ela.attn_fwd_prefix(**s)
     check(s, out, lse, requests=range(0, R, 13) if R > 20 else None)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("R,Hq,Hk,T,d,P", [
+    (6, 8, 2, 3, 128, 0), (170, 4, 1, 3, 64, 300), (6, 8, 2, 3, 128, 300),
+    (5, 20, 2, 3, 64, 0),    # 30 rows in blocks of 15
+    (3, 16, 2, 17, 64, 100),  # 136 rows a request
+])
+def test_a_key_that_a_token_does_not_see_does_not_reach_it(R, Hq, Hk, T, d, P, value):
+    """The last new token's K is not finite: the tokens before it give the same bits as without it."""
+    C = 200
+    lens = [T + (23 * r) % (C - T + 1) for r in range(R)]
+    s = make(R, Hq, Hk, T, d, P, C, lens, seed=8)
+    clean = [x.clone() for x in ela.attn_fwd_prefix(**s)]
+    for r in range(R):
+        s["k_own"][r, :, lens[r] - 1] = value
+    out, lse = ela.attn_fwd_prefix(**s)
+    assert torch.equal(out[:, :, :-1], clean[0][:, :, :-1]) and torch.equal(lse[:, :, :-1], clean[1][:, :, :-1])
+    assert torch.isfinite(clean[0]).all() and torch.isfinite(clean[1]).all()
+    if value != value:
+        assert out[:, :, -1].isnan().all() and lse[:, :, -1].isnan().all()
