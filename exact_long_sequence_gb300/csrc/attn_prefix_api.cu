@@ -71,10 +71,11 @@ void lay_out(PrefixParams& p, const PrefixShape& s, int num_sms) {
     p.orows = p.GT < 2 * p.qrows ? p.GT : 2 * p.qrows;
     // Own keys of few rows a request and key head: a kernel of their own (see there), with row
     // blocks of whole heads of the group.  Its warps: as many as there can be steps for, up to kOwnWarps an SM.
-    // Beside a prefix, up to one sequence an SM are items of the prefix kernel: that takes the GPU as
-    // long and saves the host a launch (8 requests x 8 heads on 1000 keys: 15.6 us, 16.5 us with the own kernel, a call
-    // from the host 19 and 25 us; 128 x 1 on 8192: 24.7 and 26.4 us; but 128 sequences of 40 keys 18.6 and 16.6 us).
-    // On long caches the two meet at the boundary (8 heads, 8192 own keys: 19 requests 112.3 us, 20 with the own kernel 111.3).
+    // Beside a prefix, up to one sequence an SM are items of the prefix kernel: that takes the GPU about as
+    // long and saves the host a launch (a call from the host on the first shape below: 19 us, 25 with the own kernel).
+    // GPU time of calls in a replayed graph, as items and with the own kernel: 8 requests x 8 heads on 1000 prefix keys, up to 64
+    // own, 13.5 and 12.9 us; 128 x 1 (16 query heads) on 8192, up to 256 own, 26.4 and 29.1 us; but 16 x 8 on 1000 with
+    // 40 own each 15.9 and 14.0 us, and near the boundary on long caches (19 x 8, 8192 own keys) 110.1 and 106.6 us.
     p.workers = 0;
     const bool few = s.P > 0 && static_cast<int64_t>(s.R) * s.Hk <= num_sms;
     if (s.C > 0 && !few && s.T <= kOwnRows && (p.GT <= kOwnRows || (p.GT <= kOwnMostRows && s.C <= kOwnMostKeys))) {

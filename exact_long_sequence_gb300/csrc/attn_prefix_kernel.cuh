@@ -69,12 +69,11 @@ struct PrefixParams {
     int pblocks;            // blocks of two query tiles over R GT
     int ptiles;             // prefix tiles of a key head
     int psegs;              // stretches that the tiles are cut into (PrefixCut)
-    int by_head;            // whether each head is cut by itself
+    int by_head;            // 1: each head is cut by itself, into psegs / Hk stretches; 0: the line of all heads is
     int run_len, run_per;   // tiles of a run (a head, or the line) and its stretches
     int even_base, even_rem;  // an even cut: run_per stretches of even_base tiles, the first even_rem one more
-    int early;              // ... into psegs / Hk stretches, or the line of all heads into psegs; the first
-    int lead;               // `early` of them are longer by what their CTAs can do before the others start:
-                            // lead / 2^20 tiles for each step of own work
+    int early;              // how many stretches of a run are longer, because their CTAs start before the others'; 0: an even cut
+    int lead;               // how much longer: lead / 2^20 tiles for each step of own work
     int pitems;             // psegs * pblocks (a stretch at one row block)
     int oblocks;            // row blocks of a request at a key head, for its own keys,
     int orows;              // ... of so many rows: two query tiles, or up to 16 in the own-keys kernel (at most GT)
