@@ -14,6 +14,9 @@ namespace elsattn {
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kDefaultTimeoutNs = 4000000000ull;  // 4 s for any single wait
 
+// Sizes that kernels round up to whole tiles, row blocks (of at most 256) and steps in 32 bits stay below this.
+constexpr long long kRoundedSizeLimit = (1LL << 31) - 512;
+
 struct DeviceState {
     bool ready = false;
     int num_sms = 0;

@@ -23,7 +23,8 @@ int check_shape(const PrefixShape& s) {
     if (s.R < 1 || s.Hq < 1 || s.Hk < 1 || s.T < 1 || s.P < 0 || s.C < 0) return ATTN_ERR_INVALID_ARG;
     if (s.P == 0 && s.C == 0) return ATTN_ERR_INVALID_ARG;
     if (s.Hq % s.Hk != 0) return ATTN_ERR_INVALID_ARG;
-    if (static_cast<long long>(s.R) * s.Hq >= (1LL << 31) || static_cast<long long>(s.R) * s.Hq * s.T >= (1LL << 31))
+    if (static_cast<long long>(s.R) * s.Hq >= kRoundedSizeLimit ||
+        static_cast<long long>(s.R) * s.Hq * s.T >= kRoundedSizeLimit || s.P >= kRoundedSizeLimit || s.C >= kRoundedSizeLimit)
         return ATTN_ERR_INVALID_ARG;
     if (s.d != 64 && s.d != 128) return ATTN_ERR_UNSUPPORTED;
     // the kernels count tiles and steps of work in 32 bits (2^31 of them would not fit device memory)

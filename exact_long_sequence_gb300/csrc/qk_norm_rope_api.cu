@@ -18,8 +18,8 @@ int fill_params(ReadyParams& p, const int32_t* positions, int64_t pos_axis, int6
                 const int* sections, int num_sections, int B, int Hq, int Hk, int N, int d, float eps) {
     if (!positions || !inv_freq || !sections) return ATTN_ERR_INVALID_ARG;
     if (B < 1 || Hq < 1 || Hk < 1 || N < 1) return ATTN_ERR_INVALID_ARG;
-    if (static_cast<long long>(B) * N >= (1LL << 31) || static_cast<long long>(B) * N * Hq >= (1LL << 31) ||
-        static_cast<long long>(B) * N * Hk >= (1LL << 31))
+    if (static_cast<long long>(B) * N >= kRoundedSizeLimit || static_cast<long long>(B) * N * Hq >= kRoundedSizeLimit ||
+        static_cast<long long>(B) * N * Hk >= kRoundedSizeLimit)
         return ATTN_ERR_INVALID_ARG;
     if (!(std::isfinite(eps) && eps >= 0.f)) return ATTN_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;

@@ -390,7 +390,7 @@ int attn_layernorm_rows(const void* X, const void* gamma, const void* beta, void
  *             Their sum is the number of rotated pairs: at most d / 2, a multiple
  *             of 8 (ATTN_ERR_UNSUPPORTED otherwise).
  *   interleaved : 0: pair i is elements (i, i + pairs); otherwise (2 i, 2 i + 1)
- *   d : 64 or 128;  eps : finite, >= 0;  B, Hq, Hk, N >= 1, products B*N*H < 2^31
+ *   d : 64 or 128;  eps : finite, >= 0;  B, Hq, Hk, N >= 1, products B*N*H < 2^31 - 512
  * Asynchronous on `stream`; no workspace.
  */
 int attn_qk_norm_rope(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides,
@@ -461,8 +461,8 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
  *             O: request, head, token; Kp, Vp: head, key; Ko, Vo: request, head, key);
  *             NULL: contiguous.  Positive multiples of 8 for axes longer than 1, and
  *             stride times extent at most 2^39.
- *   d       : 64 or 128;  scale : any finite value;  R, Hq, Hk, T >= 1, R*Hq*T < 2^31,
- *             and less than 2^30 tiles of work (Hk * P / 128; R * Hk * C / 16)
+ *   d       : 64 or 128;  scale : any finite value;  R, Hq, Hk, T >= 1; R*Hq*T, P and C below
+ *             2^31 - 512, and less than 2^30 tiles of work (Hk * P / 128; R * Hk * C / 16)
  *   workspace : device buffer of at least attn_fwd_prefix_workspace_bytes(), 16-byte
  *             aligned, owned by the caller, not used by other work while this call runs
  *             (calls that may overlap, captured graphs among them, need one each)
