@@ -371,6 +371,8 @@ int attn_layernorm_rows(const void* X, const void* gamma, const void* beta, void
  * elements past the rotated ones keep y.  Rounded to bf16 once, at the end.
  * The angle is exact modulo a turn for every int32 position, up to the
  * rounding of inv_freq / (2 pi) to 2^-53 of a turn (times the position).
+ * The sum of squares is fp32 too: it overflows for rows with elements beyond about
+ * 1e18, which give 0, and with eps = 0 it loses its digits for rows below about 1e-19.
  *   Q, Qout : bf16 [B, Hq, N, d] device views, d fastest, 16-byte aligned
  *   K, Kout : bf16 [B, Hk, N, d] device views; Hq and Hk are independent
  *   *_strides : host arrays of three strides in elements (batch, head, token),
