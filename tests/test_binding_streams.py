@@ -258,3 +258,25 @@ def test_calls_side_by_side_without_a_wait_give_the_serial_results(name):
         for got, w in ((a, want[0]), (b, want[1]), (a2, want[0])):
             assert all(torch.equal(x, y) for x, y in zip(got, w))
     assert ela.last_device_error() == ela.ATTN_OK
+
+
+@gpu
+def test_a_given_stream_inside_a_captured_graph():
+    """A captured call on a stream that joined the capture: its buffers belong to the graph, as the current stream's do."""
+    _build.build()
+    calls = [make(1) for make in GPU_CALLS.values()]
+    want = [call(None) for call in calls]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = [(call(None), call(side), call(side)) for call in calls]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for each, w in zip(got, want):
+            for result in each:
+                assert all(torch.equal(x, y) for x, y in zip(result, w))
+    assert ela.last_device_error() == ela.ATTN_OK
