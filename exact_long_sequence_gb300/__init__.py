@@ -64,6 +64,10 @@ EXPORTED_SYMBOLS = (
     "attn_qk_norm_rope_bwd_workspace_bytes",
     "attn_fwd_prefix",
     "attn_fwd_prefix_workspace_bytes",
+    "attn_fwd_packed",
+    "attn_fwd_packed_workspace_bytes",
+    "attn_fwd_tree",
+    "attn_fwd_tree_workspace_bytes",
 )
 
 
@@ -162,6 +166,14 @@ def load_library(path: str | None = None):
     lib.attn_fwd_prefix.restype = i
     lib.attn_fwd_prefix_workspace_bytes.argtypes = [i] * 7
     lib.attn_fwd_prefix_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_fwd_packed.argtypes = [vp] * 11 + [i] * 7 + [f, vp, ctypes.c_size_t, vp]
+    lib.attn_fwd_packed.restype = i
+    lib.attn_fwd_packed_workspace_bytes.argtypes = [i] * 6
+    lib.attn_fwd_packed_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_fwd_tree.argtypes = [vp] * 7 + [i64] + [vp] * 5 + [i] * 8 + [f, vp, ctypes.c_size_t, vp]
+    lib.attn_fwd_tree.restype = i
+    lib.attn_fwd_tree_workspace_bytes.argtypes = [i] * 5
+    lib.attn_fwd_tree_workspace_bytes.restype = ctypes.c_size_t
     if path is None:
         _lib = lib
     return lib
@@ -637,6 +649,157 @@ def attn_fwd_prefix(q, k_prefix=None, v_prefix=None, k_own=None, v_own=None, own
                              P, C, d, float(scale), workspace.data_ptr() or None, workspace.numel(),
                              _raw_stream(stream, index))
     _check(st, "attn_fwd_prefix")
+    return out, lse
+
+
+def packed_workspace_bytes(R: int, Nq: int, Nk: int, Hq: int, Hk: int, d: int) -> int:
+    """Device bytes attn_fwd_packed needs for this shape on the current device (0: invalid shape)."""
+    return int(load_library().attn_fwd_packed_workspace_bytes(R, Nq, Nk, Hq, Hk, d))
+
+
+@functools.lru_cache(maxsize=256)
+def _packed_workspace_bytes(index, *shape) -> int:
+    return _found(load_library().attn_fwd_packed_workspace_bytes(*shape))
+
+
+def _starts(name, t, R, index):
+    if t.dtype != torch.int32 or t.get_device() != index or t.shape != (R + 1,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [sequences + 1] on q's device")
+    return t.data_ptr()
+
+
+def _lse(t, shape, q, index, stream):
+    """The log-sum-exp's buffer: `t`, or a new one."""
+    if t is None:
+        return _empty(shape, torch.float32, q.device, stream)
+    if t.dtype != torch.float32 or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 tensor {list(shape)} on q's device")
+    return t
+
+
+def _workspace(t, query, key, q, index, stream):
+    """The workspace: `t`, or a new one of the size that `query` gives for `key` (kept from call to call)."""
+    if t is None:
+        return _empty((_size(query, index, *key),), torch.uint8, q.device, stream, returned=False)
+    if t.dtype != torch.uint8 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    return t
+
+
+def _packed_qkv(q, k, v):
+    """The checks both directions of the packed calls share: device index and (Hq, Nq, Hk, Nk, d)."""
+    if q.dim() != 3 or k.dim() != 3 or not q.is_cuda:
+        raise ValueError("q and k must be CUDA tensors [heads, tokens, d]")
+    Hq, Nq, d = q.shape
+    Hk, Nk, kd = k.shape
+    if kd != d:
+        raise ValueError("q and k must share d")
+    return q.get_device(), Hq, Nq, Hk, Nk, d
+
+
+def attn_fwd_packed(q, k, v, q_starts, k_starts=None, causal: bool = False, scale: float | None = None, out=None, lse=None,
+                    workspace=None, stream=None):
+    """O, LSE of sequences of different lengths whose tokens follow one another, with grouped heads.
+
+    q         : bf16 CUDA [Hq, Nq, d], d in {64, 128}
+    k, v      : bf16 [Hk, Nk, d], Hk a divisor of Hq
+    q_starts  : int32 [sequences + 1] on the device: sequence s has the queries q_starts[s] .. q_starts[s + 1] - 1
+    k_starts  : the same of its keys; None: q_starts (self-attention)
+    causal    : query t of n sees the keys j <= t + m - n of the sequence's m (its last query sees all of them);
+                otherwise every query sees all of its sequence's keys
+    out, lse  : optional bf16 view like q and fp32 [Hq, Nq] (default: new contiguous tensors).  Rows of tokens that
+                are in no sequence are left as they were.
+    workspace : optional uint8 CUDA tensor of packed_workspace_bytes() bytes
+    All bf16 tensors are views with d contiguous and other strides positive multiples of 8, so a projection's
+    token-major output may be given transposed.  Returns (out, lse); a row that sees no key is 0, with LSE -inf."""
+    lib = load_library()
+    index, Hq, Nq, Hk, Nk, d = _packed_qkv(q, k, v)
+    R = q_starts.shape[0] - 1 if q_starts.dim() == 1 else 0
+    qst = _starts("q_starts", q_starts, R, index)
+    kst = qst if k_starts is None else _starts("k_starts", k_starts, R, index)
+    if scale is None:
+        scale = _SCALES.get(d) or default_scale(d)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return attn_fwd_packed(q, k, v, q_starts, k_starts, causal, scale, out, lse, workspace, stream)
+    qp, qs = _view("q", q, q.shape, index)
+    kp, ks = _view("k", k, k.shape, index)
+    vp, vs = _view("v", v, k.shape, index)
+    if out is None:
+        out = _empty((Hq, Nq, d), torch.bfloat16, q.device, stream)
+    op, os_ = _view("out", out, q.shape, index)
+    lse = _lse(lse, (Hq, Nq), q, index, stream)
+    workspace = _workspace(workspace, _packed_workspace_bytes, (R, Nq, Nk, Hq, Hk, d), q, index, stream)
+    st = lib.attn_fwd_packed(qp, qs, kp, ks, vp, vs, qst, kst, op, os_, lse.data_ptr(), R, Nq, Nk, Hq, Hk, d,
+                             1 if causal else 0, float(scale), workspace.data_ptr() or None, workspace.numel(),
+                             _raw_stream(stream, index))
+    _check(st, "attn_fwd_packed")
+    return out, lse
+
+
+def tree_workspace_bytes(R: int, Hq: int, Hk: int, T: int, d: int) -> int:
+    """Device bytes attn_fwd_tree needs for this shape on the current device (0: invalid shape)."""
+    return int(load_library().attn_fwd_tree_workspace_bytes(R, Hq, Hk, T, d))
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace_bytes(index, *shape) -> int:
+    return _found(load_library().attn_fwd_tree_workspace_bytes(*shape))
+
+
+def attn_fwd_tree(q, k_pages, v_pages, page_table, lens, tree_mask=None, scale: float | None = None, out=None, lse=None,
+                  workspace=None, stream=None):
+    """O, LSE of T new tokens of R requests over a cache in pages: one token each, a run, or a tree of drafted tokens.
+
+    q          : bf16 CUDA [R, Hq, T, d], d in {64, 128}
+    k_pages, v_pages : bf16 [pages, Hk, page size, d], Hk a divisor of Hq, the page size a power of two from 16 to 1024
+    page_table : int32 [R, most pages of a request] on the device: the pages of each request's keys, in order.  Entries
+                 past its keys may hold anything; an entry that is no page of the cache reads as zeros.
+    lens       : int32 [R] on the device: keys of each request, the T new tokens among them as the last (more than the
+                 table holds counts as what it holds); 0: none; negative: padding, the rows are left as they were
+    tree_mask  : int32 [R, T, ceil(T / 32)] on the device: bit j % 32 of word j / 32 of row t is set where new token t
+                 sees new token j (its own bit among them).  All see the keys before the new tokens.  None: each sees
+                 the new tokens up to itself.
+    out, lse   : optional bf16 view like q and fp32 [R, Hq, T] (default: new contiguous tensors)
+    workspace  : optional uint8 CUDA tensor of tree_workspace_bytes() bytes
+    All bf16 tensors are views with d contiguous and other strides positive multiples of 8.  Returns (out, lse); a row
+    that sees no key is 0, with LSE -inf."""
+    lib = load_library()
+    if q.dim() != 4 or k_pages.dim() != 4 or not q.is_cuda:
+        raise ValueError("q and k_pages must be CUDA tensors [R, Hq, T, d] and [pages, Hk, page size, d]")
+    index = q.get_device()
+    R, Hq, T, d = q.shape
+    pages, Hk, page, kd = k_pages.shape
+    if kd != d:
+        raise ValueError("q and k_pages must share d")
+    if page_table.dtype != torch.int32 or page_table.get_device() != index or page_table.dim() != 2 or \
+            page_table.shape[0] != R or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be an int32 tensor [R, pages of a request] on q's device, its last axis contiguous")
+    if lens.dtype != torch.int32 or lens.get_device() != index or lens.shape != (R,) or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous int32 tensor [R] on q's device")
+    mask = None
+    if tree_mask is not None:
+        if tree_mask.dtype != torch.int32 or tree_mask.get_device() != index or \
+                tree_mask.shape != (R, T, (T + 31) // 32) or not tree_mask.is_contiguous():
+            raise ValueError("tree_mask must be a contiguous int32 tensor [R, T, ceil(T / 32)] on q's device")
+        mask = tree_mask.data_ptr()
+    if scale is None:
+        scale = _SCALES.get(d) or default_scale(d)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return attn_fwd_tree(q, k_pages, v_pages, page_table, lens, tree_mask, scale, out, lse, workspace, stream)
+    qp, qs = _view("q", q, q.shape, index)
+    kp, ks = _view("k_pages", k_pages, k_pages.shape, index)
+    vp, vs = _view("v_pages", v_pages, k_pages.shape, index)
+    if out is None:
+        out = _empty((R, Hq, T, d), torch.bfloat16, q.device, stream)
+    op, os_ = _view("out", out, q.shape, index)
+    lse = _lse(lse, (R, Hq, T), q, index, stream)
+    workspace = _workspace(workspace, _tree_workspace_bytes, (R, Hq, Hk, T, d), q, index, stream)
+    st = lib.attn_fwd_tree(qp, qs, kp, ks, vp, vs, page_table.data_ptr(), page_table.stride(0), lens.data_ptr(), mask, op, os_,
+                           lse.data_ptr(), R, Hq, Hk, T, pages, page, page_table.shape[1], d, float(scale),
+                           workspace.data_ptr() or None, workspace.numel(), _raw_stream(stream, index))
+    _check(st, "attn_fwd_tree")
     return out, lse
 
 

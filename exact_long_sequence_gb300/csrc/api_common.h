@@ -25,6 +25,7 @@ struct DeviceState {
     bool smem_configured[2][2][2] = {};                                   // forward <d == 128><causal><dynamic schedule>
     bool bwd_smem_configured[2][2] = {{false, false}, {false, false}};  // backward <d == 128><causal>
     bool prefix_smem_configured[2][2] = {};  // shared-prefix forward <own-keys kernel><d == 128>
+    bool packed_smem_configured[2][2] = {};  // attention over lengths <paged><d == 128>
     bool ready_configured[2][8] = {};  // query / key preparation <backward><variant>
     bool fp8_smem_configured[2][2][2] = {};  // FP8 forward <causal><dynamic schedule><K/V segments>
 };
@@ -63,6 +64,23 @@ int encode_u8_map(CUtensorMap* map, const void* base, uint64_t e0, uint64_t e1, 
                   uint64_t s2, uint32_t b0, uint32_t b1);
 
 bool aligned16(const void* p);
+
+// Strides of a view in elements; nullptr: contiguous.  TMA takes strides of a
+// multiple of 16 bytes below 2^40; an axis of one is never stepped.
+template <int N>
+int take_view(int64_t (&out)[N], const int64_t* given, const int64_t (&dims)[N], int64_t inner) {
+    int64_t dense = inner;
+    for (int i = N - 1; i >= 0; --i) {
+        out[i] = dense;
+        if (given && dims[i] > 1) {
+            out[i] = given[i];
+            if (out[i] % 8 != 0) return ATTN_ERR_MISALIGNED;
+            if (out[i] <= 0 || out[i] >= (1LL << 39) || out[i] > (1LL << 39) / dims[i]) return ATTN_ERR_INVALID_ARG;
+        }
+        dense *= dims[i];
+    }
+    return ATTN_OK;
+}
 
 // Shared argument checks of the forward and backward entry points.
 int check_args(const void* Q, const void* K, const void* V, const void* O, const void* LSE, int B, int H, int N,

@@ -1,0 +1,1124 @@
+// Attention over sequences of different lengths, for sm_103a, in two forms:
+//   packed: the tokens of all sequences follow one another in Q, K and V, and a
+//     sequence's queries see its own keys (all, or causally);
+//   paged (PAGED): T new tokens of each of R requests, whose keys and values
+//     lie in pages of a cache; the new tokens see the keys before them and, of
+//     one another, what a mask allows (a tree of drafted tokens).
+// With n_s queries and m_s keys of sequence s, and G query heads to a key head,
+//     O_i = sum_j p_ij V_j,  p_ij = exp(scale q_i . k_j - LSE_i) over the keys that i sees.
+//
+// The rows of a key head are its tokens' heads, row = token G + head: a tile of
+// 128 rows is 128 / G tokens, whose K/V are read once for all G heads, and a
+// causal tile crosses the diagonal in 128 / G keys instead of 128.
+//
+// Work is laid on a line (packed_line.h) and cut into even stretches, so that
+// all SMs end together whatever the lengths are; the lengths are device data,
+// and each CTA works out its own stretches from them.  A unit (block of rows at
+// a key head) inside one stretch is written by its CTA; the pieces of a unit
+// that stretches cut are left in fp32 and merged by attn_packed_combine_kernel,
+//     LSE = log sum_s exp(LSE_s),  O = sum_s exp(LSE_s - LSE) O_s,
+// the combination step of the online softmax.  Where all K and V together would
+// not stay in L2, the line has several stretches a CTA, run in the order of the
+// line, so that all CTAs are in one part of it at a time.
+//
+// Roles and pipeline are those of attn_prefix_kernel: two chains (S_c, O_c in
+// TMEM, softmax warpgroup c) alternate, so that the tensor core works on one
+// while the softmax of the other runs.  An item (a stretch's part of a unit) of
+// more than one query tile has a tile on each chain, and both share the K/V
+// tiles; an item of one query tile gives the chains its K/V tiles in turn.
+//   warp 0  TMA producer of K_j, V_j into a ring of stages
+//   warp 1  tcgen05.mma issuer; owns the TMEM allocation
+//   warp 2  scheduler: the CTA's items, through a ring of descriptions
+//   warp 3  Q loader
+//   warps 4-7, 8-11  softmax warpgroups
+#pragma once
+
+#include <cuda.h>
+#include <cstdint>
+#include <type_traits>
+
+#include "attn_prefix_kernel.cuh"
+#include "packed_line.h"
+
+namespace elsattn {
+
+constexpr int kPkTailBox = 32;     // keys per TMA box of a tile that is not full
+constexpr int kPkMostGroup = 64;   // most query heads of a key head
+
+struct PackedParams {
+    // packed: [R + 1] first tokens of the sequences in Q, and in K and V (each clipped to the tensors)
+    const int32_t* q_starts;
+    const int32_t* k_starts;
+    // paged: [R] keys of the requests, the new tokens among them (negative: padding), and their pages
+    const int32_t* lens;
+    const int32_t* table;      // request r's i-th page at r * table_stride + i
+    const uint32_t* mask;      // [R, T, words] bits: new token t sees new token j; nullptr: those up to itself
+    int64_t table_stride;
+    int words;                 // 32-bit words of a mask row
+    int page_log2, box;        // keys of a page; rows of a TMA box of it (at most 128)
+    int pages;                 // of the cache
+    int cap;                   // most keys of a request: the table's pages
+    int R, Hk, G, T;           // T: paged only
+    int Nq, Nk;                // packed: tokens and keys of the tensors
+    int tile_tokens, qrows;    // of a query tile: whole tokens, and rows
+    int orows;                 // partial rows kept for a piece
+    bool causal;               // token t sees the keys j <= t + nk - nq
+    int stretches;             // how many stretches the line has at most (a multiple of the grid)
+    __nv_bfloat16* o;
+    int64_t os[3];             // strides in elements: request (paged), head, token
+    float* lse;
+    int64_t ls[2];             // request (paged), head
+    float* part_o;             // [2 stretches][orows][d]: slot 2 i + 1 is the piece that begins a unit in stretch i, 2 i one that goes on
+    float* part_lse;           // [2 stretches][orows]
+    struct PackedCut* cuts;    // [stretches]
+    uint32_t* error_word;
+    uint64_t timeout_ns;
+    float scale_log2, max_scale_log2;
+    uint32_t negate_scores;
+};
+
+// The unit whose pieces begin in a stretch (pieces: 0 where none is cut there).
+struct PackedCut {
+    int pieces;
+    int head, req, tok0, nrows;
+    int pad[3];
+};
+
+struct PackedItem {
+    int ntiles;      // of K/V in this part of the unit; -1: no more items; 0: the unit sees no key
+    int tile0;       // the first of them
+    int ntiles0;     // how many of them its first query tile takes
+    int klen;        // keys of the sequence that the unit sees
+    int k0;          // packed: the sequence's first key
+    int req;         // paged: the request
+    int head;        // key head
+    int tok0;        // first token of the block, in the tensor (packed) or the request
+    int nrows;       // rows of the block
+    int sees0;       // keys that the block's first token sees (can be negative: none)
+    int step;        // ... and how many more each next token: 1 or 0
+    int slot;        // partial slot; -1: the unit is whole
+};
+static_assert(sizeof(PackedItem) == 48, "read by words");
+
+template <int D>
+struct PackedSmem {
+    static constexpr int kTile = tile_bytes(D);
+    static constexpr int kStages = kv_stages_for(D);
+    static constexpr int kQOff = 0;
+    static constexpr int kRingOff = kQTiles * kTile;
+    static constexpr int kXchgOff = kRingOff + kStages * kTile;   // [128] (m, l) of one chain, then of the other
+    static constexpr int kItemOff = kXchgOff + 128 * 8;
+    static constexpr int kBarOff = kItemOff + kPfxItemRing * static_cast<int>(sizeof(PackedItem));
+    static constexpr int kKvFull = 0;
+    static constexpr int kKvEmpty = kKvFull + kStages;
+    static constexpr int kQFull = kKvEmpty + kStages;     // [2] by slot
+    static constexpr int kQEmpty = kQFull + 2;            // [2]
+    static constexpr int kSFull = kQEmpty + 2;            // [2] by chain, as all below
+    static constexpr int kPHalf = kSFull + 2;             // [2] first half of P stored, O rescaled
+    static constexpr int kPFull = kPHalf + 2;             // [2]
+    static constexpr int kOFull = kPFull + 2;             // [2]
+    static constexpr int kOEmpty = kOFull + 2;            // [2]
+    static constexpr int kX = kOEmpty + 2;                // [2] the chain's (m, l) are in shared memory
+    static constexpr int kDrain = kX + 2;
+    static constexpr int kItemFull = kDrain + 1;          // [kPfxItemRing]
+    static constexpr int kItemEmpty = kItemFull + kPfxItemRing;
+    static constexpr int kNumBars = kItemEmpty + kPfxItemRing;
+    static constexpr int kFlagsOff = kBarOff + kNumBars * 8;
+    static constexpr int kBytes = kFlagsOff + 16 + kSmemAlign;
+    static_assert(kBytes <= kSmemLimit, "shared memory");
+    static_assert(2 * kBytes > 233472, "one CTA per SM (each allocates all of TMEM)");
+};
+
+// Sequence r: its tokens and keys, and where they begin.  Offsets that do not fit the tensors are clipped.
+struct PackedSeq {
+    LineSeq line;
+    int q0, k0;
+};
+template <bool PAGED>
+__device__ __forceinline__ PackedSeq packed_seq(const PackedParams& p, int r) {
+    PackedSeq s;
+    s.line.tile_tokens = p.tile_tokens;
+    if (PAGED) {
+        const int len = __ldg(p.lens + r);
+        s.line.nq = len < 0 ? 0 : p.T;
+        s.line.nk = min(max(len, 0), p.cap);
+        s.line.causal = p.mask == nullptr;
+        s.q0 = 0;
+        s.k0 = 0;
+    } else {
+        auto clip = [](int x, int n) { return min(max(x, 0), n); };
+        s.q0 = clip(__ldg(p.q_starts + r), p.Nq);
+        s.k0 = clip(__ldg(p.k_starts + r), p.Nk);
+        s.line.nq = max(0, clip(__ldg(p.q_starts + r + 1), p.Nq) - s.q0);
+        s.line.nk = max(0, clip(__ldg(p.k_starts + r + 1), p.Nk) - s.k0);
+        s.line.causal = p.causal;
+    }
+    return s;
+}
+
+__device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += o;
+    }
+    return v;
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_kt,
+                   const __grid_constant__ CUtensorMap tmap_vt, const __grid_constant__ PackedParams p) {
+    using L = PackedSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_base = smem_u32(smem);
+    const uint32_t bar0 = s_base + L::kBarOff;
+    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kFlagsOff);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlagsOff + 4);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int lane = threadIdx.x & 31;
+    const WaitCtx ctx{abort_flag, p.error_word, p.timeout_ns};
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0u;
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(bar(L::kKvFull + s), 1);
+            mbar_init(bar(L::kKvEmpty + s), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(L::kQFull + t), 1);
+            mbar_init(bar(L::kQEmpty + t), 1);
+            mbar_init(bar(L::kSFull + t), 1);
+            mbar_init(bar(L::kPHalf + t), 128);
+            mbar_init(bar(L::kPFull + t), 128);
+            mbar_init(bar(L::kOFull + t), 1);
+            mbar_init(bar(L::kOEmpty + t), 256);  // both warpgroups, or one that counts twice
+            mbar_init(bar(L::kX + t), 128);
+        }
+        mbar_init(bar(L::kDrain), 1);
+        for (int s = 0; s < kPfxItemRing; ++s) {
+            mbar_init(bar(L::kItemFull + s), 1);
+            mbar_init(bar(L::kItemEmpty + s), kPfxItemReaders);
+        }
+        fence_barrier_init();
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+        if (!PAGED) {
+            tma_prefetch_desc(&tmap_kt);
+            tma_prefetch_desc(&tmap_vt);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    // The combine kernel may be scheduled onto SMs as this grid's CTAs retire;
+    // it waits for the whole grid before it reads the partial results.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // Reads the next item (ring entry n); `it.ntiles` is -1 after the last.  Called by whole warps, whose
+    // lanes get one word each from shared memory and hand it round, so that the fields are uniform.
+    // keep: the caller gives the ring entry back itself.
+    auto take_item = [&](uint32_t n, PackedItem& it, bool keep = false) -> bool {
+        const uint32_t s = n % kPfxItemRing;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kItemFull + s), (n / kPfxItemRing) & 1u, ctx))) return false;
+        const int* from = reinterpret_cast<const int*>(smem + L::kItemOff + s * sizeof(PackedItem));
+        const int word = from[lane < 12 ? lane : 0];
+        it.ntiles = __shfl_sync(0xffffffffu, word, 0);
+        it.tile0 = __shfl_sync(0xffffffffu, word, 1);
+        it.ntiles0 = __shfl_sync(0xffffffffu, word, 2);
+        it.klen = __shfl_sync(0xffffffffu, word, 3);
+        it.k0 = __shfl_sync(0xffffffffu, word, 4);
+        it.req = __shfl_sync(0xffffffffu, word, 5);
+        it.head = __shfl_sync(0xffffffffu, word, 6);
+        it.tok0 = __shfl_sync(0xffffffffu, word, 7);
+        it.nrows = __shfl_sync(0xffffffffu, word, 8);
+        it.sees0 = __shfl_sync(0xffffffffu, word, 9);
+        it.step = __shfl_sync(0xffffffffu, word, 10);
+        it.slot = __shfl_sync(0xffffffffu, word, 11);
+        if (!keep && lane == 0) mbar_arrive(bar(L::kItemEmpty + s));
+        return it.ntiles >= 0;
+    };
+    // Keys of the item's tile j (1 .. 128).
+    auto tile_keys = [](const PackedItem& it, int j) -> int { return min(kBc, it.klen - (it.tile0 + j) * kBc); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        RingPos pos{0u, 0u};
+        uint32_t issued = 0;
+        bool ok = true;
+        PackedItem it;
+        for (uint32_t n = 0; ok && take_item(n, it); ++n) {
+            const int* pages = PAGED ? p.table + it.req * p.table_stride : nullptr;
+            // paged: lane l holds the page of box `base + l` of the item's keys, and has asked for the next 32
+            const int box0 = PAGED ? it.tile0 * (kBc / p.box) : 0;
+            const int boxes_all = PAGED ? (it.klen + p.box - 1) / p.box : 0;
+            auto page_of = [&](int bx) -> int {
+                const int key = bx * p.box;
+                const int page = bx < boxes_all ? __ldg(pages + (key >> p.page_log2)) : 0;
+                return static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages) ? page : p.pages;
+            };
+            int base = box0, page_now = 0, page_next = 0;
+            if (PAGED && it.ntiles > 0) {
+                page_now = page_of(base + lane);
+                page_next = page_of(base + 32 + lane);
+            }
+            for (int j = 0; j < it.ntiles && ok; ++j) {
+                const int keys = tile_keys(it, j);
+                const int key = (it.tile0 + j) * kBc;
+                int my_page = 0, nbox = 0;
+                if (PAGED) {
+                    // boxes of a tile are at most 8, so a run of 32 holds whole tiles
+                    const int b = key / p.box;
+                    if (b >= base + 32) {
+                        base += 32;
+                        page_now = page_next;
+                        page_next = page_of(base + 32 + lane);
+                    }
+                    nbox = (keys + p.box - 1) / p.box;
+                    my_page = __shfl_sync(0xffffffffu, page_now, (b - base + lane) & 31);
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvEmpty + pos.stage), pos.phase ^ 1u, ctx));
+                    if (!ok) break;
+                    const uint32_t full = bar(L::kKvFull + pos.stage);
+                    const uint32_t dst = s_base + L::kRingOff + pos.stage * L::kTile;
+                    if (PAGED) {
+                        if (lane == 0) mbar_arrive_expect_tx(full, nbox * p.box * D * 2);
+                        __syncwarp();
+                        if (lane < nbox) {  // page p.pages: outside the cache, reads as zero
+                            const int within = (key + lane * p.box) & ((1 << p.page_log2) - 1);
+#pragma unroll
+                            for (int b = 0; b < D / 64; ++b)
+                                tma_load_4d(dst + b * (kBc * 128) + lane * p.box * 128, kv == 0 ? &tmap_k : &tmap_v, full,
+                                            b * 64, within, it.head, my_page);
+                        }
+                        __syncwarp();
+                    } else if (elect_one()) {
+                        if (keys == kBc) {
+                            mbar_arrive_expect_tx(full, L::kTile);
+#pragma unroll
+                            for (int b = 0; b < D / 64; ++b)
+                                tma_load_3d(dst + b * (kBc * 128), kv == 0 ? &tmap_k : &tmap_v, full, b * 64, it.k0 + key,
+                                            it.head);
+                        } else {
+                            const int boxes = (keys + kPkTailBox - 1) / kPkTailBox;
+                            mbar_arrive_expect_tx(full, boxes * kPkTailBox * D * 2);
+                            for (int i = 0; i < boxes; ++i)
+#pragma unroll
+                                for (int b = 0; b < D / 64; ++b)
+                                    tma_load_3d(dst + b * (kBc * 128) + i * (kPkTailBox * 128), kv == 0 ? &tmap_kt : &tmap_vt,
+                                                full, b * 64, it.k0 + key + i * kPkTailBox, it.head);
+                        }
+                    }
+                    __syncwarp();
+                    pos = pos.next(L::kStages);
+                    ++issued;
+                }
+            }
+        }
+        // every issued copy lands before the CTA's shared memory is released (bounded waits)
+        const uint32_t pending = issued < static_cast<uint32_t>(L::kStages) ? issued : L::kStages;
+        RingPos back = pos;
+        for (uint32_t i = 0; i < pending; ++i) {
+            back = back.stage == 0 ? RingPos{L::kStages - 1u, back.phase ^ 1u} : RingPos{back.stage - 1, back.phase};
+            mbar_wait_drain(bar(L::kKvFull + back.stage), back.phase, 50000000ull);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t idesc_s = make_idesc_bf16_f32(kBr, kBc, false, false) | (p.negate_scores ? kIdescNegateB : 0u);
+        constexpr uint32_t idesc_o = make_idesc_bf16_f32(kBr, D, false, true);
+        const uint64_t dq0 = make_smem_desc_sw128(s_base + L::kQOff, 16, 1024);
+        const uint64_t dk0 = make_smem_desc_sw128(s_base + L::kRingOff, 16, 1024);
+        const uint64_t dv0 = make_smem_desc_sw128(s_base + L::kRingOff, kBc * 128, 1024);
+        uint32_t p_phase = 0u, o_phase = 3u;  // parities to wait for, bit c of chain c
+        RingPos kpos{0u, 0u};   // K of the current tile
+        uint32_t qpos = 0;      // query tiles taken so far: slot qpos & 1
+        uint32_t par = 0;       // chain of the item's first step
+        bool ok = true;
+        auto gemm_s = [&](int c, uint64_t a, uint64_t b) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = static_cast<uint64_t>(((kk >> 2) * (kBr * 128) + (kk & 3) * 32) >> 4);
+                mma_ss(tmem + c * kBc, a + off, b + off, idesc_s, kk > 0 ? 1u : 0u);
+            }
+        };
+        // the output product that is due: of the step before
+        struct { bool due, first, last, first_v, last_v; int chain, ksteps; RingPos v; } pv{};
+        auto run_pv = [&]() -> bool {
+            if (!pv.due) return true;
+            pv.due = false;
+            const int c = pv.chain;
+            bool w = true;
+            if (pv.first_v) w = mbar_wait(bar(L::kKvFull + pv.v.stage), pv.v.phase, ctx);
+            w = w && mbar_wait(bar(L::kPHalf + c), (p_phase >> c) & 1u, ctx);
+            if (pv.first) {
+                w = w && mbar_wait(bar(L::kOEmpty + c), (o_phase >> c) & 1u, ctx);
+                o_phase ^= 1u << c;
+            }
+            if (!__all_sync(0xffffffffu, w)) return false;
+            tc_fence_after_sync();
+            const uint64_t b = dv0 + static_cast<uint64_t>((pv.v.stage * L::kTile) >> 4);
+            // products over keys [64 half, 64 half + 64), in steps of 16 up to the tile's last key
+            auto gemm_o = [&](int half) {
+#pragma unroll
+                for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                    if (kk < pv.ksteps)
+                        mma_ts(tmem + 2 * kBc + c * D, tmem + c * kBc + kk * 8,
+                               b + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_o, (!pv.first || kk > 0) ? 1u : 0u);
+            };
+            if (elect_one()) gemm_o(0);
+            __syncwarp();
+            w = mbar_wait(bar(L::kPFull + c), (p_phase >> c) & 1u, ctx);
+            p_phase ^= 1u << c;
+            if (!__all_sync(0xffffffffu, w)) return false;
+            tc_fence_after_sync();
+            if (elect_one()) {
+                gemm_o(1);
+                if (pv.last_v) mma_commit(bar(L::kKvEmpty + pv.v.stage));
+                if (pv.last) mma_commit(bar(L::kOFull + c));
+            }
+            __syncwarp();
+            return true;
+        };
+        // The next score product goes first where its operands are there already: the tensor core
+        // works on it while the softmax of the step before runs.  Where they are not (short items,
+        // the ends of a CTA's share), the product that is due does not wait for them.
+        auto there = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_test(b, parity)); };
+        PackedItem it;
+        for (uint32_t n = 0; ok; ++n) {
+            if (pv.due && !there(bar(L::kItemFull + n % kPfxItemRing), (n / kPfxItemRing) & 1u) && !(ok = run_pv())) break;
+            if (!take_item(n, it)) break;
+            const int nt = it.ntiles;
+            if (nt == 0) continue;
+            if (it.nrows > p.qrows) {
+                // Two query tiles, chain = tile: S0_j; O1 += P1_{j-1} V_{j-1}; S1_j; O0 += P0_j V_j, the
+                // first of them over the first n0 K/V tiles (causal: it may see one tile less).
+                const int n0 = it.ntiles0;
+                const uint32_t q0 = qpos & 1u, q1 = q0 ^ 1u;
+                if (pv.due && (pv.chain == 0 || !there(bar(L::kKvFull + kpos.stage), kpos.phase) ||
+                               !there(bar(L::kQFull + q0), (qpos >> 1) & 1u)) && !(ok = run_pv()))
+                    break;
+                const uint64_t a0 = dq0 + static_cast<uint64_t>((q0 * L::kTile) >> 4);
+                const uint64_t a1 = dq0 + static_cast<uint64_t>((q1 * L::kTile) >> 4);
+                const int last_steps = (tile_keys(it, nt - 1) + 15) / 16;
+                // O_c (+)= P_c V_j, V_j at ring position v
+                auto pv_two = [&](auto chain, int j, RingPos v) -> bool {
+                    constexpr int c = decltype(chain)::value;
+                    bool w = true;
+                    if (c == 0 || j >= n0) w = mbar_wait(bar(L::kKvFull + v.stage), v.phase, ctx);  // its first use
+                    w = w && mbar_wait(bar(L::kPHalf + c), (p_phase >> c) & 1u, ctx);
+                    if (j == 0) {
+                        w = w && mbar_wait(bar(L::kOEmpty + c), (o_phase >> c) & 1u, ctx);
+                        o_phase ^= 1u << c;
+                    }
+                    if (!__all_sync(0xffffffffu, w)) return false;
+                    tc_fence_after_sync();
+                    const uint64_t b = dv0 + static_cast<uint64_t>((v.stage * L::kTile) >> 4);
+                    const int ks = j == nt - 1 ? last_steps : kBc / 16;
+                    auto gemm = [&](int half) {
+#pragma unroll
+                        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                            if (kk < ks)
+                                mma_ts(tmem + 2 * kBc + c * D, tmem + c * kBc + kk * 8,
+                                       b + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                    };
+                    if (elect_one()) gemm(0);
+                    __syncwarp();
+                    w = mbar_wait(bar(L::kPFull + c), (p_phase >> c) & 1u, ctx);
+                    p_phase ^= 1u << c;
+                    if (!__all_sync(0xffffffffu, w)) return false;
+                    tc_fence_after_sync();
+                    if (elect_one()) {
+                        gemm(1);
+                        if (c == 1) mma_commit(bar(L::kKvEmpty + v.stage));
+                        if (j == (c == 0 ? n0 : nt) - 1) mma_commit(bar(L::kOFull + c));
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                RingPos vprev{0u, 0u};
+                for (int j = 0; j < nt && ok; ++j) {
+                    bool w = mbar_wait(bar(L::kKvFull + kpos.stage), kpos.phase, ctx);
+                    if (j == 0)
+                        w = w && mbar_wait(bar(L::kQFull + q0), (qpos >> 1) & 1u, ctx) &&
+                            mbar_wait(bar(L::kQFull + q1), ((qpos + 1) >> 1) & 1u, ctx);
+                    if (!(ok = __all_sync(0xffffffffu, w))) break;
+                    const uint64_t b = dk0 + static_cast<uint64_t>((kpos.stage * L::kTile) >> 4);
+                    if (j < n0) {
+                        if (elect_one()) {
+                            gemm_s(0, a0, b);
+                            mma_commit(bar(L::kSFull + 0));
+                            if (j == n0 - 1) mma_commit(bar(L::kQEmpty + q0));
+                        }
+                        __syncwarp();
+                    }
+                    ok = j == 0 ? run_pv() : pv_two(std::integral_constant<int, 1>{}, j - 1, vprev);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        gemm_s(1, a1, b);
+                        mma_commit(bar(L::kSFull + 1));
+                        mma_commit(bar(L::kKvEmpty + kpos.stage));
+                        if (j == nt - 1) mma_commit(bar(L::kQEmpty + q1));
+                    }
+                    __syncwarp();
+                    vprev = kpos.next(L::kStages);
+                    if (j < n0 && !(ok = pv_two(std::integral_constant<int, 0>{}, j, vprev))) break;
+                    kpos = vprev.next(L::kStages);
+                }
+                if (!ok) break;
+                pv.due = true;
+                pv.chain = 1;
+                pv.v = vprev;
+                pv.ksteps = last_steps;
+                pv.first = nt == 1;
+                pv.last = true;
+                pv.first_v = nt > n0;
+                pv.last_v = true;
+                qpos += 2;
+                par = 0;
+                continue;
+            }
+            // One query tile; the chains take turns with the K/V tiles.
+            const uint32_t qslot = qpos & 1u;
+            for (int j = 0; j < nt && ok; ++j) {
+                const int c = (par + j) & 1;
+                if (pv.due && (!there(bar(L::kKvFull + kpos.stage), kpos.phase) ||
+                               (j == 0 && !there(bar(L::kQFull + qslot), (qpos >> 1) & 1u))) && !(ok = run_pv()))
+                    break;
+                bool w = mbar_wait(bar(L::kKvFull + kpos.stage), kpos.phase, ctx);
+                if (j == 0) w = w && mbar_wait(bar(L::kQFull + qslot), (qpos >> 1) & 1u, ctx);
+                if (!(ok = __all_sync(0xffffffffu, w))) break;
+                if (elect_one()) {
+                    gemm_s(c, dq0 + static_cast<uint64_t>((qslot * L::kTile) >> 4),
+                           dk0 + static_cast<uint64_t>((kpos.stage * L::kTile) >> 4));
+                    mma_commit(bar(L::kSFull + c));
+                    mma_commit(bar(L::kKvEmpty + kpos.stage));
+                    if (j == nt - 1) mma_commit(bar(L::kQEmpty + qslot));
+                }
+                __syncwarp();
+                if (!(ok = run_pv())) break;
+                pv.due = true;
+                pv.chain = c;
+                pv.v = kpos.next(L::kStages);
+                pv.ksteps = (tile_keys(it, j) + 15) / 16;
+                pv.first = j < 2;
+                pv.last = j + 2 >= nt;
+                pv.first_v = true;
+                pv.last_v = true;
+                kpos = pv.v.next(L::kStages);
+            }
+            ++qpos;
+            par = (par + nt) & 1u;
+        }
+        if (ok) run_pv();
+        // Make sure no MMA is still writing TMEM when it is released.
+        if (elect_one()) mma_commit(bar(L::kDrain));
+        __syncwarp();
+        mbar_wait_drain(bar(L::kDrain), 0, 1000000000ull);
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ scheduler
+        uint32_t n = 0;
+        bool ok = true;
+        auto publish = [&](const PackedItem& it) {
+            const uint32_t s = n % kPfxItemRing;
+            if (n >= kPfxItemRing) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kItemEmpty + s), ((n / kPfxItemRing) - 1) & 1u, ctx));
+            if (!ok) return;
+            if (lane == 0) {
+                *reinterpret_cast<PackedItem*>(smem + L::kItemOff + s * sizeof(PackedItem)) = it;
+                mbar_arrive(bar(L::kItemFull + s));
+            }
+            __syncwarp();
+            ++n;
+        };
+        PackedItem it{};
+        // The line's length: each lane sums a run of sequences.
+        const int run = (p.R + 31) / 32;
+        int64_t mine = 0;
+        for (int i = 0; i < run; ++i) {
+            const int r = lane * run + i;
+            if (r < p.R) mine += packed_seq<PAGED>(p, r).line.length();
+        }
+        mine *= p.Hk;
+        const int64_t upto = warp_scan64(mine, lane);
+        const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+        const int64_t len = line_stretch(total, p.stretches);
+        for (int i = blockIdx.x; i < p.stretches && ok; i += gridDim.x) {
+            const int64_t x0 = i * len;
+            const int64_t x1 = min(x0 + len, total);
+            PackedCut cut{};
+            if (x0 < x1) {
+                // the run of sequences that x0 is in, then the sequences in groups of 32
+                const int at = __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
+                int64_t start = __shfl_sync(0xffffffffu, upto - mine, at);
+                for (int r0 = at * run; r0 < p.R && start < x1 && ok; r0 += 32) {
+                    PackedSeq own{};
+                    if (r0 + lane < p.R) own = packed_seq<PAGED>(p, r0 + lane);
+                    const int64_t cost = own.line.nq > 0 ? own.line.length() * p.Hk : 0;
+                    const int64_t end_l = start + warp_scan64(cost, lane);
+                    uint32_t in = __ballot_sync(0xffffffffu, cost > 0 && end_l > x0 && end_l - cost < x1);
+                    for (; in != 0 && ok; in &= in - 1) {
+                        const int src = __ffs(in) - 1;
+                        PackedSeq s;
+                        s.line.nq = __shfl_sync(0xffffffffu, own.line.nq, src);
+                        s.line.nk = __shfl_sync(0xffffffffu, own.line.nk, src);
+                        s.line.tile_tokens = p.tile_tokens;
+                        s.line.causal = PAGED ? p.mask == nullptr : p.causal;
+                        s.q0 = __shfl_sync(0xffffffffu, own.q0, src);
+                        s.k0 = __shfl_sync(0xffffffffu, own.k0, src);
+                        const int64_t first = __shfl_sync(0xffffffffu, end_l - cost, src);
+                        const int64_t per = __shfl_sync(0xffffffffu, cost, src) / p.Hk;
+                        const int nb = s.line.blocks();
+                        it.req = r0 + src;
+                        it.k0 = s.k0;
+                        it.step = s.line.causal ? 1 : 0;
+                        int h = x0 > first ? static_cast<int>((x0 - first) / per) : 0;
+                        for (int64_t hs = first + h * per; h < p.Hk && hs < x1 && ok; ++h, hs += per) {
+                            // the block that x0 is in: the last one that begins at or before it
+                            int b = 0;
+                            if (x0 > hs) {
+                                int lo = 0, hi = nb;  // before(lo) <= x0 - hs, and not before(hi)
+                                while (hi - lo > 1) {
+                                    const int width = (hi - lo + 31) / 32;
+                                    const int probe = lo + lane * width;
+                                    const bool below = probe < hi && s.line.before(probe) <= x0 - hs;
+                                    const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));  // lane 0 is
+                                    lo += k * width;
+                                    hi = min(hi, lo + width);
+                                }
+                                b = lo;
+                            }
+                            int64_t us = hs + s.line.before(b);
+                            for (; b < nb && us < x1 && ok; ++b) {
+                                const int tok0 = b * s.line.block_tokens(), tokens = s.line.tokens(b);
+                                const int klen = s.line.keys(b), w = s.line.weight(b);
+                                const int tiles = (klen + kBc - 1) / kBc;
+                                const LinePart part(us, tiles, w, x0, x1);
+                                const bool none = tiles == 0 && us >= x0;  // nothing seen: only written
+                                if (part.t0 < part.t1 || none) {
+                                    it.ntiles = tiles == 0 ? 0 : part.t1 - part.t0;
+                                    it.tile0 = tiles == 0 ? 0 : part.t0;
+                                    it.klen = klen;
+                                    it.head = h;
+                                    it.tok0 = s.q0 + tok0;
+                                    it.nrows = tokens * p.G;
+                                    it.sees0 = it.step ? tok0 + 1 + s.line.nk - s.line.nq : klen;
+                                    it.ntiles0 = it.ntiles;
+                                    if (w == 2 && it.ntiles > 0) {  // at least one, which it may not see a key of
+                                        const int seen0 = s.line.sees(tok0 + s.line.tile_tokens - 1);
+                                        it.ntiles0 = max(1, min(it.ntiles, (seen0 + kBc - 1) / kBc - it.tile0));
+                                    }
+                                    it.slot = -1;
+                                    if (tiles > 0 && it.ntiles < tiles) {
+                                        it.slot = it.tile0 == 0 ? 2 * i + 1 : 2 * i;
+                                        if (it.tile0 == 0) {
+                                            const int64_t last = us + kUnitCost + static_cast<int64_t>(tiles - 1) * (kLineTile * w);
+                                            cut.pieces = static_cast<int>(last / len) - i + 1;
+                                            cut.head = h;
+                                            cut.req = it.req;
+                                            cut.tok0 = it.tok0;
+                                            cut.nrows = it.nrows;
+                                        }
+                                    }
+                                    publish(it);
+                                }
+                                us += s.line.cost(b);
+                            }
+                        }
+                    }
+                    start = __shfl_sync(0xffffffffu, end_l, 31);
+                }
+            }
+            if (lane == 0) p.cuts[i] = cut;
+        }
+        it.ntiles = -1;
+        if (ok) publish(it);
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ Q loader
+        uint32_t qpos = 0;
+        uint32_t q_slots = 0, q_parity = 0;  // slots that a copy was issued to, and the parity it completes
+        bool ok = true;
+        PackedItem it;
+        for (uint32_t n = 0; ok && take_item(n, it); ++n) {
+            if (it.ntiles == 0) continue;
+            for (int k = 0; k < (it.nrows > p.qrows ? 2 : 1) && ok; ++k, ++qpos) {
+                const uint32_t slot = qpos & 1u;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kQEmpty + slot), ((qpos >> 1) & 1u) ^ 1u, ctx));
+                if (!ok) break;
+                const uint32_t full = bar(L::kQFull + slot);
+                if (lane == 0) {  // whole tokens; what lies behind the tensor reads as zero
+                    mbar_arrive_expect_tx(full, p.qrows * D * 2);
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b)
+                        tma_load_5d(s_base + L::kQOff + slot * L::kTile + b * (kBr * 128), &tmap_q, full, b * 64, 0, it.head,
+                                    it.tok0 + k * p.tile_tokens, PAGED ? it.req : 0);
+                }
+                q_slots |= 1u << slot;
+                q_parity = (q_parity & ~(1u << slot)) | (((qpos >> 1) & 1u) << slot);
+                __syncwarp();
+            }
+        }
+        for (uint32_t s = 0; s < 2; ++s)  // the copies land before the shared memory is released
+            if (q_slots & (1u << s)) mbar_wait_drain(bar(L::kQFull + s), (q_parity >> s) & 1u, 50000000ull);
+    } else {
+        // ------------------------------------------------------------ softmax warpgroups
+        const int t = (warp - 4) >> 2;          // chain
+        const int quad = warp & 3;              // TMEM lane quadrant
+        const int rloc = quad * 32 + lane;      // row within the tile
+        const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t t_s = tmem + lane_addr + t * kBc;
+        const uint32_t t_o = tmem + lane_addr + 2 * kBc;  // O_0; O_1 is D columns further
+        float2* xchg = reinterpret_cast<float2*>(smem + L::kXchgOff);
+        const float sl2 = p.scale_log2;
+        const int row_tok = rloc / p.G, row_head = rloc - row_tok * p.G;  // this row's token in its tile, and head of the group
+        uint32_t s_cnt = 0, x_cnt = 0, ring = 0;  // ring: K/V fills before this item
+        uint32_t o_phase = 0u;                    // parity of each chain's next finished item, bit c
+        uint32_t par = 0;
+        bool ok = true;
+        PackedItem it;
+        for (uint32_t n = 0; ok && take_item(n, it); ++n) {
+            const bool two = it.nrows > p.qrows;
+            const int nt = it.ntiles;
+            const int mine = two ? t : t ^ static_cast<int>(par);  // this chain's query tile, or its first K/V tile
+            const int k = two ? mine : 0;                     // its query tile
+            const int nrow = min(p.qrows, it.nrows - k * p.qrows);
+            const bool warp_on = quad * 32 < nrow;            // the warp has rows
+            const bool row_on = rloc < nrow;
+            const int tok = it.tok0 + k * p.tile_tokens + row_tok;
+            // where this row's results go
+            const int hq = it.head * p.G + row_head;
+            const int64_t req = PAGED ? it.req : 0;
+            auto out_row = [&]() -> uint4* { return reinterpret_cast<uint4*>(p.o + req * p.os[0] + hq * p.os[1] + tok * p.os[2]); };
+            auto out_lse = [&]() -> float* { return p.lse + req * p.ls[0] + hq * p.ls[1] + tok; };
+            if (nt == 0) {  // no key for any row: O = 0, LSE = -inf
+                if (row_on && (two || t == 0)) {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) out_row()[c] = make_uint4(0, 0, 0, 0);
+                    *out_lse() = -INFINITY;
+                }
+                continue;
+            }
+            const bool both = two || nt >= 2;                 // both chains work on the item
+            const bool used = both || mine == 0;
+            const int nt_mine = two && t == 0 ? it.ntiles0 : nt;
+            float m_ref = -INFINITY;
+            float l = 0.f;
+            if (used) {
+                // Key counts from the item's first tile on: all that the unit sees, those that this row
+                // sees and that every row of the tile does.
+                const int left = it.klen - it.tile0 * kBc;
+                const int drafts = PAGED && p.mask ? it.klen - p.T - it.tile0 * kBc : 0;  // where the new tokens' keys begin
+                int lim, all_see;
+                if (PAGED && p.mask) {
+                    lim = left;
+                    all_see = drafts;
+                } else {
+                    const int tile_tok = k * p.tile_tokens;
+                    lim = min(it.klen, it.sees0 + (tile_tok + row_tok) * it.step) - it.tile0 * kBc;
+                    all_see = min(it.klen, it.sees0 + tile_tok * it.step) - it.tile0 * kBc;
+                }
+                const uint32_t* mask_row = nullptr;
+                if (PAGED && p.mask)
+                    mask_row = p.mask + (static_cast<int64_t>(it.req) * p.T + (row_on ? tok : it.tok0)) * p.words;
+                bool first = true;
+                for (int j = two ? 0 : mine; j < nt_mine; j += two ? 1 : 2) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kSFull + t), s_cnt & 1u, ctx));
+                    ++s_cnt;
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const int key0 = j * kBc;
+                    const int keys = min(kBc, left - key0);
+                    // The output product sums over keys in steps of 16.  What lies behind the last key may
+                    // hold anything (a NaN times a zero weight is a NaN): zero it, before the first product that reads it.
+                    if ((keys & 15) != 0 && (!two || t == (j < it.ntiles0 ? 0 : 1))) {
+                        const uint32_t at = ring + 2 * j + 1;  // V_j's fill
+                        const uint32_t stage = at % L::kStages;
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvFull + stage), (at / L::kStages) & 1u, ctx));
+                        if (!ok) break;
+                        const int pad = ((keys + 15) & ~15) - keys;
+                        uint8_t* v = smem + L::kRingOff + stage * L::kTile;
+                        for (int i = rloc; i < pad * (D / 8); i += 128) {
+                            const int row = keys + i / (D / 8), c8 = i % (D / 8);
+                            *reinterpret_cast<uint4*>(v + (c8 >> 3) * (kBc * 128) + row * 128 + (c8 & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    if (!warp_on) {  // none of this warp's rows exist: only keep the barriers' counts
+                        mbar_arrive(bar(L::kPHalf + t));
+                        mbar_arrive(bar(L::kPFull + t));
+                        continue;
+                    }
+                    const float m_old = m_ref;
+                    bool grow = false;
+                    float alpha = 1.f;
+                    // moves the reference maximum and l where a tile's maximum asks for it
+                    auto refer = [&](float mx) {
+                        // a row that sees no key of the tile keeps its reference (0 * -inf would be a NaN)
+                        const float m_tile = mx == -INFINITY ? -INFINITY : mx * p.max_scale_log2;
+                        grow = row_on && m_tile > m_old + kRescaleLog2Bf16;
+                        if (grow) {
+                            alpha = ex2_approx(m_old - m_tile);  // 0 the first time
+                            m_ref = m_tile;
+                        }
+                        l *= alpha;
+                    };
+                    // Rescales O when a reference moved, before the first half of P is released.
+                    // O's previous product has completed: it was issued before this S.
+                    auto rescale = [&]() {
+                        if (__any_sync(0xffffffffu, grow && !first)) {
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(t_o + t * D + c, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                tmem_st32(t_o + t * D + c, o);
+                            }
+                        }
+                        first = false;
+                    };
+                    float acc0 = 0.f, acc1 = 0.f, acc2 = 0.f, acc3 = 0.f;
+                    auto exp_chunk = [&](const float* sc, uint32_t col) {
+                        const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) {
+                            float x0, x1, x2, x3;
+                            ffma2(x0, x1, sc[2 * c], sc[2 * c + 1], sl2, -m_use);
+                            ffma2(x2, x3, sc[2 * c + 2], sc[2 * c + 3], sl2, -m_use);
+                            const float a0 = ex2_approx(x0), b0 = ex2_approx(x1);
+                            const float a1 = ex2_approx(x2), b1 = ex2_approx(x3);
+                            fadd2(acc0, acc1, a0, b0);
+                            fadd2(acc2, acc3, a1, b1);
+                            pk[c] = pack_bf16x2(a0, b0);
+                            pk[c + 1] = pack_bf16x2(a1, b1);
+                        }
+                        tmem_st16(t_s + col, pk);
+                    };
+                    if (key0 + kBc <= all_see) {  // every row sees all 128 keys
+                        uint32_t r0[32], r1[32], r2[32], r3[32];
+                        tmem_ld32(t_s + 0, r0);
+                        tmem_ld32(t_s + 32, r1);
+                        tmem_wait_ld(r0);
+                        tmem_wait_ld(r1);
+                        tmem_ld32(t_s + 64, r2);
+                        tmem_ld32(t_s + 96, r3);
+                        float* s0 = reinterpret_cast<float*>(r0);
+                        float* s1 = reinterpret_cast<float*>(r1);
+                        float* s2 = reinterpret_cast<float*>(r2);
+                        float* s3 = reinterpret_cast<float*>(r3);
+                        float mx0 = fmax3(s0[0], s0[1], s0[2]), mx1 = fmax3(s1[0], s1[1], s1[2]);
+#pragma unroll
+                        for (int c = 3; c < 31; c += 2) {
+                            mx0 = fmax3(mx0, s0[c], s0[c + 1]);
+                            mx1 = fmax3(mx1, s1[c], s1[c + 1]);
+                        }
+                        mx0 = fmax3(mx0, s0[31], fmaxf(mx1, s1[31]));
+                        tmem_wait_ld(r2);
+                        tmem_wait_ld(r3);
+                        float mx2 = fmax3(s2[0], s2[1], s2[2]), mx3 = fmax3(s3[0], s3[1], s3[2]);
+#pragma unroll
+                        for (int c = 3; c < 31; c += 2) {
+                            mx2 = fmax3(mx2, s2[c], s2[c + 1]);
+                            mx3 = fmax3(mx3, s3[c], s3[c + 1]);
+                        }
+                        refer(fmax3(mx0, fmax3(mx2, s2[31], mx3), s3[31]));
+                        exp_chunk(s0, 0);
+                        exp_chunk(s1, 16);
+                        rescale();
+                        tmem_wait_st();
+                        tc_fence_before_sync();
+                        mbar_arrive(bar(L::kPHalf + t));
+                        exp_chunk(s2, 32);
+                        exp_chunk(s3, 48);
+                    } else {
+                        // Keys that not every row sees: chunk by chunk in little code, reading the
+                        // scores twice.  Chunks past the last key are left out (the output product
+                        // stops at the step of 16 that holds it).  P of chunk i overwrites scores of
+                        // chunk i / 2, which has been read.
+                        const int nch = (keys + 31) >> 5;
+                        // bit c of chunk i: this row sees its key c
+                        auto seen_bits = [&](int i) -> uint32_t {
+                            if (PAGED && p.mask) {
+                                const int rel = key0 + 32 * i - drafts;  // the chunk's first key among the new tokens
+                                if (rel <= -32) return 0xffffffffu;
+                                auto word = [&](int w) -> uint32_t {
+                                    if (w < 0) return 0xffffffffu;  // keys before them
+                                    if (w * 32 >= p.T) return 0u;
+                                    const uint32_t m = __ldg(mask_row + w);
+                                    return p.T - w * 32 >= 32 ? m : m & ((1u << (p.T - w * 32)) - 1u);
+                                };
+                                const int w = rel >> 5;  // (rounds down)
+                                return __funnelshift_r(word(w), word(w + 1), rel & 31);
+                            }
+                            const int seen = lim - key0 - 32 * i;
+                            return seen >= 32 ? 0xffffffffu : seen <= 0 ? 0u : (1u << seen) - 1u;
+                        };
+                        uint32_t r[32];
+                        float* sc = reinterpret_cast<float*>(r);
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int i = 0; i < nch; ++i) {
+                            tmem_ld32(t_s + 32 * i, r);
+                            const uint32_t seen = seen_bits(i);
+                            tmem_wait_ld(r);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) mx = fmaxf(mx, (seen >> c) & 1u ? sc[c] : -INFINITY);
+                        }
+                        refer(mx);
+                        rescale();
+#pragma unroll 1
+                        for (int i = 0; i < nch; ++i) {
+                            tmem_ld32(t_s + 32 * i, r);
+                            const uint32_t seen = seen_bits(i);
+                            tmem_wait_ld(r);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!((seen >> c) & 1u)) sc[c] = -INFINITY;
+                            exp_chunk(sc, 16 * i);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before_sync();
+                        mbar_arrive(bar(L::kPHalf + t));
+                    }
+                    l += (acc0 + acc1) + (acc2 + acc3);
+                    tmem_wait_st();
+                    tc_fence_before_sync();
+                    mbar_arrive(bar(L::kPFull + t));
+                }
+                if (!ok) break;
+                // Epilogue: O / l and the log-sum-exp, or this piece's for the combine kernel.
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kOFull + t), (o_phase >> t) & 1u, ctx));
+                if (!ok) break;
+                const bool merge = both && !two;
+                float w_own = 1.f, w_other = 0.f;  // of this chain's O and the other's
+                float m = m_ref, sum = l;
+                if (merge) {
+                    // chain 1's (m, l) through shared memory, then chain 0's through the same place
+                    if (t == 1) {
+                        xchg[rloc] = make_float2(m_ref, l);
+                        mbar_arrive(bar(L::kX + 1));
+                    }
+                    ok = mbar_wait(bar(L::kX + (t ^ 1)), x_cnt & 1u, ctx) &&
+                         mbar_wait(bar(L::kOFull + (t ^ 1)), (o_phase >> (t ^ 1)) & 1u, ctx);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    const float2 other = xchg[rloc];
+                    if (t == 0) {
+                        xchg[rloc] = make_float2(m_ref, l);
+                        mbar_arrive(bar(L::kX + 0));
+                    }
+                    m = fmaxf(m_ref, other.x);
+                    w_own = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
+                    w_other = other.x == -INFINITY ? 0.f : ex2_approx(other.x - m);
+                    // a chain whose reference never moved has l = 0, or a NaN to pass on
+                    sum = (m_ref == -INFINITY ? l : l * w_own) + (other.x == -INFINITY ? other.y : other.y * w_other);
+                }
+                tc_fence_after_sync();
+                // a row that sees no key of this piece: O = 0, LSE = -inf
+                const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+                const float wa = w_own * inv, wb = w_other * inv;
+                const int c0 = merge ? t * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
+                const float lse = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2;
+                if (warp_on && it.slot < 0) {
+                    uint4* orow = out_row();
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t o[32], pw[16];
+                        tmem_ld32(t_o + t * D + c, o);
+                        tmem_wait_ld(o);
+                        if (merge) {
+                            uint32_t ob[32];
+                            tmem_ld32(t_o + (t ^ 1) * D + c, ob);
+                            tmem_wait_ld(ob);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                pw[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * wa + __uint_as_float(ob[2 * i]) * wb,
+                                                    __uint_as_float(o[2 * i + 1]) * wa + __uint_as_float(ob[2 * i + 1]) * wb);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                pw[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * wa, __uint_as_float(o[2 * i + 1]) * wa);
+                        }
+                        if (sum == 0.f) {  // (0 times a NaN of V would not be 0)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) pw[i] = 0u;
+                        }
+                        if (row_on) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                orow[c / 8 + i] = make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
+                        }
+                    }
+                    if (row_on && (!merge || t == 0)) *out_lse() = lse;
+                } else if (warp_on) {
+                    const int64_t part = static_cast<int64_t>(it.slot) * p.orows + k * p.qrows;
+                    // evict-last: read back right after this grid
+                    const uint64_t keep = l2_policy_evict_last();
+                    const int here = nrow - quad * 32;  // rows of this warp
+                    float* out = p.part_o + (part + quad * 32 + (lane >> 2)) * D + (lane & 3) * 2;
+#pragma unroll 1
+                    for (int half = 0; half < 32 && half < here; half += 16) {
+                        // the weights of this thread's two rows
+                        const int ra = half + (lane >> 2);
+                        const float wa0 = __shfl_sync(0xffffffffu, wa, ra), wa1 = __shfl_sync(0xffffffffu, wa, ra + 8);
+                        const float wb0 = __shfl_sync(0xffffffffu, wb, ra), wb1 = __shfl_sync(0xffffffffu, wb, ra + 8);
+                        const uint32_t lanes = static_cast<uint32_t>(half) << 16;
+#pragma unroll 1
+                        for (int c = c0; c < c1; c += 32) {
+                            uint32_t oa[16];
+                            tmem_ld16x256(t_o + lanes + t * D + c, oa);
+                            if (merge) {
+                                uint32_t ob[16];
+                                tmem_ld16x256(t_o + lanes + (t ^ 1) * D + c, ob);
+                                tmem_wait_ld16(oa);
+                                tmem_wait_ld16(ob);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    oa[i] = __float_as_uint(__uint_as_float(oa[i]) * ((i & 2) ? wa1 : wa0) +
+                                                            __uint_as_float(ob[i]) * ((i & 2) ? wb1 : wb0));
+                            } else {
+                                tmem_wait_ld16(oa);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    oa[i] = __float_as_uint(__uint_as_float(oa[i]) * ((i & 2) ? wa1 : wa0));
+                            }
+                            float* o0 = out + half * D + c;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4) {
+                                if (ra < here)
+                                    st_global_v2_hint(o0 + 2 * i, __uint_as_float(oa[i]), __uint_as_float(oa[i + 1]), keep);
+                                if (ra + 8 < here)
+                                    st_global_v2_hint(o0 + 8 * D + 2 * i, __uint_as_float(oa[i + 2]),
+                                                      __uint_as_float(oa[i + 3]), keep);
+                            }
+                        }
+                    }
+                    if (row_on && (!merge || t == 0)) st_global_hint(p.part_lse + part + rloc, lse, keep);
+                }
+                tc_fence_before_sync();
+                if (merge) {
+                    mbar_arrive(bar(L::kOEmpty + 0));
+                    mbar_arrive(bar(L::kOEmpty + 1));
+                    ++x_cnt;
+                } else {
+                    mbar_arrive_n(bar(L::kOEmpty + t), 2);
+                }
+            }
+            o_phase ^= both ? 3u : 1u << par;
+            ring += 2 * nt;
+            par = two ? 0u : (par + nt) & 1u;
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Merge the pieces of the units that stretches cut: CTA (x, i) takes rows of the unit whose pieces begin in
+// stretch i.  WARPS warps per row (pieces dealt to them in turn, each with a running maximum, then merged in a fixed
+// order); lane l holds columns [kPer l, kPer l + kPer).
+template <int D, int WARPS>
+__global__ void __launch_bounds__(256) attn_packed_combine_kernel(const __grid_constant__ PackedParams p) {
+    constexpr int kPer = D / 32;
+    constexpr int kRows = 8 / WARPS;  // rows per CTA and turn
+    __shared__ float s_acc[8][D];
+    __shared__ float2 s_stat[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = warp % WARPS;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int i = blockIdx.y;
+    const int* desc = reinterpret_cast<const int*>(p.cuts + i);
+    const int pieces = __ldcg(desc);
+    const int nrows = pieces > 0 ? __ldcg(desc + 4) : 0;
+    // every warp of the CTA takes part in its turns
+    for (int base = blockIdx.x * kRows; base < nrows; base += gridDim.x * kRows) {
+        const int row = base + warp / WARPS;
+        const bool on = row < nrows;
+        auto at = [&](int s) -> int64_t { return static_cast<int64_t>(s == 0 ? 2 * i + 1 : 2 * (i + s)) * p.orows + row; };
+        float acc[kPer];
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+        float sum = 0.f, mx = -INFINITY;
+        constexpr int kUnroll = 6;
+        for (int s0 = part; on && s0 < pieces; s0 += WARPS * kUnroll) {
+            float v[kUnroll][kPer], ls[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int s = s0 + u * WARPS;
+                ls[u] = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) v[u][c] = 0.f;
+                if (s < pieces) {
+                    ls[u] = __ldcg(p.part_lse + at(s));
+                    CombineVec<D>::load(p.part_o + at(s) * D + lane * kPer, v[u]);
+                }
+            }
+            float m = mx;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) m = fmaxf(m, ls[u]);
+            const float keep = mx == -INFINITY ? 0.f : expf(mx - m);
+            mx = m;
+            sum *= keep;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) acc[c] *= keep;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (ls[u] == -INFINITY) continue;  // no key of the piece is seen: what its row holds does not count
+                const float w = expf(ls[u] - mx);
+                sum += w;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) acc[c] = fmaf(w, v[u][c], acc[c]);
+            }
+        }
+        if (WARPS > 1) {
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) s_acc[warp][lane * kPer + c] = acc[c];
+            if (lane == 0) s_stat[warp] = make_float2(mx, sum);
+            __syncthreads();
+            if (part == 0) {
+                float m = mx;
+                for (int k = 1; k < WARPS; ++k) m = fmaxf(m, s_stat[warp + k].x);
+                const float keep = mx == -INFINITY ? 1.f : expf(mx - m);  // (nothing yet, or a NaN to pass on)
+                sum *= keep;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) acc[c] *= keep;
+                for (int k = 1; k < WARPS; ++k) {
+                    const float2 st = s_stat[warp + k];
+                    const float w = st.x == -INFINITY ? 1.f : expf(st.x - m);
+                    sum += st.y * w;
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c) acc[c] = fmaf(w, s_acc[warp + k][lane * kPer + c], acc[c]);
+                }
+                mx = m;
+            }
+            __syncthreads();
+        }
+        if (on && part == 0) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int tok = row / p.G, hq = __ldcg(desc + 1) * p.G + row - tok * p.G;
+            const int64_t req = p.lens ? __ldcg(desc + 2) : 0;
+            const int64_t token = __ldcg(desc + 3) + tok;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + req * p.os[0] + hq * p.os[1] + token * p.os[2] + lane * kPer);
+#pragma unroll
+            for (int c = 0; c < kPer; c += 2) dst[c / 2] = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+            if (lane == 0) p.lse[req * p.ls[0] + hq * p.ls[1] + token] = sum == 0.f ? -INFINITY : mx + logf(sum);
+        }
+    }
+}
+
+}  // namespace elsattn

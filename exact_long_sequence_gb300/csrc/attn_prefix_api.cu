@@ -145,23 +145,6 @@ struct PrefixSpace {
     }
 };
 
-// Strides of a view in elements; nullptr: contiguous.  TMA takes strides of a
-// multiple of 16 bytes below 2^40; an axis of one is never stepped.
-template <int N>
-int take_view(int64_t (&out)[N], const int64_t* given, const int64_t (&dims)[N], int64_t inner) {
-    int64_t dense = inner;
-    for (int i = N - 1; i >= 0; --i) {
-        out[i] = dense;
-        if (given && dims[i] > 1) {
-            out[i] = given[i];
-            if (out[i] % 8 != 0) return ATTN_ERR_MISALIGNED;
-            if (out[i] <= 0 || out[i] >= (1LL << 39) || out[i] > (1LL << 39) / dims[i]) return ATTN_ERR_INVALID_ARG;
-        }
-        dense *= dims[i];
-    }
-    return ATTN_OK;
-}
-
 template <int D>
 int launch(DeviceState& dev, const CUtensorMap (&maps)[6], const PrefixParams& p, cudaStream_t stream) {
     auto kernel = attn_prefix_kernel<D>;

@@ -1,0 +1,94 @@
+// The line of work of attention over sequences of different lengths, as the
+// kernels cut it: plain arithmetic, the same on the host and the device.
+//
+// The G query heads that share a key head are rows of one matrix: token t and
+// head g of a sequence are row t G + g of its key head.  A query tile is the
+// `tile_tokens` = 128 / G whole tokens that fit 128 rows, a block is two tiles.
+// A unit is one block of a sequence at one key head against the keys that it
+// sees.  On the line the units follow one another sequence by sequence, key
+// head by key head, block by block; a unit is kUnitCost and then its keys, each
+// as long as it costs: two for a block of two query tiles, one for a block of
+// one.  The line is cut into even stretches; a tile of 128 keys belongs to the
+// stretch that holds the first position of it, so that every position is
+// found from the lengths alone and the work of a stretch differs from the
+// others' by a tile.
+#pragma once
+
+#include <cstdint>
+
+#ifndef ELS_HD
+#ifdef __CUDACC__
+#define ELS_HD __host__ __device__ __forceinline__
+#else
+#define ELS_HD inline
+#endif
+#endif
+
+namespace elsattn {
+
+constexpr int kLineTile = 128;    // keys of a tile
+// Start and end of a unit (query rows, pipeline fill, output) in line positions.
+constexpr int kUnitCost = 192;
+// A stretch is at least this long, so that each one between the first and the last of a unit has a tile of it.
+constexpr int kLineLeast = 2 * 2 * kLineTile;
+
+// The units of one sequence at one key head.
+struct LineSeq {
+    int nq, nk;          // tokens, keys
+    int tile_tokens;
+    bool causal;         // token t sees the keys j <= t + nk - nq; otherwise all of them
+    ELS_HD int block_tokens() const { return 2 * tile_tokens; }
+    // (in 64 bits: the tokens rounded up to whole blocks may pass 32)
+    ELS_HD int blocks() const { return static_cast<int>((static_cast<int64_t>(nq) + block_tokens() - 1) / block_tokens()); }
+    ELS_HD int tokens(int b) const {
+        const int64_t left = nq - static_cast<int64_t>(b) * block_tokens();
+        return left < block_tokens() ? static_cast<int>(left) : block_tokens();
+    }
+    // Keys that token t sees.
+    ELS_HD int sees(int64_t t) const {
+        if (!causal) return nk;
+        const int64_t v = t + 1 + nk - nq;
+        return v < 0 ? 0 : v > nk ? nk : static_cast<int>(v);
+    }
+    // Keys that a block sees: those of its last token.
+    ELS_HD int keys(int b) const { return sees(static_cast<int64_t>(b) * block_tokens() + tokens(b) - 1); }
+    ELS_HD int weight(int b) const { return tokens(b) > tile_tokens ? 2 : 1; }
+    // Positions of the blocks before b (b < blocks(), so all of them are whole).
+    ELS_HD int64_t before(int b) const {
+        const int64_t n = b;
+        if (!causal) return n * (kUnitCost + 2 * static_cast<int64_t>(nk));
+        // block i sees nk - nq + (i + 1) block_tokens keys, none where that is negative
+        const int64_t off = static_cast<int64_t>(nk) - nq, bt = block_tokens();
+        int64_t i0 = off < 0 ? -off / bt : 0;
+        if (i0 > n) i0 = n;
+        return n * kUnitCost + 2 * ((n - i0) * off + bt * (n * (n + 1) / 2 - i0 * (i0 + 1) / 2));
+    }
+    ELS_HD int64_t cost(int b) const { return kUnitCost + static_cast<int64_t>(weight(b)) * keys(b); }
+    // All blocks.
+    ELS_HD int64_t length() const {
+        if (nq <= 0) return 0;
+        const int last = blocks() - 1;
+        return before(last) + cost(last);
+    }
+};
+
+// What a stretch [x0, x1) has of a unit that starts at `start` (whose tiles start at start + kUnitCost).
+struct LinePart {
+    int t0, t1;     // its tiles [t0, t1)
+    ELS_HD LinePart(int64_t start, int tiles, int weight, int64_t x0, int64_t x1) {
+        const int64_t first = start + kUnitCost;
+        const int step = kLineTile * weight;
+        const int64_t a = x0 > first ? (x0 - first + step - 1) / step : 0;
+        const int64_t b = x1 > first ? (x1 - first + step - 1) / step : 0;
+        t0 = a < tiles ? static_cast<int>(a) : tiles;
+        t1 = b < tiles ? static_cast<int>(b) : tiles;
+    }
+};
+
+// Length of the stretches that a line of `total` is cut into, `most` of them at most.
+ELS_HD int64_t line_stretch(int64_t total, int most) {
+    const int64_t even = (total + most - 1) / most;
+    return even < kLineLeast ? kLineLeast : even;
+}
+
+}  // namespace elsattn

@@ -483,6 +483,91 @@ int attn_fwd_prefix(const void* Q, const int64_t* q_strides, const void* Kp, con
  * partial rows); 0 for an invalid shape or without a device. */
 size_t attn_fwd_prefix_workspace_bytes(int R, int Hq, int Hk, int T, int P, int C, int d);
 
+/*
+ * attn_fwd_packed - attention of sequences of different lengths whose tokens
+ * follow one another in Q, K and V, with grouped heads:
+ *     O = softmax(scale * Q K^T + mask) V  and its log-sum-exp,
+ * each query over the keys of its own sequence.  The heads of a group are rows
+ * of one matrix against their key head, and the work of all sequences is cut
+ * into even shares for the SMs (the tall-and-skinny products and their balance
+ * are the AttenIO abstract's), whatever the lengths are.
+ *   Q, O    : bf16 [Hq, Nq, d] device views; Hq a multiple of Hk (at most 64 Hk, ATTN_ERR_UNSUPPORTED
+ *             beyond), query head h reads key head h / (Hq / Hk)
+ *   K, V    : bf16 [Hk, Nk, d] device views
+ *   q_starts, k_starts : int32 [R + 1] device, non-decreasing: sequence s has the queries
+ *             q_starts[s] .. q_starts[s + 1] - 1 and the keys k_starts[s] .. k_starts[s + 1] - 1,
+ *             either of which may be none.  The two may be the same array.  Read on the device, so a
+ *             captured graph may be replayed with other lengths.  Offsets outside the tensors are
+ *             clipped to them, and a sequence whose end is before its start is empty; sequences must
+ *             not overlap in Q (their rows would be written twice).
+ *   causal  : not 0: query t of a sequence's n sees the keys j <= t + m - n of its m, so that the
+ *             last query sees all of them; with more queries than keys the first see none
+ *   A row that sees no key is O = 0, LSE = -inf.  Rows of tokens that are in no sequence stay
+ *   as they were.  K and V rows of other sequences are not used, whatever they hold; a NaN or
+ *   infinity in V reaches every row of its own sequence that is computed in the same tile of 128 keys.
+ *   LSE     : fp32 [Hq, Nq] device, contiguous (natural log)
+ *   *_strides : host arrays of two strides in elements (head, token), d contiguous; NULL:
+ *             contiguous.  Positive multiples of 8 for axes longer than 1, and stride times
+ *             extent at most 2^39.
+ *   R, Nq, Nk >= 1; Hq * Nq and Hk * Nk below 2^31 - 512;  d : 64 or 128;  scale : any finite value
+ *   workspace : device buffer of at least attn_fwd_packed_workspace_bytes(), 16-byte
+ *             aligned, owned by the caller, not used by other work while this call runs
+ *             (calls that may overlap, captured graphs among them, need one each)
+ * Arithmetic as attn_fwd (fp32 scores and sums, P rounded to bf16); pieces of a row's
+ * keys are kept in fp32, O is rounded once.  The cut into pieces depends on the
+ * lengths of all sequences, so bits may differ between batches, not between equal calls.
+ * Two launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
+ */
+int attn_fwd_packed(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides, const void* V,
+                    const int64_t* v_strides, const int32_t* q_starts, const int32_t* k_starts, void* O,
+                    const int64_t* o_strides, float* LSE, int R, int Nq, int Nk, int Hq, int Hk, int d, int causal,
+                    float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Device bytes attn_fwd_packed needs as workspace on the current device (its
+ * partial rows); 0 for an invalid shape or without a device. */
+size_t attn_fwd_packed_workspace_bytes(int R, int Nq, int Nk, int Hq, int Hk, int d);
+
+/*
+ * attn_fwd_tree - attention of T new tokens of each of R requests over keys and
+ * values in the pages of a cache: single tokens, a run of tokens, or a tree of
+ * drafted tokens that are checked at once.  The request's new tokens are the
+ * last T of its keys; every new token sees the keys before them, and of the new
+ * ones those that its row of tree_mask names.  Computed as attn_fwd_packed.
+ *   Q, O    : bf16 [R, Hq, T, d] device views; Hq a multiple of Hk, as above
+ *   Kc, Vc  : bf16 [pages, Hk, page_size, d] device views; page_size a power of two
+ *             from 16 to 1024 (ATTN_ERR_UNSUPPORTED otherwise)
+ *   page_table : int32 [R][table_pages] device, rows table_stride apart: the pages of a
+ *             request's keys in order.  Only those of its keys are read; an entry
+ *             that is no page of the cache reads as zeros.
+ *   lens    : int32 [R] device: the request's keys, its T new tokens (the last of them)
+ *             among them; more than table_pages * page_size counts as that.  0: none:
+ *             O = 0, LSE = -inf.  Negative: the request is padding and its rows stay as
+ *             they were.  Of a len below T the new tokens are the last of T: those before are missing.
+ *   tree_mask : int32 [R, T, ceil(T / 32)] device, contiguous, or NULL: new token t sees
+ *             new token j where bit j % 32 of word j / 32 of its row is set (its own bit is
+ *             not implied; bits past T do not count).  NULL: it sees those up to itself.
+ *             Read on the device, as lens and page_table: a captured graph may be replayed with others.
+ *   A row that sees no key is O = 0, LSE = -inf.  Cache rows that are not a request's
+ *   keys may hold anything, NaN included.  A NaN or infinity in a new token's K reaches
+ *   only the tokens that see it; in its V it reaches every new token of that request.
+ *   LSE     : fp32 [R, Hq, T] device, contiguous (natural log)
+ *   *_strides : host arrays of three strides in elements (Q, O: request, head, token;
+ *             Kc, Vc: page, head, key), as above;  table_stride : elements, >= 0
+ *   d       : 64 or 128;  scale : any finite value;  R, T, pages, table_pages >= 1; R * Hq * T,
+ *             pages and table_pages * page_size below 2^31 - 512
+ *   workspace : attn_fwd_tree_workspace_bytes(), as above
+ * Two launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
+ */
+int attn_fwd_tree(const void* Q, const int64_t* q_strides, const void* Kc, const int64_t* k_strides, const void* Vc,
+                  const int64_t* v_strides, const int32_t* page_table, int64_t table_stride, const int32_t* lens,
+                  const int32_t* tree_mask, void* O, const int64_t* o_strides, float* LSE, int R, int Hq, int Hk, int T,
+                  int pages, int page_size, int table_pages, int d, float scale, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/* Device bytes attn_fwd_tree needs as workspace on the current device; 0 for an
+ * invalid shape or without a device. */
+size_t attn_fwd_tree_workspace_bytes(int R, int Hq, int Hk, int T, int d);
+
 #ifdef __cplusplus
 }
 #endif
