@@ -66,6 +66,8 @@ EXPORTED_SYMBOLS = (
     "attn_fwd_prefix_workspace_bytes",
     "attn_fwd_packed",
     "attn_fwd_packed_workspace_bytes",
+    "attn_bwd_packed",
+    "attn_bwd_packed_workspace_bytes",
     "attn_fwd_tree",
     "attn_fwd_tree_workspace_bytes",
 )
@@ -170,6 +172,10 @@ def load_library(path: str | None = None):
     lib.attn_fwd_packed.restype = i
     lib.attn_fwd_packed_workspace_bytes.argtypes = [i] * 6
     lib.attn_fwd_packed_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_bwd_packed.argtypes = [vp] * 19 + [i] * 7 + [f, vp, ctypes.c_size_t, vp]
+    lib.attn_bwd_packed.restype = i
+    lib.attn_bwd_packed_workspace_bytes.argtypes = [i] * 6
+    lib.attn_bwd_packed_workspace_bytes.restype = ctypes.c_size_t
     lib.attn_fwd_tree.argtypes = [vp] * 7 + [i64] + [vp] * 5 + [i] * 8 + [f, vp, ctypes.c_size_t, vp]
     lib.attn_fwd_tree.restype = i
     lib.attn_fwd_tree_workspace_bytes.argtypes = [i] * 5
@@ -735,6 +741,61 @@ def attn_fwd_packed(q, k, v, q_starts, k_starts=None, causal: bool = False, scal
                              _raw_stream(stream, index))
     _check(st, "attn_fwd_packed")
     return out, lse
+
+
+def packed_bwd_workspace_bytes(R: int, Nq: int, Nk: int, Hq: int, Hk: int, d: int) -> int:
+    """Device bytes attn_bwd_packed needs for this shape on the current device (0: invalid shape)."""
+    return int(load_library().attn_bwd_packed_workspace_bytes(R, Nq, Nk, Hq, Hk, d))
+
+
+@functools.lru_cache(maxsize=256)
+def _packed_bwd_workspace_bytes(index, *shape) -> int:
+    return _found(load_library().attn_bwd_packed_workspace_bytes(*shape))
+
+
+def attn_bwd_packed(q, k, v, o, lse, do, q_starts, k_starts=None, causal: bool = False, scale: float | None = None, dq=None,
+                    dk=None, dv=None, workspace=None, stream=None):
+    """dQ, dK, dV = gradients of attn_fwd_packed for the upstream gradient `do`.
+
+    q, k, v, q_starts, k_starts, causal, scale : as given to attn_fwd_packed; o, lse: as it returned them
+    do         : bf16 view like q
+    dq, dk, dv : optional bf16 views like q, k and v (default: new contiguous tensors).  Rows of tokens that are in no
+                 sequence are left as they were.
+    workspace  : optional uint8 CUDA tensor of packed_bwd_workspace_bytes() bytes
+    dk and dv are summed over the query heads that share a key head.  Returns (dq, dk, dv)."""
+    lib = load_library()
+    index, Hq, Nq, Hk, Nk, d = _packed_qkv(q, k, v)
+    R = q_starts.shape[0] - 1 if q_starts.dim() == 1 else 0
+    qst = _starts("q_starts", q_starts, R, index)
+    kst = qst if k_starts is None else _starts("k_starts", k_starts, R, index)
+    if lse is None:
+        raise ValueError("lse must be the one that attn_fwd_packed returned")
+    if scale is None:
+        scale = _SCALES.get(d) or default_scale(d)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return attn_bwd_packed(q, k, v, o, lse, do, q_starts, k_starts, causal, scale, dq, dk, dv, workspace, stream)
+    qp, qs = _view("q", q, q.shape, index)
+    kp, ks = _view("k", k, k.shape, index)
+    vp, vs = _view("v", v, k.shape, index)
+    op, os_ = _view("o", o, q.shape, index)
+    gp, gs = _view("do", do, q.shape, index)
+    lse = _lse(lse, (Hq, Nq), q, index, stream)
+    if dq is None:
+        dq = _empty((Hq, Nq, d), torch.bfloat16, q.device, stream)
+    if dk is None:
+        dk = _empty((Hk, Nk, d), torch.bfloat16, q.device, stream)
+    if dv is None:
+        dv = _empty((Hk, Nk, d), torch.bfloat16, q.device, stream)
+    dqp, dqs = _view("dq", dq, q.shape, index)
+    dkp, dks = _view("dk", dk, k.shape, index)
+    dvp, dvs = _view("dv", dv, k.shape, index)
+    workspace = _workspace(workspace, _packed_bwd_workspace_bytes, (R, Nq, Nk, Hq, Hk, d), q, index, stream)
+    st = lib.attn_bwd_packed(qp, qs, kp, ks, vp, vs, op, os_, lse.data_ptr(), gp, gs, qst, kst, dqp, dqs, dkp, dks, dvp, dvs,
+                             R, Nq, Nk, Hq, Hk, d, 1 if causal else 0, float(scale), workspace.data_ptr() or None,
+                             workspace.numel(), _raw_stream(stream, index))
+    _check(st, "attn_bwd_packed")
+    return dq, dk, dv
 
 
 def tree_workspace_bytes(R: int, Hq: int, Hk: int, T: int, d: int) -> int:

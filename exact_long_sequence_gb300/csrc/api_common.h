@@ -26,6 +26,7 @@ struct DeviceState {
     bool bwd_smem_configured[2][2] = {{false, false}, {false, false}};  // backward <d == 128><causal>
     bool prefix_smem_configured[2][2] = {};  // shared-prefix forward <own-keys kernel><d == 128>
     bool packed_smem_configured[2][2] = {};  // attention over lengths <paged><d == 128>
+    bool packed_bwd_smem_configured[2] = {};  // its gradient <d == 128>
     bool ready_configured[2][8] = {};  // query / key preparation <backward><variant>
     bool fp8_smem_configured[2][2][2] = {};  // FP8 forward <causal><dynamic schedule><K/V segments>
 };

@@ -569,7 +569,7 @@ __global__ void attn_bwd_prep_kernel(const __nv_bfloat16* O, const __nv_bfloat16
 }
 
 // dQ = bf16(dQ accumulator)
-__global__ void attn_bwd_post_kernel(const float* dQacc, __nv_bfloat16* dQ, size_t n4) {
+static __global__ void attn_bwd_post_kernel(const float* dQacc, __nv_bfloat16* dQ, size_t n4) {
     const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i < n4) {
         const float4 v = reinterpret_cast<const float4*>(dQacc)[i];

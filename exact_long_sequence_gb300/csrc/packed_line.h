@@ -72,12 +72,44 @@ struct LineSeq {
     }
 };
 
+// The line of the gradient: a unit is a tile of 128 keys of a sequence at one key
+// head with the tokens that see one of them, which are the last ones; its query
+// blocks of `block_tokens` = 64 / G tokens begin at the first of those.  A unit is
+// kKeyUnitBlocks blocks and then its tokens, one position each.
+constexpr int kKeyUnitBlocks = 4;
+constexpr int kKeyLineLeast = 8;   // blocks of the shortest stretch
+struct LineKeys {
+    int nq, nk;          // tokens, keys
+    int block_tokens;
+    bool causal;
+    ELS_HD int tiles() const { return static_cast<int>((static_cast<int64_t>(nk) + kLineTile - 1) / kLineTile); }
+    ELS_HD int unit_cost() const { return kKeyUnitBlocks * block_tokens; }
+    // The first token that sees a key of tile j (of tokens that there are, since the last one sees all keys).
+    ELS_HD int first(int j) const {
+        if (!causal) return 0;
+        const int64_t t = static_cast<int64_t>(j) * kLineTile - (static_cast<int64_t>(nk) - nq);
+        return t < 0 || nq == 0 ? 0 : static_cast<int>(t);
+    }
+    ELS_HD int64_t cost(int j) const { return unit_cost() + nq - first(j); }
+    // Positions of the tiles before j.
+    ELS_HD int64_t before(int j) const {
+        const int64_t n = j, off = static_cast<int64_t>(nk) - nq;
+        if (!causal || nq == 0) return n * (unit_cost() + static_cast<int64_t>(nq));
+        // tile i has all tokens while 128 i <= nk - nq, then nk - 128 i of them
+        int64_t i0 = off < 0 ? 0 : off / kLineTile + 1;
+        if (i0 > n) i0 = n;
+        return n * unit_cost() + i0 * nq + (n - i0) * nk - kLineTile * (n * (n - 1) / 2 - i0 * (i0 - 1) / 2);
+    }
+    ELS_HD int64_t length() const { return before(tiles()); }
+};
+
 // What a stretch [x0, x1) has of a unit that starts at `start` (whose tiles start at start + kUnitCost).
 struct LinePart {
     int t0, t1;     // its tiles [t0, t1)
-    ELS_HD LinePart(int64_t start, int tiles, int weight, int64_t x0, int64_t x1) {
-        const int64_t first = start + kUnitCost;
-        const int step = kLineTile * weight;
+    ELS_HD LinePart(int64_t start, int tiles, int weight, int64_t x0, int64_t x1)
+        : LinePart(start + kUnitCost, tiles, kLineTile * weight, x0, x1, 0) {}
+    // tiles that begin at `first` and every `step` positions after it
+    ELS_HD LinePart(int64_t first, int tiles, int step, int64_t x0, int64_t x1, int) {
         const int64_t a = x0 > first ? (x0 - first + step - 1) / step : 0;
         const int64_t b = x1 > first ? (x1 - first + step - 1) / step : 0;
         t0 = a < tiles ? static_cast<int>(a) : tiles;
@@ -86,9 +118,9 @@ struct LinePart {
 };
 
 // Length of the stretches that a line of `total` is cut into, `most` of them at most.
-ELS_HD int64_t line_stretch(int64_t total, int most) {
+ELS_HD int64_t line_stretch(int64_t total, int most, int least = kLineLeast) {
     const int64_t even = (total + most - 1) / most;
-    return even < kLineLeast ? kLineLeast : even;
+    return even < least ? least : even;
 }
 
 }  // namespace elsattn

@@ -528,6 +528,34 @@ int attn_fwd_packed(const void* Q, const int64_t* q_strides, const void* K, cons
 size_t attn_fwd_packed_workspace_bytes(int R, int Nq, int Nk, int Hq, int Hk, int d);
 
 /*
+ * attn_bwd_packed - gradients of attn_fwd_packed for an upstream gradient dO of
+ * O (attn_bwd's, each query against the keys of its own sequence), with P recomputed from
+ * the forward's LSE.  dK and dV are those of the key heads: summed over the query heads of a group.
+ *   Q, K, V, O, dO, dQ, dK, dV : bf16 device views shaped as in attn_fwd_packed (dO and dQ like
+ *             Q, dK like K, dV like V), strides as there; O and LSE as attn_fwd_packed wrote them
+ *   LSE     : fp32 [Hq, Nq] device, contiguous
+ *   Rows of dQ, and of dK and dV, of tokens that are in no sequence stay as they were; keys that no query sees
+ *   get 0, and so does a query that sees no key.  Rows of other sequences are not used, whatever
+ *   they hold; a NaN or infinity reaches the gradients of its own sequence, also where a mask hides it.
+ *   workspace : device buffer of at least attn_bwd_packed_workspace_bytes(), 16-byte
+ *             aligned, owned by the caller, not used by other work while this call runs
+ * Other arguments and errors as attn_fwd_packed.  dQ is summed over the key tiles in fp32 in the order in
+ * which they are done, so its last bits may differ between equal calls; dK and dV do not.
+ * No gradient flows into LSE.  Three launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
+ */
+int attn_bwd_packed(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides, const void* V,
+                    const int64_t* v_strides, const void* O, const int64_t* o_strides, const float* LSE, const void* dO,
+                    const int64_t* do_strides, const int32_t* q_starts, const int32_t* k_starts, void* dQ,
+                    const int64_t* dq_strides, void* dK, const int64_t* dk_strides, void* dV, const int64_t* dv_strides,
+                    int R, int Nq, int Nk, int Hq, int Hk, int d, int causal, float scale, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream);
+
+/* Device bytes attn_bwd_packed needs as workspace on the current device (the
+ * sums of dQ, a number per row, pieces of dK and dV); 0 for an invalid shape or
+ * without a device. */
+size_t attn_bwd_packed_workspace_bytes(int R, int Nq, int Nk, int Hq, int Hk, int d);
+
+/*
  * attn_fwd_tree - attention of T new tokens of each of R requests over keys and
  * values in the pages of a cache: single tokens, a run of tokens, or a tree of
  * drafted tokens that are checked at once.  The request's new tokens are the

@@ -81,3 +81,46 @@ def starts(lens, first=0):
     for n in lens:
         out.append(out[-1] + n)
     return out
+
+
+def packed_bwd(q, k, v, o, lse, do, q_starts, k_starts, causal, scale):
+    """The gradients' formulas for the forward's o and lse, sequence by sequence, and a bound of the kernel's error:
+    (dq, dk, dv), (tq, tk, tv); rows in no sequence are NaN.
+
+    P is rounded to bf16 (2^-8 of it), dS again (2^-8), and each result once more (2^-8); P moves with the scores and the
+    LSE as in the forward (2^-12), the difference dP - D by the rounding of fp32 sums (at most 2^-16 of their terms' sum),
+    and the sums over rows and keys by at most 2^-10 of their terms' sum (up to 2^13 of them in fp32)."""
+    Hq, Nq, d = q.shape
+    Hk = k.shape[0]
+    G = Hq // Hk
+    nan = lambda t: torch.full(t.shape, math.nan, dtype=torch.float64, device=q.device)  # noqa: E731
+    dq, dk, dv, tq, tk, tv = nan(q), nan(k), nan(v), nan(q), nan(k), nan(v)
+    step = 2.0 ** -8
+    for (q0, q1), (k0, k1) in zip(zip(q_starts, q_starts[1:]), zip(k_starts, k_starts[1:])):
+        n, m = max(0, q1 - q0), max(0, k1 - k0)
+        qs, ks = slice(q0, q0 + n), slice(k0, k0 + m)
+        i = torch.arange(n, device=q.device)[:, None]
+        seen = torch.arange(m, device=q.device) <= (i + m - n if causal else m + 0 * i)
+        for x in (dk, dv, tk, tv):
+            x[:, ks] = 0
+        for h in range(Hq):
+            Q, K, V, O, g = (x.double() for x in (q[h, qs], k[h // G, ks], v[h // G, ks], o[h, qs], do[h, qs]))
+            p = torch.where(seen, torch.exp(Q @ K.T * scale - lse[h, qs].double()[:, None]), 0.0)
+            D = (g * O).sum(-1, keepdim=True)
+            ds = p * (g @ V.T - D) * scale
+            e = ds.abs() * (2 * step + 2.0 ** -9) + p * abs(scale) * 2.0 ** -16 * (g.abs() @ V.abs().T + (g * O).abs().sum(-1, keepdim=True))
+            dq[h, qs] = ds @ K
+            tq[h, qs] = e @ K.abs() + step * dq[h, qs].abs()
+            dk[h // G, ks] += ds.T @ Q
+            tk[h // G, ks] += e.T @ Q.abs()
+            dv[h // G, ks] += p.T @ g
+            tv[h // G, ks] += (p * (step + 2.0 ** -9)).T @ g.abs()
+    return (dq, dk, dv), (tq, tk + step * dk.abs(), tv + step * dv.abs())
+
+
+def check_bwd(got, ref, tol):
+    for name, x, r, t in zip(("dq", "dk", "dv"), got, ref, tol):
+        live = ~torch.isnan(r)
+        err = (x.double() - r).abs()
+        # (a gradient that is the difference of equal sums may be far below them: 2^-133 is bf16's smallest number)
+        assert bool((err <= t + 2.0 ** -133)[live].all()), f"{name} off by {(err / (t + 2.0 ** -133))[live].max().item():.3f} of its bound"
