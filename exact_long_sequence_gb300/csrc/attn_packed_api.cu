@@ -16,7 +16,7 @@ namespace elsattn {
 namespace {
 
 // K and V that the CTAs read at a time: the line has a stretch a CTA for each so many bytes, up to kMostTurns.
-constexpr double kTurnBytes = 64e6;
+constexpr double kTurnBytes = 128e6;
 constexpr int kMostTurns = 8;
 
 // Sizes that follow from the shape.  rows: most rows of a block; kv_bytes: of K and V together.
@@ -93,19 +93,25 @@ int launch(DeviceState& dev, const CUtensorMap (&maps)[5], const PackedParams& p
             return cuda_fail(e);
         configured = true;
     }
-    kernel<<<dev.num_sms, kThreads, smem, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
-    // few rows a piece: eight warps share a row's pieces, of which there may be many
-    const bool few = p.orows <= 32;
+    // Both are programmatic dependents of what is before them on the stream: each sets up beside its end.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
-    cfg.gridDim = dim3(static_cast<unsigned>(few ? (p.orows + 1) / 2 : (p.orows + 31) / 32), static_cast<unsigned>(p.stretches));
-    cfg.blockDim = dim3(256);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms));
+    cfg.blockDim = dim3(kPkThreads);
+    cfg.dynamicSmemBytes = smem;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], p)) != cudaSuccess) return cuda_fail(e);
+    cfg.dynamicSmemBytes = 0;
+    // few rows a piece: eight warps share a row's pieces, of which there may be many
+    const bool few = p.orows <= 32;
+    // (of few stretches each row has a warp; of many, which only long calls have, CTAs take rows in turns)
+    cfg.gridDim = dim3(static_cast<unsigned>(few ? p.orows : p.stretches <= dev.num_sms ? (p.orows + 7) / 8 : (p.orows + 31) / 32),
+                       static_cast<unsigned>(p.stretches));
+    cfg.blockDim = dim3(256);
     auto combine = few ? attn_packed_combine_kernel<D, 8> : attn_packed_combine_kernel<D, 1>;
     if ((e = cudaLaunchKernelEx(&cfg, combine, p)) != cudaSuccess) return cuda_fail(e);
     return ATTN_OK;

@@ -237,6 +237,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         bool ok = true;
         uint32_t cnt = 0, items = 0;   // blocks and items so far
         PackedBwdItem it{};
+#pragma unroll 1
         for (uint32_t n = 0; ok && take_item(n, it); ++n) {
             if (it.nblocks == 0) continue;
             // K_j and V_j, once the products of the item before have read theirs
@@ -252,6 +253,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
             }
             __syncwarp();
             ++items;
+#pragma unroll 1
             for (int i = 0; i < it.nblocks; ++i, ++cnt) {
                 const uint32_t s = cnt % kStages;
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kQEmpty + s), ((cnt / kStages) & 1u) ^ 1u, ctx));
@@ -271,6 +273,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         }
         // Every issued copy lands before the CTA ends (bounded waits; also on abort).
         if (items > 0) mbar_wait_drain(bar(L::kKvFull), (items - 1) & 1u, 50000000ull);
+#pragma unroll 1
         for (uint32_t c = cnt > kStages ? cnt - kStages : 0; c < cnt; ++c)
             mbar_wait_drain(bar(L::kQFull + c % kStages), (c / kStages) & 1u, 50000000ull);
     } else if (warp == 1) {
@@ -323,6 +326,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
             __syncwarp();
             return true;
         };
+#pragma unroll 1
         for (uint32_t n = 0; ok && take_item(n, it); ++n) {
             const int nb = it.nblocks;
             if (nb == 0) continue;
@@ -331,6 +335,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
             if (!(ok = __all_sync(0xffffffffu, w))) break;
             ok = issue_sdp(0);
             if (ok && nb > 1) ok = issue_sdp(1);
+#pragma unroll 1
             for (int i = 0; i < nb && ok; ++i) {
                 const uint32_t c = cnt + i, s = c % kStages, b = c & 1u, ph = (c >> 1) & 1u;
                 const uint32_t q = s_base + L::kRingOff + s * L::kStageBytes;
@@ -383,11 +388,13 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         const int c0 = lane, c1 = lane + 32;
         const int t0 = c0 / p.G, g0 = c0 - t0 * p.G, t1 = c1 / p.G, g1 = c1 - t1 * p.G;
         auto zero_rows = [&](uint32_t off, int blocks, int block_bytes, int from, int to) {
+#pragma unroll 1
             for (int i = lane; i < blocks * (to - from) * 8; i += 32) {
                 const int ch = i & 7, row = i / 8 % (to - from) + from, blk = i / 8 / (to - from);
                 *reinterpret_cast<uint4*>(smem + off + blk * block_bytes + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
             }
         };
+#pragma unroll 1
         for (uint32_t n = 0; ok && take_item(n, it); ++n) {
             if (it.nblocks == 0) continue;
             if (it.nkeys < kBc) {  // the tile's other rows are another sequence's keys
@@ -411,6 +418,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                 dd[1] = on1 ? __ldg(p.dvec + a1) : 0.f;
             };
             fetch(0);
+#pragma unroll 1
             for (int i = 0; i < it.nblocks; ++i, ++cnt) {
                 const uint32_t s = cnt % kStages;
                 float nl[2], nd[2];
@@ -456,30 +464,42 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         PackedBwdItem it{};
         const int run = (p.R + 31) / 32;
         int64_t mine = 0;
+        PackedBwdSeq own{};
+        int64_t own_len = 0;
+#pragma unroll 1
         for (int i = 0; i < run; ++i) {
             const int r = lane * run + i;
-            if (r < p.R) mine += packed_bwd_seq(p, r).line.length();
+            if (r < p.R) {
+                own = packed_bwd_seq(p, r);
+                own_len = own.line.length();
+                mine += own_len;
+            }
         }
         mine *= p.Hk;
         const int64_t upto = warp_scan64(mine, lane);
         const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
         const int64_t len = line_stretch(total, p.stretches, kKeyLineLeast * p.block_tokens);
+#pragma unroll 1
         for (int i = blockIdx.x; i < p.stretches && ok; i += gridDim.x) {
             const int64_t x0 = i * len;
             const int64_t x1 = min(x0 + len, total);
             PackedBwdCut cut{};
             if (x0 < x1) {
-                const int at = __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
+                const int at = run == 1 ? 0 : __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
                 int64_t start = __shfl_sync(0xffffffffu, upto - mine, at);
+#pragma unroll 1
                 for (int r0 = at * run; r0 < p.R && start < x1 && ok; r0 += 32) {
-                    PackedBwdSeq own{};
-                    int64_t cost = 0;
-                    if (r0 + lane < p.R) {
-                        own = packed_bwd_seq(p, r0 + lane);
-                        cost = own.line.length() * p.Hk;
+                    if (run > 1) {
+                        own_len = 0;
+                        if (r0 + lane < p.R) {
+                            own = packed_bwd_seq(p, r0 + lane);
+                            own_len = own.line.length();
+                        }
                     }
+                    const int64_t cost = own_len * p.Hk;
                     const int64_t end_l = start + warp_scan64(cost, lane);
                     uint32_t in = __ballot_sync(0xffffffffu, cost > 0 && end_l > x0 && end_l - cost < x1);
+#pragma unroll 1
                     for (; in != 0 && ok; in &= in - 1) {
                         const int src = __ffs(in) - 1;
                         PackedBwdSeq s;
@@ -490,9 +510,10 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                         s.q0 = __shfl_sync(0xffffffffu, own.q0, src);
                         s.k0 = __shfl_sync(0xffffffffu, own.k0, src);
                         const int64_t first = __shfl_sync(0xffffffffu, end_l - cost, src);
-                        const int64_t per = __shfl_sync(0xffffffffu, cost, src) / p.Hk;
+                        const int64_t per = __shfl_sync(0xffffffffu, own_len, src);
                         const int tiles = s.line.tiles();
-                        int h = x0 > first ? static_cast<int>((x0 - first) / per) : 0;
+                        int h = x0 > first ? static_cast<int>(line_div(x0 - first, per)) : 0;
+#pragma unroll 1
                         for (int64_t hs = first + h * per; h < p.Hk && hs < x1 && ok; ++h, hs += per) {
                             // the key tile that x0 is in: the last one that begins at or before it
                             int j = 0;
@@ -509,11 +530,12 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                                 j = lo;
                             }
                             int64_t us = hs + s.line.before(j);
+#pragma unroll 1
                             for (; j < tiles && us < x1 && ok; ++j) {
                                 const int tok = s.line.first(j), ntok = s.line.nq - tok;
                                 const int nb = (ntok + p.block_tokens - 1) / p.block_tokens;
                                 const int64_t begin = us + s.line.unit_cost();
-                                const LinePart part(begin, nb, p.block_tokens, x0, x1, 0);
+                                const LinePart part(begin, nb, p.block_tokens, x0, x1);
                                 if (part.t0 < part.t1 || (nb == 0 && us >= x0)) {
                                     const int skip = nb == 0 ? 0 : part.t0 * p.block_tokens;
                                     it.nblocks = nb == 0 ? 0 : part.t1 - part.t0;
@@ -528,7 +550,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                                         it.slot = part.t0 == 0 ? 2 * i + 1 : 2 * i;
                                         if (part.t0 == 0) {
                                             const int64_t last = begin + static_cast<int64_t>(nb - 1) * p.block_tokens;
-                                            cut.pieces = static_cast<int>(last / len) - i + 1;
+                                            cut.pieces = static_cast<int>(line_div(last, len)) - i + 1;
                                             cut.head = h;
                                             cut.key0 = it.key0;
                                             cut.nkeys = it.nkeys;
@@ -562,6 +584,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
             uint4* row = reinterpret_cast<uint4*>(dst + it.head * st[0] + static_cast<int64_t>(it.key0 + (key_ok ? r : 0)) * st[1]);
             if (it.nblocks == 0) {
                 if (key_ok)
+#pragma unroll 1
                     for (int c = from; c < to; c += 8) row[c / 8] = make_uint4(0, 0, 0, 0);
                 return;
             }
@@ -612,12 +635,16 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
             // Thread r = key row r of the tile (TMEM lane r).  Warps 4-7 take the block's rows 0-31,
             // warps 12-15 rows 32-63.
             const float sl2 = p.scale_log2;
+#pragma unroll 1
             for (uint32_t n = 0; ok && take_item(n, it); ++n) {
+#pragma unroll 1
                 for (int i = 0; i < it.nblocks && ok; ++i, ++cnt) {
                     const uint32_t b = cnt & 1u, ph = (cnt >> 1) & 1u, s = cnt % kStages;
                     const uint32_t t_s = tmem + lane_addr + 2 * D + 128 * b, t_dp = t_s + 64;
                     const float* lse2 = reinterpret_cast<const float*>(smem + L::kStatOff + s * L::kStatBytes);
                     const float* dvec = lse2 + kBq;
+                    // P in fp32: dS is rounded once (from P rounded to bf16, dQ and dK were off by 1.3 times as much)
+                    float pr[32];
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kSpFull + b), ph, ctx) &&
                                                      mbar_wait(bar(L::kStat + s), (cnt / kStages) & 1u, ctx));
                     if (!ok) break;
@@ -644,6 +671,8 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                                 bb = ex2_approx(bb);
                                 if (c0 + c < from) a = 0.f;
                                 if (c0 + c + 1 < from) bb = 0.f;
+                                pr[c] = a;
+                                pr[c + 1] = bb;
                                 pk[c / 2] = pack_bf16x2(a, bb);
                             }
                         } else {
@@ -651,7 +680,9 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                             for (int c = 0; c < 32; c += 2) {
                                 float a, bb;
                                 ffma2c(a, bb, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), sl2, l[c], l[c + 1]);
-                                pk[c / 2] = pack_bf16x2(ex2_approx(a), ex2_approx(bb));
+                                pr[c] = ex2_approx(a);
+                                pr[c + 1] = ex2_approx(bb);
+                                pk[c / 2] = pack_bf16x2(pr[c], pr[c + 1]);
                             }
                         }
                         tmem_st16(t_s + c0, pk);  // over this warpgroup's own S^T columns
@@ -668,25 +699,20 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                     tc_fence_after_sync();
                     uint8_t* ds_row = smem + L::kDsOff + b * L::kDsBuf + r * 128;
                     {
-                        uint32_t dv[32], pv[16];
+                        uint32_t dv[32];
                         tmem_ld32(t_dp + c0, dv);
-                        tmem_ld16(t_s + c0, pv);
-                        float dd[32];
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const float4 t = *reinterpret_cast<const float4*>(dvec + c0 + c);
-                            dd[c] = t.x, dd[c + 1] = t.y, dd[c + 2] = t.z, dd[c + 3] = t.w;
-                        }
                         tmem_wait_ld(dv);
-                        tmem_wait_ld16(pv);
                         uint32_t pk[16];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float pa = __uint_as_float(pv[c / 2] << 16), pb = __uint_as_float(pv[c / 2] & 0xffff0000u);
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 dd = *reinterpret_cast<const float4*>(dvec + c0 + c);
                             float a, bb;  // scale * dP - scale * D, then times P
-                            ffma2c(a, bb, __uint_as_float(dv[c]), __uint_as_float(dv[c + 1]), p.scale, dd[c], dd[c + 1]);
-                            fmul2(a, bb, pa, pb);
+                            ffma2c(a, bb, __uint_as_float(dv[c]), __uint_as_float(dv[c + 1]), p.scale, dd.x, dd.y);
+                            fmul2(a, bb, pr[c], pr[c + 1]);
                             pk[c / 2] = pack_bf16x2(a, bb);
+                            ffma2c(a, bb, __uint_as_float(dv[c + 2]), __uint_as_float(dv[c + 3]), p.scale, dd.z, dd.w);
+                            fmul2(a, bb, pr[c + 2], pr[c + 3]);
+                            pk[c / 2 + 1] = pack_bf16x2(a, bb);
                         }
                         tmem_st16(t_dp + c0, pk);
 #pragma unroll
@@ -722,7 +748,9 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
             const bool col_ok = r < D;  // warp-uniform: d is a multiple of 32
             const bool issuer = warp == 8 && lane == 0;
             constexpr int kHalf = kBq / 2;
+#pragma unroll 1
             for (uint32_t n = 0; ok && take_item(n, it); ++n) {
+#pragma unroll 1
                 for (int i = 0; i < it.nblocks && ok; ++i, ++cnt) {
                     const uint32_t b = cnt & 1u, ph = (cnt >> 1) & 1u;
                     const uint32_t t_dq = tmem + lane_addr + 2 * D + 128 * b + 64;

@@ -31,6 +31,8 @@
 //   warp 2  scheduler: the CTA's items, through a ring of descriptions
 //   warp 3  Q loader
 //   warps 4-7, 8-11  softmax warpgroups
+//   warps 12-15      epilogue: O from TMEM to memory.  While they write an item's O the softmax warps are at
+//     the next item's first tiles, which is what short sequences are made of.
 #pragma once
 
 #include <cuda.h>
@@ -44,6 +46,8 @@ namespace elsattn {
 
 constexpr int kPkTailBox = 32;     // keys per TMA box of a tile that is not full
 constexpr int kPkMostGroup = 64;   // most query heads of a key head
+constexpr int kPkThreads = 512;
+constexpr int kPkReaders = 15;     // of an item: producer, MMA, Q loader, eight softmax and four epilogue warps
 
 struct PackedParams {
     // packed: [R + 1] first tokens of the sequences in Q, and in K and V (each clipped to the tensors)
@@ -106,8 +110,10 @@ struct PackedSmem {
     static constexpr int kStages = kv_stages_for(D);
     static constexpr int kQOff = 0;
     static constexpr int kRingOff = kQTiles * kTile;
-    static constexpr int kXchgOff = kRingOff + kStages * kTile;   // [128] (m, l) of one chain, then of the other
-    static constexpr int kItemOff = kXchgOff + 128 * 8;
+    // weights of the rows' O for the epilogue: [2][128] by tile; of an item on both chains [128] pairs, where
+    // chain 1 leaves its (m, l) first
+    static constexpr int kWeightOff = kRingOff + kStages * kTile;
+    static constexpr int kItemOff = kWeightOff + 128 * 8;
     static constexpr int kBarOff = kItemOff + kPfxItemRing * static_cast<int>(sizeof(PackedItem));
     static constexpr int kKvFull = 0;
     static constexpr int kKvEmpty = kKvFull + kStages;
@@ -118,8 +124,10 @@ struct PackedSmem {
     static constexpr int kPFull = kPHalf + 2;             // [2]
     static constexpr int kOFull = kPFull + 2;             // [2]
     static constexpr int kOEmpty = kOFull + 2;            // [2]
-    static constexpr int kX = kOEmpty + 2;                // [2] the chain's (m, l) are in shared memory
-    static constexpr int kDrain = kX + 2;
+    static constexpr int kWFull = kOEmpty + 2;            // [2] the chain's weights are there (of an item on both: chain 0's)
+    static constexpr int kWEmpty = kWFull + 2;            // [2] the epilogue has read them
+    static constexpr int kX = kWEmpty + 2;                // chain 1's (m, l) are there, of an item on both chains
+    static constexpr int kDrain = kX + 1;
     static constexpr int kItemFull = kDrain + 1;          // [kPfxItemRing]
     static constexpr int kItemEmpty = kItemFull + kPfxItemRing;
     static constexpr int kNumBars = kItemEmpty + kPfxItemRing;
@@ -138,6 +146,7 @@ template <bool PAGED>
 __device__ __forceinline__ PackedSeq packed_seq(const PackedParams& p, int r) {
     PackedSeq s;
     s.line.tile_tokens = p.tile_tokens;
+    s.line.group = p.G;
     if (PAGED) {
         const int len = __ldg(p.lens + r);
         s.line.nq = len < 0 ? 0 : p.T;
@@ -165,8 +174,75 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {
     return v;
 }
 
+// D (+)= A B with the operands' descriptors given by their low words (start address and leading stride); the
+// high word (stride between 8-row groups of 1024 bytes, swizzle) is the same for all of them here.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <bool ACC>
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
+        : "memory");
+}
+
+// O_c (+)= P_c V over keys [64 half, 64 half + 64), in steps of 16 of the tile's `steps`; b: V's descriptor.
+template <int D>
+__device__ __forceinline__ void packed_gemm_o(uint32_t tmem, uint32_t c, uint32_t b, int half, int steps, bool first) {
+    constexpr uint32_t idesc = make_idesc_bf16_f32(kBr, D, false, true);
+    const uint32_t o = tmem + 2 * kBc + c * D, pt = tmem + c * kBc;
+    if (steps == kBc / 16) {
+#pragma unroll
+        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+            mma_ts_lo(o, pt + kk * 8, b + ((kk * 16 * 128) >> 4), idesc, kk > 0 || !first ? 1u : 0u);
+    } else {
+#pragma unroll 1
+        for (int kk = half * 4; kk < min(half * 4 + 4, steps); ++kk)
+            mma_ts_lo(o, pt + kk * 8, b + ((kk * 16 * 128) >> 4), idesc, kk > 0 || !first ? 1u : 0u);
+    }
+}
+
+// One output product with its waits, by the MMA warp.  Not inlined: it has six callers, and the kernel's code is to
+// stay within the instruction cache (125 KB of it: every part outside the two loops ran at the
+// pace of instruction fetches).  flags: chain, first and last of its item, first and last reader of V, the
+// parities of P, O and V.
+template <int D>
+__device__ __noinline__ bool packed_pv(const WaitCtx& ctx, uint32_t bar0, uint32_t tmem, uint32_t b, uint32_t stage, int steps,
+                                       uint32_t flags) {
+    using L = PackedSmem<D>;
+    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+    const uint32_t c = flags & 1u;
+    bool w = true;
+    if (flags & 8u) w = mbar_wait(bar(L::kKvFull + stage), (flags >> 7) & 1u, ctx);
+    w = w && mbar_wait(bar(L::kPHalf + c), (flags >> 5) & 1u, ctx);
+    if (flags & 2u) w = w && mbar_wait(bar(L::kOEmpty + c), (flags >> 6) & 1u, ctx);
+    if (!__all_sync(0xffffffffu, w)) return false;
+    tc_fence_after_sync();
+    if (elect_one()) packed_gemm_o<D>(tmem, c, b, 0, steps, flags & 2u);
+    __syncwarp();
+    w = mbar_wait(bar(L::kPFull + c), (flags >> 5) & 1u, ctx);
+    if (!__all_sync(0xffffffffu, w)) return false;
+    tc_fence_after_sync();
+    if (elect_one()) {
+        packed_gemm_o<D>(tmem, c, b, 1, steps, flags & 2u);
+        if (flags & 16u) mma_commit(bar(L::kKvEmpty + stage));
+        if (flags & 4u) mma_commit(bar(L::kOFull + c));
+    }
+    __syncwarp();
+    return true;
+}
+
 template <int D, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPkThreads, 1)
 attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_kt,
                    const __grid_constant__ CUtensorMap tmap_vt, const __grid_constant__ PackedParams p) {
@@ -195,13 +271,15 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             mbar_init(bar(L::kPHalf + t), 128);
             mbar_init(bar(L::kPFull + t), 128);
             mbar_init(bar(L::kOFull + t), 1);
-            mbar_init(bar(L::kOEmpty + t), 256);  // both warpgroups, or one that counts twice
-            mbar_init(bar(L::kX + t), 128);
+            mbar_init(bar(L::kOEmpty + t), 128);
+            mbar_init(bar(L::kWFull + t), 128);
+            mbar_init(bar(L::kWEmpty + t), 128);
         }
+        mbar_init(bar(L::kX), 128);
         mbar_init(bar(L::kDrain), 1);
         for (int s = 0; s < kPfxItemRing; ++s) {
             mbar_init(bar(L::kItemFull + s), 1);
-            mbar_init(bar(L::kItemEmpty + s), kPfxItemReaders);
+            mbar_init(bar(L::kItemEmpty + s), kPkReaders);
         }
         fence_barrier_init();
         tma_prefetch_desc(&tmap_q);
@@ -220,6 +298,8 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    // Up to here nothing is read or written that an earlier grid may write or read; the setup overlaps its end.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // The combine kernel may be scheduled onto SMs as this grid's CTAs retire;
     // it waits for the whole grid before it reads the partial results.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -256,6 +336,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         uint32_t issued = 0;
         bool ok = true;
         PackedItem it;
+#pragma unroll 1
         for (uint32_t n = 0; ok && take_item(n, it); ++n) {
             const int* pages = PAGED ? p.table + it.req * p.table_stride : nullptr;
             // paged: lane l holds the page of box `base + l` of the item's keys, and has asked for the next 32
@@ -271,6 +352,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 page_now = page_of(base + lane);
                 page_next = page_of(base + 32 + lane);
             }
+#pragma unroll 1
             for (int j = 0; j < it.ntiles && ok; ++j) {
                 const int keys = tile_keys(it, j);
                 const int key = (it.tile0 + j) * kBc;
@@ -313,6 +395,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         } else {
                             const int boxes = (keys + kPkTailBox - 1) / kPkTailBox;
                             mbar_arrive_expect_tx(full, boxes * kPkTailBox * D * 2);
+#pragma unroll 1
                             for (int i = 0; i < boxes; ++i)
 #pragma unroll
                                 for (int b = 0; b < D / 64; ++b)
@@ -329,6 +412,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // every issued copy lands before the CTA's shared memory is released (bounded waits)
         const uint32_t pending = issued < static_cast<uint32_t>(L::kStages) ? issued : L::kStages;
         RingPos back = pos;
+#pragma unroll 1
         for (uint32_t i = 0; i < pending; ++i) {
             back = back.stage == 0 ? RingPos{L::kStages - 1u, back.phase ^ 1u} : RingPos{back.stage - 1, back.phase};
             mbar_wait_drain(bar(L::kKvFull + back.stage), back.phase, 50000000ull);
@@ -336,65 +420,43 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         const uint32_t idesc_s = make_idesc_bf16_f32(kBr, kBc, false, false) | (p.negate_scores ? kIdescNegateB : 0u);
-        constexpr uint32_t idesc_o = make_idesc_bf16_f32(kBr, D, false, true);
-        const uint64_t dq0 = make_smem_desc_sw128(s_base + L::kQOff, 16, 1024);
-        const uint64_t dk0 = make_smem_desc_sw128(s_base + L::kRingOff, 16, 1024);
-        const uint64_t dv0 = make_smem_desc_sw128(s_base + L::kRingOff, kBc * 128, 1024);
+        constexpr uint32_t kTile16 = L::kTile >> 4;
+        const uint32_t dq0 = desc_lo(s_base + L::kQOff, 16);
+        const uint32_t dk0 = desc_lo(s_base + L::kRingOff, 16);
+        const uint32_t dv0 = desc_lo(s_base + L::kRingOff, kBc * 128);
         uint32_t p_phase = 0u, o_phase = 3u;  // parities to wait for, bit c of chain c
         RingPos kpos{0u, 0u};   // K of the current tile
         uint32_t qpos = 0;      // query tiles taken so far: slot qpos & 1
         uint32_t par = 0;       // chain of the item's first step
         bool ok = true;
-        auto gemm_s = [&](int c, uint64_t a, uint64_t b) {
+        // S_c = Q K^T
+        auto gemm_s = [&](int c, uint32_t a, uint32_t b) {
+            mma_ss_lo<false>(tmem + c * kBc, a, b, idesc_s);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t off = static_cast<uint64_t>(((kk >> 2) * (kBr * 128) + (kk & 3) * 32) >> 4);
-                mma_ss(tmem + c * kBc, a + off, b + off, idesc_s, kk > 0 ? 1u : 0u);
+            for (int kk = 1; kk < D / 16; ++kk) {
+                const uint32_t off = static_cast<uint32_t>(((kk >> 2) * (kBr * 128) + (kk & 3) * 32) >> 4);
+                mma_ss_lo<true>(tmem + c * kBc, a + off, b + off, idesc_s);
             }
         };
+        auto gemm_o = [&](int c, uint32_t b, int half, int steps, bool first) { packed_gemm_o<D>(tmem, c, b, half, steps, first); };
         // the output product that is due: of the step before
         struct { bool due, first, last, first_v, last_v; int chain, ksteps; RingPos v; } pv{};
         auto run_pv = [&]() -> bool {
             if (!pv.due) return true;
             pv.due = false;
-            const int c = pv.chain;
-            bool w = true;
-            if (pv.first_v) w = mbar_wait(bar(L::kKvFull + pv.v.stage), pv.v.phase, ctx);
-            w = w && mbar_wait(bar(L::kPHalf + c), (p_phase >> c) & 1u, ctx);
-            if (pv.first) {
-                w = w && mbar_wait(bar(L::kOEmpty + c), (o_phase >> c) & 1u, ctx);
-                o_phase ^= 1u << c;
-            }
-            if (!__all_sync(0xffffffffu, w)) return false;
-            tc_fence_after_sync();
-            const uint64_t b = dv0 + static_cast<uint64_t>((pv.v.stage * L::kTile) >> 4);
-            // products over keys [64 half, 64 half + 64), in steps of 16 up to the tile's last key
-            auto gemm_o = [&](int half) {
-#pragma unroll
-                for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                    if (kk < pv.ksteps)
-                        mma_ts(tmem + 2 * kBc + c * D, tmem + c * kBc + kk * 8,
-                               b + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_o, (!pv.first || kk > 0) ? 1u : 0u);
-            };
-            if (elect_one()) gemm_o(0);
-            __syncwarp();
-            w = mbar_wait(bar(L::kPFull + c), (p_phase >> c) & 1u, ctx);
+            const uint32_t c = pv.chain;
+            const uint32_t flags = c | (pv.first ? 2u : 0u) | (pv.last ? 4u : 0u) | (pv.first_v ? 8u : 0u) | (pv.last_v ? 16u : 0u) |
+                                   (((p_phase >> c) & 1u) << 5) | (((o_phase >> c) & 1u) << 6) | (pv.v.phase << 7);
             p_phase ^= 1u << c;
-            if (!__all_sync(0xffffffffu, w)) return false;
-            tc_fence_after_sync();
-            if (elect_one()) {
-                gemm_o(1);
-                if (pv.last_v) mma_commit(bar(L::kKvEmpty + pv.v.stage));
-                if (pv.last) mma_commit(bar(L::kOFull + c));
-            }
-            __syncwarp();
-            return true;
+            if (pv.first) o_phase ^= 1u << c;
+            return packed_pv<D>(ctx, bar0, tmem, dv0 + pv.v.stage * kTile16, pv.v.stage, pv.ksteps, flags);
         };
         // The next score product goes first where its operands are there already: the tensor core
         // works on it while the softmax of the step before runs.  Where they are not (short items,
         // the ends of a CTA's share), the product that is due does not wait for them.
         auto there = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_test(b, parity)); };
         PackedItem it;
+#pragma unroll 1
         for (uint32_t n = 0; ok; ++n) {
             if (pv.due && !there(bar(L::kItemFull + n % kPfxItemRing), (n / kPfxItemRing) & 1u) && !(ok = run_pv())) break;
             if (!take_item(n, it)) break;
@@ -408,8 +470,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 if (pv.due && (pv.chain == 0 || !there(bar(L::kKvFull + kpos.stage), kpos.phase) ||
                                !there(bar(L::kQFull + q0), (qpos >> 1) & 1u)) && !(ok = run_pv()))
                     break;
-                const uint64_t a0 = dq0 + static_cast<uint64_t>((q0 * L::kTile) >> 4);
-                const uint64_t a1 = dq0 + static_cast<uint64_t>((q1 * L::kTile) >> 4);
+                const uint32_t a0 = dq0 + q0 * kTile16, a1 = dq0 + q1 * kTile16;
                 const int last_steps = (tile_keys(it, nt - 1) + 15) / 16;
                 // O_c (+)= P_c V_j, V_j at ring position v
                 auto pv_two = [&](auto chain, int j, RingPos v) -> bool {
@@ -423,23 +484,16 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     }
                     if (!__all_sync(0xffffffffu, w)) return false;
                     tc_fence_after_sync();
-                    const uint64_t b = dv0 + static_cast<uint64_t>((v.stage * L::kTile) >> 4);
+                    const uint32_t b = dv0 + v.stage * kTile16;
                     const int ks = j == nt - 1 ? last_steps : kBc / 16;
-                    auto gemm = [&](int half) {
-#pragma unroll
-                        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                            if (kk < ks)
-                                mma_ts(tmem + 2 * kBc + c * D, tmem + c * kBc + kk * 8,
-                                       b + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-                    };
-                    if (elect_one()) gemm(0);
+                    if (elect_one()) gemm_o(c, b, 0, ks, j == 0);
                     __syncwarp();
                     w = mbar_wait(bar(L::kPFull + c), (p_phase >> c) & 1u, ctx);
                     p_phase ^= 1u << c;
                     if (!__all_sync(0xffffffffu, w)) return false;
                     tc_fence_after_sync();
                     if (elect_one()) {
-                        gemm(1);
+                        gemm_o(c, b, 1, ks, j == 0);
                         if (c == 1) mma_commit(bar(L::kKvEmpty + v.stage));
                         if (j == (c == 0 ? n0 : nt) - 1) mma_commit(bar(L::kOFull + c));
                     }
@@ -447,13 +501,14 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     return true;
                 };
                 RingPos vprev{0u, 0u};
+#pragma unroll 1
                 for (int j = 0; j < nt && ok; ++j) {
                     bool w = mbar_wait(bar(L::kKvFull + kpos.stage), kpos.phase, ctx);
                     if (j == 0)
                         w = w && mbar_wait(bar(L::kQFull + q0), (qpos >> 1) & 1u, ctx) &&
                             mbar_wait(bar(L::kQFull + q1), ((qpos + 1) >> 1) & 1u, ctx);
                     if (!(ok = __all_sync(0xffffffffu, w))) break;
-                    const uint64_t b = dk0 + static_cast<uint64_t>((kpos.stage * L::kTile) >> 4);
+                    const uint32_t b = dk0 + kpos.stage * kTile16;
                     if (j < n0) {
                         if (elect_one()) {
                             gemm_s(0, a0, b);
@@ -490,6 +545,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             }
             // One query tile; the chains take turns with the K/V tiles.
             const uint32_t qslot = qpos & 1u;
+#pragma unroll 1
             for (int j = 0; j < nt && ok; ++j) {
                 const int c = (par + j) & 1;
                 if (pv.due && (!there(bar(L::kKvFull + kpos.stage), kpos.phase) ||
@@ -499,8 +555,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 if (j == 0) w = w && mbar_wait(bar(L::kQFull + qslot), (qpos >> 1) & 1u, ctx);
                 if (!(ok = __all_sync(0xffffffffu, w))) break;
                 if (elect_one()) {
-                    gemm_s(c, dq0 + static_cast<uint64_t>((qslot * L::kTile) >> 4),
-                           dk0 + static_cast<uint64_t>((kpos.stage * L::kTile) >> 4));
+                    gemm_s(c, dq0 + qslot * kTile16, dk0 + kpos.stage * kTile16);
                     mma_commit(bar(L::kSFull + c));
                     mma_commit(bar(L::kKvEmpty + kpos.stage));
                     if (j == nt - 1) mma_commit(bar(L::kQEmpty + qslot));
@@ -541,47 +596,64 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             ++n;
         };
         PackedItem it{};
-        // The line's length: each lane sums a run of sequences.
+        // The line's length: each lane sums a run of sequences (up to 32 of them: has one, and keeps it).
         const int run = (p.R + 31) / 32;
         int64_t mine = 0;
+        PackedSeq own{};
+        int64_t own_len = 0;
+#pragma unroll 1
         for (int i = 0; i < run; ++i) {
             const int r = lane * run + i;
-            if (r < p.R) mine += packed_seq<PAGED>(p, r).line.length();
+            if (r < p.R) {
+                own = packed_seq<PAGED>(p, r);
+                own_len = own.line.length();
+                mine += own_len;
+            }
         }
         mine *= p.Hk;
         const int64_t upto = warp_scan64(mine, lane);
         const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
         const int64_t len = line_stretch(total, p.stretches);
+#pragma unroll 1
         for (int i = blockIdx.x; i < p.stretches && ok; i += gridDim.x) {
             const int64_t x0 = i * len;
             const int64_t x1 = min(x0 + len, total);
             PackedCut cut{};
             if (x0 < x1) {
                 // the run of sequences that x0 is in, then the sequences in groups of 32
-                const int at = __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
+                const int at = run == 1 ? 0 : __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
                 int64_t start = __shfl_sync(0xffffffffu, upto - mine, at);
+#pragma unroll 1
                 for (int r0 = at * run; r0 < p.R && start < x1 && ok; r0 += 32) {
-                    PackedSeq own{};
-                    if (r0 + lane < p.R) own = packed_seq<PAGED>(p, r0 + lane);
-                    const int64_t cost = own.line.nq > 0 ? own.line.length() * p.Hk : 0;
+                    if (run > 1) {
+                        own_len = 0;
+                        if (r0 + lane < p.R) {
+                            own = packed_seq<PAGED>(p, r0 + lane);
+                            own_len = own.line.length();
+                        }
+                    }
+                    const int64_t cost = own_len * p.Hk;
                     const int64_t end_l = start + warp_scan64(cost, lane);
                     uint32_t in = __ballot_sync(0xffffffffu, cost > 0 && end_l > x0 && end_l - cost < x1);
+#pragma unroll 1
                     for (; in != 0 && ok; in &= in - 1) {
                         const int src = __ffs(in) - 1;
                         PackedSeq s;
                         s.line.nq = __shfl_sync(0xffffffffu, own.line.nq, src);
                         s.line.nk = __shfl_sync(0xffffffffu, own.line.nk, src);
                         s.line.tile_tokens = p.tile_tokens;
+                        s.line.group = p.G;
                         s.line.causal = PAGED ? p.mask == nullptr : p.causal;
                         s.q0 = __shfl_sync(0xffffffffu, own.q0, src);
                         s.k0 = __shfl_sync(0xffffffffu, own.k0, src);
                         const int64_t first = __shfl_sync(0xffffffffu, end_l - cost, src);
-                        const int64_t per = __shfl_sync(0xffffffffu, cost, src) / p.Hk;
+                        const int64_t per = __shfl_sync(0xffffffffu, own_len, src);
                         const int nb = s.line.blocks();
                         it.req = r0 + src;
                         it.k0 = s.k0;
                         it.step = s.line.causal ? 1 : 0;
-                        int h = x0 > first ? static_cast<int>((x0 - first) / per) : 0;
+                        int h = x0 > first ? static_cast<int>(line_div(x0 - first, per)) : 0;
+#pragma unroll 1
                         for (int64_t hs = first + h * per; h < p.Hk && hs < x1 && ok; ++h, hs += per) {
                             // the block that x0 is in: the last one that begins at or before it
                             int b = 0;
@@ -598,11 +670,13 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                 b = lo;
                             }
                             int64_t us = hs + s.line.before(b);
+#pragma unroll 1
                             for (; b < nb && us < x1 && ok; ++b) {
                                 const int tok0 = b * s.line.block_tokens(), tokens = s.line.tokens(b);
-                                const int klen = s.line.keys(b), w = s.line.weight(b);
+                                const int klen = s.line.keys(b);
                                 const int tiles = (klen + kBc - 1) / kBc;
-                                const LinePart part(us, tiles, w, x0, x1);
+                                const int64_t begin = us + s.line.unit_cost(b);
+                                const LinePart part(begin, tiles, kLineTile, x0, x1);
                                 const bool none = tiles == 0 && us >= x0;  // nothing seen: only written
                                 if (part.t0 < part.t1 || none) {
                                     it.ntiles = tiles == 0 ? 0 : part.t1 - part.t0;
@@ -613,7 +687,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                     it.nrows = tokens * p.G;
                                     it.sees0 = it.step ? tok0 + 1 + s.line.nk - s.line.nq : klen;
                                     it.ntiles0 = it.ntiles;
-                                    if (w == 2 && it.ntiles > 0) {  // at least one, which it may not see a key of
+                                    if (tokens > s.line.tile_tokens && it.ntiles > 0) {  // at least one, which it may not see a key of
                                         const int seen0 = s.line.sees(tok0 + s.line.tile_tokens - 1);
                                         it.ntiles0 = max(1, min(it.ntiles, (seen0 + kBc - 1) / kBc - it.tile0));
                                     }
@@ -621,8 +695,8 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                     if (tiles > 0 && it.ntiles < tiles) {
                                         it.slot = it.tile0 == 0 ? 2 * i + 1 : 2 * i;
                                         if (it.tile0 == 0) {
-                                            const int64_t last = us + kUnitCost + static_cast<int64_t>(tiles - 1) * (kLineTile * w);
-                                            cut.pieces = static_cast<int>(last / len) - i + 1;
+                                            const int64_t last = begin + static_cast<int64_t>(tiles - 1) * kLineTile;
+                                            cut.pieces = static_cast<int>(line_div(last, len)) - i + 1;
                                             cut.head = h;
                                             cut.req = it.req;
                                             cut.tok0 = it.tok0;
@@ -648,8 +722,10 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         uint32_t q_slots = 0, q_parity = 0;  // slots that a copy was issued to, and the parity it completes
         bool ok = true;
         PackedItem it;
+#pragma unroll 1
         for (uint32_t n = 0; ok && take_item(n, it); ++n) {
             if (it.ntiles == 0) continue;
+#pragma unroll 1
             for (int k = 0; k < (it.nrows > p.qrows ? 2 : 1) && ok; ++k, ++qpos) {
                 const uint32_t slot = qpos & 1u;
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kQEmpty + slot), ((qpos >> 1) & 1u) ^ 1u, ctx));
@@ -667,9 +743,10 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 __syncwarp();
             }
         }
+#pragma unroll 1
         for (uint32_t s = 0; s < 2; ++s)  // the copies land before the shared memory is released
             if (q_slots & (1u << s)) mbar_wait_drain(bar(L::kQFull + s), (q_parity >> s) & 1u, 50000000ull);
-    } else {
+    } else if (warp < 12) {
         // ------------------------------------------------------------ softmax warpgroups
         const int t = (warp - 4) >> 2;          // chain
         const int quad = warp & 3;              // TMEM lane quadrant
@@ -677,14 +754,16 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t t_s = tmem + lane_addr + t * kBc;
         const uint32_t t_o = tmem + lane_addr + 2 * kBc;  // O_0; O_1 is D columns further
-        float2* xchg = reinterpret_cast<float2*>(smem + L::kXchgOff);
+        float* weight = reinterpret_cast<float*>(smem + L::kWeightOff);
+        float2* pair = reinterpret_cast<float2*>(smem + L::kWeightOff) + rloc;
         const float sl2 = p.scale_log2;
         const int row_tok = rloc / p.G, row_head = rloc - row_tok * p.G;  // this row's token in its tile, and head of the group
         uint32_t s_cnt = 0, x_cnt = 0, ring = 0;  // ring: K/V fills before this item
-        uint32_t o_phase = 0u;                    // parity of each chain's next finished item, bit c
+        uint32_t o_phase = 0u;                    // parity of each chain's next item, bit c
         uint32_t par = 0;
         bool ok = true;
         PackedItem it;
+#pragma unroll 1
         for (uint32_t n = 0; ok && take_item(n, it); ++n) {
             const bool two = it.nrows > p.qrows;
             const int nt = it.ntiles;
@@ -694,19 +773,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             const bool warp_on = quad * 32 < nrow;            // the warp has rows
             const bool row_on = rloc < nrow;
             const int tok = it.tok0 + k * p.tile_tokens + row_tok;
-            // where this row's results go
-            const int hq = it.head * p.G + row_head;
-            const int64_t req = PAGED ? it.req : 0;
-            auto out_row = [&]() -> uint4* { return reinterpret_cast<uint4*>(p.o + req * p.os[0] + hq * p.os[1] + tok * p.os[2]); };
-            auto out_lse = [&]() -> float* { return p.lse + req * p.ls[0] + hq * p.ls[1] + tok; };
-            if (nt == 0) {  // no key for any row: O = 0, LSE = -inf
-                if (row_on && (two || t == 0)) {
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) out_row()[c] = make_uint4(0, 0, 0, 0);
-                    *out_lse() = -INFINITY;
-                }
-                continue;
-            }
+            if (nt == 0) continue;
             const bool both = two || nt >= 2;                 // both chains work on the item
             const bool used = both || mine == 0;
             const int nt_mine = two && t == 0 ? it.ntiles0 : nt;
@@ -730,6 +797,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 if (PAGED && p.mask)
                     mask_row = p.mask + (static_cast<int64_t>(it.req) * p.T + (row_on ? tok : it.tok0)) * p.words;
                 bool first = true;
+#pragma unroll 1
                 for (int j = two ? 0 : mine; j < nt_mine; j += two ? 1 : 2) {
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kSFull + t), s_cnt & 1u, ctx));
                     ++s_cnt;
@@ -746,6 +814,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         if (!ok) break;
                         const int pad = ((keys + 15) & ~15) - keys;
                         uint8_t* v = smem + L::kRingOff + stage * L::kTile;
+#pragma unroll 1
                         for (int i = rloc; i < pad * (D / 8); i += 128) {
                             const int row = keys + i / (D / 8), c8 = i % (D / 8);
                             *reinterpret_cast<uint4*>(v + (c8 >> 3) * (kBc * 128) + row * 128 + (c8 & 7) * 16) =
@@ -806,53 +875,15 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         }
                         tmem_st16(t_s + col, pk);
                     };
-                    if (key0 + kBc <= all_see) {  // every row sees all 128 keys
-                        uint32_t r0[32], r1[32], r2[32], r3[32];
-                        tmem_ld32(t_s + 0, r0);
-                        tmem_ld32(t_s + 32, r1);
-                        tmem_wait_ld(r0);
-                        tmem_wait_ld(r1);
-                        tmem_ld32(t_s + 64, r2);
-                        tmem_ld32(t_s + 96, r3);
-                        float* s0 = reinterpret_cast<float*>(r0);
-                        float* s1 = reinterpret_cast<float*>(r1);
-                        float* s2 = reinterpret_cast<float*>(r2);
-                        float* s3 = reinterpret_cast<float*>(r3);
-                        float mx0 = fmax3(s0[0], s0[1], s0[2]), mx1 = fmax3(s1[0], s1[1], s1[2]);
-#pragma unroll
-                        for (int c = 3; c < 31; c += 2) {
-                            mx0 = fmax3(mx0, s0[c], s0[c + 1]);
-                            mx1 = fmax3(mx1, s1[c], s1[c + 1]);
-                        }
-                        mx0 = fmax3(mx0, s0[31], fmaxf(mx1, s1[31]));
-                        tmem_wait_ld(r2);
-                        tmem_wait_ld(r3);
-                        float mx2 = fmax3(s2[0], s2[1], s2[2]), mx3 = fmax3(s3[0], s3[1], s3[2]);
-#pragma unroll
-                        for (int c = 3; c < 31; c += 2) {
-                            mx2 = fmax3(mx2, s2[c], s2[c + 1]);
-                            mx3 = fmax3(mx3, s3[c], s3[c + 1]);
-                        }
-                        refer(fmax3(mx0, fmax3(mx2, s2[31], mx3), s3[31]));
-                        exp_chunk(s0, 0);
-                        exp_chunk(s1, 16);
-                        rescale();
-                        tmem_wait_st();
-                        tc_fence_before_sync();
-                        mbar_arrive(bar(L::kPHalf + t));
-                        exp_chunk(s2, 32);
-                        exp_chunk(s3, 48);
-                    } else {
-                        // Keys that not every row sees: chunk by chunk in little code, reading the
-                        // scores twice.  Chunks past the last key are left out (the output product
-                        // stops at the step of 16 that holds it).  P of chunk i overwrites scores of
-                        // chunk i / 2, which has been read.
-                        const int nch = (keys + 31) >> 5;
-                        // bit c of chunk i: this row sees its key c
-                        auto seen_bits = [&](int i) -> uint32_t {
+                    const bool masked = key0 + kBc > all_see;  // some row does not see all 128 keys
+                    if (masked) {
+                        // Few tiles are (the last ones of a unit): hide keys in the scores where they are, chunk by
+                        // chunk in little code.  Bit c of `seen`: this row sees key c of the chunk.
+#pragma unroll 1
+                        for (int i = 0; i < kBc / 32; ++i) {
+                            uint32_t seen;
                             if (PAGED && p.mask) {
                                 const int rel = key0 + 32 * i - drafts;  // the chunk's first key among the new tokens
-                                if (rel <= -32) return 0xffffffffu;
                                 auto word = [&](int w) -> uint32_t {
                                     if (w < 0) return 0xffffffffu;  // keys before them
                                     if (w * 32 >= p.T) return 0u;
@@ -860,164 +891,232 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                     return p.T - w * 32 >= 32 ? m : m & ((1u << (p.T - w * 32)) - 1u);
                                 };
                                 const int w = rel >> 5;  // (rounds down)
-                                return __funnelshift_r(word(w), word(w + 1), rel & 31);
+                                seen = __funnelshift_r(word(w), word(w + 1), rel & 31);
+                            } else {
+                                const int n = lim - key0 - 32 * i;
+                                seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
                             }
-                            const int seen = lim - key0 - 32 * i;
-                            return seen >= 32 ? 0xffffffffu : seen <= 0 ? 0u : (1u << seen) - 1u;
-                        };
-                        uint32_t r[32];
-                        float* sc = reinterpret_cast<float*>(r);
-                        float mx = -INFINITY;
-#pragma unroll 1
-                        for (int i = 0; i < nch; ++i) {
+                            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+                            uint32_t r[32];
                             tmem_ld32(t_s + 32 * i, r);
-                            const uint32_t seen = seen_bits(i);
-                            tmem_wait_ld(r);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) mx = fmaxf(mx, (seen >> c) & 1u ? sc[c] : -INFINITY);
-                        }
-                        refer(mx);
-                        rescale();
-#pragma unroll 1
-                        for (int i = 0; i < nch; ++i) {
-                            tmem_ld32(t_s + 32 * i, r);
-                            const uint32_t seen = seen_bits(i);
                             tmem_wait_ld(r);
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                if (!((seen >> c) & 1u)) sc[c] = -INFINITY;
-                            exp_chunk(sc, 16 * i);
+                                if (!(seen & (1u << c))) r[c] = 0xff800000u;  // -infinity
+                            tmem_st32(t_s + 32 * i, r);
                         }
                         tmem_wait_st();
-                        tc_fence_before_sync();
-                        mbar_arrive(bar(L::kPHalf + t));
                     }
+                    // With 16 warps a thread has 128 registers, half of what the scores and their exponentials would
+                    // take: keys 64-127 are read for the maximum and then again, while keys 0-63 are at work.
+                    uint32_t ra[32], rb[32];
+                    const float* sa = reinterpret_cast<const float*>(ra);
+                    const float* sb = reinterpret_cast<const float*>(rb);
+                    auto largest = [](const float* sc) {
+                        float m0 = fmax3(sc[0], sc[1], sc[2]), m1 = fmax3(sc[3], sc[4], sc[5]);
+#pragma unroll
+                        for (int c = 6; c < 30; c += 4) {
+                            m0 = fmax3(m0, sc[c], sc[c + 1]);
+                            m1 = fmax3(m1, sc[c + 2], sc[c + 3]);
+                        }
+                        return fmax3(m0, m1, fmaxf(sc[30], sc[31]));
+                    };
+                    tmem_ld32(t_s + 64, ra);
+                    tmem_ld32(t_s + 96, rb);
+                    tmem_wait_ld(ra);
+                    tmem_wait_ld(rb);
+                    float mx = largest(sa);
+                    tmem_ld32(t_s + 0, ra);
+                    mx = fmaxf(mx, largest(sb));
+                    tmem_ld32(t_s + 32, rb);
+                    tmem_wait_ld(ra);
+                    tmem_wait_ld(rb);
+                    refer(fmax3(mx, largest(sa), largest(sb)));
+                    exp_chunk(sa, 0);
+                    tmem_ld32(t_s + 64, ra);
+                    exp_chunk(sb, 16);
+                    rescale();
+                    tmem_wait_st();
+                    tc_fence_before_sync();
+                    mbar_arrive(bar(L::kPHalf + t));
+                    tmem_ld32(t_s + 96, rb);
+                    tmem_wait_ld(ra);
+                    exp_chunk(sa, 32);
+                    tmem_wait_ld(rb);
+                    exp_chunk(sb, 48);
                     l += (acc0 + acc1) + (acc2 + acc3);
                     tmem_wait_st();
                     tc_fence_before_sync();
                     mbar_arrive(bar(L::kPFull + t));
                 }
                 if (!ok) break;
-                // Epilogue: O / l and the log-sum-exp, or this piece's for the combine kernel.
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kOFull + t), (o_phase >> t) & 1u, ctx));
-                if (!ok) break;
+                // The rows' weights for the epilogue, 1 / l, and the log-sum-exp.
                 const bool merge = both && !two;
                 float w_own = 1.f, w_other = 0.f;  // of this chain's O and the other's
                 float m = m_ref, sum = l;
+                ok = mbar_wait(bar(L::kWEmpty + t), ((o_phase >> t) & 1u) ^ 1u, ctx);
                 if (merge) {
-                    // chain 1's (m, l) through shared memory, then chain 0's through the same place
-                    if (t == 1) {
-                        xchg[rloc] = make_float2(m_ref, l);
-                        mbar_arrive(bar(L::kX + 1));
+                    if (t == 1) {  // its (m, l) lie where the other tile's weights would
+                        ok = ok && mbar_wait(bar(L::kWEmpty + 0), (o_phase & 1u) ^ 1u, ctx);
+                        if (ok) *pair = make_float2(m_ref, l);
+                        mbar_arrive(bar(L::kX));
+                    } else {
+                        // (a barrier of its own, counted by such items: chain 0 may be items ahead of chain 1)
+                        ok = ok && mbar_wait(bar(L::kX), x_cnt & 1u, ctx);
+                        const float2 other = *pair;
+                        m = fmaxf(m_ref, other.x);
+                        w_own = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
+                        w_other = other.x == -INFINITY ? 0.f : ex2_approx(other.x - m);
+                        // a chain whose reference never moved has l = 0, or a NaN to pass on
+                        sum = (m_ref == -INFINITY ? l : l * w_own) + (other.x == -INFINITY ? other.y : other.y * w_other);
                     }
-                    ok = mbar_wait(bar(L::kX + (t ^ 1)), x_cnt & 1u, ctx) &&
-                         mbar_wait(bar(L::kOFull + (t ^ 1)), (o_phase >> (t ^ 1)) & 1u, ctx);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    const float2 other = xchg[rloc];
-                    if (t == 0) {
-                        xchg[rloc] = make_float2(m_ref, l);
-                        mbar_arrive(bar(L::kX + 0));
-                    }
-                    m = fmaxf(m_ref, other.x);
-                    w_own = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
-                    w_other = other.x == -INFINITY ? 0.f : ex2_approx(other.x - m);
-                    // a chain whose reference never moved has l = 0, or a NaN to pass on
-                    sum = (m_ref == -INFINITY ? l : l * w_own) + (other.x == -INFINITY ? other.y : other.y * w_other);
                 }
-                tc_fence_after_sync();
-                // a row that sees no key of this piece: O = 0, LSE = -inf
-                const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-                const float wa = w_own * inv, wb = w_other * inv;
-                const int c0 = merge ? t * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
-                const float lse = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2;
-                if (warp_on && it.slot < 0) {
-                    uint4* orow = out_row();
-#pragma unroll 1
-                    for (int c = c0; c < c1; c += 32) {
-                        uint32_t o[32], pw[16];
-                        tmem_ld32(t_o + t * D + c, o);
-                        tmem_wait_ld(o);
-                        if (merge) {
-                            uint32_t ob[32];
-                            tmem_ld32(t_o + (t ^ 1) * D + c, ob);
-                            tmem_wait_ld(ob);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                pw[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * wa + __uint_as_float(ob[2 * i]) * wb,
-                                                    __uint_as_float(o[2 * i + 1]) * wa + __uint_as_float(ob[2 * i + 1]) * wb);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (!merge || t == 0) {
+                    // A row that sees no key of this piece: LSE = -inf, and a weight of -0 says that O is 0
+                    // (0 times a NaN of V would not be).
+                    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? -0.f : sum);
+                    if (merge) *pair = sum == 0.f ? make_float2(-0.f, 0.f) : make_float2(w_own * inv, w_other * inv);
+                    else weight[t * 128 + rloc] = inv;
+                    if (row_on) {
+                        const float lse = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2;
+                        if (it.slot < 0) {
+                            const int hq = it.head * p.G + row_head;
+                            p.lse[(PAGED ? it.req * p.ls[0] : 0) + hq * p.ls[1] + tok] = lse;
                         } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                pw[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * wa, __uint_as_float(o[2 * i + 1]) * wa);
-                        }
-                        if (sum == 0.f) {  // (0 times a NaN of V would not be 0)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) pw[i] = 0u;
-                        }
-                        if (row_on) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                orow[c / 8 + i] = make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
+                            p.part_lse[static_cast<int64_t>(it.slot) * p.orows + k * p.qrows + rloc] = lse;
                         }
                     }
-                    if (row_on && (!merge || t == 0)) *out_lse() = lse;
-                } else if (warp_on) {
-                    const int64_t part = static_cast<int64_t>(it.slot) * p.orows + k * p.qrows;
-                    // evict-last: read back right after this grid
-                    const uint64_t keep = l2_policy_evict_last();
-                    const int here = nrow - quad * 32;  // rows of this warp
-                    float* out = p.part_o + (part + quad * 32 + (lane >> 2)) * D + (lane & 3) * 2;
-#pragma unroll 1
-                    for (int half = 0; half < 32 && half < here; half += 16) {
-                        // the weights of this thread's two rows
-                        const int ra = half + (lane >> 2);
-                        const float wa0 = __shfl_sync(0xffffffffu, wa, ra), wa1 = __shfl_sync(0xffffffffu, wa, ra + 8);
-                        const float wb0 = __shfl_sync(0xffffffffu, wb, ra), wb1 = __shfl_sync(0xffffffffu, wb, ra + 8);
-                        const uint32_t lanes = static_cast<uint32_t>(half) << 16;
-#pragma unroll 1
-                        for (int c = c0; c < c1; c += 32) {
-                            uint32_t oa[16];
-                            tmem_ld16x256(t_o + lanes + t * D + c, oa);
-                            if (merge) {
-                                uint32_t ob[16];
-                                tmem_ld16x256(t_o + lanes + (t ^ 1) * D + c, ob);
-                                tmem_wait_ld16(oa);
-                                tmem_wait_ld16(ob);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    oa[i] = __float_as_uint(__uint_as_float(oa[i]) * ((i & 2) ? wa1 : wa0) +
-                                                            __uint_as_float(ob[i]) * ((i & 2) ? wb1 : wb0));
-                            } else {
-                                tmem_wait_ld16(oa);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    oa[i] = __float_as_uint(__uint_as_float(oa[i]) * ((i & 2) ? wa1 : wa0));
-                            }
-                            float* o0 = out + half * D + c;
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                if (ra < here)
-                                    st_global_v2_hint(o0 + 2 * i, __uint_as_float(oa[i]), __uint_as_float(oa[i + 1]), keep);
-                                if (ra + 8 < here)
-                                    st_global_v2_hint(o0 + 8 * D + 2 * i, __uint_as_float(oa[i + 2]),
-                                                      __uint_as_float(oa[i + 3]), keep);
-                            }
-                        }
-                    }
-                    if (row_on && (!merge || t == 0)) st_global_hint(p.part_lse + part + rloc, lse, keep);
                 }
-                tc_fence_before_sync();
-                if (merge) {
-                    mbar_arrive(bar(L::kOEmpty + 0));
-                    mbar_arrive(bar(L::kOEmpty + 1));
-                    ++x_cnt;
-                } else {
-                    mbar_arrive_n(bar(L::kOEmpty + t), 2);
-                }
+                mbar_arrive(bar(L::kWFull + t));
+                if (merge) ++x_cnt;
             }
             o_phase ^= both ? 3u : 1u << par;
             ring += 2 * nt;
             par = two ? 0u : (par + nt) & 1u;
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        // Thread r of the warpgroup has row r of a tile.  (Exchanges among threads that would make the stores of a row
+        // neighbours cost more than the stores: 9400 cycles for a unit's two tiles, 4500 like this, at d = 128.)
+        const int quad = warp & 3;
+        const int rloc = quad * 32 + lane;
+        const uint32_t t_o = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * kBc;
+        const float* weight = reinterpret_cast<const float*>(smem + L::kWeightOff);
+        const int row_tok = rloc / p.G, row_head = rloc - row_tok * p.G;
+        uint32_t o_phase = 0u, par = 0;
+        bool ok = true;
+        PackedItem it;
+#pragma unroll 1
+        for (uint32_t n = 0; ok && take_item(n, it); ++n) {
+            const bool two = it.nrows > p.qrows;
+            const int nt = it.ntiles;
+            const bool merge = !two && nt >= 2;
+#pragma unroll 1
+            for (int k = 0; k < (two ? 2 : 1) && ok; ++k) {
+                const int c = two ? k : merge ? 0 : static_cast<int>(par);  // chain
+                const int nrow = min(p.qrows, it.nrows - k * p.qrows);
+                const bool row_on = rloc < nrow;
+                const int tok = it.tok0 + k * p.tile_tokens + row_tok, hq = it.head * p.G + row_head;
+                const int64_t req = PAGED ? it.req : 0;
+                uint4* out = reinterpret_cast<uint4*>(p.o + req * p.os[0] + hq * p.os[1] + tok * p.os[2]);
+                if (nt == 0) {  // no key for any row: O = 0, LSE = -inf
+                    if (row_on) {
+#pragma unroll 1
+                        for (int i = 0; i < D / 8; ++i) out[i] = make_uint4(0, 0, 0, 0);
+                        p.lse[req * p.ls[0] + hq * p.ls[1] + tok] = -INFINITY;
+                    }
+                    continue;
+                }
+                // (an item on both chains has one pair of weights a row, posted by chain 0, and chain 1's barrier beside)
+                ok = mbar_wait(bar(L::kWFull + c), (o_phase >> c) & 1u, ctx) &&
+                     (!merge || mbar_wait(bar(L::kWFull + 1), (o_phase >> 1) & 1u, ctx));
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                const float wa = merge ? weight[2 * rloc] : weight[c * 128 + rloc];
+                const float wb = merge ? weight[2 * rloc + 1] : 0.f;
+                mbar_arrive(bar(L::kWEmpty + c));
+                if (merge) mbar_arrive(bar(L::kWEmpty + 1));
+                ok = mbar_wait(bar(L::kOFull + c), (o_phase >> c) & 1u, ctx) &&
+                     (!merge || mbar_wait(bar(L::kOFull + 1), (o_phase >> 1) & 1u, ctx));
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after_sync();
+                const uint32_t t_c = t_o + c * D;
+                if (quad * 32 >= nrow) {
+                    // none of this warp's rows exist
+                } else if (it.slot < 0) {
+                    const bool zero = __float_as_uint(wa) == 0x80000000u;
+#pragma unroll 1
+                    for (int col = 0; col < D; col += 32) {
+                        uint32_t o[32], pw[16];
+                        tmem_ld32(t_c + col, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * wa);
+                        if (merge) {
+                            // (a chain without a visible key for the row has weight 0 and finite O)
+                            uint32_t ob[32];
+                            tmem_ld32(t_c + D + col, ob);
+                            tmem_wait_ld(ob);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(fmaf(__uint_as_float(ob[i]), wb, __uint_as_float(o[i])));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            pw[i] = zero ? 0u : pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                        if (row_on) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                out[col / 8 + i] = make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
+                        }
+                    }
+                } else {
+                    // A piece, in fp32: by loads that give four threads 32 neighbouring bytes of a row.  Kept in L2
+                    // (evict last): read back right after this grid.
+                    const int ql = lane & 3, r4 = lane >> 2;
+                    const uint64_t keep = l2_policy_evict_last();
+                    const int here = nrow - quad * 32;  // rows of this warp
+                    float* part = p.part_o + (static_cast<int64_t>(it.slot) * p.orows + k * p.qrows + quad * 32 + r4) * D + 2 * ql;
+#pragma unroll 1
+                    for (int half = 0; half < 32 && half < here; half += 16, part += 16 * D) {
+                        const uint32_t t_h = t_c + (static_cast<uint32_t>(half) << 16);
+                        const float wa0 = __shfl_sync(0xffffffffu, wa, half + r4), wa1 = __shfl_sync(0xffffffffu, wa, half + r4 + 8);
+                        const float wb0 = __shfl_sync(0xffffffffu, wb, half + r4), wb1 = __shfl_sync(0xffffffffu, wb, half + r4 + 8);
+#pragma unroll 1
+                        for (int col = 0; col < D; col += 32) {
+                            uint32_t oa[16];
+                            tmem_ld16x256(t_h + col, oa);
+                            tmem_wait_ld16(oa);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                oa[i] = __float_as_uint(__uint_as_float(oa[i]) * ((i & 2) ? wa1 : wa0));
+                            if (merge) {
+                                uint32_t ob[16];
+                                tmem_ld16x256(t_h + D + col, ob);
+                                tmem_wait_ld16(ob);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    oa[i] = __float_as_uint(fmaf(__uint_as_float(ob[i]), (i & 2) ? wb1 : wb0, __uint_as_float(oa[i])));
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4) {
+                                if (half + r4 < here)
+                                    st_global_v2_hint(part + col + 2 * i, __uint_as_float(oa[i]), __uint_as_float(oa[i + 1]), keep);
+                                if (half + r4 + 8 < here)
+                                    st_global_v2_hint(part + 8 * D + col + 2 * i, __uint_as_float(oa[i + 2]),
+                                                      __uint_as_float(oa[i + 3]), keep);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before_sync();
+                mbar_arrive(bar(L::kOEmpty + c));
+                if (merge) mbar_arrive(bar(L::kOEmpty + 1));
+            }
+            if (nt > 0) {
+                o_phase ^= two || merge ? 3u : 1u << par;
+                par = two ? 0u : (par + nt) & 1u;
+            }
         }
     }
 
