@@ -29,7 +29,8 @@ void lay_out(PackedParams& p, int Hq, int Hk, int64_t tokens, double kv_bytes, i
     p.orows = rows < 2 * p.qrows ? static_cast<int>(rows) : 2 * p.qrows;
     int turns = static_cast<int>(std::fmin(std::ceil(kv_bytes / kTurnBytes), kMostTurns));
     if (turns < 1) turns = 1;
-    p.stretches = num_sms * turns;
+    while (turns > 1 && num_sms * turns > kPkMostStretches) --turns;
+    p.stretches = num_sms * turns;  // (an SM count above kPkMostStretches there is not: device_state takes sm_103 only)
 }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -106,14 +107,9 @@ int launch(DeviceState& dev, const CUtensorMap (&maps)[5], const PackedParams& p
     cfg.dynamicSmemBytes = smem;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], p)) != cudaSuccess) return cuda_fail(e);
     cfg.dynamicSmemBytes = 0;
-    // few rows a piece: eight warps share a row's pieces, of which there may be many
-    const bool few = p.orows <= 32;
-    // (of few stretches each row has a warp; of many, which only long calls have, CTAs take rows in turns)
-    cfg.gridDim = dim3(static_cast<unsigned>(few ? p.orows : p.stretches <= dev.num_sms ? (p.orows + 7) / 8 : (p.orows + 31) / 32),
-                       static_cast<unsigned>(p.stretches));
+    cfg.gridDim = dim3(static_cast<unsigned>(4 * dev.num_sms));
     cfg.blockDim = dim3(256);
-    auto combine = few ? attn_packed_combine_kernel<D, 8> : attn_packed_combine_kernel<D, 1>;
-    if ((e = cudaLaunchKernelEx(&cfg, combine, p)) != cudaSuccess) return cuda_fail(e);
+    if ((e = cudaLaunchKernelEx(&cfg, attn_packed_combine_kernel<D>, p)) != cudaSuccess) return cuda_fail(e);
     return ATTN_OK;
 }
 

@@ -75,7 +75,7 @@ int launch(DeviceState& dev, const CUtensorMap& mq, const CUtensorMap& mk, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
-    cfg.gridDim = dim3(blocks + static_cast<unsigned>(p.stretches));
+    cfg.gridDim = dim3((blocks + 1) / 2 + static_cast<unsigned>(p.stretches) * kPkbCutCtas);
     cfg.blockDim = dim3(256);
     cfg.attrs = attr;
     cfg.numAttrs = 1;

@@ -397,9 +397,10 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
 #pragma unroll 1
         for (uint32_t n = 0; ok && take_item(n, it); ++n) {
             if (it.nblocks == 0) continue;
+            // (waited for at every item: a parity tells one fill from the next, not from the one after)
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvFull), items & 1u, ctx));
+            if (!ok) break;
             if (it.nkeys < kBc) {  // the tile's other rows are another sequence's keys
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvFull), items & 1u, ctx));
-                if (!ok) break;
                 zero_rows(L::kKOff, 2 * (D / 64), L::kKvBlock, it.nkeys, kBc);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -853,20 +854,28 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_prep_kernel(const PackedR
     if (live && part == 0) dvec[static_cast<int64_t>(h) * q.Nq + tok] = -scale * acc;
 }
 
-// The first `stretches` CTAs add up the pieces of dK and dV of the units that stretches cut, in the pieces' order; the
-// others round dQ's sums to bf16, rows of tokens that are in no sequence left as they were (q_starts is non-decreasing).
+// The first kPkbCutCtas CTAs for each stretch add up the pieces of dK and dV of the unit that begins to be cut there, in the
+// pieces' order; the others round dQ's sums to bf16, rows of tokens that are in no sequence left as they were (q_starts is
+// non-decreasing).
+constexpr int kPkbCutCtas = 8;   // each has 16 of the tile's 128 keys
+
 template <int D>
 __global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_constant__ PackedBwdParams p, const PackedRowParams q) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kVecs = D / 8;  // 8 elements a thread
-    if (blockIdx.x < static_cast<unsigned>(p.stretches)) {
-        const int i = blockIdx.x;
+    const unsigned cut_ctas = static_cast<unsigned>(p.stretches) * kPkbCutCtas;
+    if (blockIdx.x < cut_ctas) {
+        const int i = blockIdx.x / kPkbCutCtas;
         const int* desc = reinterpret_cast<const int*>(p.cuts + i);
         const int pieces = __ldcg(desc);
         if (pieces == 0) return;
         const int head = __ldcg(desc + 1), key0 = __ldcg(desc + 2), nkeys = __ldcg(desc + 3);
-        for (int x = threadIdx.x; x < nkeys * 2 * kVecs; x += 256) {
-            const int r = x / (2 * kVecs), which = x / kVecs & 1, c = x % kVecs * 8;
+        constexpr int kKeys = kBc / kPkbCutCtas;
+        const int r0 = (blockIdx.x % kPkbCutCtas) * kKeys;
+#pragma unroll
+        for (int x = threadIdx.x; x < kKeys * 2 * kVecs; x += 256) {
+            const int r = r0 + x / (2 * kVecs), which = x / kVecs & 1, c = x % kVecs * 8;
+            if (r >= nkeys) break;
             float acc[8] = {};
             for (int s = 0; s < pieces; ++s) {
                 const int64_t slot = s == 0 ? 2 * static_cast<int64_t>(i) + 1 : 2 * (static_cast<int64_t>(i) + s);
@@ -882,24 +891,39 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_
         }
         return;
     }
-    const int64_t tid = static_cast<int64_t>(blockIdx.x - p.stretches) * 256 + threadIdx.x;
-    const int64_t row = tid / kVecs;
-    if (row >= static_cast<int64_t>(q.Hq) * q.Nq) return;
-    const int part = static_cast<int>(tid % kVecs);
-    const int tok = static_cast<int>(row / q.Hq), h = static_cast<int>(row - static_cast<int64_t>(tok) * q.Hq);
-    // the last sequence that begins at or before the token
-    int lo = 0, hi = p.R;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (__ldg(p.q_starts + mid) <= tok) lo = mid + 1;
-        else hi = mid;
+    // Two rows' parts a thread, both under way before the search for their sequences.
+    constexpr int kRowsCta = 256 / kVecs;
+    const int64_t rows = static_cast<int64_t>(q.Hq) * q.Nq;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x - cut_ctas) * (2 * kRowsCta) + threadIdx.x / kVecs;
+    const int part = threadIdx.x % kVecs;
+    float4 a[2], b[2];
+    int tok[2], h[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int64_t row = row0 + u * kRowsCta;
+        tok[u] = -1;
+        if (row < rows) {
+            tok[u] = static_cast<int>(row / q.Hq);
+            h[u] = static_cast<int>(row - static_cast<int64_t>(tok[u]) * q.Hq);
+            const int hk = h[u] / q.G;
+            const float4* z = reinterpret_cast<const float4*>(p.dq_acc + ((static_cast<int64_t>(hk) * q.Nq + tok[u]) * q.G + (h[u] - hk * q.G)) * D);
+            a[u] = __ldcs(z + 2 * part);
+            b[u] = __ldcs(z + 2 * part + 1);
+        }
     }
-    if (lo == 0 || tok >= __ldg(p.q_starts + lo)) return;
-    const int hk = h / q.G;
-    const float4* z = reinterpret_cast<const float4*>(p.dq_acc + ((static_cast<int64_t>(hk) * q.Nq + tok) * q.G + (h - hk * q.G)) * D);
-    const float4 a = __ldcs(z + 2 * part), b = __ldcs(z + 2 * part + 1);
-    reinterpret_cast<uint4*>(q.dq + h * q.dqs[0] + tok * q.dqs[1])[part] =
-        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        if (tok[u] < 0) return;
+        int lo = 0, hi = p.R;  // the last sequence that begins at or before the token
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (__ldg(p.q_starts + mid) <= tok[u]) lo = mid + 1;
+            else hi = mid;
+        }
+        if (lo == 0 || tok[u] >= __ldg(p.q_starts + lo)) continue;
+        reinterpret_cast<uint4*>(q.dq + h[u] * q.dqs[0] + tok[u] * q.dqs[1])[part] =
+            make_uint4(pack_bf16x2(a[u].x, a[u].y), pack_bf16x2(a[u].z, a[u].w), pack_bf16x2(b[u].x, b[u].y), pack_bf16x2(b[u].z, b[u].w));
+    }
 }
 
 }  // namespace elsattn

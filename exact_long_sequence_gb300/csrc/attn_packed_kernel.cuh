@@ -1128,37 +1128,64 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     }
 }
 
-// Merge the pieces of the units that stretches cut: CTA (x, i) takes rows of the unit whose pieces begin in
-// stretch i.  WARPS warps per row (pieces dealt to them in turn, each with a running maximum, then merged in a fixed
-// order); lane l holds columns [kPer l, kPer l + kPer).
-template <int D, int WARPS>
-__global__ void __launch_bounds__(256) attn_packed_combine_kernel(const __grid_constant__ PackedParams p) {
+// Merge the pieces of the units that stretches cut.  The cut units' rows are dealt to the warps of a grid that fills the GPU
+// (a CTA for every stretch and row block, most of them with nothing to do, took 1.4 us for each thousand); where there
+// are fewer rows than CTAs, the eight warps of a CTA share a row's pieces, each with a running maximum, and are merged in a
+// fixed order.  Lane l holds columns [kPer l, kPer l + kPer).
+constexpr int kPkMostStretches = 2048;
+
+template <int D>
+__global__ void __launch_bounds__(256, 4) attn_packed_combine_kernel(const __grid_constant__ PackedParams p) {
     constexpr int kPer = D / 32;
-    constexpr int kRows = 8 / WARPS;  // rows per CTA and turn
+    __shared__ int s_first[kPkMostStretches + 1];  // rows of the cuts before each stretch's
+    __shared__ int s_warp[8];
     __shared__ float s_acc[8][D];
     __shared__ float2 s_stat[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int part = warp % WARPS;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int i = blockIdx.y;
-    const int* desc = reinterpret_cast<const int*>(p.cuts + i);
-    const int pieces = __ldcg(desc);
-    const int nrows = pieces > 0 ? __ldcg(desc + 4) : 0;
-    // every warp of the CTA takes part in its turns
-    for (int base = blockIdx.x * kRows; base < nrows; base += gridDim.x * kRows) {
-        const int row = base + warp / WARPS;
-        const bool on = row < nrows;
+    int carry = 0;
+    for (int base = 0; base < p.stretches; base += 256) {
+        const int i = base + threadIdx.x;
+        int rows = 0;
+        if (i < p.stretches) {
+            const int* desc = reinterpret_cast<const int*>(p.cuts + i);
+            rows = __ldcg(desc) > 0 ? __ldcg(desc + 4) : 0;
+        }
+        int sum = warp_scan(rows, lane);
+        if (lane == 31) s_warp[warp] = sum;
+        __syncthreads();
+        int before = carry;
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) before += s_warp[w];
+            carry += s_warp[w];
+        }
+        if (i < p.stretches) s_first[i] = before + sum - rows;
+        __syncthreads();
+    }
+    const int total = carry;
+    const bool shared = total <= static_cast<int>(gridDim.x);
+    const int part = shared ? warp : 0, step = shared ? 8 : 1;
+    for (int x = shared ? blockIdx.x : blockIdx.x * 8 + warp; x < total; x += shared ? gridDim.x : gridDim.x * 8) {
+        int i = 0, end = p.stretches;  // the last stretch whose rows begin at or before x (it has some: the next begins after)
+        while (end - i > 1) {
+            const int mid = (i + end) / 2;
+            if (s_first[mid] <= x) i = mid;
+            else end = mid;
+        }
+        const int row = x - s_first[i];
+        const int* desc = reinterpret_cast<const int*>(p.cuts + i);
+        const int pieces = __ldcg(desc), head = __ldcg(desc + 1), req = __ldcg(desc + 2), tok0 = __ldcg(desc + 3);
         auto at = [&](int s) -> int64_t { return static_cast<int64_t>(s == 0 ? 2 * i + 1 : 2 * (i + s)) * p.orows + row; };
         float acc[kPer];
 #pragma unroll
         for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
         float sum = 0.f, mx = -INFINITY;
-        constexpr int kUnroll = 6;
-        for (int s0 = part; on && s0 < pieces; s0 += WARPS * kUnroll) {
+        constexpr int kUnroll = 4;
+        for (int s0 = part; s0 < pieces; s0 += step * kUnroll) {
             float v[kUnroll][kPer], ls[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int s = s0 + u * WARPS;
+                const int s = s0 + u * step;
                 ls[u] = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < kPer; ++c) v[u][c] = 0.f;
@@ -1184,38 +1211,37 @@ __global__ void __launch_bounds__(256) attn_packed_combine_kernel(const __grid_c
                 for (int c = 0; c < kPer; ++c) acc[c] = fmaf(w, v[u][c], acc[c]);
             }
         }
-        if (WARPS > 1) {
+        if (shared) {
 #pragma unroll
             for (int c = 0; c < kPer; ++c) s_acc[warp][lane * kPer + c] = acc[c];
             if (lane == 0) s_stat[warp] = make_float2(mx, sum);
             __syncthreads();
-            if (part == 0) {
+            if (warp == 0) {
                 float m = mx;
-                for (int k = 1; k < WARPS; ++k) m = fmaxf(m, s_stat[warp + k].x);
+                for (int k = 1; k < 8; ++k) m = fmaxf(m, s_stat[k].x);
                 const float keep = mx == -INFINITY ? 1.f : expf(mx - m);  // (nothing yet, or a NaN to pass on)
                 sum *= keep;
 #pragma unroll
                 for (int c = 0; c < kPer; ++c) acc[c] *= keep;
-                for (int k = 1; k < WARPS; ++k) {
-                    const float2 st = s_stat[warp + k];
+                for (int k = 1; k < 8; ++k) {
+                    const float2 st = s_stat[k];
                     const float w = st.x == -INFINITY ? 1.f : expf(st.x - m);
                     sum += st.y * w;
 #pragma unroll
-                    for (int c = 0; c < kPer; ++c) acc[c] = fmaf(w, s_acc[warp + k][lane * kPer + c], acc[c]);
+                    for (int c = 0; c < kPer; ++c) acc[c] = fmaf(w, s_acc[k][lane * kPer + c], acc[c]);
                 }
                 mx = m;
             }
             __syncthreads();
         }
-        if (on && part == 0) {
+        if (part == 0) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const int tok = row / p.G, hq = __ldcg(desc + 1) * p.G + row - tok * p.G;
-            const int64_t req = p.lens ? __ldcg(desc + 2) : 0;
-            const int64_t token = __ldcg(desc + 3) + tok;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + req * p.os[0] + hq * p.os[1] + token * p.os[2] + lane * kPer);
+            const int t = row / p.G, hq = head * p.G + row - t * p.G;
+            const int64_t r = p.lens ? req : 0, token = static_cast<int64_t>(tok0) + t;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + r * p.os[0] + hq * p.os[1] + token * p.os[2] + lane * kPer);
 #pragma unroll
             for (int c = 0; c < kPer; c += 2) dst[c / 2] = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
-            if (lane == 0) p.lse[req * p.ls[0] + hq * p.ls[1] + token] = sum == 0.f ? -INFINITY : mx + logf(sum);
+            if (lane == 0) p.lse[r * p.ls[0] + hq * p.ls[1] + token] = sum == 0.f ? -INFINITY : mx + logf(sum);
         }
     }
 }

@@ -96,7 +96,7 @@ struct LineSeq {
 // head with the tokens that see one of them, which are the last ones; its query
 // blocks of `block_tokens` = 64 / G tokens begin at the first of those.  A unit is
 // kKeyUnitBlocks blocks and then its tokens, one position each.
-constexpr int kKeyUnitBlocks = 4;
+constexpr int kKeyUnitBlocks = 7;
 constexpr int kKeyLineLeast = 8;   // blocks of the shortest stretch
 static ELS_HD_ONCE int64_t line_tiles_before(int nq, int nk, int unit_cost, bool causal, int64_t n) {
     const int64_t off = static_cast<int64_t>(nk) - nq;
