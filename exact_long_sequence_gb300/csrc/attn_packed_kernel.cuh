@@ -174,6 +174,35 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {
     return v;
 }
 
+// mbar_wait without a call: for the softmax warps, whose registers a call's would not fit beside.  (What they spilled came back
+// from L2, since 16 warps' stacks are more than the L1 that the tiles leave: 3000 cycles at each end of an item.)
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ int lds(uint32_t addr) {
+    int v;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool mbar_wait_inline(uint32_t bar, uint32_t parity, uint32_t abort_flag, const PackedParams& p) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 31u) == 0) {
+            if (lds(abort_flag)) return false;
+            if (global_timer_ns() - t0 > p.timeout_ns) {
+                atomicCAS(p.error_word, 0u, static_cast<uint32_t>(kDevTimeout));
+                asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
+                return false;
+            }
+        }
+    }
+}
+
 // D (+)= A B with the operands' descriptors given by their low words (start address and leading stride); the
 // high word (stride between 8-row groups of 1024 bytes, swizzle) is the same for all of them here.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); }
@@ -195,15 +224,22 @@ __device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
-// O_c (+)= P_c V over keys [64 half, 64 half + 64), in steps of 16 of the tile's `steps`; b: V's descriptor.
+// O_c (+)= P_c V over keys [64 half, 64 half + 64) of a tile of 128; b: V's descriptor.
+template <int D>
+__device__ __forceinline__ void packed_gemm_full(uint32_t tmem, uint32_t c, uint32_t b, int half, bool first) {
+    constexpr uint32_t idesc = make_idesc_bf16_f32(kBr, D, false, true);
+    const uint32_t o = tmem + 2 * kBc + c * D, pt = tmem + c * kBc;
+#pragma unroll
+    for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+        mma_ts_lo(o, pt + kk * 8, b + ((kk * 16 * 128) >> 4), idesc, kk > 0 || !first ? 1u : 0u);
+}
+// ... in steps of 16 of the tile's `steps`.
 template <int D>
 __device__ __forceinline__ void packed_gemm_o(uint32_t tmem, uint32_t c, uint32_t b, int half, int steps, bool first) {
     constexpr uint32_t idesc = make_idesc_bf16_f32(kBr, D, false, true);
     const uint32_t o = tmem + 2 * kBc + c * D, pt = tmem + c * kBc;
     if (steps == kBc / 16) {
-#pragma unroll
-        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-            mma_ts_lo(o, pt + kk * 8, b + ((kk * 16 * 128) >> 4), idesc, kk > 0 || !first ? 1u : 0u);
+        packed_gemm_full<D>(tmem, c, b, half, first);
     } else {
 #pragma unroll 1
         for (int kk = half * 4; kk < min(half * 4 + 4, steps); ++kk)
@@ -239,6 +275,39 @@ __device__ __noinline__ bool packed_pv(const WaitCtx& ctx, uint32_t bar0, uint32
     }
     __syncwarp();
     return true;
+}
+
+// Hides the keys of a tile that a row does not see: their scores, in TMEM at t_s, become -infinity, chunk by chunk
+// in little code (few tiles need it: the last ones of a unit).  `sees` keys from the tile's first on are seen; or,
+// with a row of a mask, those before new token 0, whose key is `-rel` places into the tile, and the new tokens of the row's bits.
+static __device__ __noinline__ void packed_hide(uint32_t t_s, int sees, const uint32_t* mask_row, int T, int rel) {
+#pragma unroll 1
+    for (int i = 0; i < kBc; i += 32) {
+        uint32_t seen;  // bit c: key c of the chunk
+        if (mask_row != nullptr) {
+            const int first = rel + i;  // the chunk's first key among the new tokens
+            auto word = [&](int w) -> uint32_t {
+                if (w < 0) return 0xffffffffu;  // keys before them
+                if (w * 32 >= T) return 0u;
+                const uint32_t m = __ldg(mask_row + w);
+                return T - w * 32 >= 32 ? m : m & ((1u << (T - w * 32)) - 1u);
+            };
+            const int w = first >> 5;  // (rounds down)
+            seen = __funnelshift_r(word(w), word(w + 1), first & 31);
+        } else {
+            const int n = sees - i;
+            seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+        }
+        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+        uint32_t r[32];
+        tmem_ld32(t_s + i, r);
+        tmem_wait_ld(r);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (!(seen & (1u << c))) r[c] = 0xff800000u;  // -infinity
+        tmem_st32(t_s + i, r);
+    }
+    tmem_wait_st();
 }
 
 template <int D, bool PAGED>
@@ -306,8 +375,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 
     // Reads the next item (ring entry n); `it.ntiles` is -1 after the last.  Called by whole warps, whose
     // lanes get one word each from shared memory and hand it round, so that the fields are uniform.
-    // keep: the caller gives the ring entry back itself.
-    auto take_item = [&](uint32_t n, PackedItem& it, bool keep = false) -> bool {
+    auto take_item = [&](uint32_t n, PackedItem& it) -> bool {
         const uint32_t s = n % kPfxItemRing;
         if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kItemFull + s), (n / kPfxItemRing) & 1u, ctx))) return false;
         const int* from = reinterpret_cast<const int*>(smem + L::kItemOff + s * sizeof(PackedItem));
@@ -324,7 +392,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         it.sees0 = __shfl_sync(0xffffffffu, word, 9);
         it.step = __shfl_sync(0xffffffffu, word, 10);
         it.slot = __shfl_sync(0xffffffffu, word, 11);
-        if (!keep && lane == 0) mbar_arrive(bar(L::kItemEmpty + s));
+        if (lane == 0) mbar_arrive(bar(L::kItemEmpty + s));
         return it.ntiles >= 0;
     };
     // Keys of the item's tile j (1 .. 128).
@@ -438,7 +506,6 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 mma_ss_lo<true>(tmem + c * kBc, a + off, b + off, idesc_s);
             }
         };
-        auto gemm_o = [&](int c, uint32_t b, int half, int steps, bool first) { packed_gemm_o<D>(tmem, c, b, half, steps, first); };
         // the output product that is due: of the step before
         struct { bool due, first, last, first_v, last_v; int chain, ksteps; RingPos v; } pv{};
         auto run_pv = [&]() -> bool {
@@ -472,30 +539,29 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     break;
                 const uint32_t a0 = dq0 + q0 * kTile16, a1 = dq0 + q1 * kTile16;
                 const int last_steps = (tile_keys(it, nt - 1) + 15) / 16;
-                // O_c (+)= P_c V_j, V_j at ring position v
-                auto pv_two = [&](auto chain, int j, RingPos v) -> bool {
+                // O_c (+)= P_c V_j for a tile of 128 keys, V_j at ring position v.  Inlined, without a tail's conditions:
+                // this warp's own instructions bound the loop (with the products behind a call, 2175 -> 2494 us on long documents).
+                auto pv_full = [&](auto chain, bool first, RingPos v) -> bool {
                     constexpr int c = decltype(chain)::value;
                     bool w = true;
-                    if (c == 0 || j >= n0) w = mbar_wait(bar(L::kKvFull + v.stage), v.phase, ctx);  // its first use
+                    if (c == 0) w = mbar_wait(bar(L::kKvFull + v.stage), v.phase, ctx);  // (chain 1 follows)
                     w = w && mbar_wait(bar(L::kPHalf + c), (p_phase >> c) & 1u, ctx);
-                    if (j == 0) {
+                    if (first) {
                         w = w && mbar_wait(bar(L::kOEmpty + c), (o_phase >> c) & 1u, ctx);
                         o_phase ^= 1u << c;
                     }
                     if (!__all_sync(0xffffffffu, w)) return false;
                     tc_fence_after_sync();
                     const uint32_t b = dv0 + v.stage * kTile16;
-                    const int ks = j == nt - 1 ? last_steps : kBc / 16;
-                    if (elect_one()) gemm_o(c, b, 0, ks, j == 0);
+                    if (elect_one()) packed_gemm_full<D>(tmem, c, b, 0, first);
                     __syncwarp();
                     w = mbar_wait(bar(L::kPFull + c), (p_phase >> c) & 1u, ctx);
                     p_phase ^= 1u << c;
                     if (!__all_sync(0xffffffffu, w)) return false;
                     tc_fence_after_sync();
                     if (elect_one()) {
-                        gemm_o(c, b, 1, ks, j == 0);
+                        packed_gemm_full<D>(tmem, c, b, 1, false);
                         if (c == 1) mma_commit(bar(L::kKvEmpty + v.stage));
-                        if (j == (c == 0 ? n0 : nt) - 1) mma_commit(bar(L::kOFull + c));
                     }
                     __syncwarp();
                     return true;
@@ -517,17 +583,32 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         }
                         __syncwarp();
                     }
-                    ok = j == 0 ? run_pv() : pv_two(std::integral_constant<int, 1>{}, j - 1, vprev);
+                    // (chain 0 took every tile before the last, so that V_{j-1} is there, and only the last may have a tail;
+                    // where chain 0 ends before it, its O is complete here)
+                    ok = j == 0 ? run_pv() : pv_full(std::integral_constant<int, 1>{}, j == 1, vprev);
                     if (!ok) break;
                     if (elect_one()) {
                         gemm_s(1, a1, b);
                         mma_commit(bar(L::kSFull + 1));
                         mma_commit(bar(L::kKvEmpty + kpos.stage));
                         if (j == nt - 1) mma_commit(bar(L::kQEmpty + q1));
+                        if (j == n0) mma_commit(bar(L::kOFull + 0));
                     }
                     __syncwarp();
                     vprev = kpos.next(L::kStages);
-                    if (j < n0 && !(ok = pv_two(std::integral_constant<int, 0>{}, j, vprev))) break;
+                    if (j < nt - 1) {
+                        if (!(ok = pv_full(std::integral_constant<int, 0>{}, j == 0, vprev))) break;
+                    } else if (n0 == nt) {
+                        pv.due = true;
+                        pv.chain = 0;
+                        pv.v = vprev;
+                        pv.ksteps = last_steps;
+                        pv.first = nt == 1;
+                        pv.last = true;
+                        pv.first_v = true;
+                        pv.last_v = false;
+                        if (!(ok = run_pv())) break;
+                    }
                     kpos = vprev.next(L::kStages);
                 }
                 if (!ok) break;
@@ -748,77 +829,80 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             if (q_slots & (1u << s)) mbar_wait_drain(bar(L::kQFull + s), (q_parity >> s) & 1u, 50000000ull);
     } else if (warp < 12) {
         // ------------------------------------------------------------ softmax warpgroups
+        auto inline_wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_inline(b, parity, s_base + L::kFlagsOff + 4, p); };
         const int t = (warp - 4) >> 2;          // chain
         const int quad = warp & 3;              // TMEM lane quadrant
         const int rloc = quad * 32 + lane;      // row within the tile
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t t_s = tmem + lane_addr + t * kBc;
         const uint32_t t_o = tmem + lane_addr + 2 * kBc;  // O_0; O_1 is D columns further
-        float* weight = reinterpret_cast<float*>(smem + L::kWeightOff);
-        float2* pair = reinterpret_cast<float2*>(smem + L::kWeightOff) + rloc;
         const float sl2 = p.scale_log2;
-        const int row_tok = rloc / p.G, row_head = rloc - row_tok * p.G;  // this row's token in its tile, and head of the group
-        uint32_t s_cnt = 0, x_cnt = 0, ring = 0;  // ring: K/V fills before this item
-        uint32_t o_phase = 0u;                    // parity of each chain's next item, bit c
-        uint32_t par = 0;
+        uint32_t ring = 0;   // K/V fills before this item
+        // Bits: parity of the next S; of the next item on both chains; of chain c's next item; the chain of the next item's first step.
+        constexpr uint32_t kS = 1, kXBit = 1, kOBit = 2, kParBit = 4;
+        uint32_t state = 0;
         bool ok = true;
-        PackedItem it;
+        // An item's fields stay in its ring entry, to be read where they are needed (and again at its end): held in
+        // registers beside the scores they were spilled, and 16 warps' stacks are more than the L1 that the tiles leave.
 #pragma unroll 1
-        for (uint32_t n = 0; ok && take_item(n, it); ++n) {
-            const bool two = it.nrows > p.qrows;
-            const int nt = it.ntiles;
-            const int mine = two ? t : t ^ static_cast<int>(par);  // this chain's query tile, or its first K/V tile
-            const int k = two ? mine : 0;                     // its query tile
-            const int nrow = min(p.qrows, it.nrows - k * p.qrows);
-            const bool warp_on = quad * 32 < nrow;            // the warp has rows
-            const bool row_on = rloc < nrow;
-            const int tok = it.tok0 + k * p.tile_tokens + row_tok;
-            if (nt == 0) continue;
+        for (uint32_t n = 0; ok; ++n) {
+            const uint32_t entry = n % kPfxItemRing;
+            auto field = [&](int PackedItem::*f) -> int {
+                return lds(s_base + L::kItemOff + entry * static_cast<uint32_t>(sizeof(PackedItem)) +
+                           static_cast<uint32_t>(reinterpret_cast<uintptr_t>(&(static_cast<const PackedItem*>(nullptr)->*f))));
+            };
+            if (!__all_sync(0xffffffffu, inline_wait(bar(L::kItemFull + entry), (n / kPfxItemRing) & 1u))) break;
+            const int nt = field(&PackedItem::ntiles);
+            if (nt < 0) break;
+            const bool two = field(&PackedItem::nrows) > p.qrows;
             const bool both = two || nt >= 2;                 // both chains work on the item
-            const bool used = both || mine == 0;
-            const int nt_mine = two && t == 0 ? it.ntiles0 : nt;
+            // an item of one query tile: this chain's first K/V tile (two query tiles: chain t has tile t)
+            const int mine = two ? 0 : t ^ static_cast<int>((state >> kParBit) & 1u);
             float m_ref = -INFINITY;
             float l = 0.f;
-            if (used) {
+            if (nt > 0 && (both || mine == 0)) {
+                const int nt_mine = two && t == 0 ? field(&PackedItem::ntiles0) : nt;
+                const int nrow = min(p.qrows, field(&PackedItem::nrows) - (two ? t * p.qrows : 0));
+                const bool warp_on = quad * 32 < nrow;            // the warp has rows
+                const bool row_on = rloc < nrow;
                 // Key counts from the item's first tile on: all that the unit sees, those that this row
                 // sees and that every row of the tile does.
-                const int left = it.klen - it.tile0 * kBc;
-                const int drafts = PAGED && p.mask ? it.klen - p.T - it.tile0 * kBc : 0;  // where the new tokens' keys begin
+                const int left = field(&PackedItem::klen) - field(&PackedItem::tile0) * kBc;
                 int lim, all_see;
+                const uint32_t* mask_row = nullptr;
                 if (PAGED && p.mask) {
                     lim = left;
-                    all_see = drafts;
+                    all_see = left - p.T;  // where the new tokens' keys begin
+                    const int tok = field(&PackedItem::tok0) + (two ? t * p.tile_tokens : 0) + (row_on ? rloc / p.G : 0);
+                    mask_row = p.mask + (static_cast<int64_t>(field(&PackedItem::req)) * p.T + tok) * p.words;
                 } else {
-                    const int tile_tok = k * p.tile_tokens;
-                    lim = min(it.klen, it.sees0 + (tile_tok + row_tok) * it.step) - it.tile0 * kBc;
-                    all_see = min(it.klen, it.sees0 + tile_tok * it.step) - it.tile0 * kBc;
+                    const int tile_tok = two ? t * p.tile_tokens : 0;
+                    const int sees = field(&PackedItem::sees0) - field(&PackedItem::tile0) * kBc, step = field(&PackedItem::step);
+                    lim = min(left, sees + (tile_tok + rloc / p.G) * step);
+                    all_see = min(left, sees + tile_tok * step);
                 }
-                const uint32_t* mask_row = nullptr;
-                if (PAGED && p.mask)
-                    mask_row = p.mask + (static_cast<int64_t>(it.req) * p.T + (row_on ? tok : it.tok0)) * p.words;
                 bool first = true;
 #pragma unroll 1
-                for (int j = two ? 0 : mine; j < nt_mine; j += two ? 1 : 2) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kSFull + t), s_cnt & 1u, ctx));
-                    ++s_cnt;
+                for (int j = mine; j < nt_mine; j += two ? 1 : 2) {
+                    ok = __all_sync(0xffffffffu, inline_wait(bar(L::kSFull + t), state & kS));
+                    state ^= kS;
                     if (!ok) break;
                     tc_fence_after_sync();
                     const int key0 = j * kBc;
                     const int keys = min(kBc, left - key0);
                     // The output product sums over keys in steps of 16.  What lies behind the last key may
                     // hold anything (a NaN times a zero weight is a NaN): zero it, before the first product that reads it.
-                    if ((keys & 15) != 0 && (!two || t == (j < it.ntiles0 ? 0 : 1))) {
+                    if ((keys & 15) != 0 && (!two || t == (j < field(&PackedItem::ntiles0) ? 0 : 1))) {
                         const uint32_t at = ring + 2 * j + 1;  // V_j's fill
                         const uint32_t stage = at % L::kStages;
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvFull + stage), (at / L::kStages) & 1u, ctx));
+                        ok = __all_sync(0xffffffffu, inline_wait(bar(L::kKvFull + stage), (at / L::kStages) & 1u));
                         if (!ok) break;
                         const int pad = ((keys + 15) & ~15) - keys;
-                        uint8_t* v = smem + L::kRingOff + stage * L::kTile;
+                        const uint32_t v = s_base + L::kRingOff + stage * L::kTile;
 #pragma unroll 1
                         for (int i = rloc; i < pad * (D / 8); i += 128) {
                             const int row = keys + i / (D / 8), c8 = i % (D / 8);
-                            *reinterpret_cast<uint4*>(v + (c8 >> 3) * (kBc * 128) + row * 128 + (c8 & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c8 >> 3) * (kBc * 128) + row * 128 + (c8 & 7) * 16), "r"(0) : "memory");
                         }
                         fence_proxy_async_smem();
                     }
@@ -858,14 +942,15 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         first = false;
                     };
                     float acc0 = 0.f, acc1 = 0.f, acc2 = 0.f, acc3 = 0.f;
-                    auto exp_chunk = [&](const float* sc, uint32_t col) {
+                    // P = 2^(s scale log2 e - m) of 16 keys, as bf16 pairs over the scores' first half
+                    auto exp_chunk = [&](const uint32_t (&r)[16], uint32_t col) {
                         const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-                        uint32_t pk[16];
+                        uint32_t pk[8];
 #pragma unroll
-                        for (int c = 0; c < 16; c += 2) {
+                        for (int c = 0; c < 8; c += 2) {
                             float x0, x1, x2, x3;
-                            ffma2(x0, x1, sc[2 * c], sc[2 * c + 1], sl2, -m_use);
-                            ffma2(x2, x3, sc[2 * c + 2], sc[2 * c + 3], sl2, -m_use);
+                            ffma2(x0, x1, __uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]), sl2, -m_use);
+                            ffma2(x2, x3, __uint_as_float(r[2 * c + 2]), __uint_as_float(r[2 * c + 3]), sl2, -m_use);
                             const float a0 = ex2_approx(x0), b0 = ex2_approx(x1);
                             const float a1 = ex2_approx(x2), b1 = ex2_approx(x3);
                             fadd2(acc0, acc1, a0, b0);
@@ -873,46 +958,16 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             pk[c] = pack_bf16x2(a0, b0);
                             pk[c + 1] = pack_bf16x2(a1, b1);
                         }
-                        tmem_st16(t_s + col, pk);
+                        tmem_st8(t_s + col, pk);
                     };
                     const bool masked = key0 + kBc > all_see;  // some row does not see all 128 keys
-                    if (masked) {
-                        // Few tiles are (the last ones of a unit): hide keys in the scores where they are, chunk by
-                        // chunk in little code.  Bit c of `seen`: this row sees key c of the chunk.
-#pragma unroll 1
-                        for (int i = 0; i < kBc / 32; ++i) {
-                            uint32_t seen;
-                            if (PAGED && p.mask) {
-                                const int rel = key0 + 32 * i - drafts;  // the chunk's first key among the new tokens
-                                auto word = [&](int w) -> uint32_t {
-                                    if (w < 0) return 0xffffffffu;  // keys before them
-                                    if (w * 32 >= p.T) return 0u;
-                                    const uint32_t m = __ldg(mask_row + w);
-                                    return p.T - w * 32 >= 32 ? m : m & ((1u << (p.T - w * 32)) - 1u);
-                                };
-                                const int w = rel >> 5;  // (rounds down)
-                                seen = __funnelshift_r(word(w), word(w + 1), rel & 31);
-                            } else {
-                                const int n = lim - key0 - 32 * i;
-                                seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-                            }
-                            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
-                            uint32_t r[32];
-                            tmem_ld32(t_s + 32 * i, r);
-                            tmem_wait_ld(r);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!(seen & (1u << c))) r[c] = 0xff800000u;  // -infinity
-                            tmem_st32(t_s + 32 * i, r);
-                        }
-                        tmem_wait_st();
-                    }
+                    if (masked) packed_hide(t_s, lim - key0, PAGED && p.mask ? mask_row : nullptr, p.T, key0 - all_see);
                     // With 16 warps a thread has 128 registers, half of what the scores and their exponentials would
-                    // take: keys 64-127 are read for the maximum and then again, while keys 0-63 are at work.
+                    // take: they are read for the maximum, and again 16 keys ahead of the exponentials (32 ahead, a thread
+                    // spilled 20 registers: 24 prompts of 20 to 2000 tokens in 250 us, 234 like this).
                     uint32_t ra[32], rb[32];
-                    const float* sa = reinterpret_cast<const float*>(ra);
-                    const float* sb = reinterpret_cast<const float*>(rb);
-                    auto largest = [](const float* sc) {
+                    auto largest = [](const uint32_t (&r)[32]) {
+                        const float* sc = reinterpret_cast<const float*>(r);
                         float m0 = fmax3(sc[0], sc[1], sc[2]), m1 = fmax3(sc[3], sc[4], sc[5]);
 #pragma unroll
                         for (int c = 6; c < 30; c += 4) {
@@ -925,25 +980,34 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     tmem_ld32(t_s + 96, rb);
                     tmem_wait_ld(ra);
                     tmem_wait_ld(rb);
-                    float mx = largest(sa);
+                    float mx = largest(ra);
                     tmem_ld32(t_s + 0, ra);
-                    mx = fmaxf(mx, largest(sb));
+                    mx = fmaxf(mx, largest(rb));
                     tmem_ld32(t_s + 32, rb);
                     tmem_wait_ld(ra);
                     tmem_wait_ld(rb);
-                    refer(fmax3(mx, largest(sa), largest(sb)));
-                    exp_chunk(sa, 0);
-                    tmem_ld32(t_s + 64, ra);
-                    exp_chunk(sb, 16);
+                    refer(fmax3(mx, largest(ra), largest(rb)));
                     rescale();
-                    tmem_wait_st();
-                    tc_fence_before_sync();
-                    mbar_arrive(bar(L::kPHalf + t));
-                    tmem_ld32(t_s + 96, rb);
-                    tmem_wait_ld(ra);
-                    exp_chunk(sa, 32);
-                    tmem_wait_ld(rb);
-                    exp_chunk(sb, 48);
+                    auto half_done = [&]() {  // keys 0-63
+                        tmem_wait_st();
+                        tc_fence_before_sync();
+                        mbar_arrive(bar(L::kPHalf + t));
+                    };
+                    {
+                        uint32_t s0[16], s1[16];
+                        tmem_ld16(t_s, s0);
+                        tmem_wait_ld16(s0);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            tmem_ld16(t_s + 16 * (i + 1), s1);
+                            exp_chunk(s0, 8 * i);
+                            tmem_wait_ld16(s1);
+                            if (i + 2 < 8) tmem_ld16(t_s + 16 * (i + 2), s0);
+                            exp_chunk(s1, 8 * (i + 1));
+                            if (i == 2) half_done();
+                            if (i + 2 < 8) tmem_wait_ld16(s0);
+                        }
+                    }
                     l += (acc0 + acc1) + (acc2 + acc3);
                     tmem_wait_st();
                     tc_fence_before_sync();
@@ -952,17 +1016,19 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 if (!ok) break;
                 // The rows' weights for the epilogue, 1 / l, and the log-sum-exp.
                 const bool merge = both && !two;
+                float* weight = reinterpret_cast<float*>(smem + L::kWeightOff) + rloc;
+                float2* pair = reinterpret_cast<float2*>(smem + L::kWeightOff) + rloc;
                 float w_own = 1.f, w_other = 0.f;  // of this chain's O and the other's
                 float m = m_ref, sum = l;
-                ok = mbar_wait(bar(L::kWEmpty + t), ((o_phase >> t) & 1u) ^ 1u, ctx);
+                ok = inline_wait(bar(L::kWEmpty + t), ((state >> (kOBit + t)) & 1u) ^ 1u);
                 if (merge) {
                     if (t == 1) {  // its (m, l) lie where the other tile's weights would
-                        ok = ok && mbar_wait(bar(L::kWEmpty + 0), (o_phase & 1u) ^ 1u, ctx);
+                        ok = ok && inline_wait(bar(L::kWEmpty + 0), ((state >> kOBit) & 1u) ^ 1u);
                         if (ok) *pair = make_float2(m_ref, l);
                         mbar_arrive(bar(L::kX));
                     } else {
                         // (a barrier of its own, counted by such items: chain 0 may be items ahead of chain 1)
-                        ok = ok && mbar_wait(bar(L::kX), x_cnt & 1u, ctx);
+                        ok = ok && inline_wait(bar(L::kX), (state >> kXBit) & 1u);
                         const float2 other = *pair;
                         m = fmaxf(m_ref, other.x);
                         w_own = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
@@ -970,6 +1036,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         // a chain whose reference never moved has l = 0, or a NaN to pass on
                         sum = (m_ref == -INFINITY ? l : l * w_own) + (other.x == -INFINITY ? other.y : other.y * w_other);
                     }
+                    state ^= 1u << kXBit;
                 }
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 if (!merge || t == 0) {
@@ -977,23 +1044,30 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     // (0 times a NaN of V would not be).
                     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? -0.f : sum);
                     if (merge) *pair = sum == 0.f ? make_float2(-0.f, 0.f) : make_float2(w_own * inv, w_other * inv);
-                    else weight[t * 128 + rloc] = inv;
-                    if (row_on) {
-                        const float lse = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2;
-                        if (it.slot < 0) {
-                            const int hq = it.head * p.G + row_head;
-                            p.lse[(PAGED ? it.req * p.ls[0] : 0) + hq * p.ls[1] + tok] = lse;
-                        } else {
-                            p.part_lse[static_cast<int64_t>(it.slot) * p.orows + k * p.qrows + rloc] = lse;
-                        }
-                    }
+                    else weight[t * 128] = inv;
                 }
                 mbar_arrive(bar(L::kWFull + t));
-                if (merge) ++x_cnt;
+                if (row_on && (!merge || t == 0)) {
+                    const float lse = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2;
+                    const int slot = field(&PackedItem::slot);
+                    float* to;
+                    if (slot < 0) {
+                        const int row_tok = rloc / p.G;
+                        const int tok = field(&PackedItem::tok0) + (two ? t * p.tile_tokens : 0) + row_tok, hq = field(&PackedItem::head) * p.G + rloc - row_tok * p.G;
+                        to = p.lse + (PAGED ? field(&PackedItem::req) * p.ls[0] : 0) + hq * p.ls[1] + tok;
+                    } else {
+                        to = p.part_lse + static_cast<int64_t>(slot) * p.orows + (two ? t * p.qrows : 0) + rloc;
+                    }
+                    *to = lse;
+                }
             }
-            o_phase ^= both ? 3u : 1u << par;
+            __syncwarp();  // every lane has read the ring entry
+            if (lane == 0) mbar_arrive(bar(L::kItemEmpty + entry));
+            if (nt == 0) continue;
+            const uint32_t par = (state >> kParBit) & 1u;
+            state ^= (both ? 3u : 1u << par) << kOBit;
             ring += 2 * nt;
-            par = two ? 0u : (par + nt) & 1u;
+            state = (state & ~(1u << kParBit)) | ((two ? 0u : (par + nt) & 1u) << kParBit);
         }
     } else {
         // ------------------------------------------------------------ epilogue
