@@ -36,6 +36,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cstddef>
 #include <cstdint>
 #include <type_traits>
 
@@ -847,37 +848,36 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll 1
         for (uint32_t n = 0; ok; ++n) {
             const uint32_t entry = n % kPfxItemRing;
-            auto field = [&](int PackedItem::*f) -> int {
-                return lds(s_base + L::kItemOff + entry * static_cast<uint32_t>(sizeof(PackedItem)) +
-                           static_cast<uint32_t>(reinterpret_cast<uintptr_t>(&(static_cast<const PackedItem*>(nullptr)->*f))));
+            auto field = [&](size_t at) -> int {
+                return lds(s_base + L::kItemOff + entry * static_cast<uint32_t>(sizeof(PackedItem)) + static_cast<uint32_t>(at));
             };
             if (!__all_sync(0xffffffffu, inline_wait(bar(L::kItemFull + entry), (n / kPfxItemRing) & 1u))) break;
-            const int nt = field(&PackedItem::ntiles);
+            const int nt = field(offsetof(PackedItem, ntiles));
             if (nt < 0) break;
-            const bool two = field(&PackedItem::nrows) > p.qrows;
+            const bool two = field(offsetof(PackedItem, nrows)) > p.qrows;
             const bool both = two || nt >= 2;                 // both chains work on the item
             // an item of one query tile: this chain's first K/V tile (two query tiles: chain t has tile t)
             const int mine = two ? 0 : t ^ static_cast<int>((state >> kParBit) & 1u);
             float m_ref = -INFINITY;
             float l = 0.f;
             if (nt > 0 && (both || mine == 0)) {
-                const int nt_mine = two && t == 0 ? field(&PackedItem::ntiles0) : nt;
-                const int nrow = min(p.qrows, field(&PackedItem::nrows) - (two ? t * p.qrows : 0));
+                const int nt_mine = two && t == 0 ? field(offsetof(PackedItem, ntiles0)) : nt;
+                const int nrow = min(p.qrows, field(offsetof(PackedItem, nrows)) - (two ? t * p.qrows : 0));
                 const bool warp_on = quad * 32 < nrow;            // the warp has rows
                 const bool row_on = rloc < nrow;
                 // Key counts from the item's first tile on: all that the unit sees, those that this row
                 // sees and that every row of the tile does.
-                const int left = field(&PackedItem::klen) - field(&PackedItem::tile0) * kBc;
+                const int left = field(offsetof(PackedItem, klen)) - field(offsetof(PackedItem, tile0)) * kBc;
                 int lim, all_see;
                 const uint32_t* mask_row = nullptr;
                 if (PAGED && p.mask) {
                     lim = left;
                     all_see = left - p.T;  // where the new tokens' keys begin
-                    const int tok = field(&PackedItem::tok0) + (two ? t * p.tile_tokens : 0) + (row_on ? rloc / p.G : 0);
-                    mask_row = p.mask + (static_cast<int64_t>(field(&PackedItem::req)) * p.T + tok) * p.words;
+                    const int tok = field(offsetof(PackedItem, tok0)) + (two ? t * p.tile_tokens : 0) + (row_on ? rloc / p.G : 0);
+                    mask_row = p.mask + (static_cast<int64_t>(field(offsetof(PackedItem, req))) * p.T + tok) * p.words;
                 } else {
                     const int tile_tok = two ? t * p.tile_tokens : 0;
-                    const int sees = field(&PackedItem::sees0) - field(&PackedItem::tile0) * kBc, step = field(&PackedItem::step);
+                    const int sees = field(offsetof(PackedItem, sees0)) - field(offsetof(PackedItem, tile0)) * kBc, step = field(offsetof(PackedItem, step));
                     lim = min(left, sees + (tile_tok + rloc / p.G) * step);
                     all_see = min(left, sees + tile_tok * step);
                 }
@@ -892,7 +892,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     const int keys = min(kBc, left - key0);
                     // The output product sums over keys in steps of 16.  What lies behind the last key may
                     // hold anything (a NaN times a zero weight is a NaN): zero it, before the first product that reads it.
-                    if ((keys & 15) != 0 && (!two || t == (j < field(&PackedItem::ntiles0) ? 0 : 1))) {
+                    if ((keys & 15) != 0 && (!two || t == (j < field(offsetof(PackedItem, ntiles0)) ? 0 : 1))) {
                         const uint32_t at = ring + 2 * j + 1;  // V_j's fill
                         const uint32_t stage = at % L::kStages;
                         ok = __all_sync(0xffffffffu, inline_wait(bar(L::kKvFull + stage), (at / L::kStages) & 1u));
@@ -1049,12 +1049,12 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 mbar_arrive(bar(L::kWFull + t));
                 if (row_on && (!merge || t == 0)) {
                     const float lse = sum == 0.f ? -INFINITY : (m + lg2_approx(sum)) * kLn2;
-                    const int slot = field(&PackedItem::slot);
+                    const int slot = field(offsetof(PackedItem, slot));
                     float* to;
                     if (slot < 0) {
                         const int row_tok = rloc / p.G;
-                        const int tok = field(&PackedItem::tok0) + (two ? t * p.tile_tokens : 0) + row_tok, hq = field(&PackedItem::head) * p.G + rloc - row_tok * p.G;
-                        to = p.lse + (PAGED ? field(&PackedItem::req) * p.ls[0] : 0) + hq * p.ls[1] + tok;
+                        const int tok = field(offsetof(PackedItem, tok0)) + (two ? t * p.tile_tokens : 0) + row_tok, hq = field(offsetof(PackedItem, head)) * p.G + rloc - row_tok * p.G;
+                        to = p.lse + (PAGED ? field(offsetof(PackedItem, req)) * p.ls[0] : 0) + hq * p.ls[1] + tok;
                     } else {
                         to = p.part_lse + static_cast<int64_t>(slot) * p.orows + (two ? t * p.qrows : 0) + rloc;
                     }
