@@ -19,8 +19,12 @@ namespace {
 constexpr double kTurnBytes = 128e6;
 constexpr int kMostTurns = 8;
 
-// Sizes that follow from the shape.  rows: most rows of a block; kv_bytes: of K and V together.
-void lay_out(PackedParams& p, int Hq, int Hk, int64_t tokens, double kv_bytes, int num_sms) {
+// Up to so many keys a sequence, units are not cut, which saves the launch that merges pieces.
+constexpr int kWholeKeys = 640;
+
+// Sizes that follow from the shape.  tokens, keys: most of a sequence; kv_bytes: of K and V together.
+void lay_out(PackedParams& p, int Hq, int Hk, int64_t tokens, int64_t keys, double kv_bytes, int num_sms) {
+    p.whole = keys <= kWholeKeys;
     p.Hk = Hk;
     p.G = Hq / Hk;
     p.tile_tokens = kBr / p.G;
@@ -39,7 +43,7 @@ size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 struct PackedSpace {
     size_t lse, rows, bytes;
     PackedSpace(const PackedParams& p, int d) {
-        const size_t part = 2 * static_cast<size_t>(p.stretches) * p.orows;
+        const size_t part = p.whole ? 0 : 2 * static_cast<size_t>(p.stretches) * p.orows;
         lse = align256(p.stretches * sizeof(PackedCut));
         rows = lse + align256(part * sizeof(float));
         bytes = rows + part * d * sizeof(float);
@@ -106,6 +110,7 @@ int launch(DeviceState& dev, const CUtensorMap (&maps)[5], const PackedParams& p
     cfg.blockDim = dim3(kPkThreads);
     cfg.dynamicSmemBytes = smem;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], p)) != cudaSuccess) return cuda_fail(e);
+    if (p.whole) return ATTN_OK;
     cfg.dynamicSmemBytes = 0;
     cfg.gridDim = dim3(static_cast<unsigned>(4 * dev.num_sms));
     cfg.blockDim = dim3(256);
@@ -147,7 +152,7 @@ extern "C" size_t attn_fwd_packed_workspace_bytes(int R, int Nq, int Nk, int Hq,
     DeviceState* dev = nullptr;
     if (device_state(&dev) != ATTN_OK) return 0;
     PackedParams p{};
-    lay_out(p, Hq, Hk, Nq, 4.0 * Nk * Hk * d, dev->num_sms);
+    lay_out(p, Hq, Hk, Nq, Nk, 4.0 * Nk * Hk * d, dev->num_sms);
     return PackedSpace(p, d).bytes;
 }
 
@@ -173,7 +178,7 @@ extern "C" int attn_fwd_packed(const void* Q, const int64_t* q_strides, const vo
     p.Nq = Nq;
     p.Nk = Nk;
     p.causal = causal != 0;
-    lay_out(p, Hq, Hk, Nq, 4.0 * Nk * Hk * d, dev->num_sms);
+    lay_out(p, Hq, Hk, Nq, Nk, 4.0 * Nk * Hk * d, dev->num_sms);
     if (workspace_bytes < PackedSpace(p, d).bytes) return ATTN_ERR_INVALID_ARG;
     p.q_starts = q_starts;
     p.k_starts = k_starts;
@@ -203,7 +208,8 @@ extern "C" size_t attn_fwd_tree_workspace_bytes(int R, int Hq, int Hk, int T, in
     DeviceState* dev = nullptr;
     if (device_state(&dev) != ATTN_OK) return 0;
     PackedParams p{};
-    lay_out(p, Hq, Hk, T, 0.0, dev->num_sms);
+    lay_out(p, Hq, Hk, T, 0, 0.0, dev->num_sms);
+    p.whole = false;  // (the caches' capacity is not asked for here)
     return PackedSpace(p, d).bytes;
 }
 
@@ -230,7 +236,7 @@ extern "C" int attn_fwd_tree(const void* Q, const int64_t* q_strides, const void
     if ((st = device_state(&dev)) != ATTN_OK) return st;
     p.R = R;
     p.T = T;
-    lay_out(p, Hq, Hk, T, 0.0, dev->num_sms);  // (K and V are read once: nothing to keep in L2)
+    lay_out(p, Hq, Hk, T, static_cast<int64_t>(table_pages) * page_size, 0.0, dev->num_sms);  // (K and V are read once: nothing to keep in L2)
     if (workspace_bytes < PackedSpace(p, d).bytes) return ATTN_ERR_INVALID_ARG;
     p.lens = lens;
     p.table = page_table;

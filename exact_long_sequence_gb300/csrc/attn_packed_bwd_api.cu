@@ -36,6 +36,7 @@ void lay_out(PackedBwdParams& p, int Nq, int Hq, int Hk, int d, int num_sms) {
     int turns = static_cast<int>(std::fmin(std::ceil(8.0 * Nq * Hq * d / kBwdTurnBytes), kBwdMostTurns));
     if (turns < 1) turns = 1;
     p.stretches = num_sms * turns;
+    p.whole = Nq <= kKeyLineLeast * p.block_tokens;  // no unit is longer than the shortest stretch: none is cut
 }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -48,7 +49,7 @@ struct Space {
         dvec = align256(p.stretches * sizeof(PackedBwdCut));
         dq = dvec + align256(rows * sizeof(float));
         part = dq + rows * d * sizeof(float);
-        bytes = part + 2 * static_cast<size_t>(p.stretches) * kBc * 2 * d * sizeof(float);
+        bytes = part + (p.whole ? 0 : 2 * static_cast<size_t>(p.stretches) * kBc * 2 * d * sizeof(float));
     }
 };
 
@@ -66,19 +67,25 @@ int launch(DeviceState& dev, const CUtensorMap& mq, const CUtensorMap& mk, const
     }
     const int64_t threads = static_cast<int64_t>(rows.Hq) * rows.Nq * (D / 8);
     const unsigned blocks = static_cast<unsigned>((threads + 255) / 256);
-    attn_packed_bwd_prep_kernel<D><<<blocks, 256, 0, stream>>>(rows, dvec, p.dq_acc, p.scale);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
-    kernel<<<dev.num_sms, kBwdThreads, smem, stream>>>(mq, mk, mv, mdo, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+    // Each is a programmatic dependent of what is before it on the stream, and waits for that once it is set up.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
-    cfg.gridDim = dim3((blocks + 1) / 2 + static_cast<unsigned>(p.stretches) * kPkbCutCtas);
-    cfg.blockDim = dim3(256);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(256);
+    if ((e = cudaLaunchKernelEx(&cfg, attn_packed_bwd_prep_kernel<D>, rows, dvec, p.dq_acc, p.scale)) != cudaSuccess)
+        return cuda_fail(e);
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms));
+    cfg.blockDim = dim3(kBwdThreads);
+    cfg.dynamicSmemBytes = smem;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, mdo, p)) != cudaSuccess) return cuda_fail(e);
+    cfg.dynamicSmemBytes = 0;
+    cfg.gridDim = dim3((blocks + 1) / 2 + (p.whole ? 0u : static_cast<unsigned>(p.stretches) * kPkbCutCtas));
+    cfg.blockDim = dim3(256);
     if ((e = cudaLaunchKernelEx(&cfg, attn_packed_bwd_post_kernel<D>, p, rows)) != cudaSuccess) return cuda_fail(e);
     return ATTN_OK;
 }

@@ -50,6 +50,7 @@ struct PackedBwdParams {
     int block_tokens, qrows;   // of a query block: whole tokens, and rows
     bool causal;
     int stretches;
+    bool whole;                // units are not cut: each is in the stretch that its start is in
     uint32_t* error_word;
     uint64_t timeout_ns;
     float scale, scale_log2;
@@ -210,7 +211,9 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    // (the grid before this one, which zeroes dQ's sums and works out D, has ended: an ordinary launch)
+    // Up to here nothing is read or written that an earlier grid may write or read (the one before zeroes dQ's sums
+    // and works out D): the setup overlaps its end.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     auto take_item = [&](uint32_t n, PackedBwdItem& it) -> bool {
@@ -536,7 +539,11 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                                 const int tok = s.line.first(j), ntok = s.line.nq - tok;
                                 const int nb = (ntok + p.block_tokens - 1) / p.block_tokens;
                                 const int64_t begin = us + s.line.unit_cost();
-                                const LinePart part(begin, nb, p.block_tokens, x0, x1);
+                                LinePart part(begin, nb, p.block_tokens, x0, x1);
+                                if (p.whole) {
+                                    part.t0 = us >= x0 ? 0 : nb;
+                                    part.t1 = nb;
+                                }
                                 if (part.t0 < part.t1 || (nb == 0 && us >= x0)) {
                                     const int skip = nb == 0 ? 0 : part.t0 * p.block_tokens;
                                     it.nblocks = nb == 0 ? 0 : part.t1 - part.t0;
@@ -566,7 +573,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                     start = __shfl_sync(0xffffffffu, end_l, 31);
                 }
             }
-            if (lane == 0) p.cuts[i] = cut;
+            if (lane == 0 && !p.whole) p.cuts[i] = cut;
         }
         it.nblocks = -1;
         if (ok) publish(it);
@@ -829,6 +836,8 @@ struct PackedRowParams {
 template <int D>
 __global__ void __launch_bounds__(256) attn_packed_bwd_prep_kernel(const PackedRowParams q, float* dvec, float* dq_acc, float scale) {
     constexpr int kTpr = D / 8;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t tid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const int64_t row = tid / kTpr;  // token-major: (token, head)
     const int part = static_cast<int>(tid % kTpr);
@@ -863,7 +872,7 @@ template <int D>
 __global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_constant__ PackedBwdParams p, const PackedRowParams q) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kVecs = D / 8;  // 8 elements a thread
-    const unsigned cut_ctas = static_cast<unsigned>(p.stretches) * kPkbCutCtas;
+    const unsigned cut_ctas = p.whole ? 0u : static_cast<unsigned>(p.stretches) * kPkbCutCtas;
     if (blockIdx.x < cut_ctas) {
         const int i = blockIdx.x / kPkbCutCtas;
         const int* desc = reinterpret_cast<const int*>(p.cuts + i);

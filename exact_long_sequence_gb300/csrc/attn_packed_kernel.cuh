@@ -69,6 +69,7 @@ struct PackedParams {
     int orows;                 // partial rows kept for a piece
     bool causal;               // token t sees the keys j <= t + nk - nq
     int stretches;             // how many stretches the line has at most (a multiple of the grid)
+    bool whole;                // units are not cut: each is in the stretch that its start is in
     __nv_bfloat16* o;
     int64_t os[3];             // strides in elements: request (paged), head, token
     float* lse;
@@ -758,7 +759,11 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                 const int klen = s.line.keys(b);
                                 const int tiles = (klen + kBc - 1) / kBc;
                                 const int64_t begin = us + s.line.unit_cost(b);
-                                const LinePart part(begin, tiles, kLineTile, x0, x1);
+                                LinePart part(begin, tiles, kLineTile, x0, x1);
+                                if (p.whole) {
+                                    part.t0 = us >= x0 ? 0 : tiles;
+                                    part.t1 = tiles;
+                                }
                                 const bool none = tiles == 0 && us >= x0;  // nothing seen: only written
                                 if (part.t0 < part.t1 || none) {
                                     it.ntiles = tiles == 0 ? 0 : part.t1 - part.t0;
@@ -794,7 +799,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     start = __shfl_sync(0xffffffffu, end_l, 31);
                 }
             }
-            if (lane == 0) p.cuts[i] = cut;
+            if (lane == 0 && !p.whole) p.cuts[i] = cut;
         }
         it.ntiles = -1;
         if (ok) publish(it);
