@@ -483,12 +483,13 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         const int64_t upto = warp_scan64(mine, lane);
         const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
         const int64_t len = line_stretch(total, p.stretches, kKeyLineLeast * p.block_tokens);
+        // (after a timeout too: what the merging kernel reads of the cuts has to be theirs)
 #pragma unroll 1
-        for (int i = blockIdx.x; i < p.stretches && ok; i += gridDim.x) {
+        for (int i = blockIdx.x; i < p.stretches; i += gridDim.x) {
             const int64_t x0 = i * len;
             const int64_t x1 = min(x0 + len, total);
             PackedBwdCut cut{};
-            if (x0 < x1) {
+            if (ok && x0 < x1) {
                 const int at = run == 1 ? 0 : __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
                 int64_t start = __shfl_sync(0xffffffffu, upto - mine, at);
 #pragma unroll 1
@@ -552,7 +553,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                                     it.ntok = ntok - skip;
                                     it.key0 = s.k0 + j * kLineTile;
                                     it.nkeys = min(kLineTile, s.line.nk - j * kLineTile);
-                                    it.diag = p.causal ? tok + skip + s.line.nk - s.line.nq - j * kLineTile : kLineTile;
+                                    it.diag = p.causal ? (tok + skip - s.line.nq) + (s.line.nk - j * kLineTile) : kLineTile;
                                     it.slot = -1;
                                     if (nb > 0 && it.nblocks < nb) {
                                         it.slot = part.t0 == 0 ? 2 * i + 1 : 2 * i;

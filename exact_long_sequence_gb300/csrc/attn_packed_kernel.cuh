@@ -328,6 +328,8 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int lane = threadIdx.x & 31;
     const WaitCtx ctx{abort_flag, p.error_word, p.timeout_ns};
+    // For the roles that wait for whole items, whose lengths are the sequences'; they leave with the others before, at an abort.
+    const WaitCtx ctx_item{abort_flag, p.error_word, 16 * p.timeout_ns};
 
     if (threadIdx.x == 0) {
         *abort_flag = 0u;
@@ -669,7 +671,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         bool ok = true;
         auto publish = [&](const PackedItem& it) {
             const uint32_t s = n % kPfxItemRing;
-            if (n >= kPfxItemRing) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kItemEmpty + s), ((n / kPfxItemRing) - 1) & 1u, ctx));
+            if (n >= kPfxItemRing) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kItemEmpty + s), ((n / kPfxItemRing) - 1) & 1u, ctx_item));
             if (!ok) return;
             if (lane == 0) {
                 *reinterpret_cast<PackedItem*>(smem + L::kItemOff + s * sizeof(PackedItem)) = it;
@@ -697,12 +699,13 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int64_t upto = warp_scan64(mine, lane);
         const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
         const int64_t len = line_stretch(total, p.stretches);
+        // (after a timeout too: what the merging kernel reads of the cuts has to be theirs)
 #pragma unroll 1
-        for (int i = blockIdx.x; i < p.stretches && ok; i += gridDim.x) {
+        for (int i = blockIdx.x; i < p.stretches; i += gridDim.x) {
             const int64_t x0 = i * len;
             const int64_t x1 = min(x0 + len, total);
             PackedCut cut{};
-            if (x0 < x1) {
+            if (ok && x0 < x1) {
                 // the run of sequences that x0 is in, then the sequences in groups of 32
                 const int at = run == 1 ? 0 : __ffs(__ballot_sync(0xffffffffu, upto > x0)) - 1;
                 int64_t start = __shfl_sync(0xffffffffu, upto - mine, at);
@@ -772,7 +775,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                     it.head = h;
                                     it.tok0 = s.q0 + tok0;
                                     it.nrows = tokens * p.G;
-                                    it.sees0 = it.step ? tok0 + 1 + s.line.nk - s.line.nq : klen;
+                                    it.sees0 = it.step ? tok0 - s.line.nq + s.line.nk + 1 : klen;  // (in this order: in 32 bits)
                                     it.ntiles0 = it.ntiles;
                                     if (tokens > s.line.tile_tokens && it.ntiles > 0) {  // at least one, which it may not see a key of
                                         const int seen0 = s.line.sees(tok0 + s.line.tile_tokens - 1);
@@ -815,7 +818,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll 1
             for (int k = 0; k < (it.nrows > p.qrows ? 2 : 1) && ok; ++k, ++qpos) {
                 const uint32_t slot = qpos & 1u;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kQEmpty + slot), ((qpos >> 1) & 1u) ^ 1u, ctx));
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kQEmpty + slot), ((qpos >> 1) & 1u) ^ 1u, ctx_item));
                 if (!ok) break;
                 const uint32_t full = bar(L::kQFull + slot);
                 if (lane == 0) {  // whole tokens; what lies behind the tensor reads as zero
@@ -1108,15 +1111,15 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     continue;
                 }
                 // (an item on both chains has one pair of weights a row, posted by chain 0, and chain 1's barrier beside)
-                ok = mbar_wait(bar(L::kWFull + c), (o_phase >> c) & 1u, ctx) &&
-                     (!merge || mbar_wait(bar(L::kWFull + 1), (o_phase >> 1) & 1u, ctx));
+                ok = mbar_wait(bar(L::kWFull + c), (o_phase >> c) & 1u, ctx_item) &&
+                     (!merge || mbar_wait(bar(L::kWFull + 1), (o_phase >> 1) & 1u, ctx_item));
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const float wa = merge ? weight[2 * rloc] : weight[c * 128 + rloc];
                 const float wb = merge ? weight[2 * rloc + 1] : 0.f;
                 mbar_arrive(bar(L::kWEmpty + c));
                 if (merge) mbar_arrive(bar(L::kWEmpty + 1));
-                ok = mbar_wait(bar(L::kOFull + c), (o_phase >> c) & 1u, ctx) &&
-                     (!merge || mbar_wait(bar(L::kOFull + 1), (o_phase >> 1) & 1u, ctx));
+                ok = mbar_wait(bar(L::kOFull + c), (o_phase >> c) & 1u, ctx_item) &&
+                     (!merge || mbar_wait(bar(L::kOFull + 1), (o_phase >> 1) & 1u, ctx_item));
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after_sync();
                 const uint32_t t_c = t_o + c * D;
