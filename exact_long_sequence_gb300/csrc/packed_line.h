@@ -95,7 +95,8 @@ struct LineSeq {
 // The line of the gradient: a unit is a tile of 128 keys of a sequence at one key
 // head with the tokens that see one of them, which are the last ones; its query
 // blocks of `block_tokens` = 64 / G tokens begin at the first of those.  A unit is
-// kKeyUnitBlocks blocks and then its tokens, one position each.
+// kKeyUnitBlocks blocks and then its tokens, one position each (24 texts of 10 to 2501 tokens, 24 heads of 4, with 2, 4,
+// 7, 10 and 14 blocks: 812, 793, 767, 779 and 791 us).
 constexpr int kKeyUnitBlocks = 7;
 constexpr int kKeyLineLeast = 8;   // blocks of the shortest stretch
 static ELS_HD_ONCE int64_t line_tiles_before(int nq, int nk, int unit_cost, bool causal, int64_t n) {
@@ -139,6 +140,17 @@ struct LinePart {
 ELS_HD int64_t line_stretch(int64_t total, int most, int least = kLineLeast) {
     const int64_t even = line_div(total + most - 1, most);
     return even < least ? least : even;
+}
+
+// Whether units of up to most_keys keys and most_rows rows a block are left whole on stretches of `len`, each at one stretch.
+// A cut costs pieces of its rows and their merge, a whole unit the wait for whoever has the longest: whole with up to
+// ten keys a row, and two and a half stretches to a unit.  Cut and whole (causal, 32 heads of 8 unless said): 24 prompts
+// of 20 to 2000 tokens 226 and 212 us, 1200 tokens 39 and 27, 2400 tokens at 16 heads of 4 50 and 40, 8 of 600 without
+// the mask 73 and 62; but 4 prompts of 100 to 4000 tokens 130 and 150, one of 4800 163 and 175, 7 clips of 500 to 6143
+// at 16 heads, d = 64, 380 and 414, 128 requests of one token 200 and 225.
+constexpr int kWholeRowKeys = 10;
+ELS_HD bool line_whole(int most_keys, int most_rows, int64_t len) {
+    return most_keys <= kWholeRowKeys * most_rows && 2 * (static_cast<int64_t>(kUnitCost) + most_rows + most_keys) <= 5 * len;
 }
 
 }  // namespace elsattn

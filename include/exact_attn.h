@@ -516,7 +516,7 @@ size_t attn_fwd_prefix_workspace_bytes(int R, int Hq, int Hk, int T, int P, int 
  * Arithmetic as attn_fwd (fp32 scores and sums, P rounded to bf16); pieces of a row's
  * keys are kept in fp32, O is rounded once.  The cut into pieces depends on the
  * lengths of all sequences, so bits may differ between batches, not between equal calls.
- * Two launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
+ * One or two launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
  */
 int attn_fwd_packed(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides, const void* V,
                     const int64_t* v_strides, const int32_t* q_starts, const int32_t* k_starts, void* O,
@@ -584,7 +584,7 @@ size_t attn_bwd_packed_workspace_bytes(int R, int Nq, int Nk, int Hq, int Hk, in
  *   d       : 64 or 128;  scale : any finite value;  R, T, pages, table_pages >= 1; R * Hq * T,
  *             pages and table_pages * page_size below 2^31 - 512
  *   workspace : attn_fwd_tree_workspace_bytes(), as above
- * Two launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
+ * One or two launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
  */
 int attn_fwd_tree(const void* Q, const int64_t* q_strides, const void* Kc, const int64_t* k_strides, const void* Vc,
                   const int64_t* v_strides, const int32_t* page_table, int64_t table_stride, const int32_t* lens,
