@@ -15,8 +15,9 @@ namespace elsattn {
 namespace {
 
 // Q, dO and the sums of dQ that the CTAs work on at a time: the line has a stretch a CTA for each so many bytes, up to
-// kBwdMostTurns (documents of 2000 to 16384 tokens, 16 heads of 8, with 48, 96 and 200 MB and uncut: 2927, 2926, 2909 and 3246 us).
-constexpr double kBwdTurnBytes = 96e6;
+// kBwdMostTurns (24 texts of 10 to 2501 tokens, 24 heads of 4, with 96, 200 and 300 MB: 757, 744 and 749 us; documents of 2000 to
+// 16384 tokens, 16 heads of 8, 2942, 2941 and 2947 us, and in one turn 3246 us).
+constexpr double kBwdTurnBytes = 200e6;
 constexpr int kBwdMostTurns = 4;
 
 int check(int R, int Nq, int Nk, int Hq, int Hk, int d) {
