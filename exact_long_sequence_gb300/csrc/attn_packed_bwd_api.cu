@@ -15,10 +15,11 @@ namespace elsattn {
 namespace {
 
 // Q, dO and the sums of dQ that the CTAs work on at a time: the line has a stretch a CTA for each so many bytes, up to
-// kBwdMostTurns (24 texts of 10 to 2501 tokens, 24 heads of 4, with 96, 200 and 300 MB: 757, 744 and 749 us; documents of 2000 to
-// 16384 tokens, 16 heads of 8, 2942, 2941 and 2947 us, and in one turn 3246 us).
-constexpr double kBwdTurnBytes = 200e6;
-constexpr int kBwdMostTurns = 4;
+// kBwdMostTurns.  A turn's bytes stay in L2; each costs its stretches' pieces (40 MB at d = 128).  32 texts of 2048 tokens, 32
+// heads of 8, with 4, 8, 12 and 15 turns: 4347, 3832, 3617 and 3606 us; 4 documents of 16384 with 4 and 15: 23.7 and 20.9 ms;
+// of 24 texts of 10 to 2501 tokens, 24 heads of 4, 4 turns in place of 3 cost 757 us for 744.
+constexpr double kBwdTurnBytes = 150e6;
+constexpr int kBwdMostTurns = 32;
 
 int check(int R, int Nq, int Nk, int Hq, int Hk, int d) {
     if (R < 1 || Nq < 1 || Nk < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0) return ATTN_ERR_INVALID_ARG;

@@ -116,3 +116,18 @@ def test_a_graph_whose_lengths_change_sides():
         assert ela.last_device_error() == ela.ATTN_OK
         check(out, lse, packed(q, k, v, cuts, cuts, True, ela.default_scale(d)))
         assert bool((out[:, cuts[-1]:] == 7).all()) and bool((lse[:, cuts[-1]:] == 7).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True])
+def test_several_turns(causal):
+    """As many bytes as give each CTA two stretches of the forward's line (above 128 MB of K and V) and three of the gradient's
+    (above 300 MB of Q, dO and dQ's sums), cut units among them."""
+    import torch
+
+    from test_packed import run
+    from test_packed_bwd import run as run_bwd
+    lens = torch.randint(0, 121, (150,), generator=torch.Generator().manual_seed(1)).tolist()
+    lens[70] = 3100
+    run(lens, Hq=32, Hk=32, d=128, causal=causal, seed=1)
+    run_bwd(lens, Hq=32, Hk=32, d=128, causal=causal, seed=2)
