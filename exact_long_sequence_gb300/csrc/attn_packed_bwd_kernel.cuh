@@ -22,6 +22,10 @@
 //   warp 2  row statistics of the blocks into the ring; zeroes rows of other sequences in an item's last block and key tile
 //   warp 3  scheduler: the CTA's items, through a ring of descriptions
 //   warps 4-7, 12-15  P and dS, then dV;  warps 8-11  dQ readout, then dK
+//
+// Measured, causal, d = 128: documents of 2000 to 16384 tokens, 16 heads of 8, 3.03 ms, 1.03 PFLOP/s, of which this kernel
+// 2.77 (tensor pipe 47 %, shared memory 51 % busy: operands of five products and dS through it); 24 texts of 10 to 2501
+// tokens, 24 heads of 4, 753 us, of which this kernel 570 (the ends of items) and the two passes over rows 149 (HBM, 6.3 TB/s).
 #pragma once
 
 #include <cuda.h>

@@ -33,6 +33,12 @@
 //   warps 4-7, 8-11  softmax warpgroups
 //   warps 12-15      epilogue: O from TMEM to memory.  While they write an item's O the softmax warps are at
 //     the next item's first tiles, which is what short sequences are made of.
+//
+// Measured, with 32 heads of 8, d = 128: documents of 3001 to 16384 tokens, causal, 2.17 ms, 1.42 PFLOP/s (the chain
+// of score product, softmax and output product; tensor pipe 66 % active); 24 prompts of 20 to 2000 tokens 212 us, 800
+// TFLOP/s (the ends of items, whose instructions come from far: tensor pipe 37 %); paged, single tokens of
+// 128 requests on up to 4099 keys 183 us, 5.9 TB/s, and trees of 24 drafts of 48 requests on up to 9001 167 us, 6.0 TB/s
+// (HBM).
 #pragma once
 
 #include <cuda.h>
