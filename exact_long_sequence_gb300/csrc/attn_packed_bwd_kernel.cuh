@@ -460,7 +460,9 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         bool ok = true;
         auto publish = [&](const PackedBwdItem& it) {
             const uint32_t s = n % kPkbItemRing;
-            if (n >= kPkbItemRing) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kItemEmpty + s), ((n / kPkbItemRing) - 1) & 1u, ctx));
+            if (n >= kPkbItemRing)  // for a whole item, whose length is the sequence's
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kItemEmpty + s), ((n / kPkbItemRing) - 1) & 1u,
+                                                       WaitCtx{ctx.abort_flag, ctx.error_word, 16 * ctx.timeout_ns}));
             if (!ok) return;
             if (lane == 0) {
                 *reinterpret_cast<PackedBwdItem*>(smem + L::kItemOff + s * sizeof(PackedBwdItem)) = it;

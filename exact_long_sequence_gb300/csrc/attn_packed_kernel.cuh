@@ -75,7 +75,7 @@ struct PackedParams {
     int orows;                 // partial rows kept for a piece
     bool causal;               // token t sees the keys j <= t + nk - nq
     int stretches;             // how many stretches the line has at most (a multiple of the grid)
-    bool whole;                // units are not cut: each is in the stretch that its start is in
+    bool whole;                // no unit is cut, whatever the lengths are: each is in the stretch that its middle is in
     __nv_bfloat16* o;
     int64_t os[3];             // strides in elements: request (paged), head, token
     float* lse;
