@@ -871,8 +871,7 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_prep_kernel(const PackedR
 }
 
 // The first kPkbCutCtas CTAs for each stretch add up the pieces of dK and dV of the unit that begins to be cut there, in the
-// pieces' order; the others round dQ's sums to bf16, rows of tokens that are in no sequence left as they were (q_starts is
-// non-decreasing).
+// pieces' order; the others round dQ's sums to bf16, rows of tokens that are in no sequence left as they were.
 constexpr int kPkbCutCtas = 8;   // each has 16 of the tile's 128 keys
 
 template <int D>
@@ -907,7 +906,7 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_
         }
         return;
     }
-    // Two rows' parts a thread, both under way before the search for their sequences.
+    // Two rows' parts a thread, both under way before the search for their tokens' sequences.
     constexpr int kRowsCta = 256 / kVecs;
     const int64_t rows = static_cast<int64_t>(q.Hq) * q.Nq;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x - cut_ctas) * (2 * kRowsCta) + threadIdx.x / kVecs;
@@ -927,16 +926,43 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_
             b[u] = __ldcs(z + 2 * part + 1);
         }
     }
+    // A token is in a sequence where the offsets rise past it.
+    bool in[2], missing = false;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        if (tok[u] < 0) return;
-        int lo = 0, hi = p.R;  // the last sequence that begins at or before the token
+        in[u] = false;
+        if (tok[u] < 0) continue;
+        int lo = 0, hi = p.R;
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
             if (__ldg(p.q_starts + mid) <= tok[u]) lo = mid + 1;
             else hi = mid;
         }
-        if (lo == 0 || tok[u] >= __ldg(p.q_starts + lo)) continue;
+        in[u] = lo > 0 && tok[u] < __ldg(p.q_starts + lo);
+        missing = missing || !in[u];
+    }
+    // Where the offsets fall (behind the last sequence of a padded batch, say) the search may miss a rise: then all are looked
+    // through, for the CTA's tokens at once (it has 64 rows at most, bit i is token t0 + i).
+    if (__syncthreads_or(missing)) {
+        __shared__ unsigned long long s_in;
+        if (threadIdx.x == 0) s_in = 0;
+        __syncthreads();
+        static_assert(2 * kRowsCta <= 64, "a bit for each token");
+        const int t0 = static_cast<int>(static_cast<int64_t>(blockIdx.x - cut_ctas) * (2 * kRowsCta) / q.Hq);
+        unsigned long long mine = 0;
+        for (int s = threadIdx.x; s < p.R; s += 256) {
+            const int from = max(__ldg(p.q_starts + s), t0), to = min(__ldg(p.q_starts + s + 1), t0 + 64);
+            if (from < to) mine |= (~0ull >> (64 - (to - from))) << (from - t0);
+        }
+        if (mine != 0) atomicOr(&s_in, mine);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (tok[u] >= 0) in[u] = s_in >> (tok[u] - t0) & 1;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        if (!in[u]) continue;
         reinterpret_cast<uint4*>(q.dq + h[u] * q.dqs[0] + tok[u] * q.dqs[1])[part] =
             make_uint4(pack_bf16x2(a[u].x, a[u].y), pack_bf16x2(a[u].z, a[u].w), pack_bf16x2(b[u].x, b[u].y), pack_bf16x2(b[u].z, b[u].w));
     }

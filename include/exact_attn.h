@@ -494,12 +494,12 @@ size_t attn_fwd_prefix_workspace_bytes(int R, int Hq, int Hk, int T, int P, int 
  *   Q, O    : bf16 [Hq, Nq, d] device views; Hq a multiple of Hk (at most 64 Hk, ATTN_ERR_UNSUPPORTED
  *             beyond), query head h reads key head h / (Hq / Hk)
  *   K, V    : bf16 [Hk, Nk, d] device views
- *   q_starts, k_starts : int32 [R + 1] device, non-decreasing: sequence s has the queries
+ *   q_starts, k_starts : int32 [R + 1] device: sequence s has the queries
  *             q_starts[s] .. q_starts[s + 1] - 1 and the keys k_starts[s] .. k_starts[s + 1] - 1,
  *             either of which may be none.  The two may be the same array.  Read on the device, so a
  *             captured graph may be replayed with other lengths.  Offsets outside the tensors are
- *             clipped to them, and a sequence whose end is before its start is empty; sequences must
- *             not overlap in Q (their rows would be written twice).
+ *             clipped to them, and a sequence whose end is before its start is empty (so zeros behind the
+ *             last sequence pad a batch); sequences must not overlap in Q (their rows would be written twice).
  *   causal  : not 0: query t of a sequence's n sees the keys j <= t + m - n of its m, so that the
  *             last query sees all of them; with more queries than keys the first see none
  *   A row that sees no key is O = 0, LSE = -inf.  Rows of tokens that are in no sequence stay
@@ -534,6 +534,7 @@ size_t attn_fwd_packed_workspace_bytes(int R, int Nq, int Nk, int Hq, int Hk, in
  *   Q, K, V, O, dO, dQ, dK, dV : bf16 device views shaped as in attn_fwd_packed (dO and dQ like
  *             Q, dK like K, dV like V), strides as there; O and LSE as attn_fwd_packed wrote them
  *   LSE     : fp32 [Hq, Nq] device, contiguous
+ *   q_starts, k_starts : as there; the sequences must not overlap in K either
  *   Rows of dQ, and of dK and dV, of tokens that are in no sequence stay as they were; keys that no query sees
  *   get 0, and so does a query that sees no key.  Rows of other sequences are not used, whatever
  *   they hold; a NaN or infinity reaches the gradients of its own sequence, also where a mask hides it.
