@@ -102,19 +102,21 @@ int launch(DeviceState& dev, const CUtensorMap (&maps)[5], const PackedParams& p
             return cuda_fail(e);
         configured = true;
     }
-    // Both are programmatic dependents of what is before them on the stream: each sets up beside its end.
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    // The first launch is a plain one.  As a programmatic dependent it would wait for the grid before it only, and
+    // where the caller's own grid is one that does not wait for those before, these could still run.
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms));
     cfg.blockDim = dim3(kPkThreads);
     cfg.dynamicSmemBytes = smem;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], p)) != cudaSuccess) return cuda_fail(e);
     if (p.whole) return ATTN_OK;
+    // The merge sets up beside the end of the first kernel, and waits for it.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     cfg.dynamicSmemBytes = 0;
     cfg.gridDim = dim3(static_cast<unsigned>(4 * dev.num_sms));
     cfg.blockDim = dim3(256);

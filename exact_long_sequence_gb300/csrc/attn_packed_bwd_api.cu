@@ -70,18 +70,20 @@ int launch(DeviceState& dev, const CUtensorMap& mq, const CUtensorMap& mk, const
     }
     const int64_t threads = static_cast<int64_t>(rows.Hq) * rows.Nq * (D / 8);
     const unsigned blocks = static_cast<unsigned>((threads + 255) / 256);
-    // Each is a programmatic dependent of what is before it on the stream, and waits for that once it is set up.
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    // The first launch is a plain one: a programmatic dependent waits for the grid before it only, and where the caller's
+    // own grid is one that does not wait for those before, these could still run.
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(256);
     if ((e = cudaLaunchKernelEx(&cfg, attn_packed_bwd_prep_kernel<D>, rows, dvec, p.dq_acc, p.scale)) != cudaSuccess)
         return cuda_fail(e);
+    // The other two each depend on the one before them, and wait for it once they are set up.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms));
     cfg.blockDim = dim3(kBwdThreads);
     cfg.dynamicSmemBytes = smem;

@@ -215,7 +215,7 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    // Up to here nothing is read or written that an earlier grid may write or read (the one before zeroes dQ's sums
+    // Up to here nothing is read or written that the grid before may write or read (it zeroes dQ's sums
     // and works out D): the setup overlaps its end.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -843,8 +843,7 @@ struct PackedRowParams {
 template <int D>
 __global__ void __launch_bounds__(256) attn_packed_bwd_prep_kernel(const PackedRowParams q, float* dvec, float* dq_acc, float scale) {
     constexpr int kTpr = D / 8;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the main kernel sets up beside this grid, and waits for it
     const int64_t tid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const int64_t row = tid / kTpr;  // token-major: (token, head)
     const int part = static_cast<int>(tid % kTpr);

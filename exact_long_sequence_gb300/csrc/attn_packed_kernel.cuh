@@ -377,11 +377,9 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    // Up to here nothing is read or written that an earlier grid may write or read; the setup overlaps its end.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    // The combine kernel may be scheduled onto SMs as this grid's CTAs retire;
+    // The combine kernel, where one follows, may be scheduled onto SMs as this grid's CTAs retire;
     // it waits for the whole grid before it reads the partial results.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!p.whole) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // Reads the next item (ring entry n); `it.ntiles` is -1 after the last.  Called by whole warps, whose
     // lanes get one word each from shared memory and hand it round, so that the fields are uniform.

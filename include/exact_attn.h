@@ -516,7 +516,7 @@ size_t attn_fwd_prefix_workspace_bytes(int R, int Hq, int Hk, int T, int P, int 
  * Arithmetic as attn_fwd (fp32 scores and sums, P rounded to bf16); pieces of a row's
  * keys are kept in fp32, O is rounded once.  The cut into pieces depends on the
  * lengths of all sequences, so bits may differ between batches, not between equal calls.
- * One or two launches on `stream`.  Kernel-side timeouts: attn_last_device_error().
+ * One or two launches on `stream`, the first behind all work before it there.  Kernel-side timeouts: attn_last_device_error().
  */
 int attn_fwd_packed(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides, const void* V,
                     const int64_t* v_strides, const int32_t* q_starts, const int32_t* k_starts, void* O,
