@@ -937,7 +937,7 @@ def debug_wait_timeout(timeout_ns: int, stream=None) -> int:
 
 
 def debug_arm_timeout(timeout_ns: int) -> int:
-    """Arm the one-shot abort hook: the next forward launch runs with this wait limit and
+    """Arm the one-shot abort hook: the next launch of a forward or packed call runs with this wait limit and
     withholds one of CTA 0's query-tile copies, so its wait runs out (test use only)."""
     return load_library().attn_debug_arm_timeout(int(timeout_ns))
 

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -116,6 +117,14 @@ int encode_u8_map(CUtensorMap* map, const void* base, uint64_t e0, uint64_t e1, 
     if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
     return ATTN_OK;
 }
+
+namespace {
+std::atomic<uint64_t> g_armed_timeout_ns{0};
+}  // namespace
+
+void arm_timeout(uint64_t timeout_ns) { g_armed_timeout_ns.store(timeout_ns); }
+
+uint64_t take_armed_timeout() { return g_armed_timeout_ns.exchange(0); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

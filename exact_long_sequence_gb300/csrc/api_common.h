@@ -66,6 +66,10 @@ int encode_u8_map(CUtensorMap* map, const void* base, uint64_t e0, uint64_t e1, 
 
 bool aligned16(const void* p);
 
+// Test hook (attn_debug_arm_timeout): a one-shot time limit for the next launch that takes it; 0: not armed.
+void arm_timeout(uint64_t timeout_ns);
+uint64_t take_armed_timeout();
+
 // Strides of a view in elements; nullptr: contiguous.  TMA takes strides of a
 // multiple of 16 bytes below 2^40; an axis of one is never stepped.
 template <int N>

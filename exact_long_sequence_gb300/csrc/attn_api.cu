@@ -42,13 +42,10 @@ void set_scale(FwdParams& p, float scale) {
     p.max_scale_log2 = scale == 0.f ? 0.f : p.scale_log2;
 }
 
-// Test hook (attn_debug_arm_timeout): a one-shot time limit for the next
-// forward launch, which also withholds CTA 0's first Q_0 copy; 0 = not armed.
-std::atomic<uint64_t> g_armed_timeout_ns{0};
-
-// Applies and disarms the hook, if armed.
+// Applies and disarms the test hook (attn_debug_arm_timeout), if armed: a time
+// limit, and CTA 0's first Q_0 copy is withheld.
 void take_armed_hook(FwdParams& p) {
-    const uint64_t t = g_armed_timeout_ns.exchange(0);
+    const uint64_t t = take_armed_timeout();
     if (t != 0) {
         p.timeout_ns = t;
         p.withhold_first_q = 1u;
@@ -428,7 +425,7 @@ extern "C" int attn_debug_wait_timeout(uint64_t timeout_ns, cudaStream_t stream)
 
 extern "C" int attn_debug_arm_timeout(uint64_t timeout_ns) {
     if (timeout_ns < 1000ull || timeout_ns > 1000000000ull) return ATTN_ERR_INVALID_ARG;
-    g_armed_timeout_ns.store(timeout_ns);
+    arm_timeout(timeout_ns);
     return ATTN_OK;
 }
 

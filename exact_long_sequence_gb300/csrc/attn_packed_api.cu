@@ -134,6 +134,10 @@ int run(DeviceState& dev, const CUtensorMap (&maps)[5], PackedParams& p, int d, 
     p.part_o = reinterpret_cast<float*>(ws + space.rows);
     p.error_word = dev.error_word;
     p.timeout_ns = kDefaultTimeoutNs;
+    if (const uint64_t t = take_armed_timeout()) {  // (test hook)
+        p.timeout_ns = t;
+        p.withhold_first_q = 1u;
+    }
     take_scale(p, scale);
     return d == 64 ? launch<64, PAGED>(dev, maps, p, stream) : launch<128, PAGED>(dev, maps, p, stream);
 }

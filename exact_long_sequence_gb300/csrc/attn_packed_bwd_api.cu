@@ -157,7 +157,6 @@ extern "C" int attn_bwd_packed(const void* Q, const int64_t* q_strides, const vo
     p.Nk = Nk;
     p.causal = causal != 0;
     p.error_word = dev->error_word;
-    p.timeout_ns = kDefaultTimeoutNs;
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     rows.o = static_cast<const __nv_bfloat16*>(O);
@@ -182,6 +181,11 @@ extern "C" int attn_bwd_packed(const void* Q, const int64_t* q_strides, const vo
     if ((st = q_map(&mq, Q, qs)) != ATTN_OK || (st = q_map(&mdo, dO, rows.dos)) != ATTN_OK ||
         (st = k_map(&mk, K, ks)) != ATTN_OK || (st = k_map(&mv, V, vs)) != ATTN_OK)
         return st;
+    p.timeout_ns = kDefaultTimeoutNs;
+    if (const uint64_t t = take_armed_timeout()) {  // (test hook)
+        p.timeout_ns = t;
+        p.withhold_first_block = 1u;
+    }
     return d == 64 ? launch<64>(*dev, mq, mk, mv, mdo, p, rows, dvec, stream)
                    : launch<128>(*dev, mq, mk, mv, mdo, p, rows, dvec, stream);
 }

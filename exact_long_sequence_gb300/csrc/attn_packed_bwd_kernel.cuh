@@ -58,6 +58,7 @@ struct PackedBwdParams {
     uint32_t* error_word;
     uint64_t timeout_ns;
     float scale, scale_log2;
+    uint32_t withhold_first_block;  // test hook: not 0 makes each even CTA arm its first block's barrier without the copies
 };
 
 // The unit whose pieces begin in a stretch (pieces: 0 where none is cut there).
@@ -269,10 +270,12 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
                     mbar_arrive_expect_tx(bar(L::kQFull + s), 2 * p.qrows * D * 2);
                     const uint32_t dst = s_base + L::kRingOff + s * L::kStageBytes;
                     const int tok = it.tok0 + i * p.block_tokens;
+                    if (!(p.withhold_first_block && blockIdx.x % 2 == 0 && cnt == 0)) {
 #pragma unroll
-                    for (int b = 0; b < D / 64; ++b) {
-                        tma_load_4d(dst + b * L::kQBlock, &tmap_q, bar(L::kQFull + s), b * 64, 0, it.head, tok);
-                        tma_load_4d(dst + L::kQTile + b * L::kQBlock, &tmap_do, bar(L::kQFull + s), b * 64, 0, it.head, tok);
+                        for (int b = 0; b < D / 64; ++b) {
+                            tma_load_4d(dst + b * L::kQBlock, &tmap_q, bar(L::kQFull + s), b * 64, 0, it.head, tok);
+                            tma_load_4d(dst + L::kQTile + b * L::kQBlock, &tmap_do, bar(L::kQFull + s), b * 64, 0, it.head, tok);
+                        }
                     }
                 }
                 __syncwarp();

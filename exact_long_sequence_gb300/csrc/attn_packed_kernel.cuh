@@ -87,6 +87,7 @@ struct PackedParams {
     uint64_t timeout_ns;
     float scale_log2, max_scale_log2;
     uint32_t negate_scores;
+    uint32_t withhold_first_q; // test hook: not 0 makes each even CTA arm its first query tile's barrier without the copy
 };
 
 // The unit whose pieces begin in a stretch (pieces: 0 where none is cut there).
@@ -836,10 +837,12 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 const uint32_t full = bar(L::kQFull + slot);
                 if (lane == 0) {  // whole tokens; what lies behind the tensor reads as zero
                     mbar_arrive_expect_tx(full, p.qrows * D * 2);
+                    if (!(p.withhold_first_q && blockIdx.x % 2 == 0 && qpos == 0)) {
 #pragma unroll
-                    for (int b = 0; b < D / 64; ++b)
-                        tma_load_5d(s_base + L::kQOff + slot * L::kTile + b * (kBr * 128), &tmap_q, full, b * 64, 0, it.head,
-                                    it.tok0 + k * p.tile_tokens, PAGED ? it.req : 0);
+                        for (int b = 0; b < D / 64; ++b)
+                            tma_load_5d(s_base + L::kQOff + slot * L::kTile + b * (kBr * 128), &tmap_q, full, b * 64, 0, it.head,
+                                        it.tok0 + k * p.tile_tokens, PAGED ? it.req : 0);
+                    }
                 }
                 q_slots |= 1u << slot;
                 q_parity = (q_parity & ~(1u << slot)) | (((qpos >> 1) & 1u) << slot);

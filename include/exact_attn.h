@@ -234,13 +234,15 @@ const char* attn_strerror(int status);
 int attn_debug_wait_timeout(uint64_t timeout_ns, cudaStream_t stream);
 
 /*
- * attn_debug_arm_timeout - test hook for the forward kernel's own abort path
+ * attn_debug_arm_timeout - test hook for the kernels' own abort path
  * (every wait is bounded: a role whose wait runs out records ATTN_ERR_TIMEOUT,
  * the other roles leave their loops, in-flight copies and MMAs are drained
  * and tensor memory is freed before the kernel returns).  Arms a one-shot:
  * the next forward launch of this process (attn_fwd, attn_fwd_split,
- * attn_fwd_noalloc; the first chunk of attn_fwd_host) runs with a wait limit
- * of timeout_ns (1 us .. 1 s) instead of 4 s, and its CTA 0 arms the barrier
+ * attn_fwd_noalloc; the first chunk of attn_fwd_host; attn_fwd_packed,
+ * attn_bwd_packed, attn_fwd_tree) runs with a wait limit
+ * of timeout_ns (1 us .. 1 s) instead of 4 s, and its CTA 0 (of the packed and
+ * paged calls each even CTA that has work) arms the barrier
  * of its first query-tile copy without issuing the copy, so the wait on it
  * runs out.  That launch's outputs are left partly unwritten; the status is
  * read with attn_last_device_error() (attn_noalloc_last_device_error() after
