@@ -915,6 +915,14 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_
     const int part = threadIdx.x % kVecs;
     float4 a[2], b[2];
     int tok[2], h[2];
+    auto sums = [&](int u) -> const float4* {
+        const int hk = h[u] / q.G;
+        return reinterpret_cast<const float4*>(p.dq_acc + ((static_cast<int64_t>(hk) * q.Nq + tok[u]) * q.G + (h[u] - hk * q.G)) * D) + 2 * part;
+    };
+    auto round_row = [&](int u, const float4& x, const float4& y) {
+        reinterpret_cast<uint4*>(q.dq + h[u] * q.dqs[0] + tok[u] * q.dqs[1])[part] =
+            make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    };
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int64_t row = row0 + u * kRowsCta;
@@ -922,52 +930,45 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_
         if (row < rows) {
             tok[u] = static_cast<int>(row / q.Hq);
             h[u] = static_cast<int>(row - static_cast<int64_t>(tok[u]) * q.Hq);
-            const int hk = h[u] / q.G;
-            const float4* z = reinterpret_cast<const float4*>(p.dq_acc + ((static_cast<int64_t>(hk) * q.Nq + tok[u]) * q.G + (h[u] - hk * q.G)) * D);
-            a[u] = __ldcs(z + 2 * part);
-            b[u] = __ldcs(z + 2 * part + 1);
+            const float4* z = sums(u);
+            a[u] = __ldcs(z);
+            b[u] = __ldcs(z + 1);
         }
     }
-    // A token is in a sequence where the offsets rise past it.
-    bool in[2], missing = false;
+    bool missing = false;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        in[u] = false;
-        if (tok[u] < 0) continue;
-        int lo = 0, hi = p.R;
+        if (tok[u] < 0) break;
+        int lo = 0, hi = p.R;  // a token is in a sequence where the offsets rise past it
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
             if (__ldg(p.q_starts + mid) <= tok[u]) lo = mid + 1;
             else hi = mid;
         }
-        in[u] = lo > 0 && tok[u] < __ldg(p.q_starts + lo);
-        missing = missing || !in[u];
-    }
-    // Where the offsets fall (behind the last sequence of a padded batch, say) the search may miss a rise: then all are looked
-    // through, for the CTA's tokens at once (it has 64 rows at most, bit i is token t0 + i).
-    if (__syncthreads_or(missing)) {
-        __shared__ unsigned long long s_in;
-        if (threadIdx.x == 0) s_in = 0;
-        __syncthreads();
-        static_assert(2 * kRowsCta <= 64, "a bit for each token");
-        const int t0 = static_cast<int>(static_cast<int64_t>(blockIdx.x - cut_ctas) * (2 * kRowsCta) / q.Hq);
-        unsigned long long mine = 0;
-        for (int s = threadIdx.x; s < p.R; s += 256) {
-            const int from = max(__ldg(p.q_starts + s), t0), to = min(__ldg(p.q_starts + s + 1), t0 + 64);
-            if (from < to) mine |= (~0ull >> (64 - (to - from))) << (from - t0);
+        if (lo > 0 && tok[u] < __ldg(p.q_starts + lo)) {
+            round_row(u, a[u], b[u]);
+            tok[u] = -1;
+        } else {
+            missing = true;
         }
-        if (mine != 0) atomicOr(&s_in, mine);
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            if (tok[u] >= 0) in[u] = s_in >> (tok[u] - t0) & 1;
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        if (!in[u]) continue;
-        reinterpret_cast<uint4*>(q.dq + h[u] * q.dqs[0] + tok[u] * q.dqs[1])[part] =
-            make_uint4(pack_bf16x2(a[u].x, a[u].y), pack_bf16x2(a[u].z, a[u].w), pack_bf16x2(b[u].x, b[u].y), pack_bf16x2(b[u].z, b[u].w));
+    // Where the offsets fall (behind the last sequence of a padded batch, say) the search may miss a rise: then the warp looks
+    // through all of them for the CTA's tokens at once (it has 64 rows at most; bit i is token t0 + i).  The sums are read
+    // again: kept until here they cost 10 us of 76 (20588 tokens, 24 heads of 128).
+    if (!__any_sync(0xffffffffu, missing)) return;
+    static_assert(2 * kRowsCta <= 64, "a bit for each token");
+    const int t0 = static_cast<int>(static_cast<int64_t>(blockIdx.x - cut_ctas) * (2 * kRowsCta) / q.Hq);
+    uint64_t bits = 0;
+    for (int s = threadIdx.x & 31; s < p.R; s += 32) {
+        const int from = max(__ldg(p.q_starts + s), t0), to = min(__ldg(p.q_starts + s + 1), t0 + 64);
+        if (from < to) bits |= (~0ull >> (64 - (to - from))) << (from - t0);
     }
+    const uint32_t low = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
+    const uint32_t high = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32));
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        if (tok[u] >= 0 && ((tok[u] - t0 < 32 ? low >> (tok[u] - t0) : high >> (tok[u] - t0 - 32)) & 1u))
+            round_row(u, __ldcs(sums(u)), __ldcs(sums(u) + 1));
 }
 
 }  // namespace elsattn
