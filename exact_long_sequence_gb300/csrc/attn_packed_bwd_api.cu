@@ -44,12 +44,12 @@ void lay_out(PackedBwdParams& p, int Nq, int Hq, int Hk, int d, int num_sms) {
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// Workspace: cuts, D of every row, dQ's sums, pieces of dV and dK.
+// Workspace: cuts and whether the offsets fall, D of every row, dQ's sums, pieces of dV and dK.
 struct Space {
     size_t dvec, dq, part, bytes;
     Space(const PackedBwdParams& p, int Nq, int d) {
         const size_t rows = static_cast<size_t>(p.Hk) * p.G * Nq;
-        dvec = align256(p.stretches * sizeof(PackedBwdCut));
+        dvec = align256(p.stretches * sizeof(PackedBwdCut) + sizeof(int));
         dq = dvec + align256(rows * sizeof(float));
         part = dq + rows * d * sizeof(float);
         bytes = part + (p.whole ? 0 : 2 * static_cast<size_t>(p.stretches) * kBc * 2 * d * sizeof(float));
@@ -144,6 +144,7 @@ extern "C" int attn_bwd_packed(const void* Q, const int64_t* q_strides, const vo
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* dvec = reinterpret_cast<float*>(ws + space.dvec);
     p.cuts = reinterpret_cast<PackedBwdCut*>(ws);
+    p.falls = reinterpret_cast<int*>(p.cuts + p.stretches);
     p.dvec = dvec;
     p.dq_acc = reinterpret_cast<float*>(ws + space.dq);
     p.part = reinterpret_cast<float*>(ws + space.part);

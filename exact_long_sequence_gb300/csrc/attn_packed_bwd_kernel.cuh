@@ -50,6 +50,7 @@ struct PackedBwdParams {
     int64_t dks[2], dvs[2];    // strides in elements: head, token
     float* part;               // [2 stretches][128 keys][dV | dK][d] fp32, slots as in the forward
     struct PackedBwdCut* cuts; // [stretches]
+    int* falls;                // whether q_starts falls somewhere (a sequence's end before its start)
     int R, Hk, G, Nq, Nk;
     int block_tokens, qrows;   // of a query block: whole tokens, and rows
     bool causal;
@@ -479,15 +480,19 @@ attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         int64_t mine = 0;
         PackedBwdSeq own{};
         int64_t own_len = 0;
+        bool falls = false;
 #pragma unroll 1
         for (int i = 0; i < run; ++i) {
             const int r = lane * run + i;
             if (r < p.R) {
                 own = packed_bwd_seq(p, r);
+                falls = falls || __ldg(p.q_starts + r + 1) < __ldg(p.q_starts + r);
                 own_len = own.line.length();
                 mine += own_len;
             }
         }
+        falls = __any_sync(0xffffffffu, falls);
+        if (blockIdx.x == 0 && lane == 0) *p.falls = falls;
         mine *= p.Hk;
         const int64_t upto = warp_scan64(mine, lane);
         const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
@@ -877,7 +882,7 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_prep_kernel(const PackedR
 constexpr int kPkbCutCtas = 8;   // each has 16 of the tile's 128 keys
 
 template <int D>
-__global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_constant__ PackedBwdParams p, const PackedRowParams q) {
+__global__ void __launch_bounds__(256, 6) attn_packed_bwd_post_kernel(const __grid_constant__ PackedBwdParams p, const PackedRowParams q) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kVecs = D / 8;  // 8 elements a thread
     const unsigned cut_ctas = p.whole ? 0u : static_cast<unsigned>(p.stretches) * kPkbCutCtas;
@@ -915,14 +920,6 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_
     const int part = threadIdx.x % kVecs;
     float4 a[2], b[2];
     int tok[2], h[2];
-    auto sums = [&](int u) -> const float4* {
-        const int hk = h[u] / q.G;
-        return reinterpret_cast<const float4*>(p.dq_acc + ((static_cast<int64_t>(hk) * q.Nq + tok[u]) * q.G + (h[u] - hk * q.G)) * D) + 2 * part;
-    };
-    auto round_row = [&](int u, const float4& x, const float4& y) {
-        reinterpret_cast<uint4*>(q.dq + h[u] * q.dqs[0] + tok[u] * q.dqs[1])[part] =
-            make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-    };
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int64_t row = row0 + u * kRowsCta;
@@ -930,45 +927,50 @@ __global__ void __launch_bounds__(256) attn_packed_bwd_post_kernel(const __grid_
         if (row < rows) {
             tok[u] = static_cast<int>(row / q.Hq);
             h[u] = static_cast<int>(row - static_cast<int64_t>(tok[u]) * q.Hq);
-            const float4* z = sums(u);
-            a[u] = __ldcs(z);
-            b[u] = __ldcs(z + 1);
+            const int hk = h[u] / q.G;
+            const float4* z = reinterpret_cast<const float4*>(p.dq_acc + ((static_cast<int64_t>(hk) * q.Nq + tok[u]) * q.G + (h[u] - hk * q.G)) * D);
+            a[u] = __ldcs(z + 2 * part);
+            b[u] = __ldcs(z + 2 * part + 1);
         }
     }
-    bool missing = false;
+    auto round_row = [&](int u) {
+        reinterpret_cast<uint4*>(q.dq + h[u] * q.dqs[0] + tok[u] * q.dqs[1])[part] =
+            make_uint4(pack_bf16x2(a[u].x, a[u].y), pack_bf16x2(a[u].z, a[u].w), pack_bf16x2(b[u].x, b[u].y), pack_bf16x2(b[u].z, b[u].w));
+    };
+    // Up to 256 offsets the CTA looks through all of them for its tokens at once (it has 64 rows at most; bit i is token t0 + i).
+    // So it does where offsets fall (behind the last sequence of a padded batch, say), which cannot be searched.  Looked
+    // through and searched, calls at 24 heads of 128: 24 texts, 20588 tokens, 740 and 752 us; 256 sequences in 40000 rows, half of
+    // them padding, 459 and 495; 2048 in as many 938 (eight goes) and 897.
+    if (p.R <= 256 || *p.falls != 0) {
+        __shared__ unsigned long long s_in;
+        if (threadIdx.x == 0) s_in = 0;
+        __syncthreads();
+        static_assert(2 * kRowsCta <= 64, "a bit for each token");
+        const int t0 = static_cast<int>(static_cast<int64_t>(blockIdx.x - cut_ctas) * (2 * kRowsCta) / q.Hq);
+        unsigned long long bits = 0;
+        for (int s = threadIdx.x; s < p.R; s += 256) {
+            const int from = max(__ldg(p.q_starts + s), t0), to = min(__ldg(p.q_starts + s + 1), t0 + 64);
+            if (from < to) bits |= (~0ull >> (64 - (to - from))) << (from - t0);
+        }
+        if (bits != 0) atomicOr(&s_in, bits);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (tok[u] >= 0 && (s_in >> (tok[u] - t0) & 1)) round_row(u);
+        return;
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        if (tok[u] < 0) break;
-        int lo = 0, hi = p.R;  // a token is in a sequence where the offsets rise past it
+        if (tok[u] < 0) return;
+        int lo = 0, hi = p.R;  // the last sequence that begins at or before the token
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
             if (__ldg(p.q_starts + mid) <= tok[u]) lo = mid + 1;
             else hi = mid;
         }
-        if (lo > 0 && tok[u] < __ldg(p.q_starts + lo)) {
-            round_row(u, a[u], b[u]);
-            tok[u] = -1;
-        } else {
-            missing = true;
-        }
+        if (lo == 0 || tok[u] >= __ldg(p.q_starts + lo)) continue;
+        round_row(u);
     }
-    // Where the offsets fall (behind the last sequence of a padded batch, say) the search may miss a rise: then the warp looks
-    // through all of them for the CTA's tokens at once (it has 64 rows at most; bit i is token t0 + i).  The sums are read
-    // again: kept until here they cost 10 us of 76 (20588 tokens, 24 heads of 128).
-    if (!__any_sync(0xffffffffu, missing)) return;
-    static_assert(2 * kRowsCta <= 64, "a bit for each token");
-    const int t0 = static_cast<int>(static_cast<int64_t>(blockIdx.x - cut_ctas) * (2 * kRowsCta) / q.Hq);
-    uint64_t bits = 0;
-    for (int s = threadIdx.x & 31; s < p.R; s += 32) {
-        const int from = max(__ldg(p.q_starts + s), t0), to = min(__ldg(p.q_starts + s + 1), t0 + 64);
-        if (from < to) bits |= (~0ull >> (64 - (to - from))) << (from - t0);
-    }
-    const uint32_t low = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
-    const uint32_t high = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32));
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-        if (tok[u] >= 0 && ((tok[u] - t0 < 32 ? low >> (tok[u] - t0) : high >> (tok[u] - t0 - 32)) & 1u))
-            round_row(u, __ldcs(sums(u)), __ldcs(sums(u) + 1));
 }
 
 }  // namespace elsattn

@@ -23,6 +23,11 @@ STARTS = [
     [90, 95, 30, 0, 20, 10, 0],               # sequences out of order
     [99, 0, 0, 0, 0],                         # none at all
     [-7, -3, 0, 100, 100, -(1 << 31)],
+    [0, 60, 100] + [0] * 400,                 # more of them than the gradient's last kernel looks through in one go
+    [0] + [7 * i for i in range(1, 12)] + [-1] * 300,
+    [1 << 30, 50, 20] + [61] * 300 + [90, 80],
+    [3, 60, 60, 61] + [91] * 300,             # as many that do not fall
+    list(range(5, 96)) + [95] * 257,
 ]
 
 
