@@ -21,9 +21,9 @@ constexpr double kTurnBytes = 128e6;
 constexpr int kMostTurns = 8;
 
 // Up to so many keys in all (of a request's cache: the host knows no lengths, but these bounds), no unit is cut and the launch that
-// merges pieces is left out: replayed from a graph, with it and without, 4 sequences of 64 tokens 11.4 and 9.1 us, one of 600 at
-// 8 heads 18.6 and 14.9, at 32 heads of 8 25.2 and 17.2; with more keys few heads lose (1200 at 8 heads 21.9 and 23.1, 2400 33.0 and
-// 36.0), and the kernel decides by the lengths (line_whole).
+// merges pieces is left out.  Cut and merged, and like this (causal, d = 128, replayed from a graph): 4 sequences of 64 tokens at
+// 8 heads 10.8 and 9.5 us, one of 600 19.0 and 15.8, at 32 heads of 8 26.1 and 17.8; with more keys few heads lose (1200 at 8 heads
+// 22.8 and 24.0, 2400 33.9 and 36.5), and the kernel decides by the lengths (line_whole).
 constexpr int kWholeKeys = 640;
 
 // Sizes that follow from the shape.  tokens, keys: most of a sequence; kv_bytes: of K and V together.

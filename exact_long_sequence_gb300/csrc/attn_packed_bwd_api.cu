@@ -16,8 +16,9 @@ namespace {
 
 // Q, dO and the sums of dQ that the CTAs work on at a time: the line has a stretch a CTA for each so many bytes, up to
 // kBwdMostTurns.  A turn's bytes stay in L2; each costs its stretches' pieces (40 MB at d = 128).  32 texts of 2048 tokens, 32
-// heads of 8, with 4, 8, 12 and 15 turns: 4347, 3832, 3617 and 3606 us; 4 documents of 16384 with 4 and 15: 23.7 and 20.9 ms;
-// of 24 texts of 10 to 2501 tokens, 24 heads of 4, 4 turns in place of 3 cost 757 us for 744.
+// heads of 8, with 4, 8, 12 and 15 turns: 4347, 3832, 3617 and 3606 us; 4 documents of 16384 with 4 and 15: 23.7 and 20.9 ms.
+// Between 150 and 200 MB a turn it is about even: the fourth turn of 24 texts of 10 to 2501 tokens, 24 heads of 4, costs
+// 757 us for 744, and documents of up to 16384 tokens, 16 heads of 8, read 2.7 GB in place of 6.5 in the same time.
 constexpr double kBwdTurnBytes = 150e6;
 constexpr int kBwdMostTurns = 32;
 
@@ -39,7 +40,9 @@ void lay_out(PackedBwdParams& p, int Nq, int Hq, int Hk, int d, int num_sms) {
     int turns = static_cast<int>(std::fmin(std::ceil(8.0 * Nq * Hq * d / kBwdTurnBytes), kBwdMostTurns));
     if (turns < 1) turns = 1;
     p.stretches = num_sms * turns;
-    p.whole = Nq <= kKeyLineLeast * p.block_tokens;  // no unit is longer than the shortest stretch: none is cut
+    // Up to eight blocks of tokens no unit is cut: each is left whole in the stretch where it starts (it may be nearly two of the
+    // shortest stretches long, with its own 7 blocks), and the workspace holds no pieces.
+    p.whole = Nq <= kKeyLineLeast * p.block_tokens;
 }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }

@@ -23,9 +23,13 @@
 //   warp 3  scheduler: the CTA's items, through a ring of descriptions
 //   warps 4-7, 12-15  P and dS, then dV;  warps 8-11  dQ readout, then dK
 //
-// Measured, causal, d = 128: documents of 2000 to 16384 tokens, 16 heads of 8, 3.03 ms, 1.03 PFLOP/s, of which this kernel
+// Measured, causal, d = 128: documents of 2000 to 16384 tokens, 16 heads of 8, 3.04 ms, 1.02 PFLOP/s, of which this kernel
 // 2.77 (tensor pipe 47 %, shared memory 51 % busy: operands of five products and dS through it); 24 texts of 10 to 2501
-// tokens, 24 heads of 4, 753 us, of which this kernel 570 (the ends of items) and the two passes over rows 149 (HBM, 6.3 TB/s).
+// tokens, 24 heads of 4, 741 us, of which this kernel 565 and the two passes over rows 146 (HBM, 6.4 TB/s).  In both this
+// kernel is bound by the chain of a block's products: 1.41 us a block and key tile on the documents (1972 an SM), where the products
+// alone would take 0.81, and 1.57 on the texts (360 an SM).  Of the texts' blocks 60 of 64 rows are filled (ten tokens of six
+// heads), and their tiles cross the diagonal: 16 % more products than the formulas ask for.  The ends of items and the
+// imbalance of the CTAs are a tenth of it.
 #pragma once
 
 #include <cuda.h>

@@ -34,11 +34,14 @@
 //   warps 12-15      epilogue: O from TMEM to memory.  While they write an item's O the softmax warps are at
 //     the next item's first tiles, which is what short sequences are made of.
 //
-// Measured, with 32 heads of 8, d = 128: documents of 3001 to 16384 tokens, causal, 2.17 ms, 1.42 PFLOP/s (the chain
-// of score product, softmax and output product; tensor pipe 66 % active); 24 prompts of 20 to 2000 tokens 212 us, 800
-// TFLOP/s (the ends of items, whose instructions come from far: tensor pipe 37 %); paged, single tokens of
-// 128 requests on up to 4099 keys 183 us, 5.9 TB/s, and trees of 24 drafts of 48 requests on up to 9001 167 us, 6.0 TB/s
-// (HBM).
+// Measured, with 32 heads of 8, d = 128: documents of 3001 to 16384 tokens, causal, 2.19 ms, 1.41 PFLOP/s (the chain
+// of score product, softmax and output product; tensor pipe 66 % active); 24 prompts of 20 to 2000 tokens 214 to 229 us, 740 to
+// 793 TFLOP/s (the ends of items, whose instructions come from far, and whole units of unequal size: tensor pipe 37 %); paged,
+// single tokens of 128 requests on up to 4099 keys 186 us, 5.8 TB/s, and trees of 24 drafts of 48 requests on up to 9001
+// 170 us, 5.9 TB/s (HBM).
+//
+// Bytes that a thread spills and reads back, at its 128 registers: packed 20 and 40 (d = 128), 16 and 32 (64); paged 12 and 28
+// (d = 128), 164 and 356 (64).
 #pragma once
 
 #include <cuda.h>
@@ -183,8 +186,6 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {
     return v;
 }
 
-// mbar_wait without a call: for the softmax warps, whose registers a call's would not fit beside.  (What they spilled came back
-// from L2, since 16 warps' stacks are more than the L1 that the tiles leave: 3000 cycles at each end of an item.)
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -195,6 +196,8 @@ __device__ __forceinline__ int lds(uint32_t addr) {
     asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+// mbar_wait without a call: for the softmax warps, whose registers a call's would not fit beside.  (What they spilled came back
+// from L2, since 16 warps' stacks are more than the L1 that the tiles leave: 3000 cycles at each end of an item.)
 __device__ __forceinline__ bool mbar_wait_inline(uint32_t bar, uint32_t parity, uint32_t abort_flag, const PackedParams& p) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
@@ -988,7 +991,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     if (masked) packed_hide(t_s, lim - key0, PAGED && p.mask ? mask_row : nullptr, p.T, key0 - all_see);
                     // With 16 warps a thread has 128 registers, half of what the scores and their exponentials would
                     // take: they are read for the maximum, and again 16 keys ahead of the exponentials (32 ahead, a thread
-                    // spilled 20 registers: 24 prompts of 20 to 2000 tokens in 250 us, 234 like this).
+                    // spilled 20 registers more: 24 prompts of 20 to 2000 tokens in 250 us, 234 like this).
                     uint32_t ra[32], rb[32];
                     auto largest = [](const uint32_t (&r)[32]) {
                         const float* sc = reinterpret_cast<const float*>(r);

@@ -144,10 +144,10 @@ ELS_HD int64_t line_stretch(int64_t total, int most, int least = kLineLeast) {
 
 // Whether units of up to most_keys keys and most_rows rows a block are left whole on stretches of `len`, each at one stretch.
 // A cut costs pieces of its rows and their merge, a whole unit the wait for whoever has the longest: whole with up to
-// ten keys a row, and two and a half stretches to a unit.  Cut and whole (causal, 32 heads of 8 unless said): 24 prompts
-// of 20 to 2000 tokens 226 and 212 us, 1200 tokens 39 and 27, 2400 tokens at 16 heads of 4 50 and 40, 8 of 600 without
-// the mask 73 and 62; but 4 prompts of 100 to 4000 tokens 130 and 150, one of 4800 163 and 175, 7 clips of 500 to 6143
-// at 16 heads, d = 64, 380 and 414, 128 requests of one token 200 and 225.
+// ten keys a row, and two and a half stretches to a unit.  Cut and whole, us (causal, 32 heads of 8 unless said, replayed from a
+// graph): 24 prompts of 20 to 2000 tokens 223 and 204 (210 and 199 in the order of their lengths), 1200 tokens 40 and 28, 2400
+// tokens at 16 heads of 4 51 and 40, 8 of 600 without the mask 73 and 62; but 4 prompts of 100 to 4000 tokens 157 and 163, one of
+// 4800 164 and 175, 7 clips of 500 to 6143 at 16 heads, d = 64, 372 and 406, 128 requests of one token 184 and 204.
 constexpr int kWholeRowKeys = 10;
 ELS_HD bool line_whole(int most_keys, int most_rows, int64_t len) {
     return most_keys <= kWholeRowKeys * most_rows && 2 * (static_cast<int64_t>(kUnitCost) + most_rows + most_keys) <= 5 * len;

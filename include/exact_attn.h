@@ -526,7 +526,8 @@ int attn_fwd_packed(const void* Q, const int64_t* q_strides, const void* K, cons
                     float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Device bytes attn_fwd_packed needs as workspace on the current device (its
- * partial rows); 0 for an invalid shape or without a device. */
+ * partial rows); 0 for an invalid shape or without a device.  Room for the most that any lengths can cut: next to
+ * nothing up to 640 keys in all, else up to 40 MB at d = 128 (20 MB at 64), for each 128 MB of K and V again, at most 8 times. */
 size_t attn_fwd_packed_workspace_bytes(int R, int Nq, int Nk, int Hq, int Hk, int d);
 
 /*
@@ -555,7 +556,8 @@ int attn_bwd_packed(const void* Q, const int64_t* q_strides, const void* K, cons
 
 /* Device bytes attn_bwd_packed needs as workspace on the current device (the
  * sums of dQ, a number per row, pieces of dK and dV); 0 for an invalid shape or
- * without a device. */
+ * without a device.  4 (d + 1) bytes for each row of Q, and, for more tokens than 8 blocks of 64 / (Hq / Hk), room for the most
+ * that any lengths can cut: 40 MB at d = 128 (20 MB at 64), for each 150 MB of Q, dO and the sums again, at most 32 times. */
 size_t attn_bwd_packed_workspace_bytes(int R, int Nq, int Nk, int Hq, int Hk, int d);
 
 /*
@@ -595,8 +597,8 @@ int attn_fwd_tree(const void* Q, const int64_t* q_strides, const void* Kc, const
                   int pages, int page_size, int table_pages, int d, float scale, void* workspace, size_t workspace_bytes,
                   cudaStream_t stream);
 
-/* Device bytes attn_fwd_tree needs as workspace on the current device; 0 for an
- * invalid shape or without a device. */
+/* Device bytes attn_fwd_tree needs as workspace on the current device (up to 40 MB at d = 128, 20 MB at 64, whatever
+ * the cache holds); 0 for an invalid shape or without a device. */
 size_t attn_fwd_tree_workspace_bytes(int R, int Hq, int Hk, int T, int d);
 
 #ifdef __cplusplus
