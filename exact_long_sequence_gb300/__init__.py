@@ -709,7 +709,8 @@ def attn_fwd_packed(q, k, v, q_starts, k_starts=None, causal: bool = False, scal
 
     q         : bf16 CUDA [Hq, Nq, d], d in {64, 128}
     k, v      : bf16 [Hk, Nk, d], Hk a divisor of Hq
-    q_starts  : int32 [sequences + 1] on the device: sequence s has the queries q_starts[s] .. q_starts[s + 1] - 1
+    q_starts  : int32 [sequences + 1] on the device: sequence s has the queries q_starts[s] .. q_starts[s + 1] - 1; none
+                where its end is not behind its start (zeros behind the last sequence pad a batch)
     k_starts  : the same of its keys; None: q_starts (self-attention)
     causal    : query t of n sees the keys j <= t + m - n of the sequence's m (its last query sees all of them);
                 otherwise every query sees all of its sequence's keys

@@ -1,5 +1,7 @@
-"""Packed and paged calls on tensors of more than 2^31 elements, and the gradient in its most turns (GPU).  Only some
-sequences, at the ends and in the middle, are compared with the definition."""
+"""Packed and paged calls on tensors of more than 2^31 elements or on 2^24 keys, and the gradient in its most turns (GPU).
+Only some sequences, at the ends and in the middle, are compared with the definition."""
+import math
+
 import pytest
 import torch
 
@@ -66,3 +68,18 @@ def test_pages(token_major):
     out, lse = ela.attn_fwd_tree(q, kc, vc, table, dev(lens), bits(seen).cuda())
     assert ela.last_device_error() == ela.ATTN_OK
     check(out, lse, tree(q, kc, vc, table, lens, seen, ela.default_scale(d)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_keys(d):
+    """A request whose table names four pages again and again: the softmax over them once, and the log-sum-exp moved by the
+    logarithm of how often.  A piece's rows are sums of 2^17 keys' terms in fp32, in steps of 16: off by at most 2^13 roundings of
+    2^-24, which check()'s 2^-11 of the terms' sum holds."""
+    page, times = 1024, 4096
+    kc, vc, q = rand(1, 4, 1, page, d), rand(2, 4, 1, page, d), rand(3, 1, 4, 1, d)
+    table = torch.arange(4, dtype=torch.int32, device="cuda").repeat(times)[None].contiguous()
+    out, lse = ela.attn_fwd_tree(q, kc, vc, table, dev([4 * page * times]))
+    assert ela.last_device_error() == ela.ATTN_OK
+    seen = torch.ones((1, 1, 1), dtype=torch.bool, device="cuda")
+    ro, rl, ra = tree(q, kc, vc, table[:, :4], [4 * page], seen, ela.default_scale(d))
+    check(out, lse, (ro, rl + math.log(times), ra))
